@@ -27,6 +27,8 @@ __all__ = [
     "geg_version", "geg_launch_count", "GEG_OP_NF4_FWD", "GEG_OP_MXFP4_FWD", "GEG_OP_NF4_DGRAD",
     "GEG_OP_NF4_BLOCK", "GEG_OP_MXFP4_BLOCK", "GEG_OP_MXFP4_DGRAD", "DEVERR_NEGATIVE_SIZE", "DEVERR_SIZES_EXCEED_M", "DEVERR_FP16_RANGE",
     "DEVERR_BAD_EXPERT_ID",
+    "gmxfp4_quantize", "route_topk", "route_topk_grad", "route_combine_grad",
+    "gnf4_moe_layer", "gmxfp4_moe_layer", "router_gate", "dispatch_rows", "combine_rows",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -121,6 +123,18 @@ def lib() -> ctypes.CDLL:
             for name in ("gnf4_expert_block", "gmxfp4_expert_block"):
                 f = getattr(L, name)
                 f.argtypes, f.restype = block_args, ctypes.c_int
+            L.gmxfp4_quantize.argtypes = [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P]
+            L.geg_route_topk.argtypes = [_P, _I32, _I64, _I32, _I32, _I32, _P, _P, _P, _P]
+            L.geg_route_topk_grad.argtypes = [_P, _P, _I32, _P, _P, _I64, _I32, _I32, _I32, _P, _P]
+            L.geg_route_combine_grad.argtypes = [_P, _P, _P, _P, _P, _I64, _I32, _I64, _P, _P, _P]
+            L.geg_moe_layer_workspace_bytes.argtypes = [_I64, _I32, _I64]
+            L.geg_moe_layer_workspace_bytes.restype = _SZ
+            for name in ("gmxfp4_quantize", "geg_route_topk", "geg_route_topk_grad", "geg_route_combine_grad"):
+                getattr(L, name).restype = ctypes.c_int
+            for name in ("gnf4_moe_layer", "gmxfp4_moe_layer"):
+                f = getattr(L, name)
+                f.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I32, _P, _SZ, _P, _P]
+                f.restype = ctypes.c_int
             L.geg_workspace_bytes.argtypes = [_I32, _I64, _I64, _I64, _I32, _P]
             L.geg_workspace_bytes.restype = _SZ
             L.geg_workspace_init.argtypes, L.geg_workspace_init.restype = [_P, _SZ, _P], ctypes.c_int
@@ -726,3 +740,293 @@ def gnf4_quantize(w, stream=None):
     absmax = torch.empty(w.shape[:-1] + (K // 64,), dtype=torch.float32, device=w.device)
     _check(lib().gnf4_quantize(_ptr(w), _ptr(codes), _ptr(absmax), rows, K, _stream(stream)))
     return codes, absmax
+
+
+# ----------------------------------------------------------------------------- MXFP4 packer, gate, few-token layer
+_DTYPES = {}
+
+
+def _dtype(t, name):
+    """GEG_BF16 / GEG_F16 / GEG_F32 of a tensor, refused otherwise."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise GegError(2, f"{name}: expected a bfloat16, float16 or float32 tensor, got {t.dtype}")
+    return code
+
+
+def _on_device(ref, *ts):
+    """Every tensor on ref's device, and that the current one: kernels launch on the
+    current device's streams."""
+    import torch
+    _require_gpu(ref)
+    for t in ts:
+        if t is not None and t.device != ref.device:
+            _require_gpu(t)
+            raise GegError(4, f"tensors on several devices: {ref.device} and {t.device}")
+    if ref.device.index != torch.cuda.current_device():
+        raise GegError(4, f"tensors are on {ref.device} but the current device is "
+                          f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device(...)")
+
+
+def _outlive(stream, *ts):
+    """Tensors allocated here for a call on another stream than the current one stay
+    allocated until that stream's work is done."""
+    import torch
+    if stream is None:
+        return
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    if stream != torch.cuda.current_stream():
+        for t in ts:
+            if t is not None:
+                t.record_stream(stream)
+
+
+_stream_ws = {}
+
+
+def _layer_workspace(ws, need, device, stream):
+    """The caller's workspace, or one of this library's own for the (device, stream)
+    pair, so that calls on two streams never share one. During a graph capture each
+    call gets its own from the graph's memory pool, which lives as long as the graph."""
+    import torch
+    if ws is not None:
+        return ws.ensure(need, stream)
+    if torch.cuda.is_current_stream_capturing():
+        return Workspace(need, device)
+    h = _stream(stream).value or 0
+    ws = _stream_ws.get((device.index, h))
+    if ws is None:
+        ws = _stream_ws[device.index, h] = Workspace(max(need, 1 << 20), device)
+    return ws.ensure(need, stream)
+
+
+def gmxfp4_quantize(x, values: bool = False, stream=None):
+    """MXFP4-pack x [..., K] (bf16, fp16 or fp32; K % 32 == 0) on the GPU -> (blocks uint8
+    [..., K/2], scales uint8 [..., K/32]), with values=True also the values that the
+    codes stand for, in x's type (exact): what a quantisation-aware forward pass uses.
+
+    A 2-D x may have rows further apart than K (a slice of columns); its rows have to
+    start at multiples of 16 bytes. Blocks holding an inf or NaN decode to NaN."""
+    import torch
+    dt = _dtype(x, "x")
+    K = x.shape[-1] if x.dim() else 0
+    if K <= 0 or K % 32:
+        raise GegError(2, f"x: the last dimension must be a positive multiple of 32, got shape {list(x.shape)}")
+    rows = x.numel() // K
+    if x.is_contiguous():
+        ld = K
+    elif x.dim() == 2 and x.stride(1) == 1 and x.stride(0) >= K:
+        ld = x.stride(0)
+    else:
+        raise GegError(2, f"x: expected a contiguous tensor, or a 2-D one of contiguous rows, got strides "
+                          f"{list(x.stride())} of shape {list(x.shape)}")
+    _on_device(x)
+    lead = x.shape[:-1]
+    codes = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
+    scales = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
+    vals = torch.empty(x.shape, dtype=x.dtype, device=x.device) if values else None
+    _check(lib().gmxfp4_quantize(_ptr(x), dt, rows, K, ld, _ptr(codes), _ptr(scales), _ptr(vals), _stream(stream)))
+    _outlive(stream, codes, scales, vals)
+    return (codes, scales, vals) if values else (codes, scales)
+
+
+def route_topk(logits, k: int, renormalize: bool = True, error_word=None, stream=None):
+    """The router's gate: logits [T, E] (bf16, fp16 or fp32) -> (weights fp32 [T, k], ids
+    int32 [T, k]): the k largest logits, largest first, ties to the lower expert, and
+    their softmax weights, over all experts or renormalised over the chosen ones. NaN
+    logits count as -inf and flag DEVERR_NON_FINITE in error_word (None, or a device
+    int32 tensor of one element, OR-ed in)."""
+    import torch
+    dt = _dtype(logits, "logits")
+    if logits.dim() != 2 or not logits.is_contiguous():
+        raise GegError(2, f"logits: expected a contiguous [T, E] tensor, got {list(logits.shape)}")
+    T, E = logits.shape
+    _check_tensor(error_word, "error_word", torch.int32, (1,))
+    _on_device(logits, error_word)
+    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+    _check(lib().geg_route_topk(_ptr(logits), dt, T, E, k, int(renormalize), _ptr(weights), _ptr(ids),
+                                _ptr(error_word), _stream(stream)))
+    _outlive(stream, weights, ids)
+    return weights, ids
+
+
+def route_topk_grad(dweights, logits, ids, weights, renormalize: bool = True, stream=None):
+    """Gradient of route_topk's weights: dweights fp32 [T, k] and the forward's logits,
+    ids and weights -> dlogits [T, E] in the logits' type."""
+    import torch
+    dt = _dtype(logits, "logits")
+    if logits.dim() != 2 or not logits.is_contiguous() or ids.dim() != 2:
+        raise GegError(2, "logits: expected a contiguous [T, E] tensor and ids [T, k]")
+    T, E = logits.shape
+    k = ids.shape[1]
+    _check_tensor(ids, "ids", torch.int32, (T, k))
+    _check_tensor(weights, "weights", torch.float32, (T, k))
+    _check_tensor(dweights, "dweights", torch.float32, (T, k))
+    _on_device(logits, ids, weights, dweights)
+    dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _check(lib().geg_route_topk_grad(_ptr(dweights), _ptr(logits), dt, _ptr(ids), _ptr(weights), T, E, k,
+                                     int(renormalize), _ptr(dlogits), _stream(stream)))
+    _outlive(stream, dlogits)
+    return dlogits
+
+
+def route_combine_grad(dout, y, row_of, weights, src_of=None, stream=None):
+    """Gradient of route_combine: dout bf16 [T, N], the forward's y bf16 [T*k, N], row_of
+    int32 [T*k] and weights fp32 [T, k] -> (dy bf16 [T*k, N], dweights fp32 [T, k]).
+    Rows of dy that no entry lands on are set to 0 when route_sort's src_of is given,
+    else left as they were allocated."""
+    import torch
+    if weights.dim() != 2 or dout.dim() != 2:
+        raise GegError(2, "weights: expected [T, k], dout [T, N]")
+    T, k = weights.shape
+    N = dout.shape[1]
+    _check_tensor(dout, "dout", torch.bfloat16, (T, N))
+    _check_tensor(y, "y", torch.bfloat16, (T * k, N))
+    _check_tensor(row_of, "row_of", torch.int32, (T * k,))
+    _check_tensor(src_of, "src_of", torch.int32, (T * k,))
+    _check_tensor(weights, "weights", torch.float32, (T, k))
+    _on_device(dout, y, row_of, weights, src_of)
+    dy = torch.empty((T * k, N), dtype=torch.bfloat16, device=dout.device)
+    dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
+    _check(lib().geg_route_combine_grad(_ptr(dout), _ptr(y), _ptr(row_of), _ptr(src_of), _ptr(weights), T, k, N,
+                                        _ptr(dy), _ptr(dw), _stream(stream)))
+    _outlive(stream, dy, dw)
+    return dy, dw
+
+
+def _moe_layer(nf4, x, topk_ids, topk_weights, w13, s13, w2, s2, out, workspace, opts, stream, check_errors):
+    import torch
+    if x.dim() != 2 or topk_ids.dim() != 2 or w13.dim() != 3:
+        raise GegError(2, "x: expected [T, H], topk_ids [T, k], w13 [E, 2I, H/2]")
+    T, H = x.shape
+    k = topk_ids.shape[1]
+    E, I = w13.shape[0], w13.shape[1] // 2
+    _check_tensor(x, "x", torch.bfloat16, (T, H))
+    _check_tensor(topk_ids, "topk_ids", torch.int32, (T, k))
+    _check_tensor(topk_weights, "topk_weights", torch.float32, (T, k))
+    _check_packed(nf4, w13, s13, E, 2 * I, H, "w13", "scales13")
+    _check_packed(nf4, w2, s2, E, H, I, "w2", "scales2")
+    _check_tensor(out, "out", torch.bfloat16, (T, H))
+    _on_device(x, topk_ids, topk_weights, w13, s13, w2, s2, out)
+    mine = out is None
+    if mine:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    L = lib()
+    ws = _layer_workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x.device, stream)
+    f = L.gnf4_moe_layer if nf4 else L.gmxfp4_moe_layer
+    _check(f(_ptr(x), _ptr(topk_ids), _ptr(topk_weights), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(out), T, k, H,
+             I, E, _ptr(ws.buf), ws.nbytes, ctypes.byref(opts) if opts else None, _stream(stream)))
+    if mine:
+        _outlive(stream, out)
+    _check_device_errors(ws, check_errors, stream)
+    return out
+
+
+def gnf4_moe_layer(x, topk_ids, topk_weights, w13, absmax13, w2, absmax2, out=None,
+                   workspace: Workspace | None = None, opts: Opts | None = None, stream=None,
+                   check_errors: bool = False):
+    """The routed experts of a whole MoE layer for a few tokens (T <= 16, T * k <= 256), in
+    two launches: x bf16 [T, H], topk_ids int32 [T, k] and topk_weights fp32 [T, k] (as
+    route_topk returns them), NF4 weights as gnf4_expert_block takes them -> out bf16
+    [T, H] = sum over slots of weight * down(silu(gate) * up). Larger batches:
+    route_sort, gnf4_expert_block, route_combine."""
+    return _moe_layer(True, x, topk_ids, topk_weights, w13, absmax13, w2, absmax2, out, workspace, opts, stream,
+                      check_errors)
+
+
+def gmxfp4_moe_layer(x, topk_ids, topk_weights, blocks13, scales13, blocks2, scales2, out=None,
+                     workspace: Workspace | None = None, opts: Opts | None = None, stream=None,
+                     check_errors: bool = False):
+    """The same layer on MXFP4 weights as gmxfp4_expert_block takes them."""
+    if blocks13.dim() == 4:
+        blocks13 = blocks13.reshape(blocks13.shape[0], blocks13.shape[1], -1)
+    if blocks2.dim() == 4:
+        blocks2 = blocks2.reshape(blocks2.shape[0], blocks2.shape[1], -1)
+    return _moe_layer(False, x, topk_ids, topk_weights, blocks13, scales13, blocks2, scales2, out, workspace, opts,
+                      stream, check_errors)
+
+
+def _make_router_gate():
+    import torch
+
+    class RouterGate(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, logits, k, renormalize):
+            weights, ids = route_topk(logits, k, renormalize)
+            ctx.save_for_backward(logits, ids, weights)
+            ctx.renormalize = renormalize
+            ctx.mark_non_differentiable(ids)
+            return weights, ids
+
+        @staticmethod
+        def backward(ctx, dweights, _):
+            logits, ids, weights = ctx.saved_tensors
+            return route_topk_grad(dweights.contiguous(), logits, ids, weights, ctx.renormalize), None, None
+
+    return RouterGate
+
+
+def _make_dispatch_rows():
+    import torch
+
+    class DispatchRows(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, topk_ids, E):
+            sizes, row_of, src_of, xs = route_sort(topk_ids, E, x)
+            ctx.save_for_backward(row_of)
+            ctx.k = topk_ids.shape[1]
+            ctx.mark_non_differentiable(sizes, row_of, src_of)
+            return xs, sizes, row_of, src_of
+
+        @staticmethod
+        def backward(ctx, dxs, *_):
+            row_of, = ctx.saved_tensors
+            return route_combine(dxs.contiguous(), row_of, None, ctx.k), None, None
+
+    return DispatchRows
+
+
+def _make_combine_rows():
+    import torch
+
+    class CombineRows(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, y, weights, row_of, src_of):
+            ctx.save_for_backward(y, weights, row_of, src_of)
+            return route_combine(y, row_of, weights, weights.shape[1])
+
+        @staticmethod
+        def backward(ctx, dout):
+            y, weights, row_of, src_of = ctx.saved_tensors
+            dy, dw = route_combine_grad(dout.contiguous(), y, row_of, weights, src_of)
+            return dy, dw, None, None
+
+    return CombineRows
+
+
+_RouterGate = _LazyFn(_make_router_gate)
+_DispatchRows = _LazyFn(_make_dispatch_rows)
+_CombineRows = _LazyFn(_make_combine_rows)
+
+
+def router_gate(logits, k: int, renormalize: bool = True):
+    """route_topk as a torch autograd op: (weights fp32 [T, k], ids int32 [T, k]), the
+    weights differentiable with respect to the logits."""
+    return _RouterGate.apply(logits, int(k), bool(renormalize))
+
+
+def dispatch_rows(x, topk_ids, E: int):
+    """route_sort with the gather as a torch autograd op: x bf16 [T, H] -> (x_sorted bf16
+    [T*k, H], sizes, row_of, src_of); the backward adds each token's k rows."""
+    return _DispatchRows.apply(x, topk_ids, int(E))
+
+
+def combine_rows(y, weights, row_of, src_of):
+    """route_combine as a torch autograd op, differentiable with respect to the expert
+    outputs y bf16 [T*k, N] and the router weights fp32 [T, k]."""
+    return _CombineRows.apply(y, weights, row_of, src_of)

@@ -905,6 +905,192 @@ geg_status geg_route_combine(const void* y, const int32_t* row_of, const float* 
   return GEG_OK;
 }
 
+static size_t dtype_bytes(int32_t dtype) { return dtype == GEG_F32 ? 4 : 2; }
+
+geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K, int64_t ld, uint8_t* blocks,
+                           uint8_t* scales, void* values, hipStream_t stream) {
+  if (dtype < GEG_BF16 || dtype > GEG_F32) return fail(GEG_ERR_BAD_OPTION, "dtype must be GEG_BF16, GEG_F16 or GEG_F32");
+  if (rows < 0 || K <= 0 || K % 32) return fail(GEG_ERR_BAD_SHAPE, "need rows >= 0, K > 0, K % 32 == 0");
+  if (ld < K) return fail(GEG_ERR_BAD_SHAPE, "the row pitch ld must be at least K");
+  // one thread per 4 values at least, at most 2^31 - 1 workgroups of 256
+  if (K > ((int64_t)1 << 40) || rows > ((int64_t)1 << 40) / K || ld > ((int64_t)1 << 60) / std::max<int64_t>(rows, 1))
+    return fail(GEG_ERR_BAD_SHAPE, "rows * K must not exceed 2^40");
+  if (rows == 0) return GEG_OK;
+  if (!x || !blocks || !scales) return fail(GEG_ERR_NULL_POINTER, "x, blocks and scales are required");
+  if (!aligned(x, 16) || (rows > 1 && (ld * dtype_bytes(dtype)) % 16) || !aligned(blocks, 4) ||
+      (values && !aligned(values, 16)))
+    return fail(GEG_ERR_MISALIGNED, "x, its row pitch and values must be 16-byte aligned, blocks 4-byte");
+  geg_status st;
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{x, "x"}, {blocks, "blocks"}, {scales, "scales"},
+                           {values, "values"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  // a single row has no pitch
+  hipError_t e = geg::launch_mxfp4_quantize(x, dtype, rows, K, rows == 1 ? K : ld, blocks, scales, values, cu_count(),
+                                            stream);
+  if (e != hipSuccess) return hip_fail(e, "MXFP4 quantisation launch");
+  ++g_launches;
+  return GEG_OK;
+}
+
+static geg_status check_gate(int32_t dtype, int64_t T, int32_t E, int32_t k) {
+  if (dtype < GEG_BF16 || dtype > GEG_F32) return fail(GEG_ERR_BAD_OPTION, "dtype must be GEG_BF16, GEG_F16 or GEG_F32");
+  if (T < 0 || E <= 0 || k <= 0) return fail(GEG_ERR_BAD_SHAPE, "need T >= 0, E > 0, k > 0");
+  if (E > geg::kMaxExperts) return fail(GEG_ERR_BAD_SHAPE, "E exceeds 1024 experts");
+  if (k > E || k > 64) return fail(GEG_ERR_BAD_SHAPE, "k must not exceed E or 64");
+  if (T >= (int64_t)INT32_MAX || T * (int64_t)k >= (int64_t)INT32_MAX)
+    return fail(GEG_ERR_BAD_SHAPE, "T * k must be below 2^31");
+  return GEG_OK;
+}
+
+geg_status geg_route_topk(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                          float* weights, int32_t* ids, uint32_t* error_word, hipStream_t stream) {
+  geg_status st;
+  if ((st = check_gate(dtype, T, E, k)) != GEG_OK) return st;
+  if (T == 0) return GEG_OK;
+  if (!logits || !weights || !ids) return fail(GEG_ERR_NULL_POINTER, "logits, weights and ids are required");
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(weights, 4) || !aligned(ids, 4) || !aligned(error_word, 4))
+    return fail(GEG_ERR_MISALIGNED, "logits, weights, ids and error_word must be aligned to their elements");
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{logits, "logits"}, {weights, "weights"}, {ids, "ids"},
+                           {error_word, "error_word"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  hipError_t e = geg::launch_route_topk(logits, dtype, T, E, k, renormalize != 0, weights, ids, error_word, stream);
+  if (e != hipSuccess) return hip_fail(e, "gate launch");
+  ++g_launches;
+  return GEG_OK;
+}
+
+geg_status geg_route_topk_grad(const float* dweights, const void* logits, int32_t dtype, const int32_t* ids,
+                               const float* weights, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                               void* dlogits, hipStream_t stream) {
+  geg_status st;
+  if ((st = check_gate(dtype, T, E, k)) != GEG_OK) return st;
+  if (T == 0) return GEG_OK;
+  if (!dweights || !logits || !ids || !weights || !dlogits)
+    return fail(GEG_ERR_NULL_POINTER, "dweights, logits, ids, weights and dlogits are required");
+  if (dlogits == logits) return fail(GEG_ERR_BAD_OPTION, "dlogits may not be logits");
+  if (!aligned(logits, dtype_bytes(dtype)) || !aligned(dlogits, dtype_bytes(dtype)) || !aligned(dweights, 4) ||
+      !aligned(weights, 4) || !aligned(ids, 4))
+    return fail(GEG_ERR_MISALIGNED, "every tensor must be aligned to its elements");
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{dweights, "dweights"}, {logits, "logits"},
+                           {ids, "ids"}, {weights, "weights"}, {dlogits, "dlogits"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  hipError_t e = geg::launch_route_topk_grad(dweights, logits, dtype, ids, weights, T, E, k, renormalize != 0, dlogits,
+                                             stream);
+  if (e != hipSuccess) return hip_fail(e, "gate gradient launch");
+  ++g_launches;
+  return GEG_OK;
+}
+
+geg_status geg_route_combine_grad(const void* dout, const void* y, const int32_t* row_of, const int32_t* src_of,
+                                  const float* weights, int64_t T, int32_t k, int64_t N, void* dy, float* dweights,
+                                  hipStream_t stream) {
+  if (T < 0 || k <= 0 || N <= 0 || N % 8) return fail(GEG_ERR_BAD_SHAPE, "need T >= 0, k > 0, N > 0, N % 8 == 0");
+  if (T >= (int64_t)INT32_MAX || T * (int64_t)k >= (int64_t)INT32_MAX)
+    return fail(GEG_ERR_BAD_SHAPE, "T * k must be below 2^31");
+  if (T == 0) return GEG_OK;
+  if (!dout || !row_of || !dy || (dweights && !y))
+    return fail(GEG_ERR_NULL_POINTER, "dout, row_of, dy and (for dweights) y are required");
+  if (dy == y) return fail(GEG_ERR_BAD_OPTION, "dy may not be y");
+  if (!aligned(dout, 16) || !aligned(y, 16) || !aligned(dy, 16) || !aligned(row_of, 4) || !aligned(src_of, 4) ||
+      !aligned(weights, 4) || !aligned(dweights, 4))
+    return fail(GEG_ERR_MISALIGNED, "dout, y and dy must be 16-byte aligned, the others 4-byte");
+  geg_status st;
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{dout, "dout"}, {y, "y"}, {row_of, "row_of"},
+                           {src_of, "src_of"}, {weights, "weights"}, {dy, "dy"}, {dweights, "dweights"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  hipError_t e = geg::launch_route_combine_grad(reinterpret_cast<const uint16_t*>(dout),
+                                                reinterpret_cast<const uint16_t*>(y), row_of, src_of, weights, T, k, N,
+                                                reinterpret_cast<uint16_t*>(dy), dweights, stream);
+  if (e != hipSuccess) return hip_fail(e, "combine gradient launch");
+  ++g_launches;
+  return GEG_OK;
+}
+
+// Workspace of the few-token layer: the header, the grouping, act fp32 [T k, I].
+static constexpr size_t kMoeActOff = kHeader + ((size_t)geg::kMoePlanWords * 4 + 255) / 256 * 256;
+
+size_t geg_moe_layer_workspace_bytes(int64_t T, int32_t k, int64_t I) {
+  if (T < 0 || k <= 0 || I <= 0 || T > geg::kMoeMaxTokens || T * k > geg::kMoeMaxEntries || I > kMaxWindow) return 0;
+  return kMoeActOff + round256((size_t)(T * k) * (size_t)I * 4);
+}
+
+static geg_status moe_layer(int fmt, const void* x, const int32_t* ids, const float* weights, const uint8_t* w13,
+                            const void* s13, const uint8_t* w2, const void* s2, void* out, int64_t T, int32_t k,
+                            int64_t H, int64_t I, int32_t E, void* ws, size_t ws_bytes, const geg_opts* opts,
+                            hipStream_t stream) {
+  CuScope cu_scope(opts);
+  const int64_t kmult = fmt == geg::NF4 ? 64 : 32;
+  if (opts && opts->cu_limit < 0) return fail(GEG_ERR_BAD_OPTION, "cu_limit must be >= 0");
+  if (T < 0 || k <= 0) return fail(GEG_ERR_BAD_SHAPE, "need T >= 0, k > 0");
+  if (T > geg::kMoeMaxTokens || T * k > geg::kMoeMaxEntries)
+    return fail(GEG_ERR_BAD_SHAPE,
+                "the few-token layer takes T <= 16 tokens and T * k <= 256 entries; larger batches go through "
+                "geg_route_sort, the expert block and geg_route_combine");
+  if (I <= 0 || I > kMaxWindow || I % kmult)
+    return fail(GEG_ERR_BAD_SHAPE, "I must be a positive multiple of " + std::to_string(kmult));
+  geg_status st;
+  if ((st = check_shape(T, 2 * I, H, E, kmult)) != GEG_OK) return st;
+  if ((st = check_shape(T, H, I, E, kmult)) != GEG_OK) return st;
+  if (T == 0) return GEG_OK;
+  if (!x || !ids || !weights || !w13 || !s13 || !w2 || !s2 || !out)
+    return fail(GEG_ERR_NULL_POINTER, "a required pointer is NULL");
+  if (!ws) return fail(GEG_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(out, 16) || !aligned(ids, 4) ||
+      !aligned(weights, 4) || (fmt == geg::NF4 && (!aligned(s13, 4) || !aligned(s2, 4))))
+    return fail(GEG_ERR_MISALIGNED, "x, the packed weights and out must be 16-byte aligned");
+  if (!aligned(ws, 256)) return fail(GEG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < geg_moe_layer_workspace_bytes(T, k, I))
+    return fail(GEG_ERR_WORKSPACE, "workspace smaller than geg_moe_layer_workspace_bytes(): need " +
+                                       std::to_string(geg_moe_layer_workspace_bytes(T, k, I)));
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{x, "x"}, {ids, "topk_ids"}, {weights, "topk_weights"},
+                           {w13, "w13"}, {s13, "scales13"}, {w2, "w2"}, {s2, "scales2"}, {out, "out"},
+                           {ws, "workspace"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  uint8_t* wsb = reinterpret_cast<uint8_t*>(ws);
+  geg::MoeArgs g{};
+  g.x = reinterpret_cast<const uint16_t*>(x);
+  g.ids = ids;
+  g.weights = weights;
+  g.w13 = w13;
+  g.s13 = s13;
+  g.w2 = w2;
+  g.s2 = s2;
+  g.out = reinterpret_cast<uint16_t*>(out);
+  g.err = reinterpret_cast<uint32_t*>(wsb);
+  g.plan = reinterpret_cast<int32_t*>(wsb + kHeader);
+  g.act = reinterpret_cast<float*>(wsb + kMoeActOff);
+  g.H = H;
+  g.I = I;
+  g.T = (int32_t)T;
+  g.k = k;
+  g.E = E;
+  hipError_t e = geg::launch_moe_layer(fmt, g, cu_count(), stream);
+  if (e != hipSuccess) return hip_fail(e, "MoE layer launch");
+  g_launches += 2;
+  return GEG_OK;
+}
+
+geg_status gnf4_moe_layer(const void* x, const int32_t* topk_ids, const float* topk_weights, const uint8_t* w13,
+                          const float* absmax13, const uint8_t* w2, const float* absmax2, void* out, int64_t T,
+                          int32_t k, int64_t H, int64_t I, int32_t E, void* workspace, size_t workspace_bytes,
+                          const geg_opts* opts, hipStream_t stream) {
+  return moe_layer(geg::NF4, x, topk_ids, topk_weights, w13, absmax13, w2, absmax2, out, T, k, H, I, E, workspace,
+                   workspace_bytes, opts, stream);
+}
+
+geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float* topk_weights,
+                            const uint8_t* blocks13, const uint8_t* scales13, const uint8_t* blocks2,
+                            const uint8_t* scales2, void* out, int64_t T, int32_t k, int64_t H, int64_t I, int32_t E,
+                            void* workspace, size_t workspace_bytes, const geg_opts* opts, hipStream_t stream) {
+  return moe_layer(geg::MXFP4, x, topk_ids, topk_weights, blocks13, scales13, blocks2, scales2, out, T, k, H, I, E,
+                   workspace, workspace_bytes, opts, stream);
+}
+
 size_t geg_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E,
                            const geg_opts* opts) {
   if (op < 0 || op > 6 || M < 0 || N <= 0 || K <= 0 || E <= 0) return 0;

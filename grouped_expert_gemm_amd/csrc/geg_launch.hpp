@@ -107,6 +107,44 @@ hipError_t launch_mxfp8_quantize(const uint16_t* a, int64_t M, int64_t K, uint8_
 hipError_t launch_w4a8(const uint8_t* aq, const uint8_t* as, const int32_t* sizes, const uint8_t* wq,
                        const uint8_t* ws, uint16_t* out, int64_t M, int64_t N, int64_t K, int32_t E, uint32_t* err,
                        int cus, hipStream_t s);
+// Element types of the operators that take several (GEG_BF16, GEG_F16, GEG_F32).
+enum DType : int { kBF16 = 0, kF16 = 1, kF32 = 2 };
+// MXFP4 quantisation: rows of K values, ld apart -> codes [rows, K/2], scales
+// [rows, K/32] and, unless NULL, the values the codes stand for [rows, K].
+hipError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld, uint8_t* codes,
+                                 uint8_t* scales, void* values, int cus, hipStream_t s);
+// Router gate: top-k of logits [T, E] with softmax weights, its gradient, and the
+// gradient of the weighted combine (see gate.hip).
+hipError_t launch_route_topk(const void* logits, int dtype, int64_t T, int32_t E, int32_t k, int renorm,
+                             float* weights, int32_t* ids, uint32_t* err, hipStream_t s);
+hipError_t launch_route_topk_grad(const float* dw, const void* logits, int dtype, const int32_t* ids,
+                                  const float* weights, int64_t T, int32_t E, int32_t k, int renorm, void* dlogits,
+                                  hipStream_t s);
+hipError_t launch_route_combine_grad(const uint16_t* dout, const uint16_t* y, const int32_t* row_of,
+                                     const int32_t* src_of, const float* w, int64_t T, int32_t k, int64_t N,
+                                     uint16_t* dy, float* dw, hipStream_t s);
+// The routed experts of an MoE layer for a few tokens (see moe.hip).
+constexpr int kMoeMaxTokens = 16;
+constexpr int kMoeMaxEntries = 256;   // T * k
+constexpr int kMoeRowBlock = 16;      // most output columns per workgroup of the second kernel
+constexpr int kMoePlanWords = 4 + 3 * kMoeMaxEntries;   // items, then {expert, first | size << 16}, then entries
+struct MoeArgs {
+  const uint16_t* x;      // bf16 [T, H]
+  const int32_t* ids;     // [T, k]
+  const float* weights;   // [T, k]
+  const uint8_t* w13;     // codes [E, 2I, H/2]
+  const void* s13;
+  const uint8_t* w2;      // codes [E, H, I/2]
+  const void* s2;
+  uint16_t* out;          // bf16 [T, H]
+  float* act;             // workspace: fp32 [T k, I] in the second kernel's order
+  int32_t* plan;          // workspace: the grouping, kMoePlanWords
+  uint32_t* err;
+  int64_t H, I;
+  int32_t T, k, E;
+  int32_t rb;             // output columns per workgroup of the second kernel (set by the launcher)
+};
+hipError_t launch_moe_layer(int fmt, MoeArgs g, int cus, hipStream_t s);
 // Low-rank adapter: U = s X T_e^T (T fp32 [E, r, C], U fp32 [M, r]); G_e = s
 // sum_rows Wd^T Nw (fp32, [E, Wc, r] or with jc [E, r, Wc]); out[e] = in[e]^T
 // for fp32 [E, P, Qd]. The delta U Q^T itself is added in the tiled kernel's

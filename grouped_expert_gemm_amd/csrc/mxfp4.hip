@@ -1,0 +1,213 @@
+// MXFP4 quantisation (OCP MX v1.0 conversion) of bf16, fp16 or fp32 rows: per 32
+// consecutive values with largest magnitude amax,
+//     X = max(floor(log2 amax) - 2, -127)     (0 for an all-zero block)
+//     code = nearest e2m1 value of x / 2^X, ties to the even code, saturating at 6,
+// the sign kept (-0 for negatives that round to 0); the scale byte is X + 127. A
+// block that holds an inf or a NaN gets scale byte 255, which decodes to NaN.
+//
+// Memory bound: a value is read once and 17/32 of a byte written (plus the value
+// itself when asked for). A thread takes one 16-byte piece of its row (8 or 4
+// values), the 4 or 8 lanes of a block share amax through lane exchanges, and the
+// codes come from gfx950's scaled fp4 conversion (two values per instruction,
+// round to nearest even, saturating; the division by 2^X is exact). Values that it
+// might flush (blocks whose scale is below 2^-100) go through exact fp32
+// arithmetic instead.
+#include <algorithm>
+
+#include "geg_device.hpp"
+#include "geg_launch.hpp"
+
+namespace geg {
+
+namespace {
+
+// Code of t = x / 2^X (exact) by arithmetic: round to nearest on the grid of the
+// value's binade (steps 0.5, 1, 2), ties to even; a tie between binades lands on
+// the even code too.
+__device__ __forceinline__ uint32_t e2m1_rne_sat(float t) {
+  const uint32_t s = (__float_as_uint(t) >> 28) & 8u;
+  const float a = fabsf(t);
+  uint32_t c;
+  if (a < 2.f)
+    c = (uint32_t)__builtin_rintf(2.f * a);
+  else if (a < 4.f)
+    c = (uint32_t)__builtin_rintf(a) + 2u;
+  else
+    c = min((uint32_t)__builtin_rintf(0.5f * fminf(a, 16.f)) + 4u, 7u);
+  return c | s;
+}
+
+__device__ __forceinline__ float e2m1_to_f32(uint32_t c) {
+  const uint32_t m = c & 7u;
+  const float a = m < 4u ? 0.5f * (float)m : (m < 6u ? (float)m - 2.f : 2.f * (float)m - 8.f);
+  return (c & 8u) ? -a : a;
+}
+
+// 16 bytes of a row as fp32 values.
+template <int DT>
+__device__ __forceinline__ void unpack16(const u32x4& v, float* f) {
+  if constexpr (DT == kF32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = v[i];
+      if constexpr (DT == kBF16) {
+        f[2 * i] = __uint_as_float(w << 16);
+        f[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+      } else {
+        const f16x2 h = __builtin_bit_cast(f16x2, w);
+        const _Float16 h0 = h[0], h1 = h[1];
+        f[2 * i] = (float)h0;
+        f[2 * i + 1] = (float)h1;
+      }
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ u32x4 pack16(const float* f) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == kF32) {
+      r[i] = __float_as_uint(f[i]);
+    } else if constexpr (DT == kBF16) {
+      r[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    } else {
+      f16x2 h;
+      h[0] = (_Float16)f[2 * i];
+      h[1] = (_Float16)f[2 * i + 1];
+      r[i] = __builtin_bit_cast(uint32_t, h);
+    }
+  }
+  return r;
+}
+
+// One 16-byte piece: codes (16 or 32 bits) and, on the block's first lane, the
+// scale byte; with VALUES also the decoded piece. Every lane of a block calls it.
+template <int DT, bool VALUES>
+__device__ __forceinline__ void quantize_piece(const u32x4& v, int64_t piece, uint8_t* __restrict__ codes,
+                                               uint8_t* __restrict__ scales, void* __restrict__ values) {
+  constexpr int EPT = DT == kF32 ? 4 : 8;   // values per piece
+  constexpr int LPB = 32 / EPT;             // pieces per block
+  float f[EPT];
+  unpack16<DT>(v, f);
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < EPT; ++i) mx = max(mx, __float_as_uint(f[i]) & 0x7FFFFFFFu);
+#pragma unroll
+  for (int o = 1; o < LPB; o <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, o));
+  const int field = (int)(mx >> 23);
+  // floor(log2 amax) - 2 + 127 = field - 2 for a normal amax; smaller ones clamp to 0
+  const int byte = mx == 0 ? 127 : (field == 255 ? 255 : max(field - 2, 0));
+  uint32_t word = 0;
+  float q[EPT];
+  if (byte >= 27 && byte < 255) {
+    const float sc = __uint_as_float((uint32_t)byte << 23);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, f[0], f[1], sc, 0);
+    word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, f[2], f[3], sc, 1);
+    if constexpr (EPT == 8) {
+      word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, f[4], f[5], sc, 2);
+      word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, f[6], f[7], sc, 3);
+    }
+    if constexpr (VALUES) {
+#define GEG_PAIR(p)                                                              \
+  {                                                                              \
+    const auto d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(word, sc, p);        \
+    const float d0 = d[0], d1 = d[1];                                            \
+    q[2 * p] = d0;                                                               \
+    q[2 * p + 1] = d1;                                                           \
+  }
+      GEG_PAIR(0)
+      GEG_PAIR(1)
+      if constexpr (EPT == 8) {
+        GEG_PAIR(2)
+        GEG_PAIR(3)
+      }
+#undef GEG_PAIR
+    }
+  } else if (byte == 255) {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) q[i] = __uint_as_float(0x7FC00000u);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) {
+      const uint32_t c = e2m1_rne_sat(__builtin_ldexpf(f[i], 127 - byte));
+      word |= c << (4 * i);
+      q[i] = __builtin_ldexpf(e2m1_to_f32(c), byte - 127);
+    }
+  }
+  if constexpr (EPT == 8)
+    reinterpret_cast<uint32_t*>(codes)[piece] = word;
+  else
+    reinterpret_cast<uint16_t*>(codes)[piece] = (uint16_t)word;
+  if ((piece & (LPB - 1)) == 0) scales[piece / LPB] = (uint8_t)byte;
+  if constexpr (VALUES) reinterpret_cast<u32x4*>(values)[piece] = pack16<DT>(q);
+}
+
+// UNR pieces per thread, 256 apart, their loads all in flight first. Pieces of a
+// row are consecutive; `ppr` pieces per row, rows `ld16` 16-byte units apart
+// (ld16 == ppr: the matrix is one run of pieces).
+template <int DT, bool VALUES, int UNR>
+__global__ __launch_bounds__(kThreads) void mxfp4_quantize_kernel(const u32x4* __restrict__ x, int64_t pieces,
+                                                                  int64_t ppr, int64_t ld16,
+                                                                  uint8_t* __restrict__ codes,
+                                                                  uint8_t* __restrict__ scales,
+                                                                  void* __restrict__ values) {
+  const int64_t p0 = (int64_t)blockIdx.x * (UNR * kThreads) + threadIdx.x;
+  u32x4 v[UNR];
+#pragma unroll
+  for (int u = 0; u < UNR; ++u) {
+    const int64_t p = p0 + u * kThreads;
+    if (p < pieces) {
+      const int64_t at = ld16 == ppr ? p : (p / ppr) * ld16 + p % ppr;
+      v[u] = x[at];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < UNR; ++u) {
+    // pieces come in whole blocks of 4 or 8 consecutive lanes, so the lanes of a
+    // block pass this test together
+    const int64_t p = p0 + u * kThreads;
+    if (p < pieces) quantize_piece<DT, VALUES>(v[u], p, codes, scales, values);
+  }
+}
+
+template <int DT, bool VALUES>
+hipError_t launch_dt(const void* x, int64_t rows, int64_t K, int64_t ld, uint8_t* codes, uint8_t* scales,
+                     void* values, int cus, hipStream_t s) {
+  constexpr int EPT = DT == kF32 ? 4 : 8;
+  const int64_t ppr = K / EPT, pieces = rows * ppr;
+  const u32x4* xv = reinterpret_cast<const u32x4*>(x);
+  // four pieces per thread once that still fills the chip
+  if (pieces >= (int64_t)cus * kThreads * 8) {
+    const int64_t grid = (pieces + 4 * kThreads - 1) / (4 * kThreads);
+    hipLaunchKernelGGL((mxfp4_quantize_kernel<DT, VALUES, 4>), dim3((unsigned)grid), dim3(kThreads), 0, s, xv, pieces,
+                       ppr, ld / EPT, codes, scales, values);
+  } else {
+    const int64_t grid = (pieces + kThreads - 1) / kThreads;
+    hipLaunchKernelGGL((mxfp4_quantize_kernel<DT, VALUES, 1>), dim3((unsigned)grid), dim3(kThreads), 0, s, xv, pieces,
+                       ppr, ld / EPT, codes, scales, values);
+  }
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t launch_values(const void* x, int64_t rows, int64_t K, int64_t ld, uint8_t* codes, uint8_t* scales,
+                         void* values, int cus, hipStream_t s) {
+  return values ? launch_dt<DT, true>(x, rows, K, ld, codes, scales, values, cus, s)
+                : launch_dt<DT, false>(x, rows, K, ld, codes, scales, values, cus, s);
+}
+
+}  // namespace
+
+hipError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld, uint8_t* codes,
+                                 uint8_t* scales, void* values, int cus, hipStream_t s) {
+  if (dtype == kBF16) return launch_values<kBF16>(x, rows, K, ld, codes, scales, values, cus, s);
+  if (dtype == kF16) return launch_values<kF16>(x, rows, K, ld, codes, scales, values, cus, s);
+  return launch_values<kF32>(x, rows, K, ld, codes, scales, values, cus, s);
+}
+
+}  // namespace geg

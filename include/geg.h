@@ -373,6 +373,103 @@ geg_status gmxfp4_grouped_dgrad_lora(const void* dy, const int32_t* sizes, const
                                      int64_t N, int64_t K, int32_t E, int32_t r, void* workspace,
                                      size_t workspace_bytes, const geg_opts* opts, hipStream_t stream);
 
+/* Element types of the operators that take several. */
+#define GEG_BF16 0
+#define GEG_F16 1
+#define GEG_F32 2
+
+/*
+ * gmxfp4_quantize — MXFP4 quantisation of activations or weights on the device (OCP
+ * MX v1.0 conversion; the packer beside gnf4_quantize, and the activation side of
+ * gmxfp4_w4a4_grouped_gemm). Per row and 32 consecutive values with largest magnitude
+ * amax: X = max(floor(log2 amax) - 2, -127) (0 for an all-zero block); each code is the
+ * nearest e2m1 value of x / 2^X, ties to the even code, saturating at 6, the sign
+ * kept; the scale byte is X + 127. A block that holds an inf or a NaN gets scale byte
+ * 255 (it decodes to NaN; its codes are 0).
+ *   x       dtype (GEG_BF16 / GEG_F16 / GEG_F32) [rows, K], rows ld elements apart
+ *           (ld >= K; the base and the row pitch in bytes multiples of 16)
+ *   blocks  u8 [rows, K/2] out (low nibble = even k), 4-B aligned
+ *   scales  u8 [rows, K/32] out
+ *   values  NULL, or dtype [rows, K] out, 16-B aligned: what the codes stand for
+ *           (exact in every one of the types)
+ *   K % 32 == 0.
+ */
+geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K, int64_t ld, uint8_t* blocks,
+                           uint8_t* scales, void* values, hipStream_t stream);
+
+/*
+ * geg_route_topk — the router's gate: the k largest of a token's logits (ties to the
+ * lower expert, largest first) and their softmax weights,
+ *   weights[t, s] = exp(l_s - m) / sum_j exp(l_j - m),  m = max_j l_j,
+ * the sum over all E experts, or with renormalize != 0 over the chosen k (the softmax
+ * of the chosen logits). fp32 arithmetic. The ids and weights are what geg_route_sort,
+ * geg_route_combine and the MoE layer take.
+ *   logits   dtype [T, E], E <= 1024
+ *   weights  fp32 [T, k] out, ids int32 [T, k] out; 1 <= k <= min(E, 64)
+ *   error_word  device uint32 that receives GEG_DEVERR_NON_FINITE when a logit is NaN
+ *            (OR-ed in; the caller clears it), or NULL
+ * A NaN logit counts as -inf; a token whose logits are all -inf gets the ids 0..k-1 and
+ * weights 0; +inf logits share the weight equally.
+ */
+geg_status geg_route_topk(const void* logits, int32_t dtype, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                          float* weights, int32_t* ids, uint32_t* error_word, hipStream_t stream);
+
+/*
+ * geg_route_topk_grad — gradient of geg_route_topk's weights: dlogits from
+ * dweights fp32 [T, k] and the forward's logits, ids and weights. With S = sum_s
+ * weights_s dweights_s, a chosen expert gets weights_s (dweights_s - S); the others 0
+ * (renormalised) or -p_e S with p the softmax over all experts. dlogits has the
+ * logits' dtype [T, E]; it may not be logits itself. Ids outside [0, E) add nothing.
+ */
+geg_status geg_route_topk_grad(const float* dweights, const void* logits, int32_t dtype, const int32_t* ids,
+                               const float* weights, int64_t T, int32_t E, int32_t k, int32_t renormalize,
+                               void* dlogits, hipStream_t stream);
+
+/*
+ * geg_route_combine_grad — gradient of geg_route_combine:
+ *   dy[row_of[t*k + s], :] = bf16( weights[t, s] * dout[t, :] )
+ *   dweights[t, s] = sum_n dout[t, n] * y[row_of[t*k + s], n]     (fp32)
+ *   dout bf16 [T, N], y bf16 [T*k, N], row_of int32 [T*k] (values in [-1, T*k),
+ *   no row twice), weights fp32 [T, k] or NULL for all ones; N % 8 == 0
+ *   src_of   int32 [T*k] of geg_route_sort, or NULL: with it, rows of dy that no entry
+ *            lands on (src_of < 0) are set to 0; without it they are left untouched
+ *   dy bf16 [T*k, N] (not y itself), dweights fp32 [T, k] or NULL (then y may be NULL)
+ * Entries with row_of < 0 get dweights 0.
+ */
+geg_status geg_route_combine_grad(const void* dout, const void* y, const int32_t* row_of, const int32_t* src_of,
+                                  const float* weights, int64_t T, int32_t k, int64_t N, void* dy, float* dweights,
+                                  hipStream_t stream);
+
+/*
+ * gnf4_moe_layer / gmxfp4_moe_layer — the routed experts of a whole MoE layer for a few
+ * tokens, in two launches: no sort, no gathered rows, no combine pass. For T <= 16
+ * tokens with T * k <= 256 (larger batches: geg_route_sort, g*_expert_block,
+ * geg_route_combine):
+ *   act[t, s] = silu(x_t . G_e) * (x_t . U_e),  e = topk_ids[t, s]
+ *   out[t, :] = bf16( sum over slots s of topk_weights[t, s] * act[t, s] . W2_e^T )
+ *   x        bf16 [T, H]
+ *   topk_ids int32 [T, k], topk_weights fp32 [T, k] (geg_route_topk's; a token may name
+ *            an expert twice)
+ *   w13, w2 and their scales as g*_expert_block takes them (rows 2i / 2i+1 of w13 are
+ *            gate and up of unit i); H and I multiples of 64 (NF4) or 32 (MXFP4)
+ *   out      bf16 [T, H], 16-B aligned
+ *   workspace: geg_moe_layer_workspace_bytes(T, k, I) bytes
+ *   opts     only cu_limit is used
+ * Entries whose id lies outside [0, E) are dropped and flag GEG_DEVERR_BAD_EXPERT_ID; a
+ * token without any valid entry gets zeros. act stays in fp32; NF4 multiplies x as fp16
+ * (GEG_DEVERR_FP16_RANGE when it overflows) and the table's values as fp16, MXFP4's
+ * products are exact in fp32. Deterministic.
+ */
+size_t geg_moe_layer_workspace_bytes(int64_t T, int32_t k, int64_t I);
+geg_status gnf4_moe_layer(const void* x, const int32_t* topk_ids, const float* topk_weights, const uint8_t* w13,
+                          const float* absmax13, const uint8_t* w2, const float* absmax2, void* out, int64_t T,
+                          int32_t k, int64_t H, int64_t I, int32_t E, void* workspace, size_t workspace_bytes,
+                          const geg_opts* opts, hipStream_t stream);
+geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float* topk_weights,
+                            const uint8_t* blocks13, const uint8_t* scales13, const uint8_t* blocks2,
+                            const uint8_t* scales2, void* out, int64_t T, int32_t k, int64_t H, int64_t I, int32_t E,
+                            void* workspace, size_t workspace_bytes, const geg_opts* opts, hipStream_t stream);
+
 /* Workspace bytes needed by one call of operation `op` with these sizes and options. */
 size_t geg_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E,
                            const geg_opts* opts);
