@@ -27,7 +27,7 @@ __all__ = [
     "geg_version", "geg_launch_count", "GEG_OP_NF4_FWD", "GEG_OP_MXFP4_FWD", "GEG_OP_NF4_DGRAD",
     "GEG_OP_NF4_BLOCK", "GEG_OP_MXFP4_BLOCK", "GEG_OP_MXFP4_DGRAD", "DEVERR_NEGATIVE_SIZE", "DEVERR_SIZES_EXCEED_M", "DEVERR_FP16_RANGE",
     "DEVERR_BAD_EXPERT_ID",
-    "gmxfp4_quantize", "route_topk", "route_topk_grad", "route_combine_grad",
+    "gmxfp4_quantize", "gmxfp4_w4a4_grouped_gemm", "GEG_OP_MXFP4_W4A4", "route_topk", "route_topk_grad", "route_combine_grad",
     "gnf4_moe_layer", "gmxfp4_moe_layer", "router_gate", "dispatch_rows", "combine_rows",
 ]
 
@@ -38,6 +38,7 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "geg.h")
 GEG_OP_NF4_FWD, GEG_OP_MXFP4_FWD, GEG_OP_NF4_DGRAD = 0, 1, 2
 GEG_OP_NF4_BLOCK, GEG_OP_MXFP4_BLOCK, GEG_OP_MXFP4_DGRAD = 3, 4, 5
 GEG_OP_MXFP4_W4A8 = 6
+GEG_OP_MXFP4_W4A4 = 8
 DEVERR_NEGATIVE_SIZE, DEVERR_SIZES_EXCEED_M, DEVERR_FP16_RANGE = 0x1, 0x2, 0x4
 DEVERR_BAD_EXPERT_ID, DEVERR_NON_FINITE = 0x8, 0x10
 
@@ -95,7 +96,7 @@ def lib() -> ctypes.CDLL:
             L = ctypes.CDLL(LIB_PATH)
             gemm_args = [_P, _P, _P, _P, _P, _I64, _I64, _I64, _I32, _P, _SZ, _P, _P]
             for name in ("gnf4_grouped_gemm", "gmxfp4_grouped_gemm", "gnf4_grouped_dgrad",
-                         "gmxfp4_grouped_dgrad", "gmxfp4_w4a8_grouped_gemm"):
+                         "gmxfp4_grouped_dgrad", "gmxfp4_w4a8_grouped_gemm", "gmxfp4_w4a4_grouped_gemm"):
                 f = getattr(L, name)
                 f.argtypes, f.restype = gemm_args, ctypes.c_int
             L.gmxfp8_quantize.argtypes, L.gmxfp8_quantize.restype = [_P, _P, _P, _I64, _I64, _P], ctypes.c_int
@@ -832,6 +833,37 @@ def gmxfp4_quantize(x, values: bool = False, stream=None):
     _check(lib().gmxfp4_quantize(_ptr(x), dt, rows, K, ld, _ptr(codes), _ptr(scales), _ptr(vals), _stream(stream)))
     _outlive(stream, codes, scales, vals)
     return (codes, scales, vals) if values else (codes, scales)
+
+
+def gmxfp4_w4a4_grouped_gemm(a, sizes, blocks, scales, out=None, workspace: Workspace | None = None,
+                             opts: Opts | None = None, stream=None, check_errors: bool = False):
+    """W4A4: a bf16 [M, K] quantised to MXFP4 inside the call, times MXFP4 blocks uint8
+    [E, N, K/2] (or [E, N, K/32, 16]) with scales uint8 [E, N, K/32], on the block-scaled
+    matrix instruction with two 4-bit operands -> out bf16 [M, N]. Rows with an inf or
+    NaN come out NaN and flag DEVERR_NON_FINITE."""
+    import torch
+    if blocks.dim() == 4:
+        blocks = blocks.reshape(blocks.shape[0], blocks.shape[1], -1)
+    if a.dim() != 2 or blocks.dim() != 3:
+        raise GegError(2, "a: expected [M, K], blocks [E, N, K/2]")
+    M, K = a.shape
+    E, N = blocks.shape[0], blocks.shape[1]
+    _check_tensor(a, "a", torch.bfloat16, (M, K))
+    _check_tensor(sizes, "sizes", torch.int32, (E,))
+    _check_packed(False, blocks, scales, E, N, K, "blocks", "scales")
+    _check_tensor(out, "out", torch.bfloat16, (M, N))
+    _on_device(a, sizes, blocks, scales, out)
+    mine = out is None
+    if mine:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+    L, o = lib(), ctypes.byref(opts) if opts else None
+    ws = _layer_workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a.device, stream)
+    _check(L.gmxfp4_w4a4_grouped_gemm(_ptr(a), _ptr(sizes), _ptr(blocks), _ptr(scales), _ptr(out), M, N, K, E,
+                                      _ptr(ws.buf), ws.nbytes, o, _stream(stream)))
+    if mine:
+        _outlive(stream, out)
+    _check_device_errors(ws, check_errors, stream)
+    return out
 
 
 def route_topk(logits, k: int, renormalize: bool = True, error_word=None, stream=None):

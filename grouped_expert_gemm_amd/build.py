@@ -19,7 +19,7 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgeg.so")
 
 SOURCES = ["geg.cpp", "skinny.hip", "tile.hip", "util.hip", "vec.hip", "narrow.hip", "route.hip", "w4a8.hip", "lora.hip",
-           "noalloc.hip", "mxfp4.hip", "gate.hip", "moe.hip"]
+           "noalloc.hip", "mxfp4.hip", "gate.hip", "moe.hip", "w4a4.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

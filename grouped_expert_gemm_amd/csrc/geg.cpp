@@ -174,6 +174,20 @@ geg_status make_plan(int op, int64_t M, int64_t N, int64_t K, int32_t E, const g
     p.total_bytes = p.a16_off + p.a16_bytes;
     return GEG_OK;
   }
+  if (op == GEG_OP_MXFP4_W4A4) {   // tiles: e2m1 codes [M, K/2] and scales [ceil(K/512)][M][16]
+    if (force == 1 || force == 3)
+      return fail(GEG_ERR_BAD_OPTION, "W4A4 runs on its tiles (force_path 2) or its narrow kernel (4)");
+    const int rb = geg::w4a4_narrow_rb(M, K, E, force);
+    if (force == 4 && rb == 0) return fail(GEG_ERR_BAD_OPTION, "K is too large for the W4A4 narrow kernel");
+    p.narrow = rb > 0;
+    p.cb = rb;
+    p.total_bytes = p.a16_off = kHeader;
+    if (rb == 0) {
+      p.a16_bytes = round256((size_t)M * (size_t)(K / 2)) + round256((size_t)((K + 511) / 512) * (size_t)M * 16);
+      p.total_bytes += p.a16_bytes;
+    }
+    return GEG_OK;
+  }
   if (op == GEG_OP_MXFP4_DGRAD) {   // bf16 dY feeds the MFMAs as it is
     p.run_tile = M > 0;
     p.total_bytes = kHeader;
@@ -659,6 +673,49 @@ geg_status gmxfp4_w4a8_grouped_gemm(const void* a, const int32_t* sizes, const u
   return GEG_OK;
 }
 
+geg_status gmxfp4_w4a4_grouped_gemm(const void* a, const int32_t* sizes, const uint8_t* blocks,
+                                    const uint8_t* scales, void* out, int64_t M, int64_t N, int64_t K,
+                                    int32_t E, void* workspace, size_t workspace_bytes,
+                                    const geg_opts* opts, hipStream_t stream) {
+  CuScope cu_scope(opts);
+  geg_status st = check_shape(M, N, K, E, 32);
+  if (st != GEG_OK) return st;
+  Plan p;
+  if ((st = make_plan(GEG_OP_MXFP4_W4A4, M, N, K, E, opts, p)) != GEG_OK) return st;
+  if (M == 0) return GEG_OK;
+  if (!a || !sizes || !blocks || !scales || !out) return fail(GEG_ERR_NULL_POINTER, "a required pointer is NULL");
+  if (!workspace) return fail(GEG_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(a, 16) || !aligned(blocks, 16) || !aligned(out, 4) || !aligned(sizes, 4))
+    return fail(GEG_ERR_MISALIGNED, "a and blocks must be 16-byte aligned, out 4-byte");
+  if (!aligned(workspace, 256)) return fail(GEG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (workspace_bytes < p.total_bytes)
+    return fail(GEG_ERR_WORKSPACE, "workspace smaller than geg_workspace_bytes(): need " +
+                                       std::to_string(p.total_bytes));
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{a, "a"}, {sizes, "sizes"}, {blocks, "blocks"},
+                           {scales, "scales"}, {out, "out"}, {workspace, "workspace"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  uint8_t* wsb = reinterpret_cast<uint8_t*>(workspace);
+  uint8_t* aq = wsb + p.a16_off;
+  uint8_t* as = aq + round256((size_t)M * (size_t)(K / 2));
+  geg::W4A4Args g{reinterpret_cast<const uint16_t*>(a), aq, as, sizes, blocks, scales,
+                  reinterpret_cast<uint16_t*>(out), M, N, K, E, reinterpret_cast<uint32_t*>(wsb)};
+  const int cus = cu_count();
+  hipError_t e = hipSuccess;
+  if (!p.narrow) {
+    e = geg::launch_w4a4_quantize(g.a, M, K, aq, as, g.err, cus, stream);
+    if (e != hipSuccess) return hip_fail(e, "activation quantisation launch");
+    ++g_launches;
+  }
+  e = record_event(opts, 0, stream);
+  if (e == hipSuccess)
+    e = p.narrow ? geg::launch_w4a4_narrow(g, p.cb, cus, stream) : geg::launch_w4a4_tile(g, cus, stream);
+  if (e == hipSuccess) e = record_event(opts, 1, stream);
+  if (e != hipSuccess) return hip_fail(e, "W4A4 kernel launch");
+  ++g_launches;
+  return GEG_OK;
+}
+
 geg_status gmxfp8_quantize(const void* a, uint8_t* codes, uint8_t* scales, int64_t M, int64_t K,
                            hipStream_t stream) {
   if (M < 0 || K <= 0 || K % 32) return fail(GEG_ERR_BAD_SHAPE, "need M >= 0, K > 0, K % 32 == 0");
@@ -1093,7 +1150,7 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
 
 size_t geg_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E,
                            const geg_opts* opts) {
-  if (op < 0 || op > 6 || M < 0 || N <= 0 || K <= 0 || E <= 0) return 0;
+  if (op < 0 || (op > 6 && op != GEG_OP_MXFP4_W4A4) || M < 0 || N <= 0 || K <= 0 || E <= 0) return 0;
   if (op == GEG_OP_NF4_BLOCK || op == GEG_OP_MXFP4_BLOCK) {
     size_t act_off = 0, total = 0;
     if (block_layout(op == GEG_OP_NF4_BLOCK ? geg::NF4 : geg::MXFP4, M, N, K, E, opts, act_off, total) != GEG_OK)

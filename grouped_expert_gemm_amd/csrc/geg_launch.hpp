@@ -113,6 +113,28 @@ enum DType : int { kBF16 = 0, kF16 = 1, kF32 = 2 };
 // [rows, K/32] and, unless NULL, the values the codes stand for [rows, K].
 hipError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld, uint8_t* codes,
                                  uint8_t* scales, void* values, int cus, hipStream_t s);
+// W4A4: the grouped GEMM with both operands in MXFP4 (see w4a4.hip). The narrow kernel
+// (w4a4_narrow_rb > 0) quantises g.a itself; the tiles read g.aq and g.as, which
+// launch_w4a4_quantize makes: codes [M, K/2], scales [ceil(K/512)][M][16].
+constexpr int64_t kW4A4NarrowAvg = 32;   // rows per expert on average up to which the narrow kernel runs
+constexpr int kMaxLds = 160 << 10;       // LDS of a CU
+struct W4A4Args {
+  const uint16_t* a;      // bf16 [M, K]
+  const uint8_t* aq;      // their codes and scales (tiles)
+  const uint8_t* as;
+  const int32_t* sizes;   // [E]
+  const uint8_t* wq;      // e2m1 weight bytes [E, N, K/2]
+  const uint8_t* ws;      // e8m0 weight scales [E, N, K/32]
+  uint16_t* out;          // bf16 [M, N]
+  int64_t M, N, K;
+  int32_t E;
+  uint32_t* err;
+};
+int w4a4_narrow_rb(int64_t M, int64_t K, int32_t E, int force);
+hipError_t launch_w4a4_narrow(const W4A4Args& g, int rb, int cus, hipStream_t s);
+hipError_t launch_w4a4_quantize(const uint16_t* a, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, uint32_t* err,
+                                int cus, hipStream_t s);
+hipError_t launch_w4a4_tile(const W4A4Args& g, int cus, hipStream_t s);
 // Router gate: top-k of logits [T, E] with softmax weights, its gradient, and the
 // gradient of the weighted combine (see gate.hip).
 hipError_t launch_route_topk(const void* logits, int dtype, int64_t T, int32_t E, int32_t k, int renorm,

@@ -105,7 +105,8 @@ typedef enum {
 #define GEG_DEVERR_FP16_RANGE 0x4u    /* an NF4-path operand overflowed fp16 (|x| > 65504 on a
                                          decode path) or is not finite                         */
 #define GEG_DEVERR_BAD_EXPERT_ID 0x8u /* geg_route_sort: a top-k id outside [0, E) (entry dropped) */
-#define GEG_DEVERR_NON_FINITE 0x10u  /* W4A8: an activation is inf or NaN (its block's codes are unspecified) */
+#define GEG_DEVERR_NON_FINITE 0x10u  /* W4A8, W4A4: an activation is inf or NaN (W4A8: its block's codes are
+                                         unspecified; W4A4: its row is NaN); geg_route_topk: a NaN logit */
 
 /* Optional knobs (NULL = automatic). Used by tests to pin a path. */
 typedef struct {
@@ -137,6 +138,7 @@ typedef struct {
 #define GEG_OP_MXFP4_BLOCK 4 /* N = H (hidden), K = I (intermediate) */
 #define GEG_OP_MXFP4_DGRAD 5
 #define GEG_OP_MXFP4_W4A8 6   /* gmxfp4_w4a8_grouped_gemm */
+#define GEG_OP_MXFP4_W4A4 8   /* gmxfp4_w4a4_grouped_gemm */
 
 /*
  * gnf4_grouped_gemm — out[M, N] = per expert, a_e . W_e^T with W_e in NF4.
@@ -396,6 +398,26 @@ geg_status gmxfp4_grouped_dgrad_lora(const void* dy, const int32_t* sizes, const
  */
 geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K, int64_t ld, uint8_t* blocks,
                            uint8_t* scales, void* values, hipStream_t stream);
+
+/*
+ * gmxfp4_w4a4_grouped_gemm — the MXFP4 grouped GEMM with the activations quantised to
+ * MXFP4 too (gmxfp4_quantize's conversion, inside the call), on the block-scaled matrix
+ * instruction with two 4-bit operands:
+ *   out[rows of e, :] = bf16( Q(a_e) . W_e^T ), fp32 accumulation.
+ *   a, sizes, blocks, scales, out, M, N, K, E: as gmxfp4_grouped_gemm (K % 32 == 0)
+ *   workspace: geg_workspace_bytes(GEG_OP_MXFP4_W4A4, ...) bytes; holds the error word
+ *            and, for batches past the narrow kernel's, the codes [M, K/2] and scales
+ *   opts: force_path 0 by size, 2 tiles, 4 narrow kernel (1 and 3 are refused);
+ *         kernel_events[0..1] bracket the GEMM kernel
+ * Batches of at most 32 rows per expert on average run in one launch that streams the
+ * weights once per 16 or 32 rows; larger ones quantise first and run 256 x 256 tiles. A
+ * row whose activations hold an inf or NaN comes out NaN and flags
+ * GEG_DEVERR_NON_FINITE.
+ */
+geg_status gmxfp4_w4a4_grouped_gemm(const void* a, const int32_t* sizes, const uint8_t* blocks,
+                                    const uint8_t* scales, void* out, int64_t M, int64_t N, int64_t K,
+                                    int32_t E, void* workspace, size_t workspace_bytes,
+                                    const geg_opts* opts, hipStream_t stream);
 
 /*
  * geg_route_topk — the router's gate: the k largest of a token's logits (ties to the

@@ -95,6 +95,32 @@ def test_layer_refusals():
     assert L().geg_moe_layer_workspace_bytes(17, 1, 64) == 0
 
 
+def _w4a4(a=P, sizes=P, w=P, s=P, out=P, M=16, N=64, K=128, E=4, ws=P, nbytes=1 << 20, opts=None):
+    import ctypes
+    return L().gmxfp4_w4a4_grouped_gemm(a, sizes, w, s, out, M, N, K, E, ws, nbytes,
+                                        ctypes.byref(opts) if opts else None, None)
+
+
+def test_w4a4_refusals():
+    assert _w4a4(K=48) == 2 and _w4a4(M=-1) == 2 and _w4a4(N=0) == 2 and _w4a4(E=1025) == 2
+    assert _w4a4(N=65536, K=65536) == 2
+    assert _w4a4(M=0, a=None, ws=None) == 0
+    for p in ("a", "sizes", "w", "s", "out"):
+        assert _w4a4(**{p: None}) == 1, p
+    assert _w4a4(a=P + 8) == 3 and _w4a4(w=P + 4) == 3 and _w4a4(out=P + 2) == 3
+    assert _w4a4(ws=None) == 5 and _w4a4(ws=P + 16) == 5
+    assert _w4a4(opts=geg.Opts(1, 0)) == 8 and _w4a4(opts=geg.Opts(3, 0)) == 8 and _w4a4(opts=geg.Opts(0, 0, None, -1)) == 8
+    assert _w4a4(opts=geg.Opts(4, 0), K=65536, N=64) == 8      # the narrow kernel's rows past LDS
+    assert _w4a4() not in (0, 1, 2, 3, 5, 8)
+    # header only on the narrow kernel; codes and scales [ceil(K/512)][M][16] for the tiles
+    op = geg.GEG_OP_MXFP4_W4A4
+    assert geg.geg_workspace_bytes(op, 16, 64, 128, 4) == 256
+    assert geg.geg_workspace_bytes(op, 8192, 5760, 2880, 32) == 256 + 8192 * 1440 + 6 * 8192 * 16
+    assert geg.geg_workspace_bytes(op, 64, 64, 512, 4, geg.Opts(2, 0)) == 256 + 64 * 256 + 64 * 16
+    need = geg.geg_workspace_bytes(op, 8192, 64, 128, 4)
+    assert _w4a4(M=8192, nbytes=need - 1) == 5 and _w4a4(M=8192, nbytes=need) not in (0, 1, 2, 3, 5, 8)
+
+
 def test_python_refusals():
     torch = pytest.importorskip("torch")
     bf, i32, f32, u8 = torch.bfloat16, torch.int32, torch.float32, torch.uint8
@@ -111,6 +137,9 @@ def test_python_refusals():
                  lambda: geg.route_topk(l, 2, error_word=torch.zeros(2, dtype=i32)),
                  lambda: geg.route_topk_grad(w, l, ids.long(), w), lambda: geg.route_topk_grad(w[:3], l, ids, w),
                  lambda: geg.route_combine_grad(x, y[:7], row, w), lambda: geg.route_combine_grad(x, y, row, w, row[:3]),
+                 lambda: geg.gmxfp4_w4a4_grouped_gemm(x.float(), torch.zeros(3, dtype=i32), w2, m2),
+                 lambda: geg.gmxfp4_w4a4_grouped_gemm(x, torch.zeros(3, dtype=i32), w2, s2),
+                 lambda: geg.gmxfp4_w4a4_grouped_gemm(x, torch.zeros(2, dtype=i32), w2, m2),
                  lambda: geg.gnf4_moe_layer(x, ids, w, w13, m13, w2, s2),
                  lambda: geg.gmxfp4_moe_layer(x, ids, w, w13, s13, w2, m2),
                  lambda: geg.gnf4_moe_layer(x, ids.long(), w, w13, s13, w2, s2),
@@ -121,6 +150,7 @@ def test_python_refusals():
             call()
     for call in (lambda: geg.gmxfp4_quantize(x), lambda: geg.route_topk(l, 2),
                  lambda: geg.route_topk_grad(w, l, ids, w), lambda: geg.route_combine_grad(x, y, row, w),
+                 lambda: geg.gmxfp4_w4a4_grouped_gemm(x, torch.zeros(3, dtype=i32), w2, m2),
                  lambda: geg.gnf4_moe_layer(x, ids, w, w13, s13, w2, s2),
                  lambda: geg.gmxfp4_moe_layer(x, ids, w, w13, m13, w2, m2)):
         with pytest.raises(geg.GegError, match="GPU"):
