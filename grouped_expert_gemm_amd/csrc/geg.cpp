@@ -1067,12 +1067,13 @@ geg_status geg_route_combine_grad(const void* dout, const void* y, const int32_t
   return GEG_OK;
 }
 
-// Workspace of the few-token layer: the header, the grouping, act fp32 [T k, I].
+// Workspace of the few-token layer: the header, the grouping, act fp16 [T k, I], its
+// scales fp32 [T k, I/32].
 static constexpr size_t kMoeActOff = kHeader + ((size_t)geg::kMoePlanWords * 4 + 255) / 256 * 256;
 
 size_t geg_moe_layer_workspace_bytes(int64_t T, int32_t k, int64_t I) {
   if (T < 0 || k <= 0 || I <= 0 || T > geg::kMoeMaxTokens || T * k > geg::kMoeMaxEntries || I > kMaxWindow) return 0;
-  return kMoeActOff + round256((size_t)(T * k) * (size_t)I * 4);
+  return kMoeActOff + round256((size_t)(T * k) * (size_t)I * 2) + round256((size_t)(T * k) * (size_t)(I / 32) * 4);
 }
 
 static geg_status moe_layer(int fmt, const void* x, const int32_t* ids, const float* weights, const uint8_t* w13,
@@ -1120,7 +1121,8 @@ static geg_status moe_layer(int fmt, const void* x, const int32_t* ids, const fl
   g.out = reinterpret_cast<uint16_t*>(out);
   g.err = reinterpret_cast<uint32_t*>(wsb);
   g.plan = reinterpret_cast<int32_t*>(wsb + kHeader);
-  g.act = reinterpret_cast<float*>(wsb + kMoeActOff);
+  g.act = reinterpret_cast<uint16_t*>(wsb + kMoeActOff);
+  g.act_scale = reinterpret_cast<float*>(wsb + kMoeActOff + round256((size_t)(T * k) * (size_t)I * 2));
   g.H = H;
   g.I = I;
   g.T = (int32_t)T;

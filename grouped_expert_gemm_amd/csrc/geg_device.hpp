@@ -362,6 +362,14 @@ __device__ __forceinline__ uint16_t to_bf16(float a) {
   return __builtin_bit_cast(uint16_t, (__bf16)a);
 }
 
+// Workgroup barrier for LDS: this wavefront's LDS accesses are done, its loads from
+// memory may still be in flight (__syncthreads waits for those too, which would end a
+// prefetch). The clobber keeps the compiler from moving memory accesses across.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0); vmcnt, expcnt: no wait
+  asm volatile("s_barrier" ::: "memory");
+}
+
 // ------------------------------------------------------------------ routing plan
 // Each workgroup rebuilds, in LDS, the exclusive prefix sum of the per-expert row
 // counts ("grouped-nf4-gemm releases", v0.2.6: rows are grouped by expert and

@@ -159,14 +159,15 @@ struct MoeArgs {
   const uint8_t* w2;      // codes [E, H, I/2]
   const void* s2;
   uint16_t* out;          // bf16 [T, H]
-  float* act;             // workspace: fp32 [T k, I] in the second kernel's order
+  uint16_t* act;          // workspace: fp16 [T k, I] in the second kernel's order, and
+  float* act_scale;       // its powers of two [T k, I/32]
   int32_t* plan;          // workspace: the grouping, kMoePlanWords
   uint32_t* err;
   int64_t H, I;
   int32_t T, k, E;
-  int32_t rb;             // output columns per workgroup of the second kernel (set by the launcher)
+  int32_t rb;             // output columns per workgroup of the second kernel (its launcher's)
 };
-hipError_t launch_moe_layer(int fmt, MoeArgs g, int cus, hipStream_t s);
+hipError_t launch_moe_layer(int fmt, const MoeArgs& g, int cus, hipStream_t s);
 // Low-rank adapter: U = s X T_e^T (T fp32 [E, r, C], U fp32 [M, r]); G_e = s
 // sum_rows Wd^T Nw (fp32, [E, Wc, r] or with jc [E, r, Wc]); out[e] = in[e]^T
 // for fp32 [E, P, Qd]. The delta U Q^T itself is added in the tiled kernel's

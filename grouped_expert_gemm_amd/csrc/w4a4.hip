@@ -383,7 +383,7 @@ __global__ __launch_bounds__(kThreads) void w4a4_narrow_kernel(W4A4Args g) {
       have_chunk = cur.chunk;
       row0 = p_off[cur.e] + (int64_t)cur.chunk * 16 * RB;
       rows = (int)min<int64_t>(16 * RB, p_off[cur.e + 1] - row0);
-      __syncthreads();   // the rows before are no longer read
+      lds_barrier();   // the rows before are no longer read
       const int ppr = nst * 16;   // 8-value pieces per padded row
       for (int p = t; p < rows * ppr; p += kThreads) {
         const int r = p / ppr, c = p % ppr;
@@ -400,7 +400,7 @@ __global__ __launch_bounds__(kThreads) void w4a4_narrow_kernel(W4A4Args g) {
           if (byte == 255) atomicOr(g.err, kErrNonFinite);
         }
       }
-      __syncthreads();
+      lds_barrier();
     }
     f32x4 acc[RB];
 #pragma unroll
@@ -436,7 +436,7 @@ __global__ __launch_bounds__(kThreads) void w4a4_narrow_kernel(W4A4Args g) {
     f32x4* pp = part + par * 4 * RB * 64;
 #pragma unroll
     for (int b = 0; b < RB; ++b) pp[(wave * RB + b) * 64 + lane] = acc[b];
-    __syncthreads();
+    lds_barrier();
     if (t < 64 * RB) {
       const int b = t >> 6, r = 16 * b + r16;
       f32x4 v = pp[t];

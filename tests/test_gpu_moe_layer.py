@@ -36,7 +36,9 @@ def _reference(c):
 
     Allowed: the bf16 result (2^-8); fp32 sums of n products, n 2^-24 of their magnitudes;
     NF4's table as fp16, 2^-11 of every product; silu's slope is at most 1.1; the hardware
-    exponential and reciprocal, 2^-20 of act."""
+    exponential and reciprocal, 2^-20 of act; act as fp16 scaled per 32 values so that the
+    largest lies in [2^14, 2^15): 2^-11 of each, or for those below fp16's normal range
+    (2^-14) half its last step, 2^-25 against at least 2^14: 2^-39 of the block's largest."""
     x, w = c["x"].double().numpy(), c["w"].double().numpy()
     T, H, I = c["T"], c["H"], c["I"]
     table = 2.0 ** -11 if c["fmt"] == "nf4" else 0.0
@@ -51,6 +53,8 @@ def _reference(c):
             silu = g / (1 + np.exp(-g))
             act = silu * u
             dact = 1.1 * dg * np.abs(u) + np.abs(silu) * du + 1.1 * dg * du + 2.0 ** -20 * np.abs(act)
+            block = np.repeat(np.abs(act).reshape(-1, 32).max(1), 32)
+            dact = dact * (1 + 2.0 ** -11) + 2.0 ** -11 * np.abs(act) + 2.0 ** -39 * block
             d2 = np.abs(c["d2"][e])
             out[t] += w[t, s] * (c["d2"][e] @ act)
             off[t] += w[t, s] * (d2 @ dact + (table + (I + 64) * 2.0 ** -24) * (d2 @ (np.abs(act) + dact)))
@@ -80,6 +84,21 @@ def _check(c, **kw):
                                        (5, 4, 6, 64, 2240)])
 def test_layer_matches_fp64(fmt, T, k, E, H, I):
     _check(_case(fmt, T, k, E, H, I))
+
+
+@pytest.mark.parametrize("scale", [1e-12, 3e4])
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+def test_activations_of_any_scale(fmt, scale):
+    # act runs as the square of the gate/up weights' scale: far outside fp16 without its own
+    c = _case(fmt, 3, 2, 4, 256, 128)
+    if fmt == "nf4":
+        c["s13"] = (c["s13"] * scale).astype(np.float32)
+        c["d13"] = P.dequant_nf4(c["q13"], c["s13"])
+    else:
+        shift = int(np.round(np.log2(scale)))
+        c["s13"] = (c["s13"].astype(np.int32) + shift).astype(np.uint8)
+        c["d13"] = P.dequant_mxfp4(c["q13"], c["s13"])
+    _check(c)
 
 
 @pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 32, 96), (3, 2, 4, 96, 32), (2, 4, 4, 2880, 160), (16, 4, 8, 160, 2880)])

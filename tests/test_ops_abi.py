@@ -88,7 +88,7 @@ def test_layer_refusals():
             assert _layer(name, **{p: P + 8}) == 3, p
         assert _layer(name, ws=None) == 5 and _layer(name, ws=P + 16) == 5
         need = L().geg_moe_layer_workspace_bytes(4, 2, 64)
-        assert need == 256 + 3328 + 8 * 64 * 4
+        assert need == 256 + 3328 + 8 * 64 * 2 + 256   # act fp16 and its scales
         assert _layer(name, nbytes=need - 1) == 5
         assert _layer(name, nbytes=need) not in (0, 1, 2, 3, 5, 8)
     assert _layer(s13=P + 2) == 3 and _layer("gmxfp4_moe_layer", s13=P + 1) not in (0, 3)
