@@ -8,17 +8,17 @@
 //
 // Bound by streaming the packed weights of the experts that the tokens touch, each
 // byte once: the (token, slot) entries are grouped by expert in LDS (at most 256
-// entries: their places come from counting, no sort), and a wavefront that holds a
-// piece of an expert's weight rows in registers takes the dot products of all of
-// that expert's tokens with it, two at a time, before it moves on.
+// entries: their places come from counting, no sort) into items of one expert and at
+// most four entries, and a wavefront decodes a piece of an item's weight rows once for
+// the dot products of all its entries.
 //
 // A wavefront takes ROWS weight rows at a time: LPR lanes per row (64, 32 or 16, by the
 // row length), U = ROWS LPR / 64 row groups, each lane a 16-byte chunk of 32 codes per
 // row and pass, against the tokens' same 32 values with packed fp32-accumulated dot
 // products. NF4 codes go through the byte table in LDS (two fp16 values per 32-bit
 // read), MXFP4 through the scaled fp4 conversion; the block scale multiplies the
-// chunk's fp32 dot product. One workgroup of 16 wavefronts per CU shares the table, the
-// grouping and the staged tokens.
+// chunk's fp32 dot product. One workgroup per CU shares the table, the grouping and the
+// staged tokens.
 //
 // act goes from one kernel to the other as fp16 with a power-of-two scale per 32 values
 // that puts the block's largest in [2^14, 2^15): 11 bits for everything within 2^-29 of
@@ -38,12 +38,20 @@ namespace {
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 
-constexpr int MT = 1024;             // threads per workgroup
-constexpr int MW = MT / 64;          // wavefronts
-constexpr int MG = 4;                // entries per item (an expert with more gets several)
-constexpr int UP_ROWS = 4;           // first kernel: weight rows per wavefront and unit,
-constexpr int UNIT_ROWS = UP_ROWS * MW;   // per workgroup: 64, the 32 act values of a block
-static_assert(UNIT_ROWS == 64, "a unit of the first kernel makes one block of act");
+constexpr int MG = 4;   // most entries per item
+
+// One token: 16 wavefronts of 4 weight rows and one entry each, so that every load is out
+// as soon as possible. More: 8 wavefronts of 8 rows and up to four entries (with twice the
+// registers each; 16 would spill). Either way a unit of the first kernel is 64 rows, the
+// 32 values of a block of act.
+template <bool ONE>
+struct Shape {
+  static constexpr int kMT = ONE ? 1024 : 512;   // threads per workgroup
+  static constexpr int kMW = kMT / 64;
+  static constexpr int kRows = ONE ? 4 : 8;      // weight rows per wavefront
+  static constexpr int kMost = ONE ? 1 : MG;     // entries taken at once
+  static_assert(kMW * kRows == 64, "a unit makes one block of act");
+};
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mrsrc(const void* base, int64_t bytes) {
   const int32_t n = bytes > 0x7FFFFFF0 ? 0x7FFFFFF0 : (int32_t)bytes;
@@ -77,78 +85,97 @@ __device__ __forceinline__ float fold16(float a, float b) {
   return __uint_as_float(x) + __uint_as_float(y);
 }
 
-// Grouping of the T k entries by expert, in LDS. Entry f's place is the number of
-// entries with a smaller expert, or the same and a smaller index; dropped entries
-// (an id outside [0, E)) get none. item[q] is the q-th run of at most MG places of one
-// expert.
+// Maximum over each half wavefront, on all its lanes.
+__device__ __forceinline__ uint32_t max32(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, false));   // row_ror:8
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, false));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, false));
+  const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  const uint32_t x = r[0], y = r[1];
+  return max(x, y);
+}
+
+// Grouping of the T k entries by expert, in LDS. An entry's place is the number of
+// entries with a smaller expert, or the same and a smaller index; dropped entries (an id
+// outside [0, E)) get none. An item is a run of at most MOST places of one expert.
 struct Groups {
-  int32_t id[kMoeMaxEntries];       // expert of each entry, -1 for a dropped one
-  int32_t ent[kMoeMaxEntries];      // entry at each place
-  int32_t lead[kMoeMaxEntries];     // at a run's first place its expert, else -1
-  int32_t count[kMoeMaxEntries];    // at a run's first place its entries
-  int32_t expert[kMoeMaxEntries];   // of each item: expert, first place, entries
+  int32_t key[kMoeMaxEntries];         // of each entry: expert * 256 + index; dropped: the largest
+  int32_t id[kMoeMaxEntries + MG];     // at each place: its expert (-1 past the last), its
+  int32_t ent[kMoeMaxEntries];         // entry and token
+  int32_t tok[kMoeMaxEntries];
+  int32_t expert[kMoeMaxEntries];      // of each item: expert, first place, entries
   int32_t first[kMoeMaxEntries];
   int32_t size[kMoeMaxEntries];
   int32_t items;
 };
 
 // Every thread of the workgroup calls it (barriers inside). `err` (may be NULL)
-// receives the flag of a dropped entry. `mine` is entry threadIdx.x's expert.
-__device__ __forceinline__ void group_entries(Groups& g, int mine, int n, int E, uint32_t* err) {
+// receives the flag of a dropped entry. `mine` is entry threadIdx.x's id.
+template <int MT, int MOST>
+__device__ __forceinline__ void group_entries(Groups& g, int mine, int n, int k, int E, uint32_t* err) {
+  constexpr int TPE = MT / kMoeMaxEntries;   // lanes per entry, each counting a share of the others
+  static_assert(TPE == 4 || TPE == 2, "two or four lanes per entry");
+  static_assert(kMaxExperts * kMoeMaxEntries < INT32_MAX, "keys fit");
   const int t = threadIdx.x;
-  if (t < n && (mine < 0 || mine >= E)) {
-    if (err) atomicOr(err, kErrBadExpertId);
-    mine = -1;
-  }
   if (t < kMoeMaxEntries) {
-    g.id[t] = t < n ? mine : -1;
-    g.lead[t] = -1;
+    const bool ok = t < n && mine >= 0 && mine < E;
+    if (t < n && !ok && err) atomicOr(err, kErrBadExpertId);
+    g.key[t] = ok ? mine * kMoeMaxEntries + t : INT32_MAX;
   }
+  if (t < kMoeMaxEntries + MG) g.id[t] = -1;
   lds_barrier();
-  if (t < n && mine >= 0) {
-    int place = 0, rank = 0, cnt = 0;
-    for (int f0 = 0; f0 < n; f0 += 4) {   // the same address on every lane: broadcast reads
-      const i32x4 v = *reinterpret_cast<const i32x4*>(g.id + f0);
+  const int f = t / TPE, key = g.key[f];
+  int place = 0;
+  for (int f0 = 4 * (t % TPE); f0 < n; f0 += 4 * TPE) {
+    const i32x4 v = *reinterpret_cast<const i32x4*>(g.key + f0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = v[j];
-        const bool before = f0 + j < t;
-        place += e >= 0 && (e < mine || (e == mine && before));
-        rank += e == mine && before;
-        cnt += e == mine;
-      }
-    }
-    g.ent[place] = t;
-    if (rank % MG == 0) {
-      g.lead[place] = mine;
-      g.count[place] = min(MG, cnt - rank);
-    }
+    for (int j = 0; j < 4; ++j) place += v[j] < key;
+  }
+  place += __builtin_amdgcn_update_dpp(0, place, 0xB1, 0xF, 0xF, false);                  // lane ^ 1
+  if (TPE == 4) place += __builtin_amdgcn_update_dpp(0, place, 0x4E, 0xF, 0xF, false);   // lane ^ 2
+  if (t % TPE == 0 && key != INT32_MAX) {
+    g.id[place] = key / kMoeMaxEntries;
+    g.ent[place] = f;
+    g.tok[place] = f / k;
   }
   lds_barrier();
   if (t < 64) {
-    int q = 0;   // runs so far, 64 places per ballot
-    for (int base = 0; base < n; base += 64) {
-      const int e = g.lead[base + t];
-      const uint64_t at = __ballot(e >= 0);
-      if (e >= 0) {
-        const int to = q + __builtin_popcountll(at & ((1ull << t) - 1));
-        g.expert[to] = e;
-        g.first[to] = base + t;
-        g.size[to] = g.count[base + t];
+    // items of three and four entries first: the work that is left for a last, partial
+    // round is then the cheap one
+    int items = 0;
+    for (int big = 1; big >= 0; --big) {
+      int run = 0;   // first place of the run that reaches into the window of 64 places
+      for (int base = 0; base < n; base += 64) {
+        const int p = base + t, e = g.id[p];
+        const uint64_t starts = __ballot(e >= 0 && (p == 0 || g.id[p - 1] != e));
+        const uint64_t upto = starts & (~0ull >> (63 - t));
+        const int start = upto ? base + 63 - __builtin_clzll(upto) : run;
+        int cnt = 1;
+#pragma unroll
+        for (int j = 1; j < MOST; ++j) cnt += g.id[p + j] == e;
+        const bool lead = e >= 0 && (p - start) % MOST == 0 && (cnt > 2) == (big != 0);
+        const uint64_t leads = __ballot(lead);
+        if (lead) {
+          const int to = items + __builtin_popcountll(leads & ((1ull << t) - 1));
+          g.expert[to] = e;
+          g.first[to] = p;
+          g.size[to] = cnt;
+        }
+        items += __builtin_popcountll(leads);
+        if (starts) run = base + 63 - __builtin_clzll(starts);
       }
-      q += __builtin_popcountll(at);
     }
-    if (t == 0) g.items = q;
+    if (t == 0) g.items = items;
   }
   lds_barrier();
 }
 
-// Sums of per-lane values d[u][m] over the LPR lanes of their rows, added into
-// acc[(m0 + m) * R + row], R = U * 64 / LPR rows, by the lanes that end up with them.
-// (An odd count's missing second entry adds a duplicate to a row that nobody reads.)
-template <int LPR, int U, int RV>
-__device__ __forceinline__ void add_sums(const float (&d)[U][RV], int lane, int m0, float* acc) {
-  constexpr int G = 64 / LPR, R = U * G;
+// Sums of per-lane values d[u][m] over the LPR lanes of their rows: put(row, m, sum) on
+// one lane for each of the unit's rows and entries.
+template <int LPR, int U, int RV, typename Put>
+__device__ __forceinline__ void sum_lanes(const float (&d)[U][RV], int lane, Put put) {
+  constexpr int G = 64 / LPR;
   constexpr int F = LPR / 16;   // row groups folded into the wavefront's four rows of 16 lanes
   static_assert(U % F == 0, "whole folds");
   const int row16 = lane >> 4;
@@ -173,11 +200,10 @@ __device__ __forceinline__ void add_sums(const float (&d)[U][RV], int lane, int 
   // (F = 2); lane groups 0..3 (F = 1)
   const int row = F == 4 ? (((row16 & 1) << 1) | (row16 >> 1)) : (F == 2 ? G * (row16 & 1) + (row16 >> 1) : row16);
   if ((lane & 15) == 0) {
-    float* p = acc + m0 * R + row;
 #pragma unroll
     for (int u = 0; u < U / F; ++u)
 #pragma unroll
-      for (int m = 0; m < RV; ++m) p[m * R + u * F * G] += v[u][m];
+      for (int m = 0; m < RV; ++m) put(u * F * G + row, m, v[u][m]);
   }
 }
 
@@ -209,22 +235,74 @@ struct Codes {
         scale[u] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(S, (uint32_t)(n * (K >> 5) + c) | off_mask, 0, 0);
     }
   }
-  // Makes row group u's codes new values to the compiler, and keeps what follows behind
-  // what came before: decoded values are then neither kept from one pair of tokens to the
-  // next nor made for several row groups at once (16 registers per code word: spills).
-  __device__ __forceinline__ void next(int u) {
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      uint32_t v = code[u][j];
-      asm volatile("" : "+v"(v));
-      code[u][j] = v;
-    }
-  }
   __device__ __forceinline__ float scale_f32(int u) const {
     return F == NF4 ? __uint_as_float(scale[u]) : e8m0_to_f32(scale[u]);
   }
 };
+
+// tot[u][m] += scale[u] xscale[m] (dot product of row group u's chunk with entry m's 32
+// values), for the four quarters j of the chunk in turn: a quarter's values of all row
+// groups are decoded once for all entries. x(j, m): entry m's 8 values of quarter j as
+// fp16 (FT = NF4) or bf16 (MXFP4) pairs.
+template <Fmt F, int FT, int LPR, int U, int RV, typename X>
+__device__ __forceinline__ void dot_pass(const Codes<F, LPR, U>& w, X x, const float* xscale, const uint32_t* blut,
+                                         uint32_t lane_off, float (&tot)[U][RV]) {
+  constexpr std::integral_constant<int, FT> ft{};
+  float d[U][RV];
+  u32x4 xv[2][RV];   // the next quarter's values are fetched ahead
+#pragma unroll
+  for (int m = 0; m < RV; ++m) xv[0][m] = x(0, m);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    u32x4 v[U];
+    if (j < 3) {
+#pragma unroll
+      for (int m = 0; m < RV; ++m) xv[(j + 1) & 1][m] = x(j + 1, m);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {   // values k = 8j .. 8j+7, natural order
+      if constexpr (F == NF4)
+        v[u] = nf4_byte_lut_decode8(blut, w.code[u][j], lane_off);
+      else if constexpr (FT == NF4)
+        v[u] = mxfp4_decode8_f16(w.code[u][j]);
+      else
+        v[u] = mxfp4_decode8(w.code[u][j], 1.0f);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int m = 0; m < RV; ++m) {
+        if (j == 0) d[u][m] = 0.f;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) d[u][m] = fdot2(v[u][p], xv[j & 1][m][p], d[u][m], ft);
+        // finished here, not where it is used: with a quarter's values live at a time
+        // nothing spills
+        asm volatile("" : "+v"(d[u][m]));
+      }
+    __builtin_amdgcn_sched_barrier(0);
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const float s = w.scale_f32(u);   // 0 for chunks past the row
+#pragma unroll
+    for (int m = 0; m < RV; ++m) tot[u][m] += d[u][m] * (xscale ? s * xscale[m] : s);
+  }
+}
+
+// f(RV) with the entries taken at once for an item of cnt: 1, 2 or 4.
+template <int MOST, typename Fn>
+__device__ __forceinline__ void by_entries(int cnt, Fn f) {
+  if constexpr (MOST == 1) {
+    f(std::integral_constant<int, 1>{});
+  } else {
+    if (cnt == 1)
+      f(std::integral_constant<int, 1>{});
+    else if (cnt == 2)
+      f(std::integral_constant<int, 2>{});
+    else
+      f(std::integral_constant<int, 4>{});
+  }
+}
 
 template <Fmt F>
 __device__ __forceinline__ const void* expert_scales(const void* s, int e, int64_t N, int64_t K) {
@@ -245,39 +323,53 @@ template <Fmt F>
 constexpr int x_lds_bytes() { return F == NF4 ? 64 << 10 : 140 << 10; }
 
 // First kernel. Units (item, 64 rows of its gate/up weight = 32 values of act) over a grid
-// of one workgroup per CU, 4 rows per wavefront; a wavefront's codes of the next unit are
+// of one workgroup per CU; a wavefront's codes of the next unit are
 // in flight while it works on this one. x is staged in LDS when all tokens fit (XL), as
 // fp16 for NF4 (flagged when it overflows; MXFP4 keeps bf16, exact), else each lane loads
 // its slice from memory. The sums meet in LDS, where a half wavefront per entry forms the
 // 32 act values, their scale and their fp16 form (value i = 32 c + 8 j + b of a row at
 // ((j (I / 32) + c) 8 + b): the order in which the second kernel's lanes read it).
 // Workgroup 0 also writes the grouping.
-template <Fmt F, int LPR, int RV, bool XL>
-__global__ __launch_bounds__(MT) void moe_up_kernel(MoeArgs g) {
-  constexpr int G = 64 / LPR, U = UP_ROWS / G;
-  constexpr std::integral_constant<int, F> fmt{};
-  __shared__ __attribute__((aligned(16))) Groups grp;
-  __shared__ __attribute__((aligned(16))) uint32_t blut[F == NF4 ? kNf4ByteLutWords : 4];
-  __shared__ __attribute__((aligned(16))) uint8_t xs[XL ? x_lds_bytes<F>() : 16];
-  __shared__ float accs[2][MW][MG * UP_ROWS];
+template <Fmt F, int LPR, bool XL, bool ONE>
+__global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
+  constexpr int MT = Shape<ONE>::kMT, MW = Shape<ONE>::kMW, ROWS = Shape<ONE>::kRows, MOST = Shape<ONE>::kMost;
+  constexpr int G = 64 / LPR, U = ROWS / G;
+  // the byte table first: at LDS address 0 a code byte's address needs no base added
+  __shared__ struct __attribute__((aligned(16))) {
+    uint32_t blut[F == NF4 ? kNf4ByteLutWords : 4];
+    uint8_t xs[XL ? x_lds_bytes<F>() : 16];
+    Groups grp;
+    float accs[2][MW][MOST * ROWS];
+  } lds;
+  uint32_t* const blut = lds.blut;
+  uint8_t* const xs = lds.xs;
+  Groups& grp = lds.grp;
   const int n = g.T * g.k;
   const int64_t H = g.H, N = 2 * g.I;
   const int C = (int)(H >> 5), CI = (int)(g.I >> 5);
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   uint32_t range = 0;
-  const int my_id = t < n ? g.ids[t] : 0;   // in flight during the set-up
-  if constexpr (XL) {
-    const int pieces = g.T * 4 * C;   // 8 values each
-    for (int p = t; p < pieces; p += MT) {
+  // The tokens' loads go out before the weights' (loads complete in order): the first XP
+  // pieces of 8 values per thread wait in registers, more are stored right away.
+  constexpr int XP = 4;
+  const int pieces = g.T * 4 * C;
+  u32x4 xp[XP];
+  auto put_x = [&](int p, u32x4 v) {
+    if (p < pieces) {
       const int tok = p / (4 * C), q = p % (4 * C);   // piece q of the token: chunk q / 4, piece q % 4
-      u32x4 v = reinterpret_cast<const u32x4*>(g.x)[p];
       if constexpr (F == NF4) v = bf16x8_to_f16(v, range);
       *reinterpret_cast<u32x4*>(xs + ((4 * tok + (q & 3)) * C + (q >> 2)) * 16) = v;
     }
+  };
+  const int my_id = t < n ? g.ids[t] : 0;
+  if constexpr (XL) {
+#pragma unroll
+    for (int i = 0; i < XP; ++i)
+      if (t + i * MT < pieces) xp[i] = reinterpret_cast<const u32x4*>(g.x)[t + i * MT];
+    for (int p = t + XP * MT; p < pieces; p += MT) put_x(p, reinterpret_cast<const u32x4*>(g.x)[p]);
   }
-  if constexpr (F == NF4) nf4_byte_lut_fill<64, MT>(blut);
-  group_entries(grp, my_id, n, g.E, blockIdx.x == 0 ? g.err : nullptr);
+  group_entries<MT, MOST>(grp, my_id, n, g.k, g.E, blockIdx.x == 0 ? g.err : nullptr);
   const int items = grp.items;
   if (blockIdx.x == 0 && t < kMoeMaxEntries) {
     if (t == 0) g.plan[0] = items;
@@ -298,78 +390,64 @@ __global__ __launch_bounds__(MT) void moe_up_kernel(MoeArgs g) {
     const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s13, e, N, H), scale_bytes<F>(N, H));
     const int c = c0 + li;
     // chunks past the row read as zero: their offsets lie past every buffer
-    w.load(W, S, (int64_t)(unit % CI) * UNIT_ROWS + UP_ROWS * wave, gl, H, c, c < C ? 0u : 0xFFFFFFF0u);
+    w.load(W, S, (int64_t)(unit % CI) * 64 + ROWS * wave, gl, H, c, c < C ? 0u : 0xFFFFFFF0u);
   };
   Codes<F, LPR, U> nxt;
-  int par = 0;
   if ((int)blockIdx.x < total) load(blockIdx.x, 0, nxt);
-  for (int unit = blockIdx.x; unit < total; unit += gridDim.x, par ^= 1) {
+  // the table and the tokens while the first weights are on their way
+  if constexpr (F == NF4) nf4_byte_lut_fill<64, MT>(blut);
+  if constexpr (XL) {
+#pragma unroll
+    for (int i = 0; i < XP; ++i) put_x(t + i * MT, xp[i]);
+  }
+  lds_barrier();
+  int seq = 0;
+  for (int unit = blockIdx.x; unit < total; unit += gridDim.x, ++seq) {
     const int q = unit / CI;
     const int first = __builtin_amdgcn_readfirstlane(grp.first[q]);
     const int cnt = __builtin_amdgcn_readfirstlane(grp.size[q]);
-    float* acc = accs[par][wave];
-    if (lane < MG * UP_ROWS) acc[lane] = 0.f;
-    __builtin_amdgcn_wave_barrier();
-    for (int c0 = 0; c0 < C; c0 += LPR) {
-      const int c = c0 + li;
-      const uint32_t off_mask = c < C ? 0u : 0xFFFFFFF0u;
-      Codes<F, LPR, U> w = nxt;
-      if (c0 + LPR < C)
-        load(unit, c0 + LPR, nxt);
-      else if (unit + (int)gridDim.x < total)
-        load(unit + gridDim.x, 0, nxt);
-      for (int m0 = 0; m0 < cnt; m0 += RV) {
-        u32x4 xv[RV][4];
+    float(*acc)[MOST * ROWS] = lds.accs[seq & 1];
+    by_entries<MOST>(cnt, [&](auto rv) {
+      constexpr int RV = decltype(rv)::value;
+      int tok[RV];
 #pragma unroll
-        for (int m = 0; m < RV; ++m) {
-          const int tok = __builtin_amdgcn_readfirstlane(grp.ent[first + min(m0 + m, cnt - 1)]) / g.k;
+      for (int m = 0; m < RV; ++m) tok[m] = __builtin_amdgcn_readfirstlane(grp.tok[first + min(m, cnt - 1)]);
+      float tot[U][RV];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (XL) {
-              xv[m][j] = *reinterpret_cast<const u32x4*>(xs + ((4 * tok + j) * C + min(c, C - 1)) * 16);
-            } else {
-              xv[m][j] = __builtin_amdgcn_raw_buffer_load_b128(
-                  X, (uint32_t)(((int64_t)tok * H + 32 * c) * 2 + 16 * j) | off_mask, 0, 0);
-              if constexpr (F == NF4) xv[m][j] = bf16x8_to_f16(xv[m][j], range);
-            }
-          }
-        }
-        float d[U][RV];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          w.next(u);
-#pragma unroll
-          for (int m = 0; m < RV; ++m) d[u][m] = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            u32x4 v;   // values k = 8j .. 8j+7, natural order
-            if constexpr (F == NF4)
-              v = nf4_byte_lut_decode8(blut, w.code[u][j], lane_off);
-            else
-              v = mxfp4_decode8(w.code[u][j], 1.0f);
-#pragma unroll
-            for (int m = 0; m < RV; ++m)
-#pragma unroll
-              for (int p = 0; p < 4; ++p) d[u][m] = fdot2(v[p], xv[m][j][p], d[u][m], fmt);
-          }
-          const float s = w.scale_f32(u);
-#pragma unroll
-          for (int m = 0; m < RV; ++m) {
-            d[u][m] = off_mask ? 0.f : s * d[u][m];
-            asm volatile("" : "+v"(d[u][m]));   // finished here, not where it is used
-          }
-        }
-        add_sums<LPR, U, RV>(d, lane, m0, acc);
+        for (int m = 0; m < RV; ++m) tot[u][m] = 0.f;
+      for (int c0 = 0; c0 < C; c0 += LPR) {
+        const int c = c0 + li, cc = min(c, C - 1);
+        const uint32_t off_mask = c < C ? 0u : 0xFFFFFFF0u;
+        const Codes<F, LPR, U> w = nxt;
+        if (c0 + LPR < C)
+          load(unit, c0 + LPR, nxt);
+        else if (unit + (int)gridDim.x < total)
+          load(unit + gridDim.x, 0, nxt);
+        dot_pass<F, F>(
+            w,
+            [&](int j, int m) -> u32x4 {
+              if constexpr (XL) {
+                return *reinterpret_cast<const u32x4*>(xs + ((4 * tok[m] + j) * C + cc) * 16);
+              } else {
+                u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
+                    X, (uint32_t)(((int64_t)tok[m] * H + 32 * c) * 2 + 16 * j) | off_mask, 0, 0);
+                if constexpr (F == NF4) v = bf16x8_to_f16(v, range);
+                return v;
+              }
+            },
+            nullptr, blut, lane_off, tot);
       }
-    }
+      sum_lanes<LPR, U, RV>(tot, lane, [&](int row, int m, float v) { acc[wave][m * ROWS + row] = v; });
+    });
     lds_barrier();   // the sums of this unit; the other parity's are free again after the next one
-    const int m = t >> 5, i = t & 31;
+    // two wavefronts, others from unit to unit, form the block of act: 32 lanes per entry
+    const int m = ((wave - 2 * seq) & (MW - 1)) * 2 + (lane >> 5), i = lane & 31;
     if (m < cnt) {
-      const float* a = accs[par][i >> 1] + m * UP_ROWS + 2 * (i & 1);
+      const float* a = acc[2 * i / ROWS] + m * ROWS + 2 * i % ROWS;
       const float v = swiglu(a[0], a[1]);
-      uint32_t mx = __float_as_uint(v) & 0x7FFFFFFFu;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) mx = max(mx, (uint32_t)__shfl_xor((int)mx, o));
+      const uint32_t mx = max32(__float_as_uint(v) & 0x7FFFFFFFu);
       // the block's largest to [2^14, 2^15); 2^ex stays a normal fp32 value
       const int ex = max((int)(mx >> 23) - 127 - 14, -126);
       const int64_t slot = grp.ent[first + m];
@@ -385,126 +463,127 @@ __global__ __launch_bounds__(MT) void moe_up_kernel(MoeArgs g) {
 }
 
 // Second kernel. A workgroup owns RB rows of W2 (columns of out), RB / ROWS subgroups; its
-// wavefronts share the (item, subgroup) pieces of work, each adding its weighted sums
-// into an own [RB][T] array in LDS; the arrays are added in wavefront order, so results
-// do not depend on timing.
-template <Fmt F, int LPR, int RV, int ROWS>
-__global__ __launch_bounds__(MT) void moe_down_kernel(MoeArgs g) {
+// wavefronts share the (item, subgroup) pieces of work, the codes of the next piece in
+// flight while one is worked on, each adding its weighted sums into an own [RB][T] array
+// in LDS; the arrays are added in wavefront order, so results do not depend on timing.
+template <Fmt F, int LPR, bool ONE>
+__global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
+  constexpr int MT = Shape<ONE>::kMT, MW = Shape<ONE>::kMW, ROWS = Shape<ONE>::kRows, MOST = Shape<ONE>::kMost;
   constexpr int G = 64 / LPR, U = ROWS / G;
-  constexpr std::integral_constant<int, NF4> f16{};   // both formats multiply fp16 pairs
-  __shared__ __attribute__((aligned(16))) uint32_t blut[F == NF4 ? kNf4ByteLutWords : 4];
-  __shared__ float outs[MW][kMoeRowBlock * kMoeMaxTokens];   // [wavefront][row][token]
-  __shared__ float accs[MW][MG * ROWS];
+  __shared__ struct __attribute__((aligned(16))) {
+    uint32_t blut[F == NF4 ? kNf4ByteLutWords : 4];    // at LDS address 0
+    float outs[MW][kMoeRowBlock * kMoeMaxTokens];      // [wavefront][row][token]
+    int32_t item[2 * kMoeMaxEntries];                  // expert; first place | entries << 16
+    int32_t ent[kMoeMaxEntries], tok[kMoeMaxEntries];  // at each place
+    float weight[kMoeMaxEntries];
+  } lds;
+  uint32_t* const blut = lds.blut;
   const int64_t H = g.H, K = g.I;
-  const int C = (int)(K >> 5);
+  const int C = (int)(K >> 5), T = g.T, n = T * g.k;
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int gl = lane / LPR, li = lane % LPR;
   const uint32_t lane_off = nf4_byte_lut_lane(lane);
-  const int items = g.plan[0];
-  if constexpr (F == NF4) nf4_byte_lut_fill<64, MT>(blut);
   const int RB = g.rb, subs = RB / ROWS;
+  const int items = g.plan[0];
+  for (int i = t; i < 2 * n; i += MT) lds.item[i] = g.plan[4 + i];
+  if (t < n) {
+    // places past the last hold nothing: any entry will do
+    const int f = min((uint32_t)g.plan[4 + 2 * kMoeMaxEntries + t], (uint32_t)(n - 1));
+    lds.ent[t] = f;
+    lds.tok[t] = f / g.k;
+    lds.weight[t] = g.weights[f];
+  }
+  lds_barrier();
   const int64_t blocks = (H + RB - 1) / RB;
-  float* acc = accs[wave];
+  const int works = items * subs;
+  Codes<F, LPR, U> nxt;
+  auto load = [&](int64_t b, int wk, int c0) {
+    const int q = wk / subs, sub = wk % subs;
+    const int e = __builtin_amdgcn_readfirstlane(lds.item[2 * q]);
+    const __amdgpu_buffer_rsrc_t W = mrsrc(g.w2 + (int64_t)e * H * (K >> 1), H * (K >> 1));
+    const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s2, e, H, K), scale_bytes<F>(H, K));
+    const int c = c0 + li;
+    nxt.load(W, S, b * RB + sub * ROWS, gl, K, c, c < C ? 0u : 0xFFFFFFF0u);
+  };
+  if (wave < works) load(blockIdx.x, wave, 0);
+  for (int i = lane; i < RB * T; i += 64) lds.outs[wave][i] = 0.f;
+  if constexpr (F == NF4) nf4_byte_lut_fill<64, MT>(blut);
+  lds_barrier();
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-    for (int i = t; i < MW * kMoeRowBlock * kMoeMaxTokens; i += MT) (&outs[0][0])[i] = 0.f;
-    __syncthreads();
-    for (int wk = wave; wk < items * subs; wk += MW) {
+    for (int wk = wave; wk < works; wk += MW) {
       const int q = wk / subs, sub = wk % subs;
-      const int64_t n0 = b * RB + (int64_t)sub * ROWS;
-      const int e = g.plan[4 + 2 * q];
-      const int fc = g.plan[4 + 2 * q + 1];
+      const int fc = __builtin_amdgcn_readfirstlane(lds.item[2 * q + 1]);
       const int first = fc & 0xFFFF, cnt = fc >> 16;
-      const __amdgpu_buffer_rsrc_t W = mrsrc(g.w2 + (int64_t)e * H * (K >> 1), H * (K >> 1));
-      const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s2, e, H, K), scale_bytes<F>(H, K));
-      const int32_t* ent = g.plan + 4 + 2 * kMoeMaxEntries + first;
-      for (int i = lane; i < MG * ROWS; i += 64) acc[i] = 0.f;
-      __builtin_amdgcn_wave_barrier();
-      for (int c0 = 0; c0 < C; c0 += LPR) {
-        const int c = c0 + li, cc = min(c, C - 1);
-        const uint32_t off_mask = c < C ? 0u : 0xFFFFFFF0u;
-        Codes<F, LPR, U> w;
-        w.load(W, S, n0, gl, K, c, off_mask);
-        for (int m0 = 0; m0 < cnt; m0 += RV) {
-            u32x4 xv[RV][4];
+      by_entries<MOST>(cnt, [&](auto rv) {
+        constexpr int RV = decltype(rv)::value;
+        float tot[U][RV];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int m = 0; m < RV; ++m) tot[u][m] = 0.f;
+        for (int c0 = 0; c0 < C; c0 += LPR) {
+          const int c = c0 + li, cc = min(c, C - 1);
+          const Codes<F, LPR, U> w = nxt;
+          const u32x4* a[RV];
           float xs[RV];
 #pragma unroll
           for (int m = 0; m < RV; ++m) {
-            const int64_t f = ent[min(m0 + m, cnt - 1)];
-            const u32x4* a = reinterpret_cast<const u32x4*>(g.act + f * K) + cc;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) xv[m][j] = a[j * C];
-            xs[m] = g.act_scale[f * C + cc] * g.weights[f];
+            const int64_t f = __builtin_amdgcn_readfirstlane(lds.ent[first + min(m, cnt - 1)]);
+            a[m] = reinterpret_cast<const u32x4*>(g.act + f * K);
+            xs[m] = g.act_scale[f * C + cc];
           }
-          float d[U][RV];
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            w.next(u);
-#pragma unroll
-            for (int m = 0; m < RV; ++m) d[u][m] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              u32x4 v;
-              if constexpr (F == NF4)
-                v = nf4_byte_lut_decode8(blut, w.code[u][j], lane_off);
-              else
-                v = mxfp4_decode8_f16(w.code[u][j]);
-#pragma unroll
-              for (int m = 0; m < RV; ++m)
-#pragma unroll
-                for (int p = 0; p < 4; ++p) d[u][m] = fdot2(v[p], xv[m][j][p], d[u][m], f16);
-            }
-            const float s = w.scale_f32(u);
-#pragma unroll
-            for (int m = 0; m < RV; ++m) {
-              d[u][m] = off_mask ? 0.f : (s * xs[m]) * d[u][m];
-              asm volatile("" : "+v"(d[u][m]));
-            }
-          }
-          add_sums<LPR, U, RV>(d, lane, m0, acc);
+          if (c0 + LPR < C)
+            load(b, wk, c0 + LPR);
+          else if (wk + MW < works)
+            load(b, wk + MW, 0);
+          else if (b + gridDim.x < blocks)
+            load(b + gridDim.x, wave, 0);
+          dot_pass<F, NF4>(w, [&](int j, int m) -> u32x4 { return a[m][j * C + cc]; }, xs, blut, lane_off, tot);
         }
-      }
-      __builtin_amdgcn_wave_barrier();
-      asm volatile("" ::: "memory");
-      // one lane per row of the subgroup adds the item's rows to its tokens
-      if (lane < ROWS)
-        for (int m = 0; m < cnt; ++m)
-          outs[wave][(sub * ROWS + lane) * kMoeMaxTokens + ent[m] / g.k] += acc[m * ROWS + lane];
-      __builtin_amdgcn_wave_barrier();
-      asm volatile("" ::: "memory");
+        sum_lanes<LPR, U, RV>(tot, lane, [&](int row, int m, float v) {
+          if (m < cnt)
+            lds.outs[wave][(sub * ROWS + row) * T + lds.tok[first + m]] += lds.weight[first + m] * v;
+        });
+      });
     }
-    __syncthreads();
-    for (int i = t; i < RB * g.T; i += MT) {
-      const int row = i % RB, tok = i / RB;
-      float v = 0.f;
+    lds_barrier();
+    for (int i = t; i < RB * T; i += MT) {
+      float o[MW], v = 0.f;
 #pragma unroll
-      for (int w = 0; w < MW; ++w) v += outs[w][row * kMoeMaxTokens + tok];
-      const int64_t col = b * RB + row;
-      if (col < H) g.out[(int64_t)tok * H + col] = to_bf16(v);
+      for (int w = 0; w < MW; ++w) o[w] = lds.outs[w][i];
+#pragma unroll
+      for (int w = 0; w < MW; ++w) {
+        v += o[w];
+        lds.outs[w][i] = 0.f;
+      }
+      const int64_t col = b * RB + i / T;
+      if (col < H) g.out[(int64_t)(i % T) * H + col] = to_bf16(v);
     }
-    __syncthreads();
+    lds_barrier();
   }
 }
 
-template <Fmt F, int LPR, int RV>
-hipError_t up_x(const MoeArgs& g, int cus, hipStream_t s) {
-  const bool xl = (int64_t)g.T * g.H * 2 <= x_lds_bytes<F>();
-  if (xl)
-    hipLaunchKernelGGL((moe_up_kernel<F, LPR, RV, true>), dim3((unsigned)cus), dim3(MT), 0, s, g);
+template <Fmt F, int LPR, bool ONE>
+hipError_t up(const MoeArgs& g, int cus, hipStream_t s) {
+  const dim3 grid((unsigned)cus), block(Shape<ONE>::kMT);
+  if ((int64_t)g.T * g.H * 2 <= x_lds_bytes<F>())
+    hipLaunchKernelGGL((moe_up_kernel<F, LPR, true, ONE>), grid, block, 0, s, g);
   else
-    hipLaunchKernelGGL((moe_up_kernel<F, LPR, RV, false>), dim3((unsigned)cus), dim3(MT), 0, s, g);
+    hipLaunchKernelGGL((moe_up_kernel<F, LPR, false, ONE>), grid, block, 0, s, g);
   return hipGetLastError();
 }
 
 // Rows of W2 per workgroup: one round of the chip where that stays within the LDS
-// arrays, in whole subgroups of ROWS.
-template <Fmt F, int LPR, int RV, int ROWS>
-hipError_t down_one(MoeArgs g, int cus, hipStream_t s) {
+// arrays.
+template <Fmt F, int LPR, bool ONE>
+hipError_t down(MoeArgs g, int cus, hipStream_t s) {
+  constexpr int ROWS = Shape<ONE>::kRows;
   const int64_t rb = ((g.H + cus - 1) / cus + ROWS - 1) / ROWS * ROWS;
   g.rb = (int)std::min<int64_t>(rb, kMoeRowBlock);
   const int64_t blocks = (g.H + g.rb - 1) / g.rb;
-  hipLaunchKernelGGL((moe_down_kernel<F, LPR, RV, ROWS>), dim3((unsigned)std::min<int64_t>(blocks, cus)), dim3(MT), 0,
-                     s, g);
+  hipLaunchKernelGGL((moe_down_kernel<F, LPR, ONE>), dim3((unsigned)std::min<int64_t>(blocks, cus)),
+                     dim3(Shape<ONE>::kMT), 0, s, g);
   return hipGetLastError();
 }
 
@@ -518,24 +597,18 @@ hipError_t by_lanes(int64_t K, Fn f) {
   return f(std::integral_constant<int, 64>{});
 }
 
-template <Fmt F>
+template <Fmt F, bool ONE>
 hipError_t layer(const MoeArgs& g, int cus, hipStream_t s) {
-  const bool single = g.T == 1;
-  hipError_t e = by_lanes(g.H, [&](auto l) {
-    constexpr int LPR = decltype(l)::value;
-    return single ? up_x<F, LPR, 1>(g, cus, s) : up_x<F, LPR, 2>(g, cus, s);
-  });
+  const hipError_t e = by_lanes(g.H, [&](auto l) { return up<F, decltype(l)::value, ONE>(g, cus, s); });
   if (e != hipSuccess) return e;
-  return by_lanes(g.I, [&](auto l) {
-    constexpr int LPR = decltype(l)::value;
-    return single ? down_one<F, LPR, 1, 4>(g, cus, s) : down_one<F, LPR, 2, 8>(g, cus, s);
-  });
+  return by_lanes(g.I, [&](auto l) { return down<F, decltype(l)::value, ONE>(g, cus, s); });
 }
 
 }  // namespace
 
 hipError_t launch_moe_layer(int fmt, const MoeArgs& g, int cus, hipStream_t s) {
-  return fmt == NF4 ? layer<NF4>(g, cus, s) : layer<MXFP4>(g, cus, s);
+  if (g.T == 1) return fmt == NF4 ? layer<NF4, true>(g, cus, s) : layer<MXFP4, true>(g, cus, s);
+  return fmt == NF4 ? layer<NF4, false>(g, cus, s) : layer<MXFP4, false>(g, cus, s);
 }
 
 }  // namespace geg

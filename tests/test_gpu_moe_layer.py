@@ -110,6 +110,7 @@ def test_mxfp4_sizes_that_are_multiples_of_32_only(T, k, E, H, I):
 def test_every_token_on_one_expert_and_an_expert_named_twice(fmt):
     _check(_case(fmt, 16, 2, 4, 256, 128, ids=[[3, 1]] * 16))
     _check(_case(fmt, 3, 4, 4, 256, 128, ids=[[2, 2, 0, 2]] * 3))
+    _check(_case(fmt, 1, 6, 4, 256, 128, ids=[[2, 2, 0, 2, 2, 2]]))
     # more entries on one expert than one pass over its weights takes
     _check(_case(fmt, 16, 16, 4, 128, 64, ids=[[1] * 16] * 16))
 
