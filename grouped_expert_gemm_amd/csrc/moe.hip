@@ -50,6 +50,7 @@ struct Shape {
   static constexpr int kMW = kMT / 64;
   static constexpr int kRows = ONE ? 4 : 8;      // weight rows per wavefront
   static constexpr int kMost = ONE ? 1 : MG;     // entries taken at once
+  static constexpr int kAhead = ONE ? 3 : 1;     // passes whose codes are in flight
   static_assert(kMW * kRows == 64, "a unit makes one block of act");
 };
 
@@ -333,6 +334,7 @@ constexpr int x_lds_bytes() { return F == NF4 ? 64 << 10 : 140 << 10; }
 template <Fmt F, int LPR, bool XL, bool ONE>
 __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
   constexpr int MT = Shape<ONE>::kMT, MW = Shape<ONE>::kMW, ROWS = Shape<ONE>::kRows, MOST = Shape<ONE>::kMost;
+  constexpr int AHEAD = Shape<ONE>::kAhead;
   constexpr int G = 64 / LPR, U = ROWS / G;
   // the byte table first: at LDS address 0 a code byte's address needs no base added
   __shared__ struct __attribute__((aligned(16))) {
@@ -383,17 +385,24 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
   const uint32_t lane_off = nf4_byte_lut_lane(lane);
   const int total = items * CI;
   const __amdgpu_buffer_rsrc_t X = mrsrc(g.x, (int64_t)g.T * H * 2);
-  // codes of pass c0 of a unit
-  auto load = [&](int unit, int c0, Codes<F, LPR, U>& w) {
-    const int e = __builtin_amdgcn_readfirstlane(grp.expert[unit / CI]);
+  // The passes of this workgroup's units in turn, AHEAD of them with their codes in flight.
+  Codes<F, LPR, U> pre[AHEAD];
+  int l_unit = blockIdx.x, l_c0 = 0;   // the next pass to load
+  auto load_next = [&](Codes<F, LPR, U>& w) {
+    if (l_unit >= total) return;
+    const int e = __builtin_amdgcn_readfirstlane(grp.expert[l_unit / CI]);
     const __amdgpu_buffer_rsrc_t W = mrsrc(g.w13 + (int64_t)e * N * (H >> 1), N * (H >> 1));
     const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s13, e, N, H), scale_bytes<F>(N, H));
-    const int c = c0 + li;
+    const int c = l_c0 + li;
     // chunks past the row read as zero: their offsets lie past every buffer
-    w.load(W, S, (int64_t)(unit % CI) * 64 + ROWS * wave, gl, H, c, c < C ? 0u : 0xFFFFFFF0u);
+    w.load(W, S, (int64_t)(l_unit % CI) * 64 + ROWS * wave, gl, H, c, c < C ? 0u : 0xFFFFFFF0u);
+    if ((l_c0 += LPR) >= C) {
+      l_c0 = 0;
+      l_unit += gridDim.x;
+    }
   };
-  Codes<F, LPR, U> nxt;
-  if ((int)blockIdx.x < total) load(blockIdx.x, 0, nxt);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load_next(pre[i]);
   // the table and the tokens while the first weights are on their way
   if constexpr (F == NF4) nf4_byte_lut_fill<64, MT>(blut);
   if constexpr (XL) {
@@ -420,11 +429,10 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
       for (int c0 = 0; c0 < C; c0 += LPR) {
         const int c = c0 + li, cc = min(c, C - 1);
         const uint32_t off_mask = c < C ? 0u : 0xFFFFFFF0u;
-        const Codes<F, LPR, U> w = nxt;
-        if (c0 + LPR < C)
-          load(unit, c0 + LPR, nxt);
-        else if (unit + (int)gridDim.x < total)
-          load(unit + gridDim.x, 0, nxt);
+        const Codes<F, LPR, U> w = pre[0];
+#pragma unroll
+        for (int i = 0; i + 1 < AHEAD; ++i) pre[i] = pre[i + 1];
+        load_next(pre[AHEAD - 1]);
         dot_pass<F, F>(
             w,
             [&](int j, int m) -> u32x4 {
@@ -469,6 +477,7 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
 template <Fmt F, int LPR, bool ONE>
 __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
   constexpr int MT = Shape<ONE>::kMT, MW = Shape<ONE>::kMW, ROWS = Shape<ONE>::kRows, MOST = Shape<ONE>::kMost;
+  constexpr int AHEAD = Shape<ONE>::kAhead;
   constexpr int G = 64 / LPR, U = ROWS / G;
   __shared__ struct __attribute__((aligned(16))) {
     uint32_t blut[F == NF4 ? kNf4ByteLutWords : 4];    // at LDS address 0
@@ -497,16 +506,27 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
   lds_barrier();
   const int64_t blocks = (H + RB - 1) / RB;
   const int works = items * subs;
-  Codes<F, LPR, U> nxt;
-  auto load = [&](int64_t b, int wk, int c0) {
-    const int q = wk / subs, sub = wk % subs;
-    const int e = __builtin_amdgcn_readfirstlane(lds.item[2 * q]);
+  // the passes of this wavefront's pieces of work, block by block
+  Codes<F, LPR, U> pre[AHEAD];
+  int64_t l_b = blockIdx.x;
+  int l_wk = wave, l_c0 = 0;
+  auto load_next = [&](Codes<F, LPR, U>& w) {
+    if (l_b >= blocks || wave >= works) return;
+    const int e = __builtin_amdgcn_readfirstlane(lds.item[2 * (l_wk / subs)]);
     const __amdgpu_buffer_rsrc_t W = mrsrc(g.w2 + (int64_t)e * H * (K >> 1), H * (K >> 1));
     const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s2, e, H, K), scale_bytes<F>(H, K));
-    const int c = c0 + li;
-    nxt.load(W, S, b * RB + sub * ROWS, gl, K, c, c < C ? 0u : 0xFFFFFFF0u);
+    const int c = l_c0 + li;
+    w.load(W, S, l_b * RB + (l_wk % subs) * ROWS, gl, K, c, c < C ? 0u : 0xFFFFFFF0u);
+    if ((l_c0 += LPR) >= C) {
+      l_c0 = 0;
+      if ((l_wk += MW) >= works) {
+        l_wk = wave;
+        l_b += gridDim.x;
+      }
+    }
   };
-  if (wave < works) load(blockIdx.x, wave, 0);
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i) load_next(pre[i]);
   for (int i = lane; i < RB * T; i += 64) lds.outs[wave][i] = 0.f;
   if constexpr (F == NF4) nf4_byte_lut_fill<64, MT>(blut);
   lds_barrier();
@@ -524,7 +544,7 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
           for (int m = 0; m < RV; ++m) tot[u][m] = 0.f;
         for (int c0 = 0; c0 < C; c0 += LPR) {
           const int c = c0 + li, cc = min(c, C - 1);
-          const Codes<F, LPR, U> w = nxt;
+          const Codes<F, LPR, U> w = pre[0];
           const u32x4* a[RV];
           float xs[RV];
 #pragma unroll
@@ -533,12 +553,9 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
             a[m] = reinterpret_cast<const u32x4*>(g.act + f * K);
             xs[m] = g.act_scale[f * C + cc];
           }
-          if (c0 + LPR < C)
-            load(b, wk, c0 + LPR);
-          else if (wk + MW < works)
-            load(b, wk + MW, 0);
-          else if (b + gridDim.x < blocks)
-            load(b + gridDim.x, wave, 0);
+#pragma unroll
+          for (int i = 0; i + 1 < AHEAD; ++i) pre[i] = pre[i + 1];
+          load_next(pre[AHEAD - 1]);
           dot_pass<F, NF4>(w, [&](int j, int m) -> u32x4 { return a[m][j * C + cc]; }, xs, blut, lane_off, tot);
         }
         sum_lanes<LPR, U, RV>(tot, lane, [&](int row, int m, float v) {
@@ -587,14 +604,16 @@ hipError_t down(MoeArgs g, int cus, hipStream_t s) {
   return hipGetLastError();
 }
 
-// f(LPR) with the lanes per weight row for a contraction of K: enough for the row's
-// chunks in one pass, at most 64.
+// f(LPR) with the lanes per weight row for a contraction of K (C chunks): the number that
+// leaves the fewest lanes idle over the row's passes, the larger on a tie (90 chunks: three
+// passes of 32 lanes; two of 64 would idle 38 of 128).
 template <typename Fn>
 hipError_t by_lanes(int64_t K, Fn f) {
   const int64_t C = K >> 5;
-  if (C <= 16) return f(std::integral_constant<int, 16>{});
-  if (C <= 32) return f(std::integral_constant<int, 32>{});
-  return f(std::integral_constant<int, 64>{});
+  auto lanes = [&](int64_t l) { return (C + l - 1) / l * l; };
+  if (lanes(64) <= lanes(32) && lanes(64) <= lanes(16)) return f(std::integral_constant<int, 64>{});
+  if (lanes(32) <= lanes(16)) return f(std::integral_constant<int, 32>{});
+  return f(std::integral_constant<int, 16>{});
 }
 
 template <Fmt F, bool ONE>
