@@ -87,6 +87,8 @@ _SZ = ctypes.c_size_t
 def lib() -> ctypes.CDLL:
     """Load libgeg.so (built in-tree by grouped_expert_gemm_amd.build)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lib_lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -236,7 +238,7 @@ def _require_gpu(*ts):
 def _check_tensor(t, name, dtype, shape):
     """dtype, shape and dense row-major layout of one operand: the C entry points
     take bare pointers and sizes, so this is the only place they can be checked."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()):
         return
     if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
         raise GegError(2, f"{name}: expected a contiguous {dtype} tensor of shape {list(shape)}, got "
@@ -762,22 +764,37 @@ def _on_device(ref, *ts):
     """Every tensor on ref's device, and that the current one: kernels launch on the
     current device's streams."""
     import torch
-    _require_gpu(ref)
+    dev = ref.device
+    if dev.type != "cuda":
+        _require_gpu(ref)
     for t in ts:
-        if t is not None and t.device != ref.device:
+        if t is not None and t.device != dev:
             _require_gpu(t)
-            raise GegError(4, f"tensors on several devices: {ref.device} and {t.device}")
-    if ref.device.index != torch.cuda.current_device():
-        raise GegError(4, f"tensors are on {ref.device} but the current device is "
+            raise GegError(4, f"tensors on several devices: {dev} and {t.device}")
+    if dev.index != torch._C._cuda_getDevice():
+        raise GegError(4, f"tensors are on {dev} but the current device is "
                           f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device(...)")
+
+
+def _raw_stream(stream, ref):
+    """The hipStream_t of a call: the given stream's, or the current one of ref's device
+    (read without building a torch.cuda.Stream, which costs as much as a launch)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(ref.device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _outlive(stream, *ts):
     """Tensors allocated here for a call on another stream than the current one stay
     allocated until that stream's work is done."""
-    import torch
     if stream is None:
         return
+    import torch
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     if stream != torch.cuda.current_stream():
@@ -789,20 +806,21 @@ def _outlive(stream, *ts):
 _stream_ws = {}
 
 
-def _layer_workspace(ws, need, device, stream):
+def _layer_workspace(ws, need, ref, stream, raw):
     """The caller's workspace, or one of this library's own for the (device, stream)
     pair, so that calls on two streams never share one. During a graph capture each
     call gets its own from the graph's memory pool, which lives as long as the graph."""
     import torch
-    if ws is not None:
-        return ws.ensure(need, stream)
-    if torch.cuda.is_current_stream_capturing():
-        return Workspace(need, device)
-    h = _stream(stream).value or 0
-    ws = _stream_ws.get((device.index, h))
     if ws is None:
-        ws = _stream_ws[device.index, h] = Workspace(max(need, 1 << 20), device)
-    return ws.ensure(need, stream)
+        if torch.cuda.is_current_stream_capturing():
+            return Workspace(need, ref.device)
+        key = (ref.device.index, raw)
+        ws = _stream_ws.get(key)
+        if ws is None:
+            ws = _stream_ws[key] = Workspace(0, ref.device)
+    if ws.buf is None or ws.buf.numel() < need:
+        ws.ensure(max(need, 1 << 20), stream)
+    return ws
 
 
 def gmxfp4_quantize(x, values: bool = False, stream=None):
@@ -827,10 +845,11 @@ def gmxfp4_quantize(x, values: bool = False, stream=None):
                           f"{list(x.stride())} of shape {list(x.shape)}")
     _on_device(x)
     lead = x.shape[:-1]
-    codes = torch.empty(lead + (K // 2,), dtype=torch.uint8, device=x.device)
-    scales = torch.empty(lead + (K // 32,), dtype=torch.uint8, device=x.device)
-    vals = torch.empty(x.shape, dtype=x.dtype, device=x.device) if values else None
-    _check(lib().gmxfp4_quantize(_ptr(x), dt, rows, K, ld, _ptr(codes), _ptr(scales), _ptr(vals), _stream(stream)))
+    codes = x.new_empty(lead + (K // 2,), dtype=torch.uint8)
+    scales = codes.new_empty(lead + (K // 32,))
+    vals = x.new_empty(x.shape) if values else None
+    _check(lib().gmxfp4_quantize(x.data_ptr(), dt, rows, K, ld, codes.data_ptr(), scales.data_ptr(), _addr(vals),
+                                 _raw_stream(stream, x)))
     _outlive(stream, codes, scales, vals)
     return (codes, scales, vals) if values else (codes, scales)
 
@@ -855,11 +874,12 @@ def gmxfp4_w4a4_grouped_gemm(a, sizes, blocks, scales, out=None, workspace: Work
     _on_device(a, sizes, blocks, scales, out)
     mine = out is None
     if mine:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
+        out = a.new_empty((M, N))
     L, o = lib(), ctypes.byref(opts) if opts else None
-    ws = _layer_workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a.device, stream)
-    _check(L.gmxfp4_w4a4_grouped_gemm(_ptr(a), _ptr(sizes), _ptr(blocks), _ptr(scales), _ptr(out), M, N, K, E,
-                                      _ptr(ws.buf), ws.nbytes, o, _stream(stream)))
+    raw = _raw_stream(stream, a)
+    ws = _layer_workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a, stream, raw)
+    _check(L.gmxfp4_w4a4_grouped_gemm(a.data_ptr(), sizes.data_ptr(), blocks.data_ptr(), scales.data_ptr(),
+                                      out.data_ptr(), M, N, K, E, ws.buf.data_ptr(), ws.buf.numel(), o, raw))
     if mine:
         _outlive(stream, out)
     _check_device_errors(ws, check_errors, stream)
@@ -879,10 +899,10 @@ def route_topk(logits, k: int, renormalize: bool = True, error_word=None, stream
     T, E = logits.shape
     _check_tensor(error_word, "error_word", torch.int32, (1,))
     _on_device(logits, error_word)
-    weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
-    ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-    _check(lib().geg_route_topk(_ptr(logits), dt, T, E, k, int(renormalize), _ptr(weights), _ptr(ids),
-                                _ptr(error_word), _stream(stream)))
+    weights = logits.new_empty((T, k), dtype=torch.float32)
+    ids = logits.new_empty((T, k), dtype=torch.int32)
+    _check(lib().geg_route_topk(logits.data_ptr(), dt, T, E, k, int(renormalize), weights.data_ptr(), ids.data_ptr(),
+                                _addr(error_word), _raw_stream(stream, logits)))
     _outlive(stream, weights, ids)
     return weights, ids
 
@@ -900,9 +920,9 @@ def route_topk_grad(dweights, logits, ids, weights, renormalize: bool = True, st
     _check_tensor(weights, "weights", torch.float32, (T, k))
     _check_tensor(dweights, "dweights", torch.float32, (T, k))
     _on_device(logits, ids, weights, dweights)
-    dlogits = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    _check(lib().geg_route_topk_grad(_ptr(dweights), _ptr(logits), dt, _ptr(ids), _ptr(weights), T, E, k,
-                                     int(renormalize), _ptr(dlogits), _stream(stream)))
+    dlogits = logits.new_empty((T, E))
+    _check(lib().geg_route_topk_grad(dweights.data_ptr(), logits.data_ptr(), dt, ids.data_ptr(), weights.data_ptr(), T,
+                                     E, k, int(renormalize), dlogits.data_ptr(), _raw_stream(stream, logits)))
     _outlive(stream, dlogits)
     return dlogits
 
@@ -923,10 +943,11 @@ def route_combine_grad(dout, y, row_of, weights, src_of=None, stream=None):
     _check_tensor(src_of, "src_of", torch.int32, (T * k,))
     _check_tensor(weights, "weights", torch.float32, (T, k))
     _on_device(dout, y, row_of, weights, src_of)
-    dy = torch.empty((T * k, N), dtype=torch.bfloat16, device=dout.device)
-    dw = torch.empty((T, k), dtype=torch.float32, device=dout.device)
-    _check(lib().geg_route_combine_grad(_ptr(dout), _ptr(y), _ptr(row_of), _ptr(src_of), _ptr(weights), T, k, N,
-                                        _ptr(dy), _ptr(dw), _stream(stream)))
+    dy = y.new_empty((T * k, N))
+    dw = weights.new_empty((T, k))
+    _check(lib().geg_route_combine_grad(dout.data_ptr(), y.data_ptr(), row_of.data_ptr(), _addr(src_of),
+                                        weights.data_ptr(), T, k, N, dy.data_ptr(), dw.data_ptr(),
+                                        _raw_stream(stream, dout)))
     _outlive(stream, dy, dw)
     return dy, dw
 
@@ -947,12 +968,14 @@ def _moe_layer(nf4, x, topk_ids, topk_weights, w13, s13, w2, s2, out, workspace,
     _on_device(x, topk_ids, topk_weights, w13, s13, w2, s2, out)
     mine = out is None
     if mine:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+        out = x.new_empty((T, H))
     L = lib()
-    ws = _layer_workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x.device, stream)
+    raw = _raw_stream(stream, x)
+    ws = _layer_workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x, stream, raw)
     f = L.gnf4_moe_layer if nf4 else L.gmxfp4_moe_layer
-    _check(f(_ptr(x), _ptr(topk_ids), _ptr(topk_weights), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2), _ptr(out), T, k, H,
-             I, E, _ptr(ws.buf), ws.nbytes, ctypes.byref(opts) if opts else None, _stream(stream)))
+    _check(f(x.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
+             s2.data_ptr(), out.data_ptr(), T, k, H, I, E, ws.buf.data_ptr(), ws.buf.numel(),
+             ctypes.byref(opts) if opts else None, raw))
     if mine:
         _outlive(stream, out)
     _check_device_errors(ws, check_errors, stream)
