@@ -311,24 +311,24 @@ __global__ __launch_bounds__(TThreads, 1) void w4a4_tile_kernel(W4A4Args g) {
 }
 
 // ------------------------------------------------------------------ narrow
-// Units of 16 output columns of one expert and up to 16 RB of its rows. A workgroup takes
-// a contiguous run of units, so it quantises an expert's rows into LDS once per run. Its
-// four wavefronts split the contraction: each streams its quarter of the 16 weight rows
-// straight into registers (64 consecutive bytes of each row per instruction), up to kCh
-// steps in flight, the next unit's first ones issued before this unit's arithmetic; the
-// four partial sums meet in LDS and are added in wavefront order.
-constexpr int kCh = 8;
+// Wavefront units: 16 output columns of one expert and up to 16 RB of its rows (a group),
+// over the whole contraction. A workgroup takes a contiguous run of units, group by
+// group: it quantises a group's rows into LDS once, then its wavefronts stream the weight
+// rows of their units straight into registers (64 consecutive bytes of each of 16 rows per
+// instruction), PD steps of 128 k ahead at all times, across units and groups: no barrier
+// and no cross-wavefront sum between them.
+constexpr int NThreads = 512, NWaves = NThreads / 64;
+constexpr int PD = 8;   // steps in flight per wavefront; a unit's steps are padded to whole PDs
 
 template <int RB>
-__global__ __launch_bounds__(kThreads) void w4a4_narrow_kernel(W4A4Args g) {
+__global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int64_t K = g.K, N = g.N, KS = K >> 5;
-  const int nst = (int)((K + BK - 1) / BK);
+  const int nst = (int)((K + BK - 1) / BK), nch = (nst + PD - 1) / PD;
   const int ld = nst * 64 + 16;   // bytes of a quantised row (an odd number of 16-byte units)
   const int sld = nst * 4;        // bytes of a row's scales
-  f32x4* part = reinterpret_cast<f32x4*>(lds);                      // [2][4][RB][64]
-  uint8_t* codes = lds + 2 * 4 * RB * 64 * 16;                      // [16 RB][ld]
-  uint8_t* ascale = codes + 16 * RB * ld;                           // [16 RB][sld]
+  uint8_t* codes = lds;                     // [16 RB][ld]
+  uint8_t* ascale = codes + 16 * RB * ld;   // [16 RB][sld]
   int32_t* p_off = reinterpret_cast<int32_t*>(ascale + 16 * RB * sld);
   int32_t* p_u = p_off + g.E + 1;
   const int nblk = (int)((N + 15) / 16);
@@ -340,133 +340,142 @@ __global__ __launch_bounds__(kThreads) void w4a4_narrow_kernel(W4A4Args g) {
   const int r16 = lane & 15, grp = lane >> 4;
   const int lo = (int)((int64_t)total * blockIdx.x / gridDim.x);
   const int hi = (int)((int64_t)total * (blockIdx.x + 1) / gridDim.x);
-  if (lo >= hi) return;
-  const int sp = (nst + 3) / 4, first = wave * sp, last = min(first + sp, nst);   // this wavefront's steps
-  const int nch = (sp + kCh - 1) / kCh;
 
-  struct Where {
-    int e, chunk, nb;
+  // The group of unit u: its expert, its chunk of rows, its first unit.
+  struct Group {
+    int e, chunk, u0;
   };
-  auto where = [&](int u) {
-    Where w;
+  auto group_of = [&](int u) {
+    Group w;
     w.e = __builtin_amdgcn_readfirstlane(find_expert(p_u, g.E, u));
-    const int lu = u - __builtin_amdgcn_readfirstlane(p_u[w.e]);
-    w.chunk = lu / nblk;
-    w.nb = lu % nblk;
+    const int base = __builtin_amdgcn_readfirstlane(p_u[w.e]);
+    w.chunk = (u - base) / nblk;
+    w.u0 = base + w.chunk * nblk;
     return w;
   };
-  auto load = [&](const Where& w, int ch, u32x4* code, uint32_t* scale) {
-    const __amdgpu_buffer_rsrc_t W = wrsrc(g.wq + (int64_t)w.e * N * (K >> 1), N * (K >> 1));
-    const __amdgpu_buffer_rsrc_t S = wrsrc(g.ws + (int64_t)w.e * N * KS, N * KS);
-    const int64_t n = 16 * (int64_t)w.nb + r16;   // rows past N read zeros
-#pragma unroll
-    for (int i = 0; i < kCh; ++i) {
-      const int st = first + ch * kCh + i;
-      const bool ok = st < last && 4 * (int64_t)st + grp < KS && n < N;
-      code[i] = __builtin_amdgcn_raw_buffer_load_b128(
-          W, oob_unless(ok, (uint32_t)(n * (K >> 1) + 64 * (int64_t)st + 16 * grp)), 0, 0);
-      scale[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(
-          S, oob_unless(ok, (uint32_t)(n * KS + 4 * (int64_t)st + grp)), 0, 0);
-    }
+  u32x4 code[PD];
+  uint32_t scale[PD];
+  // Steps ch PD .. +PD-1 of the unit at columns 16 nb of expert e into the PD slots (none:
+  // zeros, without a memory access). Rows past N lie past the buffers and read zeros. What
+  // a lane reads past its row's end (the last step's blocks past K, padding steps) meets
+  // zero activations or is skipped; only scales there are masked (0xFF would be a NaN).
+  struct Next {
+    __amdgpu_buffer_rsrc_t W, S;
+    uint32_t wo, so;
+  };
+  auto aim = [&](bool any, int e, int nb, int ch) {
+    Next x;
+    x.W = wrsrc(g.wq + (int64_t)e * N * (K >> 1), any ? N * (K >> 1) : 0);
+    x.S = wrsrc(g.ws + (int64_t)e * N * KS, any ? N * KS : 0);
+    const int64_t n = 16 * (int64_t)nb + r16;
+    x.wo = (uint32_t)(n * (K >> 1) + 64 * PD * (int64_t)ch + 16 * grp);
+    x.so = (uint32_t)(n * KS + 4 * PD * (int64_t)ch + grp);
+    return x;
+  };
+  auto load = [&](int i, const Next& x) {
+    code[i] = __builtin_amdgcn_raw_buffer_load_b128(x.W, x.wo + 64 * i, 0, 0);
+    scale[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(x.S, x.so + 4 * i, 0, 0);
   };
 
-  u32x4 code[kCh];
-  uint32_t scale[kCh];
-  Where cur = where(lo);
-  load(cur, 0, code, scale);
-  int have_e = -1, have_chunk = -1, par = 0;
-  int64_t row0 = 0;
-  int rows = 0;
-  for (int u = lo; u < hi; ++u) {
-    if (cur.e != have_e || cur.chunk != have_chunk) {
-      have_e = cur.e;
-      have_chunk = cur.chunk;
-      row0 = p_off[cur.e] + (int64_t)cur.chunk * 16 * RB;
-      rows = (int)min<int64_t>(16 * RB, p_off[cur.e + 1] - row0);
-      lds_barrier();   // the rows before are no longer read
-      const int ppr = nst * 16;   // 8-value pieces per padded row
-      for (int p = t; p < rows * ppr; p += kThreads) {
-        const int r = p / ppr, c = p % ppr;
-        float f[8], q[8];
-        u32x4 v = u32x4{0, 0, 0, 0};
-        const bool in = 8 * (int64_t)c < K;
-        if (in) v = reinterpret_cast<const u32x4*>(g.a + (row0 + r) * K)[c];
-        unpack16<kBF16>(v, f);
-        uint32_t word;
-        const int byte = mxfp4_block_piece<8, false>(f, word, q);
-        *reinterpret_cast<uint32_t*>(codes + r * ld + 4 * c) = word;
-        if ((c & 3) == 0) {
-          ascale[r * sld + (c >> 2)] = (uint8_t)(in ? byte : 0);
-          if (byte == 255) atomicOr(g.err, kErrNonFinite);
-        }
-      }
-      lds_barrier();
+  bool have = false;   // this wavefront's next unit has its first PD steps in flight
+  Group cur = lo < hi ? group_of(lo) : Group{0, 0, 0};
+  for (int s0 = lo; s0 < hi;) {
+    const int s1 = min(hi, cur.u0 + nblk);   // this group's units in the run: [s0, s1)
+    const Group nxt = s1 < hi ? group_of(s1) : cur;
+    const int s2 = s1 < hi ? min(hi, nxt.u0 + nblk) : s1;
+    int u = s0 + wave;
+    if (!have && u < s1) {
+      const Next x = aim(true, cur.e, u - cur.u0, 0);
+#pragma unroll
+      for (int i = 0; i < PD; ++i) load(i, x);
     }
-    f32x4 acc[RB];
+    const int64_t row0 = p_off[cur.e] + (int64_t)cur.chunk * 16 * RB;
+    const int rows = (int)min<int64_t>(16 * RB, p_off[cur.e + 1] - row0);
+    lds_barrier();   // the rows before are no longer read
+    {
+      const int ppr = nst * 16, pieces = rows * ppr;   // 8-value pieces per padded row
+      for (int p0 = t; p0 < pieces; p0 += 4 * NThreads) {
+        u32x4 v[4];
 #pragma unroll
-    for (int b = 0; b < RB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-    const Where nxt = u + 1 < hi ? where(u + 1) : cur;
-    for (int ch = 0; ch < nch; ++ch) {
-      u32x4 c[kCh];
-      uint32_t s[kCh];
+        for (int i = 0; i < 4; ++i) {
+          const int p = p0 + i * NThreads, r = p / ppr, c = p % ppr;
+          v[i] = u32x4{0, 0, 0, 0};
+          if (p < pieces && 8 * (int64_t)c < K) v[i] = reinterpret_cast<const u32x4*>(g.a + (row0 + r) * K)[c];
+        }
 #pragma unroll
-      for (int i = 0; i < kCh; ++i) {
-        c[i] = code[i];
-        s[i] = scale[i];
-      }
-      // the next loads: the rest of this unit, then the next unit's first
-      if (ch + 1 < nch)
-        load(cur, ch + 1, code, scale);
-      else if (u + 1 < hi)
-        load(nxt, 0, code, scale);
-#pragma unroll
-      for (int i = 0; i < kCh; ++i) {
-        const int st = first + ch * kCh + i;
-        if (st < last) {
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-            if (b == 0 || 16 * b < rows) {
-              const int r = 16 * b + r16;
-              const u32x4 a = *reinterpret_cast<const u32x4*>(codes + r * ld + 64 * st + 16 * grp);
-              acc[b] = mfma_fp4<0>(c[i], a, acc[b], s[i], ascale[r * sld + 4 * st + grp]);
+        for (int i = 0; i < 4; ++i) {
+          const int p = p0 + i * NThreads, r = p / ppr, c = p % ppr;
+          if (p < pieces) {   // whole blocks: the four lanes of one pass together
+            float f[8], q[8];
+            unpack16<kBF16>(v[i], f);
+            uint32_t word;
+            const int byte = mxfp4_block_piece<8, false>(f, word, q);
+            *reinterpret_cast<uint32_t*>(codes + r * ld + 4 * c) = word;
+            if ((c & 3) == 0) {
+              ascale[r * sld + (c >> 2)] = (uint8_t)(8 * (int64_t)c < K ? byte : 0);
+              if (byte == 255) atomicOr(g.err, kErrNonFinite);
             }
+          }
         }
       }
     }
-    f32x4* pp = part + par * 4 * RB * 64;
-#pragma unroll
-    for (int b = 0; b < RB; ++b) pp[(wave * RB + b) * 64 + lane] = acc[b];
     lds_barrier();
-    if (t < 64 * RB) {
-      const int b = t >> 6, r = 16 * b + r16;
-      f32x4 v = pp[t];
+    const bool some = u < s1;
+    for (; u < s1; u += NWaves) {
+      // where this wavefront goes next: its next unit here, or its first of the next group
+      const bool here = u + NWaves < s1;
+      const int u2 = here ? u + NWaves : s1 + wave;
+      have = here || u2 < s2;
+      const int e2 = here ? cur.e : nxt.e, nb2 = u2 - (here ? cur.u0 : nxt.u0);
+      f32x4 acc[RB];
 #pragma unroll
-      for (int w = 1; w < 4; ++w) {
-        const f32x4 o = pp[w * RB * 64 + t];
+      for (int b = 0; b < RB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int ch = 0; ch < nch; ++ch) {
+        const bool more = ch + 1 < nch;
+        const Next x = aim(more || have, more ? cur.e : e2, more ? u - cur.u0 : nb2, more ? ch + 1 : 0);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] += o[q];
+        for (int i = 0; i < PD; ++i) {
+          const int st = ch * PD + i;
+          if (st < nst) {
+            const uint32_t sw = 4 * st + grp < KS ? scale[i] : 0;
+#pragma unroll
+            for (int b = 0; b < RB; ++b)
+              if (b == 0 || 16 * b < rows) {
+                const int r = 16 * b + r16;
+                const u32x4 a = *reinterpret_cast<const u32x4*>(codes + r * ld + 64 * st + 16 * grp);
+                acc[b] = mfma_fp4<0>(code[i], a, acc[b], sw, ascale[r * sld + 4 * st + grp]);
+              }
+          }
+          load(i, x);
+        }
       }
-      if (r < rows) {
-        const int64_t n = 16 * (int64_t)cur.nb + 4 * grp;
-        uint16_t* dst = g.out + (row0 + r) * N + n;
-        if ((N & 3) == 0 && (reinterpret_cast<uintptr_t>(g.out) & 7) == 0) {
-          if (n < N) *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        } else {
+      const int64_t n = 16 * (int64_t)(u - cur.u0) + 4 * grp;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (n + q < N) dst[q] = to_bf16(v[q]);
+      for (int b = 0; b < RB; ++b) {
+        const int r = 16 * b + r16;
+        if (r < rows) {
+          uint16_t* dst = g.out + (row0 + r) * N + n;
+          if ((N & 3) == 0 && (reinterpret_cast<uintptr_t>(g.out) & 7) == 0) {
+            if (n < N)
+              *reinterpret_cast<u32x2*>(dst) = u32x2{pack_bf16x2(acc[b][0], acc[b][1]), pack_bf16x2(acc[b][2], acc[b][3])};
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (n + q < N) dst[q] = to_bf16(acc[b][q]);
+          }
         }
       }
     }
-    par ^= 1;
+    if (!some) have = false;   // no unit in this group: nothing was started for the next
     cur = nxt;
+    s0 = s1;
   }
 }
 
 template <int RB>
 size_t narrow_lds(int64_t K, int32_t E) {
   const int64_t nst = (K + BK - 1) / BK;
-  return (size_t)(2 * 4 * RB * 64 * 16 + 16 * RB * (nst * 64 + 16 + nst * 4) + 8 * ((int64_t)E + 1));
+  return (size_t)(16 * RB * (nst * 64 + 16 + nst * 4) + 8 * ((int64_t)E + 1));
 }
 
 template <int RB>
@@ -480,9 +489,10 @@ hipError_t narrow_one(const W4A4Args& g, int cus, hipStream_t s) {
   }
   const int64_t nblk = (g.N + 15) / 16;
   const int64_t units = ((g.M + 16 * RB - 1) / (16 * RB) + std::min<int64_t>(g.E, g.M)) * nblk;
-  const int64_t per_cu = std::max<int64_t>(1, std::min<int64_t>(4, kMaxLds / (int64_t)bytes));
+  // two workgroups of 8 wavefronts per CU where the rows leave room for both
+  const int64_t per_cu = 2 * (int64_t)bytes <= kMaxLds ? 2 : 1;
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(units, per_cu * cus));
-  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(kThreads), (unsigned)bytes, s, g);
+  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(NThreads), (unsigned)bytes, s, g);
   return hipGetLastError();
 }
 
