@@ -182,7 +182,7 @@ geg_status make_plan(int op, int64_t M, int64_t N, int64_t K, int32_t E, const g
     p.narrow = rb > 0;
     p.cb = rb;
     p.total_bytes = p.a16_off = kHeader;
-    if (rb == 0) {
+    if (rb == 0 || !geg::w4a4_narrow_fused(M, E)) {
       p.a16_bytes = round256((size_t)M * (size_t)(K / 2)) + round256((size_t)((K + 511) / 512) * (size_t)M * 16);
       p.total_bytes += p.a16_bytes;
     }
@@ -702,10 +702,12 @@ geg_status gmxfp4_w4a4_grouped_gemm(const void* a, const int32_t* sizes, const u
                   reinterpret_cast<uint16_t*>(out), M, N, K, E, reinterpret_cast<uint32_t*>(wsb)};
   const int cus = cu_count();
   hipError_t e = hipSuccess;
-  if (!p.narrow) {
-    e = geg::launch_w4a4_quantize(g.a, M, K, aq, as, g.err, cus, stream);
+  if (p.a16_bytes) {
+    e = geg::launch_w4a4_quantize(g.a, M, K, aq, as, g.err, !p.narrow, cus, stream);
     if (e != hipSuccess) return hip_fail(e, "activation quantisation launch");
     ++g_launches;
+  } else {
+    g.aq = nullptr;
   }
   e = record_event(opts, 0, stream);
   if (e == hipSuccess)

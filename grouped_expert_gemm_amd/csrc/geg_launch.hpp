@@ -114,8 +114,9 @@ enum DType : int { kBF16 = 0, kF16 = 1, kF32 = 2 };
 hipError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t K, int64_t ld, uint8_t* codes,
                                  uint8_t* scales, void* values, int cus, hipStream_t s);
 // W4A4: the grouped GEMM with both operands in MXFP4 (see w4a4.hip). The narrow kernel
-// (w4a4_narrow_rb > 0) quantises g.a itself; the tiles read g.aq and g.as, which
-// launch_w4a4_quantize makes: codes [M, K/2], scales [ceil(K/512)][M][16].
+// (w4a4_narrow_rb > 0) quantises g.a itself when w4a4_narrow_fused and g.aq is NULL;
+// otherwise g.aq and g.as hold what launch_w4a4_quantize makes: codes [M, K/2], scales
+// [M, K/32] (narrow) or [ceil(K/512)][M][16] (tiles).
 constexpr int64_t kW4A4NarrowAvg = 32;   // rows per expert on average up to which the narrow kernel runs
 constexpr int kMaxLds = 160 << 10;       // LDS of a CU
 struct W4A4Args {
@@ -132,8 +133,9 @@ struct W4A4Args {
 };
 int w4a4_narrow_rb(int64_t M, int64_t K, int32_t E, int force);
 hipError_t launch_w4a4_narrow(const W4A4Args& g, int rb, int cus, hipStream_t s);
+bool w4a4_narrow_fused(int64_t M, int32_t E);
 hipError_t launch_w4a4_quantize(const uint16_t* a, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, uint32_t* err,
-                                int cus, hipStream_t s);
+                                bool tiles, int cus, hipStream_t s);
 hipError_t launch_w4a4_tile(const W4A4Args& g, int cus, hipStream_t s);
 // Router gate: top-k of logits [T, E] with softmax weights, its gradient, and the
 // gradient of the weighted combine (see gate.hip).

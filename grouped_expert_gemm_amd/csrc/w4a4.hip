@@ -11,8 +11,9 @@
 // of one activation row (l % 16).
 //
 // Two kernels. With at most kW4A4NarrowAvg rows per expert on average the narrow one
-// streams the weights straight into registers and quantises its rows itself; larger
-// batches quantise in a launch of their own and run 256 x 256 tiles through LDS.
+// streams the weights straight into registers, larger batches run 256 x 256 tiles through
+// LDS. A launch of its own quantises the activations, except for the smallest batches,
+// where the narrow kernel does.
 #include <algorithm>
 
 #include "geg_device.hpp"
@@ -47,10 +48,11 @@ __device__ __forceinline__ f32x4 mfma_fp4(const u32x4& w, const u32x4& a, const 
 }
 
 // ------------------------------------------------------------------ activations for the tiles
-// bf16 [M, K] -> codes [M, K/2] and scales [K/512 rounded up][M][16]: byte 4 b + s of a
-// row's 16 is the scale of 32-block 4 s + b of the 512-wide piece, so a lane of group b
-// reads the bytes of its four steps s as one dword. Blocks past K get 0. One thread per
-// 8 values, four lanes to a block.
+// bf16 [M, K] -> codes [M, K/2] and scales. For the narrow kernel [M, K/32]; for the tiles
+// [K/512 rounded up][M][16]: byte 4 b + s of a row's 16 is the scale of 32-block 4 s + b of
+// the 512-wide piece, so a lane of group b reads the bytes of its four steps s as one
+// dword; blocks past K get 0. One thread per 8 values, four lanes to a block.
+template <bool TILES>
 __global__ __launch_bounds__(kThreads) void w4a4_quantize_kernel(const uint16_t* __restrict__ a, int64_t M, int64_t KS,
                                                                  uint32_t* __restrict__ codes,
                                                                  uint8_t* __restrict__ scales, uint32_t* err) {
@@ -64,10 +66,16 @@ __global__ __launch_bounds__(kThreads) void w4a4_quantize_kernel(const uint16_t*
     codes[p] = word;
     if ((p & 3) == 0) {
       if (byte == 255) atomicOr(err, kErrNonFinite);
-      const int64_t b = p >> 2, m = b / KS, kb = b - m * KS;
-      scales[((kb >> 4) * M + m) * 16 + 4 * (kb & 3) + ((kb >> 2) & 3)] = (uint8_t)byte;
+      const int64_t b = p >> 2;
+      if constexpr (TILES) {
+        const int64_t m = b / KS, kb = b - m * KS;
+        scales[((kb >> 4) * M + m) * 16 + 4 * (kb & 3) + ((kb >> 2) & 3)] = (uint8_t)byte;
+      } else {
+        scales[b] = (uint8_t)byte;
+      }
     }
   }
+  if constexpr (!TILES) return;
   const int64_t pad = ((KS + 15) & ~(int64_t)15) - KS;   // blocks past K of the last piece
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < M * pad; i += stride) {
     const int64_t m = i / pad, kb = KS + i - m * pad;
@@ -320,7 +328,7 @@ __global__ __launch_bounds__(TThreads, 1) void w4a4_tile_kernel(W4A4Args g) {
 constexpr int NThreads = 512, NWaves = NThreads / 64;
 constexpr int PD = 8;   // steps in flight per wavefront; a unit's steps are padded to whole PDs
 
-template <int RB>
+template <int RB, bool PRE>
 __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int64_t K = g.K, N = g.N, KS = K >> 5;
@@ -392,7 +400,33 @@ __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
     const int64_t row0 = p_off[cur.e] + (int64_t)cur.chunk * 16 * RB;
     const int rows = (int)min<int64_t>(16 * RB, p_off[cur.e + 1] - row0);
     lds_barrier();   // the rows before are no longer read
-    {
+    if constexpr (PRE) {
+      // 16 bytes of codes or 4 of scales at a time; what lies past K is zero
+      const int cpr = nst * 4, words = nst;
+      for (int p0 = t; p0 < rows * cpr; p0 += 4 * NThreads) {
+        u32x4 v[4];
+        int at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = p0 + i * NThreads, r = p / cpr, c = p - r * cpr;
+          at[i] = p < rows * cpr ? r * ld + 16 * c : -1;
+          v[i] = u32x4{0, 0, 0, 0};
+          if (at[i] >= 0 && c < KS) v[i] = reinterpret_cast<const u32x4*>(g.aq + (row0 + r) * (K >> 1))[c];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (at[i] >= 0) *reinterpret_cast<u32x4*>(codes + at[i]) = v[i];
+      }
+      for (int p = t; p < rows * words; p += NThreads) {
+        const int r = p / words, w = p - r * words;
+        const uint8_t* src = g.as + (row0 + r) * KS + 4 * w;
+        uint32_t v = 0;
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (4 * w + b < KS) v |= (uint32_t)src[b] << (8 * b);
+        *reinterpret_cast<uint32_t*>(ascale + r * sld + 4 * w) = v;
+      }
+    } else {
       const int ppr = nst * 16, pieces = rows * ppr;   // 8-value pieces per padded row
       for (int p0 = t; p0 < pieces; p0 += 4 * NThreads) {
         u32x4 v[4];
@@ -478,10 +512,10 @@ size_t narrow_lds(int64_t K, int32_t E) {
   return (size_t)(16 * RB * (nst * 64 + 16 + nst * 4) + 8 * ((int64_t)E + 1));
 }
 
-template <int RB>
+template <int RB, bool PRE>
 hipError_t narrow_one(const W4A4Args& g, int cus, hipStream_t s) {
   const size_t bytes = narrow_lds<RB>(g.K, g.E);
-  auto k = w4a4_narrow_kernel<RB>;
+  auto k = w4a4_narrow_kernel<RB, PRE>;
   if (bytes > (64u << 10)) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                        kMaxLds);
@@ -508,16 +542,25 @@ int w4a4_narrow_rb(int64_t M, int64_t K, int32_t E, int force) {
   return narrow_lds<1>(K, E) <= (size_t)kMaxLds ? 1 : 0;
 }
 
+// Whether the narrow kernel quantises its rows itself (each workgroup a group's rows again)
+// instead of reading what a launch before it quantised: up to one row per expert on
+// average. At 8 (K = 2880, E = 32) it took 46 us of which 14 were the conversion.
+bool w4a4_narrow_fused(int64_t M, int32_t E) { return M <= (int64_t)E; }
+
 hipError_t launch_w4a4_narrow(const W4A4Args& g, int rb, int cus, hipStream_t s) {
-  return rb == 2 ? narrow_one<2>(g, cus, s) : narrow_one<1>(g, cus, s);
+  if (g.aq) return rb == 2 ? narrow_one<2, true>(g, cus, s) : narrow_one<1, true>(g, cus, s);
+  return rb == 2 ? narrow_one<2, false>(g, cus, s) : narrow_one<1, false>(g, cus, s);
 }
 
 hipError_t launch_w4a4_quantize(const uint16_t* a, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, uint32_t* err,
-                                int cus, hipStream_t s) {
+                                bool tiles, int cus, hipStream_t s) {
   const int64_t KS = K >> 5, pieces = M * KS * 4;
-  const int64_t grid = std::min<int64_t>((pieces + kThreads - 1) / kThreads, (int64_t)cus * 16);
-  hipLaunchKernelGGL(w4a4_quantize_kernel, dim3((unsigned)grid), dim3(kThreads), 0, s, a, M, KS,
-                     reinterpret_cast<uint32_t*>(codes), scales, err);
+  const dim3 grid((unsigned)std::min<int64_t>((pieces + kThreads - 1) / kThreads, (int64_t)cus * 16)), block(kThreads);
+  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+  if (tiles)
+    hipLaunchKernelGGL(w4a4_quantize_kernel<true>, grid, block, 0, s, a, M, KS, c, scales, err);
+  else
+    hipLaunchKernelGGL(w4a4_quantize_kernel<false>, grid, block, 0, s, a, M, KS, c, scales, err);
   return hipGetLastError();
 }
 

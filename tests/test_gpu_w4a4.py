@@ -56,7 +56,8 @@ def _check(c, path, **kw):
 
 
 SHAPES = [([1], 16, 32), ([3, 0, 2], 48, 64), ([1, 1, 1, 1], 320, 2880), ([17, 5, 0, 33], 64, 160), ([16, 32, 1], 1, 96),
-          ([2, 7], 23, 512), ([9, 40], 130, 544), ([70, 0, 3], 272, 1024), ([5], 36, 4320)]
+          ([2, 7], 23, 512), ([9, 40], 130, 544), ([70, 0, 3], 272, 1024), ([5], 36, 4320),
+          ([1, 0, 0, 2, 0], 50, 96), ([0, 3, 0, 0], 33, 1056)]
 
 
 @pytest.mark.parametrize("path", [0, TILES, NARROW])
@@ -69,6 +70,13 @@ def test_product_matches_fp64(sizes, N, K, path):
 def test_every_contraction_tail_of_the_tiles(K):
     # steps of 128, pieces of 512, pairs of pieces, and every remainder of each
     _check(_case([5, 20], 40, K), TILES)
+
+
+@pytest.mark.parametrize("K", list(range(32, 1216, 32)))
+def test_every_contraction_tail_of_the_narrow_kernel(K):
+    # rows quantised by the kernel itself (no more rows than experts), and before it
+    _check(_case([2, 0, 0], 20, K), NARROW)
+    _check(_case([5, 20], 40, K), NARROW)
 
 
 @pytest.mark.parametrize("sizes,N,K", [([300, 129, 0, 256, 7, 257], 264, 352), ([513], 513, 640), ([128, 127], 255, 256)])
@@ -131,6 +139,11 @@ def test_a_row_with_nan_is_nan_and_flagged_the_others_unchanged(path):
     assert ws.read_error() == geg.DEVERR_NON_FINITE
     bad = torch.zeros(23, dtype=torch.bool)
     bad[[7, 21]] = True
+    few = _case([2, 0, 0], 40, 160)        # no more rows than experts
+    few["a"][1, 33] = float("nan")
+    ws.reset()
+    one = _call(few, path, workspace=ws)
+    assert ws.read_error() == geg.DEVERR_NON_FINITE and bool(one[1].isnan().all()) and not bool(one[0].isnan().any())
     assert bool(got[bad.cuda()].isnan().all()) and torch.equal(got[~bad.cuda()], ref[~bad.cuda()])
 
 

@@ -112,9 +112,10 @@ def test_w4a4_refusals():
     assert _w4a4(opts=geg.Opts(1, 0)) == 8 and _w4a4(opts=geg.Opts(3, 0)) == 8 and _w4a4(opts=geg.Opts(0, 0, None, -1)) == 8
     assert _w4a4(opts=geg.Opts(4, 0), K=65536, N=64) == 8      # the narrow kernel's rows past LDS
     assert _w4a4() not in (0, 1, 2, 3, 5, 8)
-    # header only on the narrow kernel; codes and scales [ceil(K/512)][M][16] for the tiles
+    # header only up to one row per expert; else codes and scales [ceil(K/512)][M][16]
     op = geg.GEG_OP_MXFP4_W4A4
-    assert geg.geg_workspace_bytes(op, 16, 64, 128, 4) == 256
+    assert geg.geg_workspace_bytes(op, 4, 64, 128, 4) == 256
+    assert geg.geg_workspace_bytes(op, 5, 64, 128, 4) == 256 + 512 + 256
     assert geg.geg_workspace_bytes(op, 8192, 5760, 2880, 32) == 256 + 8192 * 1440 + 6 * 8192 * 16
     assert geg.geg_workspace_bytes(op, 64, 64, 512, 4, geg.Opts(2, 0)) == 256 + 64 * 256 + 64 * 16
     need = geg.geg_workspace_bytes(op, 8192, 64, 128, 4)
