@@ -323,18 +323,23 @@ __global__ __launch_bounds__(TThreads, 1) void w4a4_tile_kernel(W4A4Args g) {
 // over the whole contraction. A workgroup takes a contiguous run of units, group by
 // group: it quantises a group's rows into LDS once, then its wavefronts stream the weight
 // rows of their units straight into registers (64 consecutive bytes of each of 16 rows per
-// instruction), PD steps of 128 k ahead at all times, across units and groups: no barrier
-// and no cross-wavefront sum between them.
+// instruction and pair), PD pairs of steps ahead at all times, across units and groups: no
+// barrier and no cross-wavefront sum between them.
 constexpr int NThreads = 512, NWaves = NThreads / 64;
-constexpr int PD = 8;   // steps in flight per wavefront; a unit's steps are padded to whole PDs
+constexpr int PD = 4;   // pairs of steps in flight per wavefront; a unit's pairs are padded to whole PDs
 
-template <int RB, bool PRE>
+// Steps go in pairs of 256 k whose eight 32-blocks are dealt so that lane group g takes
+// blocks 2 g and 2 g + 1, one per step (both operands alike, so the sums are the same): a
+// lane's scale bytes of a pair are then adjacent: one 2-byte load instead of two of a byte
+// (EVEN: rows of an even number of scales at an even address; otherwise two all the same).
+
+template <int RB, bool PRE, bool EVEN>
 __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int64_t K = g.K, N = g.N, KS = K >> 5;
-  const int nst = (int)((K + BK - 1) / BK), nch = (nst + PD - 1) / PD;
-  const int ld = nst * 64 + 16;   // bytes of a quantised row (an odd number of 16-byte units)
-  const int sld = nst * 4;        // bytes of a row's scales
+  const int np = (int)((K + 2 * BK - 1) / (2 * BK)), nch = (np + PD - 1) / PD;   // pairs; PDs of them
+  const int ld = np * 128 + 16;   // bytes of a quantised row (an odd number of 16-byte units)
+  const int sld = np * 8;         // bytes of a row's scales
   uint8_t* codes = lds;                     // [16 RB][ld]
   uint8_t* ascale = codes + 16 * RB * ld;   // [16 RB][sld]
   int32_t* p_off = reinterpret_cast<int32_t*>(ascale + 16 * RB * sld);
@@ -361,11 +366,11 @@ __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
     w.u0 = base + w.chunk * nblk;
     return w;
   };
-  u32x4 code[PD];
-  uint32_t scale[PD];
-  // Steps ch PD .. +PD-1 of the unit at columns 16 nb of expert e into the PD slots (none:
+  u32x4 code[PD][2];
+  uint32_t scale[PD], scale1[EVEN ? 1 : PD];
+  // Pairs ch PD .. +PD-1 of the unit at columns 16 nb of expert e into the PD slots (none:
   // zeros, without a memory access). Rows past N lie past the buffers and read zeros. What
-  // a lane reads past its row's end (the last step's blocks past K, padding steps) meets
+  // a lane reads past its row's end (the last pair's blocks past K, padding pairs) meets
   // zero activations or is skipped; only scales there are masked (0xFF would be a NaN).
   struct Next {
     __amdgpu_buffer_rsrc_t W, S;
@@ -376,13 +381,19 @@ __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
     x.W = wrsrc(g.wq + (int64_t)e * N * (K >> 1), any ? N * (K >> 1) : 0);
     x.S = wrsrc(g.ws + (int64_t)e * N * KS, any ? N * KS : 0);
     const int64_t n = 16 * (int64_t)nb + r16;
-    x.wo = (uint32_t)(n * (K >> 1) + 64 * PD * (int64_t)ch + 16 * grp);
-    x.so = (uint32_t)(n * KS + 4 * PD * (int64_t)ch + grp);
+    x.wo = (uint32_t)(n * (K >> 1) + 128 * PD * (int64_t)ch + 32 * grp);
+    x.so = (uint32_t)(n * KS + 8 * PD * (int64_t)ch + 2 * grp);
     return x;
   };
   auto load = [&](int i, const Next& x) {
-    code[i] = __builtin_amdgcn_raw_buffer_load_b128(x.W, x.wo + 64 * i, 0, 0);
-    scale[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(x.S, x.so + 4 * i, 0, 0);
+    code[i][0] = __builtin_amdgcn_raw_buffer_load_b128(x.W, x.wo + 128 * i, 0, 0);
+    code[i][1] = __builtin_amdgcn_raw_buffer_load_b128(x.W, x.wo + 128 * i + 16, 0, 0);
+    if constexpr (EVEN) {
+      scale[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(x.S, x.so + 8 * i, 0, 0);
+    } else {
+      scale[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(x.S, x.so + 8 * i, 0, 0);
+      scale1[i] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(x.S, x.so + 8 * i + 1, 0, 0);
+    }
   };
 
   bool have = false;   // this wavefront's next unit has its first PD steps in flight
@@ -402,7 +413,7 @@ __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
     lds_barrier();   // the rows before are no longer read
     if constexpr (PRE) {
       // 16 bytes of codes or 4 of scales at a time; what lies past K is zero
-      const int cpr = nst * 4, words = nst;
+      const int cpr = np * 8, words = np * 2;
       for (int p0 = t; p0 < rows * cpr; p0 += 4 * NThreads) {
         u32x4 v[4];
         int at[4];
@@ -427,7 +438,7 @@ __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
         *reinterpret_cast<uint32_t*>(ascale + r * sld + 4 * w) = v;
       }
     } else {
-      const int ppr = nst * 16, pieces = rows * ppr;   // 8-value pieces per padded row
+      const int ppr = np * 32, pieces = rows * ppr;   // 8-value pieces per padded row
       for (int p0 = t; p0 < pieces; p0 += 4 * NThreads) {
         u32x4 v[4];
 #pragma unroll
@@ -469,15 +480,21 @@ __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
         const Next x = aim(more || have, more ? cur.e : e2, more ? u - cur.u0 : nb2, more ? ch + 1 : 0);
 #pragma unroll
         for (int i = 0; i < PD; ++i) {
-          const int st = ch * PD + i;
-          if (st < nst) {
-            const uint32_t sw = 4 * st + grp < KS ? scale[i] : 0;
+          const int p = ch * PD + i;
+          if (p < np) {
+            // blocks 2 grp, 2 grp + 1 of the pair; those past K: 0
+            const int left = (int)(KS - 8 * (int64_t)p) - 2 * grp;
+            const uint32_t both = EVEN ? scale[i] : scale[i] | (scale1[EVEN ? 0 : i] << 8);
+            const uint32_t sw = left >= 2 ? both : (left == 1 ? both & 0xFFu : 0u);
 #pragma unroll
             for (int b = 0; b < RB; ++b)
               if (b == 0 || 16 * b < rows) {
                 const int r = 16 * b + r16;
-                const u32x4 a = *reinterpret_cast<const u32x4*>(codes + r * ld + 64 * st + 16 * grp);
-                acc[b] = mfma_fp4<0>(code[i], a, acc[b], sw, ascale[r * sld + 4 * st + grp]);
+                const uint8_t* row = codes + r * ld + 128 * p + 32 * grp;
+                const u32x4 a0 = *reinterpret_cast<const u32x4*>(row), a1 = *reinterpret_cast<const u32x4*>(row + 16);
+                const uint32_t sa = *reinterpret_cast<const uint16_t*>(ascale + r * sld + 8 * p + 2 * grp);
+                acc[b] = mfma_fp4<0>(code[i][0], a0, acc[b], sw, sa);
+                acc[b] = mfma_fp4<1>(code[i][1], a1, acc[b], sw, sa);
               }
           }
           load(i, x);
@@ -508,14 +525,14 @@ __global__ __launch_bounds__(NThreads, 4) void w4a4_narrow_kernel(W4A4Args g) {
 
 template <int RB>
 size_t narrow_lds(int64_t K, int32_t E) {
-  const int64_t nst = (K + BK - 1) / BK;
-  return (size_t)(16 * RB * (nst * 64 + 16 + nst * 4) + 8 * ((int64_t)E + 1));
+  const int64_t np = (K + 2 * BK - 1) / (2 * BK);
+  return (size_t)(16 * RB * (np * 128 + 16 + np * 8) + 8 * ((int64_t)E + 1));
 }
 
-template <int RB, bool PRE>
+template <int RB, bool PRE, bool EVEN>
 hipError_t narrow_one(const W4A4Args& g, int cus, hipStream_t s) {
   const size_t bytes = narrow_lds<RB>(g.K, g.E);
-  auto k = w4a4_narrow_kernel<RB, PRE>;
+  auto k = w4a4_narrow_kernel<RB, PRE, EVEN>;
   if (bytes > (64u << 10)) {
     hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(k), hipFuncAttributeMaxDynamicSharedMemorySize,
                                        kMaxLds);
@@ -548,8 +565,16 @@ int w4a4_narrow_rb(int64_t M, int64_t K, int32_t E, int force) {
 bool w4a4_narrow_fused(int64_t M, int32_t E) { return M <= (int64_t)E; }
 
 hipError_t launch_w4a4_narrow(const W4A4Args& g, int rb, int cus, hipStream_t s) {
-  if (g.aq) return rb == 2 ? narrow_one<2, true>(g, cus, s) : narrow_one<1, true>(g, cus, s);
-  return rb == 2 ? narrow_one<2, false>(g, cus, s) : narrow_one<1, false>(g, cus, s);
+  const bool even = ((g.K >> 5) & 1) == 0 && (reinterpret_cast<uintptr_t>(g.ws) & 1) == 0;
+  auto run = [&](auto r, auto p) {
+    constexpr int RB = decltype(r)::value;
+    constexpr bool PRE = decltype(p)::value;
+    return even ? narrow_one<RB, PRE, true>(g, cus, s) : narrow_one<RB, PRE, false>(g, cus, s);
+  };
+  constexpr std::integral_constant<int, 1> one{};
+  constexpr std::integral_constant<int, 2> two{};
+  if (g.aq) return rb == 2 ? run(two, std::true_type{}) : run(one, std::true_type{});
+  return rb == 2 ? run(two, std::false_type{}) : run(one, std::false_type{});
 }
 
 hipError_t launch_w4a4_quantize(const uint16_t* a, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, uint32_t* err,
