@@ -106,14 +106,6 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
 
-// 16 scale bytes d (byte 4 s + b: block b of step s) to lane order (byte 4 b + s).
-__device__ __forceinline__ u32x4 scales_by_block(const u32x4& d) {
-  const uint32_t t0 = perm(d[1], d[0], 0x05010400u), t1 = perm(d[3], d[2], 0x05010400u);
-  const uint32_t t2 = perm(d[1], d[0], 0x07030602u), t3 = perm(d[3], d[2], 0x07030602u);
-  return u32x4{perm(t1, t0, 0x05040100u), perm(t1, t0, 0x07060302u), perm(t3, t2, 0x05040100u),
-               perm(t3, t2, 0x07060302u)};
-}
-
 // One workgroup per CU, persistent over tiles (expert, column block, row block; row
 // blocks fastest, so that the tiles that share weights run together on one XCD). Each
 // 128-wide step is staged by loads that write LDS directly (16 bytes per lane, 1 KB per
@@ -181,34 +173,37 @@ __global__ __launch_bounds__(TThreads, 1) void w4a4_tile_kernel(W4A4Args g) {
       }
     };
     // Scales of piece ss: wavefronts 0-3 load the activations' straight into `sc` (64 rows
-    // each), wavefronts 4-7 a column's weight bytes each lane into registers.
-    const int wcol = t - 256;   // this thread's weight column (wavefronts 4-7)
-    const uint8_t* wsp = g.ws + ((int64_t)e * N + n0 + min(max(wcol, 0), ncols - 1)) * KS;
-    auto scales = [&](int ss, uint8_t* sc, u32x4& d) {
+    // each); every thread loads half a weight column's 16 bytes (two steps' four) into
+    // registers. (All wavefronts alike: a value that only some load would be copied where
+    // the paths join, behind a wait for every load in flight.)
+    const int wcol = t >> 1, whalf = t & 1;
+    const uint8_t* wsp = g.ws + ((int64_t)e * N + n0 + min(wcol, ncols - 1)) * KS + 8 * whalf;
+    // rows of the tile past M read zeros, rows of the next expert their own bytes
+    const int64_t sleft = (M - row0) * 16;
+    auto scales = [&](int ss, uint8_t* sc, u32x2& d) {
       if (wave < 4) {
-        // rows of the tile past M read zeros, rows of the next expert their own bytes
-        const int64_t left = (M - row0) * 16;
-        const __amdgpu_buffer_rsrc_t RS = wrsrc(g.as + ((int64_t)min(ss, nss - 1) * M + row0) * 16, left);
+        const __amdgpu_buffer_rsrc_t RS = wrsrc(g.as + ((int64_t)min(ss, nss - 1) * M + row0) * 16, sleft);
         __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, (lds_ptr_t)(sc + wave * 1024), 16,
                                                  (uint32_t)(wave * 1024 + 16 * lane), 0, 0, 0);
-      } else if (16 * (int64_t)(ss + 1) <= KS) {
-        __builtin_memcpy(&d, wsp + 16 * ss, 16);
+      }
+      if (16 * (ss + 1) <= (int)KS) {
+        __builtin_memcpy(&d, wsp + 16 * ss, 8);
       } else {
         // the last piece, byte by byte; blocks past K get 0
+        d = u32x2{0, 0};
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t v = 0;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int64_t kb = 16 * (int64_t)ss + 4 * w + b;
-            if (kb < KS) v |= (uint32_t)wsp[kb] << (8 * b);
-          }
-          d[w] = v;
-        }
+        for (int b = 0; b < 8; ++b)
+          if (16 * ss + 8 * whalf + b < (int)KS) d[b >> 2] |= (uint32_t)wsp[16 * ss + b] << (8 * (b & 3));
       }
     };
-    auto put_scales = [&](uint8_t* sc, const u32x4& d) {
-      if (wave >= 4) *reinterpret_cast<u32x4*>(sc + (TM + wcol) * 16) = scales_by_block(d);
+    // byte 4 b + s of a column's 16 in LDS: block b of step s (from byte 4 s + b)
+    auto put_scales = [&](uint8_t* sc, const u32x2& d) {
+      uint8_t* p = sc + (TM + wcol) * 16 + 2 * whalf;
+      const uint32_t lo = perm(d[1], d[0], 0x05010400u), hi = perm(d[1], d[0], 0x07030602u);
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)lo;
+      *reinterpret_cast<uint16_t*>(p + 4) = (uint16_t)(lo >> 16);
+      *reinterpret_cast<uint16_t*>(p + 8) = (uint16_t)hi;
+      *reinterpret_cast<uint16_t*>(p + 12) = (uint16_t)(hi >> 16);
     };
 
     const bool live = 128 * wm < rows;
@@ -217,7 +212,7 @@ __global__ __launch_bounds__(TThreads, 1) void w4a4_tile_kernel(W4A4Args g) {
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x4 d = u32x4{0, 0, 0, 0};
+    u32x2 d = u32x2{0, 0};
 
     // Step S of piece ss: its operands are in `cur` (barrier of the step before); stage
     // st + 3 goes to `nxt`, the buffer that step st - 1 read. With S == 0 the next piece's
