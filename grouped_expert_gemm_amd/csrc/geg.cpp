@@ -174,7 +174,7 @@ geg_status make_plan(int op, int64_t M, int64_t N, int64_t K, int32_t E, const g
     p.total_bytes = p.a16_off + p.a16_bytes;
     return GEG_OK;
   }
-  if (op == GEG_OP_MXFP4_W4A4) {   // tiles: e2m1 codes [M, K/2] and scales [ceil(K/512)][M][16]
+  if (op == GEG_OP_MXFP4_W4A4) {   // tiles: e2m1 codes [ceil(K/128)][M][64] and scales [ceil(K/512)][M][16]
     if (force == 1 || force == 3)
       return fail(GEG_ERR_BAD_OPTION, "W4A4 runs on its tiles (force_path 2) or its narrow kernel (4)");
     const int rb = geg::w4a4_narrow_rb(M, K, E, force);
@@ -183,7 +183,7 @@ geg_status make_plan(int op, int64_t M, int64_t N, int64_t K, int32_t E, const g
     p.cb = rb;
     p.total_bytes = p.a16_off = kHeader;
     if (rb == 0 || !geg::w4a4_narrow_fused(M, E)) {
-      p.a16_bytes = round256((size_t)M * (size_t)(K / 2)) + round256((size_t)((K + 511) / 512) * (size_t)M * 16);
+      p.a16_bytes = round256((size_t)M * (size_t)((K + 127) / 128 * 64)) + round256((size_t)((K + 511) / 512) * (size_t)M * 16);
       p.total_bytes += p.a16_bytes;
     }
     return GEG_OK;
@@ -697,7 +697,7 @@ geg_status gmxfp4_w4a4_grouped_gemm(const void* a, const int32_t* sizes, const u
     if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
   uint8_t* wsb = reinterpret_cast<uint8_t*>(workspace);
   uint8_t* aq = wsb + p.a16_off;
-  uint8_t* as = aq + round256((size_t)M * (size_t)(K / 2));
+  uint8_t* as = aq + round256((size_t)M * (size_t)((K + 127) / 128 * 64));
   geg::W4A4Args g{reinterpret_cast<const uint16_t*>(a), aq, as, sizes, blocks, scales,
                   reinterpret_cast<uint16_t*>(out), M, N, K, E, reinterpret_cast<uint32_t*>(wsb)};
   const int cus = cu_count();

@@ -63,16 +63,15 @@ __global__ __launch_bounds__(kThreads) void w4a4_quantize_kernel(const uint16_t*
     unpack16<kBF16>(reinterpret_cast<const u32x4*>(a)[p], f);
     uint32_t word;
     const int byte = mxfp4_block_piece<8, false>(f, word, q);
-    codes[p] = word;
-    if ((p & 3) == 0) {
-      if (byte == 255) atomicOr(err, kErrNonFinite);
-      const int64_t b = p >> 2;
-      if constexpr (TILES) {
-        const int64_t m = b / KS, kb = b - m * KS;
-        scales[((kb >> 4) * M + m) * 16 + 4 * (kb & 3) + ((kb >> 2) & 3)] = (uint8_t)byte;
-      } else {
-        scales[b] = (uint8_t)byte;
-      }
+    const int64_t b = p >> 2;
+    if ((p & 3) == 0 && byte == 255) atomicOr(err, kErrNonFinite);
+    if constexpr (TILES) {
+      const int64_t m = b / KS, kb = b - m * KS;
+      codes[((kb >> 2) * M + m) * 16 + 4 * (kb & 3) + (p & 3)] = word;
+      if ((p & 3) == 0) scales[((kb >> 4) * M + m) * 16 + 4 * (kb & 3) + ((kb >> 2) & 3)] = (uint8_t)byte;
+    } else {
+      codes[p] = word;
+      if ((p & 3) == 0) scales[b] = (uint8_t)byte;
     }
   }
   if constexpr (!TILES) return;
@@ -86,15 +85,14 @@ __global__ __launch_bounds__(kThreads) void w4a4_quantize_kernel(const uint16_t*
 // ------------------------------------------------------------------ tiles
 constexpr int TM = 256, TN = 256;          // rows, columns per tile
 constexpr int TThreads = 512;              // 8 wavefronts: 2 (rows of 128) x 4 (columns of 64)
-constexpr int kSideStage = TM * (BK / 2);  // bytes of one operand per step
-constexpr int kTileStage = 2 * kSideStage;
-static_assert(TM == TN, "both operands stage alike");
+constexpr int kRowStage = TM * (BK / 2);   // bytes of the activations per step
+constexpr int kColStage = TN * BK;         // bytes of the weights per two steps
 
 // Row r of a staged operand holds 4 chunks of 16 bytes, chunk c at c ^ ((r / 4) % 4): the
 // fragment reads (16 rows at one chunk each) then touch 8 distinct 16-byte bank groups
 // per 8 lanes.
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
-  return (uint32_t)(r * (BK / 2) + ((c ^ ((r >> 2) & 3)) << 4));
+  return (uint32_t)(r * (BK / 2) + ((c ^ ((r >> 1) & 2)) << 4));
 }
 
 // This wavefront's LDS accesses are done and at most N of its loads in flight, then the
@@ -109,24 +107,32 @@ __device__ __forceinline__ void step_barrier() {
 // One workgroup per CU, persistent over tiles (expert, column block, row block; row
 // blocks fastest, so that the tiles that share weights run together on one XCD). Each
 // 128-wide step is staged by loads that write LDS directly (16 bytes per lane, 1 KB per
-// instruction), three steps ahead in four buffers, which are distinct LDS objects named
-// at compile time: the compiler then adds no wait for loads that fill the others. Scales
-// go by pieces of four steps: the activations' 4 KB by direct loads, the weights' bytes
-// (rows of K / 32 bytes, of any alignment) through registers, put in lane order on the
-// way to LDS; one dword per lane then serves four steps, the instruction picking the
-// byte. A wavefront computes 128 x 64: per step 8 + 4 fragments for 32 instructions, so
-// LDS (12 KB per wavefront and step) and the matrix pipes are about equally loaded, and
-// the HBM stream of the weights is what the kernel waits for.
-__global__ __launch_bounds__(TThreads, 1) void w4a4_tile_kernel(W4A4Args g) {
+// instruction) into one of four buffers, which are distinct LDS objects named at compile
+// time: the compiler then adds no wait for loads that fill the others. A wavefront
+// computes 128 x 64, 8 + 4 fragments for the 32 instructions of a step, in two halves:
+//   half 1: the second half's row fragments are read while the first half's multiply;
+//   barrier: every read of this step's buffer is done, the next step's has landed;
+//   half 2: the next step's first fragments are read and the step four ahead starts into
+//           this buffer while the second half's rows multiply.
+// So the matrix pipes work while LDS is read, and three to four steps are in flight. The
+// steps run on across tiles: the last ones of a tile start the next tile's first (a
+// tile's steps are padded to whole pieces of four), and a tile's results are stored from
+// registers meanwhile. Scales go by pieces of four steps through registers into LDS in
+// lane order (byte 4 b + s of a row's 16: block b of step s): one dword per lane serves
+// four steps, the instruction picking the byte.
+template <bool SHORT>
+__device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
   __shared__ int32_t p_u[kMaxExperts + 1];
-  __shared__ __attribute__((aligned(16))) uint8_t lds0[kTileStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds1[kTileStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds2[kTileStage];
-  __shared__ __attribute__((aligned(16))) uint8_t lds3[kTileStage];
-  __shared__ __attribute__((aligned(16))) uint8_t sc0[(TM + TN) * 16];
-  __shared__ __attribute__((aligned(16))) uint8_t sc1[(TM + TN) * 16];
-  const int64_t K = g.K, N = g.N, KS = K >> 5, M = g.M;
+  __shared__ __attribute__((aligned(16))) uint8_t a0[kRowStage];
+  __shared__ __attribute__((aligned(16))) uint8_t a1[kRowStage];
+  __shared__ __attribute__((aligned(16))) uint8_t a2[kRowStage];
+  __shared__ __attribute__((aligned(16))) uint8_t a3[kRowStage];
+  __shared__ __attribute__((aligned(16))) uint8_t w0[kColStage];
+  __shared__ __attribute__((aligned(16))) uint8_t w1[kColStage];
+  __shared__ __attribute__((aligned(16))) uint8_t sc[2][(TM + TN) * 16];
+  const int64_t K = g.K, N = g.N, M = g.M;
+  const int KS = (int)(K >> 5), KB = (int)(K >> 1);
   const int n_tiles = (int)((N + TN - 1) / TN);
   const int32_t total = build_plan(p_off, p_u, g.sizes, g.E, M, g.err,
                                    [&](int32_t s) -> int32_t { return (s + TM - 1) / TM * n_tiles; });
@@ -134,184 +140,239 @@ __global__ __launch_bounds__(TThreads, 1) void w4a4_tile_kernel(W4A4Args g) {
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int r16 = lane & 15, grp = lane >> 4;
-  const int nst = (int)((K + BK - 1) / BK), nss = (nst + 3) / 4;
+  const int nss = (KS + 15) / 16;   // pieces of four steps
   const int G = gridDim.x;
   const int slot = (G % 8 == 0) ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
+  if (slot >= total) return;
+
+  struct Tile {
+    int64_t row0, n0, w0;   // first row, first column, first weight row in [E N]
+    int rows, ncols;
+  };
+  auto tile_of = [&](int32_t u) {
+    Tile x;
+    const int e = __builtin_amdgcn_readfirstlane(find_expert(p_u, g.E, u));
+    const int32_t lu = u - __builtin_amdgcn_readfirstlane(p_u[e]);
+    const int32_t o0 = __builtin_amdgcn_readfirstlane(p_off[e]), o1 = __builtin_amdgcn_readfirstlane(p_off[e + 1]);
+    const int rblocks = (o1 - o0 + TM - 1) / TM;
+    const int nt = lu / rblocks, mt = lu - nt * rblocks;
+    x.row0 = o0 + (int64_t)mt * TM;
+    x.rows = (int)min<int64_t>(TM, o1 - x.row0);
+    x.n0 = (int64_t)nt * TN;
+    x.ncols = (int)min<int64_t>(TN, N - x.n0);
+    x.w0 = (int64_t)e * N + x.n0;
+    return x;
+  };
 
   // Staging: a wavefront fills rows 16 wave + 128 i .. +15 (i = 0, 1) of each operand;
-  // lane l lands in slot l % 4 of row l / 4 and fetches the chunk that belongs there.
-  const int cp_r = 16 * wave + (lane >> 2), cp_c = (lane & 3) ^ ((cp_r >> 2) & 3);
-  const uint32_t rd_a = chunk_at(128 * wm + r16, grp);               // fragment i: + 1024 i
-  const uint32_t rd_w = kSideStage + chunk_at(64 * wn + r16, grp);   // fragment j: + 1024 j
+  // lane l lands in slot l % 4 of row l / 4 and fetches the chunk that belongs there. Rows
+  // past the expert's and columns past N (any = false: all) read as zeros, and so do
+  // chunks past K.
+  const int cp_r = 16 * wave + (lane >> 2), cp_c = (lane & 3) ^ ((cp_r >> 1) & 2);
+  const uint32_t cp_a = (uint32_t)(cp_r * 64 + 16 * cp_c);
+  const int cp_k = (lane & 7) ^ (lane >> 3);
+  const uint32_t cp_w = (uint32_t)((8 * wave + (lane >> 3)) * KB + 16 * cp_k), cp_next = (uint32_t)(64 * KB);
+  const int nst = (KS + 3) / 4;
+  auto stage_a = [&](const Tile& x, bool any, int st, uint8_t* L) {
+    const __amdgpu_buffer_rsrc_t R = wrsrc(g.aq + (st * M + x.row0) * 64, any && st < nst ? x.rows * 64 : 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(R, (lds_ptr_t)(L + (16 * wave + 128 * i) * 64), 16, cp_a + i * 8192, 0, 0,
+                                               0);
+  };
+  auto stage_w = [&](const Tile& x, bool any, int pr, uint8_t* L) {
+    const __amdgpu_buffer_rsrc_t R = wrsrc(g.wq + x.w0 * KB, any ? (int64_t)x.ncols * KB : 0);
+    const uint32_t off = oob_unless(8 * pr + cp_k < KS, cp_w + 128 * pr);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(R, (lds_ptr_t)(L + (8 * wave + 64 * i) * 128), 16, off + i * cp_next, 0, 0,
+                                               0);
+  };
+  // Scales of a piece: thread t has bytes 8 (t % 2) .. +7 of row (column) t / 2's 16. The
+  // activations' are in lane order already; the weights' rows hold K / 32 bytes at any
+  // alignment: 8 bytes that end with the row at the latest, shifted, so that blocks past K
+  // get 0 (SHORT: rows of fewer than 8 bytes, byte by byte).
+  const int s_row = t >> 1, s_half = t & 1;
+  u32x2 s_a, s_w;
+  auto load_scales = [&](const Tile& x, bool any, int ss) {
+    const __amdgpu_buffer_rsrc_t RS = wrsrc(g.as + ((int64_t)ss * M + x.row0) * 16, any ? (M - x.row0) * 16 : 0);
+    s_a = __builtin_amdgcn_raw_buffer_load_b64(RS, (uint32_t)(16 * s_row + 8 * s_half), 0, 0);
+    const uint8_t* row = g.ws + (x.w0 + min(s_row, x.ncols - 1)) * KS;
+    const int o = 16 * ss + 8 * s_half;
+    if constexpr (!SHORT) {
+      __builtin_memcpy(&s_w, row + min(o, KS - 8), 8);
+    } else {
+      s_w = u32x2{0, 0};
+#pragma unroll
+      for (int b = 0; b < 8; ++b)
+        if (o + b < KS) s_w[b >> 2] |= (uint32_t)row[o + b] << (8 * (b & 3));
+    }
+  };
+  auto put_scales = [&](int ss, uint8_t* to) {
+    *reinterpret_cast<u32x2*>(to + 16 * s_row + 8 * s_half) = s_a;
+    const int o = 16 * ss + 8 * s_half, over = SHORT ? 0 : o - min(o, KS - 8);   // bytes loaded too early
+    uint64_t v = __builtin_bit_cast(uint64_t, s_w);
+    v = over >= 8 ? 0 : v >> (8 * over);
+    // (block pairs of this half's two steps; the other thread of the row has the other two)
+    const uint32_t d0 = (uint32_t)v, d1 = (uint32_t)(v >> 32);
+    const uint32_t b01 = perm(d1, d0, 0x05010400u), b23 = perm(d1, d0, 0x07030602u);
+    const uint32_t mine = s_half ? b23 : b01;
+    const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(s_half ? b01 : b23), 0xB1, 0xF, 0xF, true);
+    const uint32_t lo = s_half ? other : mine, hi = s_half ? mine : other;
+    *reinterpret_cast<u32x2*>(to + (TM + s_row) * 16 + 8 * s_half) =
+        u32x2{perm(hi, lo, 0x05040100u), perm(hi, lo, 0x07060302u)};
+  };
+
+  const uint32_t rd_a = chunk_at(128 * wm + r16, grp);               // row fragment i: + 1024 i
+  // column fragment j: + 2048 j; second step of the two: ^ 64
+  const uint32_t rd_w = (uint32_t)((64 * wn + r16) * 128 + ((grp ^ (r16 & 7)) << 4));
   const uint32_t rd_sa = (uint32_t)((128 * wm + r16) * 16 + 4 * grp);       // + 256 i
   const uint32_t rd_sw = (uint32_t)((TM + 64 * wn + r16) * 16 + 4 * grp);   // + 256 j
-
-  for (int32_t base = 0; base < total; base += G) {
-    const int32_t u = base + slot;
-    if (u >= total) break;
-    const int e = find_expert(p_u, g.E, u);
-    const int32_t lu = u - p_u[e];
-    const int rblocks = (p_off[e + 1] - p_off[e] + TM - 1) / TM;
-    const int nt = lu / rblocks, mt = lu % rblocks;
-    const int64_t row0 = p_off[e] + (int64_t)mt * TM;
-    const int rows = (int)min<int64_t>(TM, p_off[e + 1] - row0);
-    const int64_t n0 = (int64_t)nt * TN;
-    const int ncols = (int)min<int64_t>(TN, N - n0);
-    // rows past the expert's and columns past N read as zeros
-    const __amdgpu_buffer_rsrc_t RA = wrsrc(g.aq + row0 * (K >> 1), (int64_t)rows * (K >> 1));
-    const __amdgpu_buffer_rsrc_t RW = wrsrc(g.wq + ((int64_t)e * N + n0) * (K >> 1), (int64_t)ncols * (K >> 1));
-
-    auto stage = [&](int st, uint8_t* L) {
-      const bool ok = (int64_t)st * 4 + cp_c < KS;
+  u32x4 w[2][4], alo[4], ahi[4];
+  uint32_t sw[2][4], slo[4], shi[4];
+  f32x4 acc[8][4];
+  auto read_w = [&](const uint8_t* L, int odd, u32x4* d) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t off = oob_unless(ok, (uint32_t)((cp_r + 128 * i) * (K >> 1) + 64 * (int64_t)st + 16 * cp_c));
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(RA, (lds_ptr_t)(L + (16 * wave + 128 * i) * (BK / 2)), 16, off, 0, 0,
-                                                 0);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            RW, (lds_ptr_t)(L + kSideStage + (16 * wave + 128 * i) * (BK / 2)), 16, off, 0, 0, 0);
-      }
-    };
-    // Scales of piece ss: wavefronts 0-3 load the activations' straight into `sc` (64 rows
-    // each); every thread loads half a weight column's 16 bytes (two steps' four) into
-    // registers. (All wavefronts alike: a value that only some load would be copied where
-    // the paths join, behind a wait for every load in flight.)
-    const int wcol = t >> 1, whalf = t & 1;
-    const uint8_t* wsp = g.ws + ((int64_t)e * N + n0 + min(wcol, ncols - 1)) * KS + 8 * whalf;
-    // rows of the tile past M read zeros, rows of the next expert their own bytes
-    const int64_t sleft = (M - row0) * 16;
-    auto scales = [&](int ss, uint8_t* sc, u32x2& d) {
-      if (wave < 4) {
-        const __amdgpu_buffer_rsrc_t RS = wrsrc(g.as + ((int64_t)min(ss, nss - 1) * M + row0) * 16, sleft);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, (lds_ptr_t)(sc + wave * 1024), 16,
-                                                 (uint32_t)(wave * 1024 + 16 * lane), 0, 0, 0);
-      }
-      if (16 * (ss + 1) <= (int)KS) {
-        __builtin_memcpy(&d, wsp + 16 * ss, 8);
-      } else {
-        // the last piece, byte by byte; blocks past K get 0
-        d = u32x2{0, 0};
+    for (int j = 0; j < 4; ++j) d[j] = *reinterpret_cast<const u32x4*>(L + (rd_w ^ (64 * odd)) + 2048 * j);
+  };
+  auto read_a = [&](const uint8_t* L, int i0, u32x4* d) {
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
-          if (16 * ss + 8 * whalf + b < (int)KS) d[b >> 2] |= (uint32_t)wsp[16 * ss + b] << (8 * (b & 3));
-      }
-    };
-    // byte 4 b + s of a column's 16 in LDS: block b of step s (from byte 4 s + b)
-    auto put_scales = [&](uint8_t* sc, const u32x2& d) {
-      uint8_t* p = sc + (TM + wcol) * 16 + 2 * whalf;
-      const uint32_t lo = perm(d[1], d[0], 0x05010400u), hi = perm(d[1], d[0], 0x07030602u);
-      *reinterpret_cast<uint16_t*>(p) = (uint16_t)lo;
-      *reinterpret_cast<uint16_t*>(p + 4) = (uint16_t)(lo >> 16);
-      *reinterpret_cast<uint16_t*>(p + 8) = (uint16_t)hi;
-      *reinterpret_cast<uint16_t*>(p + 12) = (uint16_t)(hi >> 16);
-    };
+    for (int i = 0; i < 4; ++i) d[i] = *reinterpret_cast<const u32x4*>(L + rd_a + 1024 * (i0 + i));
+  };
+  auto read_s = [&](const uint8_t* from, uint32_t at, uint32_t* d) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] = *reinterpret_cast<const uint32_t*>(from + at + 256 * i);
+  };
 
-    const bool live = 128 * wm < rows;
-    f32x4 acc[8][4];
+  int32_t u = slot;
+  Tile cur = tile_of(u);
+  bool live = 128 * wm < cur.rows;
+  int par = 0;   // scale buffer of the piece at hand
+  load_scales(cur, true, 0);
+  stage_w(cur, true, 0, w0);
+  stage_a(cur, true, 0, a0);
+  stage_a(cur, true, 1, a1);
+  stage_a(cur, true, 2, a2);
+  put_scales(0, sc[0]);
+  step_barrier<4>();
+  read_w(w0, 0, w[0]);
+  read_a(a0, 0, alo);
+  read_s(sc[0], rd_sw, sw[0]);
+  read_s(sc[0], rd_sa, slo);
+
+  for (;;) {
+    const bool more = u + G < total;
+    const Tile nxt = more ? tile_of(u + G) : cur;
+    const bool nlive = more && 128 * wm < nxt.rows;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    u32x2 d = u32x2{0, 0};
-
-    // Step S of piece ss: its operands are in `cur` (barrier of the step before); stage
-    // st + 3 goes to `nxt`, the buffer that step st - 1 read. With S == 0 the next piece's
-    // scales start, with S == 3 they are published. At the end stage st + 1 has landed
-    // (the 8 loads of the two stages after it may be in flight).
-    auto step = [&](auto Sc, int ss, const uint8_t* cur, uint8_t* nxt, const uint8_t* sc, uint8_t* scn) {
-      constexpr int S = decltype(Sc)::value;
-      if constexpr (S == 0) scales(ss + 1, scn, d);
-      stage(4 * ss + S + 3, nxt);
-      if (live) {
-        u32x4 w[4], a[8];
-        uint32_t sw[4], sa[8];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          w[j] = *reinterpret_cast<const u32x4*>(cur + rd_w + 1024 * j);
-          sw[j] = *reinterpret_cast<const uint32_t*>(sc + rd_sw + 256 * j);
+    for (int ss = 0; ss < nss; ++ss) {
+      const bool last = ss + 1 == nss;
+      // Step S of the piece in buffer `L`, the next one in `L1`. A piece's scales stay in
+      // registers; sw alternates between two sets, as the weights' fragments do.
+      auto step = [&](auto Sc, const uint8_t* L, const uint8_t* L1, uint8_t* L3, const uint8_t* W1, uint8_t* W2) {
+        constexpr int S = decltype(Sc)::value;
+        constexpr int c = S & 1, n = c ^ 1;
+        if constexpr (S == 0) load_scales(last ? nxt : cur, !last || more, last ? 0 : ss + 1);
+        if (live) {
+          read_a(L, 4, ahi);
+          if constexpr (S == 0) read_s(sc[par], rd_sa + 1024, shi);
         }
+        // the stage three ahead: of this tile, or of the next one (its first three)
+        if constexpr (S == 0) stage_w(cur, true, 2 * ss + 1, W2);
+        if constexpr (S == 2) stage_w(last ? nxt : cur, !last || more, last ? 0 : 2 * ss + 2, W2);
+        if constexpr (S == 0)
+          stage_a(cur, true, 4 * ss + 3, L3);
+        else
+          stage_a(last ? nxt : cur, !last || more, last ? S - 1 : 4 * ss + S + 3, L3);
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          a[i] = *reinterpret_cast<const u32x4*>(cur + rd_a + 1024 * i);
-          sa[i] = *reinterpret_cast<const uint32_t*>(sc + rd_sa + 256 * i);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<S>(w[c][j], alo[i], acc[i][j], sw[0][j], slo[i]);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (S == 3) put_scales(last ? 0 : ss + 1, sc[par ^ 1]);
+        // in flight: the two stages after the next one and, until it is used, the scales'
+        // two loads
+        step_barrier<S == 0 ? 10 : S == 2 ? 8 : 4>();
+        if (S == 3 && last ? nlive : live) {
+          read_w(W1, n, w[n]);
+          read_a(L1, 0, alo);
+          if constexpr (S == 3) {
+            read_s(sc[par ^ 1], rd_sw, sw[1]);
+            read_s(sc[par ^ 1], rd_sa, slo);
+          }
+        }
+        if (live) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = mfma_fp4<S>(w[j], a[i], acc[i][j], sw[j], sa[i]);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      if constexpr (S == 3) put_scales(scn, d);
-      step_barrier<8>();
-    };
-    constexpr std::integral_constant<int, 0> s0{};
-    constexpr std::integral_constant<int, 1> s1{};
-    constexpr std::integral_constant<int, 2> s2{};
-    constexpr std::integral_constant<int, 3> s3{};
-
-    scales(0, sc0, d);
-    stage(0, lds0);
-    stage(1, lds1);
-    stage(2, lds2);
-    put_scales(sc0, d);
-    step_barrier<8>();
-    int ss = 0;
-    for (; 4 * (ss + 2) <= nst; ss += 2) {
-      step(s0, ss, lds0, lds3, sc0, sc1);
-      step(s1, ss, lds1, lds0, sc0, sc1);
-      step(s2, ss, lds2, lds1, sc0, sc1);
-      step(s3, ss, lds3, lds2, sc0, sc1);
-      step(s0, ss + 1, lds0, lds3, sc1, sc0);
-      step(s1, ss + 1, lds1, lds0, sc1, sc0);
-      step(s2, ss + 1, lds2, lds1, sc1, sc0);
-      step(s3, ss + 1, lds3, lds2, sc1, sc0);
+            for (int j = 0; j < 4; ++j) acc[4 + i][j] = mfma_fp4<S>(w[c][j], ahi[i], acc[4 + i][j], sw[0][j], shi[i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (S == 3) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sw[0][j] = sw[1][j];
+        }
+      };
+      step(std::integral_constant<int, 0>{}, a0, a1, a3, w0, w1);
+      step(std::integral_constant<int, 1>{}, a1, a2, a0, w1, w1);
+      step(std::integral_constant<int, 2>{}, a2, a3, a1, w1, w0);
+      step(std::integral_constant<int, 3>{}, a3, a0, a2, w0, w0);
+      par ^= 1;
     }
-    const int rest = nst - 4 * ss;
-    if (rest > 0) step(s0, ss, lds0, lds3, sc0, sc1);
-    if (rest > 1) step(s1, ss, lds1, lds0, sc0, sc1);
-    if (rest > 2) step(s2, ss, lds2, lds1, sc0, sc1);
-    if (rest > 3) step(s3, ss, lds3, lds2, sc0, sc1);
-    if (rest > 4) step(s0, ss + 1, lds0, lds3, sc1, sc0);
-    if (rest > 5) step(s1, ss + 1, lds1, lds0, sc1, sc0);
-    if (rest > 6) step(s2, ss + 1, lds2, lds1, sc1, sc0);
-    step_barrier<0>();   // loads past the last step have landed: the buffers are free
 
-    // Epilogue: the wavefront's 128 x 64 block as bf16 rows of 128 bytes in its own 16 KB
-    // (16-byte piece p of row r at p ^ (r % 8)), then 16-byte pieces of whole rows.
+    // Results. Lane (r16, grp) has columns 16 j + 4 grp .. +3 of row 16 i + r16; trading
+    // rows of 16 lanes between two neighbouring j gives every lane 8 adjacent columns, 64
+    // consecutive bytes of each of 16 rows per store.
     if (live) {
-      uint8_t* L = (wave < 4 ? (wave < 2 ? lds0 : lds1) : (wave < 6 ? lds2 : lds3)) + (wave & 1) * (kTileStage / 2);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = 16 * i + r16;
-          const u32x2 v = u32x2{pack_bf16x2(acc[i][j][0], acc[i][j][1]), pack_bf16x2(acc[i][j][2], acc[i][j][3])};
-          *reinterpret_cast<u32x2*>(L + r * 128 + (((2 * j + (grp >> 1)) ^ (r & 7)) << 4) + 8 * (grp & 1)) = v;
-        }
-      __builtin_amdgcn_wave_barrier();
-      asm volatile("" ::: "memory");
       const bool wide = (N & 7) == 0 && (reinterpret_cast<uintptr_t>(g.out) & 15) == 0;
-      const int pc = lane & 7;
-      const int64_t col = n0 + 64 * wn + 8 * pc;
+      // lane groups 0, 2: columns 0-7, 8-15 of block j; 1, 3: of block j + 1
+      const int col = 16 * (grp & 1) + 8 * (grp >> 1);
+      uint16_t* dst = g.out + (cur.row0 + 128 * wm + r16) * N + cur.n0 + 64 * wn + col;
+      const int left = (int)(min<int64_t>(N - cur.n0, TN)) - 64 * wn - col;   // columns from this lane's first on
+      const int rows = cur.rows - 128 * wm - r16;
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int r = 8 * q + (lane >> 3), lr = 128 * wm + r;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(L + r * 128 + ((pc ^ (r & 7)) << 4));
-        if (lr < rows) {
-          uint16_t* dst = g.out + (row0 + lr) * N + col;
-          if (wide) {
-            if (col < N) *reinterpret_cast<u32x4*>(dst) = v;
-          } else {
+      for (int i = 0; i < 8; ++i) {
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
-              if (col + b < N) dst[b] = (uint16_t)(v[b >> 1] >> (16 * (b & 1)));
+        for (int j = 0; j < 4; j += 2) {
+          u32x4 v;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t p = pack_bf16x2(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
+            const uint32_t q = pack_bf16x2(acc[i][j + 1][2 * h], acc[i][j + 1][2 * h + 1]);
+            const auto r = __builtin_amdgcn_permlane16_swap(p, q, false, false);
+            v[h] = r[0];
+            v[2 + h] = r[1];
+          }
+          if (16 * i < rows && 16 * j < left) {
+            uint16_t* d = dst + (int64_t)(16 * i) * N + 16 * j;
+            if (wide) {
+              *reinterpret_cast<u32x4*>(d) = v;
+            } else {
+#pragma clang loop unroll(disable)
+              for (int b = 0; b < min(8, left - 16 * j); ++b) {
+                const uint32_t x = b < 4 ? (b < 2 ? v[0] : v[1]) : (b < 6 ? v[2] : v[3]);
+                d[b] = (uint16_t)(x >> (16 * (b & 1)));
+              }
+            }
           }
         }
       }
     }
-    step_barrier<63>();   // LDS reads done before the next tile's loads land
+    if (!more) break;
+    u += G;
+    cur = nxt;
+    live = nlive;
   }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no load into LDS outlives the workgroup
 }
+
+__global__ __launch_bounds__(TThreads, 1) void w4a4_tile_kernel(W4A4Args g) { w4a4_tiles<false>(g); }
+__global__ __launch_bounds__(TThreads, 1) void w4a4_tile_short_kernel(W4A4Args g) { w4a4_tiles<true>(g); }
 
 // ------------------------------------------------------------------ narrow
 // Wavefront units: 16 output columns of one expert and up to 16 RB of its rows (a group),
@@ -588,7 +649,10 @@ hipError_t launch_w4a4_tile(const W4A4Args& g, int cus, hipStream_t s) {
   const int64_t n_tiles = (g.N + TN - 1) / TN;
   const int64_t bound = ((g.M + TM - 1) / TM + std::min<int64_t>(g.E, g.M)) * n_tiles;
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(bound, (int64_t)cus));
-  hipLaunchKernelGGL(w4a4_tile_kernel, dim3((unsigned)grid), dim3(TThreads), 0, s, g);
+  if (g.K < 256)
+    hipLaunchKernelGGL(w4a4_tile_short_kernel, dim3((unsigned)grid), dim3(TThreads), 0, s, g);
+  else
+    hipLaunchKernelGGL(w4a4_tile_kernel, dim3((unsigned)grid), dim3(TThreads), 0, s, g);
   return hipGetLastError();
 }
 
