@@ -115,13 +115,13 @@ hipError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t
                                  uint8_t* scales, void* values, int cus, hipStream_t s);
 // W4A4: the grouped GEMM with both operands in MXFP4 (see w4a4.hip). The narrow kernel
 // (w4a4_narrow_rb > 0) quantises g.a itself when w4a4_narrow_fused and g.aq is NULL;
-// otherwise g.aq and g.as hold what launch_w4a4_quantize makes: codes [M, K/2], scales
-// [M, K/32] (narrow) or [ceil(K/512)][M][16] (tiles).
+// otherwise g.aq and g.as hold what launch_w4a4_quantize makes: codes [M, K/2] and scales
+// [M, K/32] (narrow), or [ceil(K/128)][M][64] and [ceil(K/512)][M][16] (tiles).
 constexpr int64_t kW4A4NarrowAvg = 32;   // rows per expert on average up to which the narrow kernel runs
 constexpr int kMaxLds = 160 << 10;       // LDS of a CU
 struct W4A4Args {
   const uint16_t* a;      // bf16 [M, K]
-  const uint8_t* aq;      // their codes and scales (tiles)
+  const uint8_t* aq;      // their codes and scales
   const uint8_t* as;
   const int32_t* sizes;   // [E]
   const uint8_t* wq;      // e2m1 weight bytes [E, N, K/2]

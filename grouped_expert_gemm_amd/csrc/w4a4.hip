@@ -48,8 +48,9 @@ __device__ __forceinline__ f32x4 mfma_fp4(const u32x4& w, const u32x4& a, const 
 }
 
 // ------------------------------------------------------------------ activations for the tiles
-// bf16 [M, K] -> codes [M, K/2] and scales. For the narrow kernel [M, K/32]; for the tiles
-// [K/512 rounded up][M][16]: byte 4 b + s of a row's 16 is the scale of 32-block 4 s + b of
+// bf16 [M, K] -> codes and scales. For the narrow kernel codes [M, K/2] and scales
+// [M, K/32]; for the tiles codes [K/128 rounded up][M][64] (what lies past K is not written:
+// the weights read as zeros there) and scales [K/512 rounded up][M][16]: byte 4 b + s of a row's 16 is the scale of 32-block 4 s + b of
 // the 512-wide piece, so a lane of group b reads the bytes of its four steps s as one
 // dword; blocks past K get 0. One thread per 8 values, four lanes to a block.
 template <bool TILES>
@@ -88,9 +89,10 @@ constexpr int TThreads = 512;              // 8 wavefronts: 2 (rows of 128) x 4 
 constexpr int kRowStage = TM * (BK / 2);   // bytes of the activations per step
 constexpr int kColStage = TN * BK;         // bytes of the weights per two steps
 
-// Row r of a staged operand holds 4 chunks of 16 bytes, chunk c at c ^ ((r / 4) % 4): the
-// fragment reads (16 rows at one chunk each) then touch 8 distinct 16-byte bank groups
-// per 8 lanes.
+// A row of the staged activations holds 4 chunks of 16 bytes, chunk c of row r at
+// c ^ (2 ((r / 4) % 2)); a row of the staged weights 8, at c ^ (r % 8). A fragment read
+// (16 rows, chunk g for lane group g) then meets no bank conflict (with the activations'
+// chunks at c ^ ((r / 4) % 4) every read took twice its time).
 __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
   return (uint32_t)(r * (BK / 2) + ((c ^ ((r >> 1) & 2)) << 4));
 }
@@ -105,21 +107,33 @@ __device__ __forceinline__ void step_barrier() {
 }
 
 // One workgroup per CU, persistent over tiles (expert, column block, row block; row
-// blocks fastest, so that the tiles that share weights run together on one XCD). Each
-// 128-wide step is staged by loads that write LDS directly (16 bytes per lane, 1 KB per
-// instruction) into one of four buffers, which are distinct LDS objects named at compile
-// time: the compiler then adds no wait for loads that fill the others. A wavefront
-// computes 128 x 64, 8 + 4 fragments for the 32 instructions of a step, in two halves:
-//   half 1: the second half's row fragments are read while the first half's multiply;
-//   barrier: every read of this step's buffer is done, the next step's has landed;
-//   half 2: the next step's first fragments are read and the step four ahead starts into
-//           this buffer while the second half's rows multiply.
-// So the matrix pipes work while LDS is read, and three to four steps are in flight. The
-// steps run on across tiles: the last ones of a tile start the next tile's first (a
-// tile's steps are padded to whole pieces of four), and a tile's results are stored from
-// registers meanwhile. Scales go by pieces of four steps through registers into LDS in
-// lane order (byte 4 b + s of a row's 16: block b of step s): one dword per lane serves
-// four steps, the instruction picking the byte.
+// blocks fastest, so that the tiles that share weights run together on one XCD). Loads
+// write LDS directly (16 bytes per lane, 1 KB per instruction): the activations a step at
+// a time into four buffers, the weights two steps at a time into two, all distinct LDS
+// objects named at compile time: the compiler then adds no wait for loads that fill the
+// others. What a load instruction covers decides its speed: rows of 64 bytes came at 37
+// GB/s per CU, 128 at 50 and whole runs at 65 (1440-byte rows from L2). So the
+// activations are quantised into step order, where a step's rows are one run, and a
+// weight row is read 128 bytes at a time.
+//
+// A wavefront computes 128 x 64, 8 + 4 fragments for the 32 instructions of a step, in
+// two halves:
+//   half 1: the second half's row fragments are read and the activations three steps
+//           ahead start into the previous step's buffer while the first half's multiply;
+//   barrier: every read of this step's buffers is done, the next step's have landed;
+//   half 2: the next step's first fragments are read and, every other step, the weights
+//           of the pair after the next start while the second half's rows multiply.
+// So the matrix pipes work while LDS is read. The steps run on across tiles: the last
+// ones of a tile start the next tile's first (a tile's steps are padded to whole pieces
+// of four). Scales go by pieces of four steps through registers into LDS in lane order
+// (byte 4 b + s of a row's 16: block b of step s): one dword per lane serves four steps,
+// the instruction picking the byte.
+//
+// 2048 tokens x 4 of 32 experts, K 2880, N 5760: 151-157 us, 1219 tiles in five rounds of
+// the 256 CUs. Before its last step (161 us) it took 111 us without its loads, 124 without
+// its multiplications and 135 without its stores: no one of the three bounds it alone. Not kept: stores that the
+// next tile's first waits leave in flight (nothing gained), stores past the caches
+// (3% slower).
 template <bool SHORT>
 __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
@@ -164,10 +178,11 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
     return x;
   };
 
-  // Staging: a wavefront fills rows 16 wave + 128 i .. +15 (i = 0, 1) of each operand;
-  // lane l lands in slot l % 4 of row l / 4 and fetches the chunk that belongs there. Rows
-  // past the expert's and columns past N (any = false: all) read as zeros, and so do
-  // chunks past K.
+  // Staging: of the activations a wavefront fills rows 16 wave + 128 i .. +15 (i = 0, 1), 4
+  // lanes to a row, of the weights rows 8 wave + 64 i .. +7 (i = 0 .. 3), 8 lanes to a row;
+  // lane l lands in slot l % 4 (l % 8) of its row and fetches the chunk that belongs there.
+  // Rows past the expert's and columns past N (any = false: all) read as zeros, and so do
+  // the weights' chunks past K.
   const int cp_r = 16 * wave + (lane >> 2), cp_c = (lane & 3) ^ ((cp_r >> 1) & 2);
   const uint32_t cp_a = (uint32_t)(cp_r * 64 + 16 * cp_c);
   const int cp_k = (lane & 7) ^ (lane >> 3);
@@ -253,8 +268,9 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
   stage_a(cur, true, 0, a0);
   stage_a(cur, true, 1, a1);
   stage_a(cur, true, 2, a2);
+  stage_w(cur, true, 1, w1);
   put_scales(0, sc[0]);
-  step_barrier<4>();
+  step_barrier<8>();
   read_w(w0, 0, w[0]);
   read_a(a0, 0, alo);
   read_s(sc[0], rd_sw, sw[0]);
@@ -281,8 +297,6 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
           if constexpr (S == 0) read_s(sc[par], rd_sa + 1024, shi);
         }
         // the stage three ahead: of this tile, or of the next one (its first three)
-        if constexpr (S == 0) stage_w(cur, true, 2 * ss + 1, W2);
-        if constexpr (S == 2) stage_w(last ? nxt : cur, !last || more, last ? 0 : 2 * ss + 2, W2);
         if constexpr (S == 0)
           stage_a(cur, true, 4 * ss + 3, L3);
         else
@@ -295,9 +309,10 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
         }
         __builtin_amdgcn_sched_barrier(0);
         if constexpr (S == 3) put_scales(last ? 0 : ss + 1, sc[par ^ 1]);
-        // in flight: the two stages after the next one and, until it is used, the scales'
-        // two loads
-        step_barrier<S == 0 ? 10 : S == 2 ? 8 : 4>();
+        // what may stay in flight: the loads begun after those the next step reads. Per
+        // step: 0 the scales' two, a3; 1 a4, w of 4 and 5; 2 a5; 3 a6, w of 6 and 7.
+        constexpr int scale_loads = SHORT ? 0 : 2;
+        step_barrier<S == 0 ? 8 + scale_loads : S == 1 ? 4 + scale_loads : S == 2 ? 8 : 4>();
         if (S == 3 && last ? nlive : live) {
           read_w(W1, n, w[n]);
           read_a(L1, 0, alo);
@@ -306,6 +321,8 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
             read_s(sc[par ^ 1], rd_sa, slo);
           }
         }
+        if constexpr (S == 1) stage_w(last ? nxt : cur, !last || more, last ? 0 : 2 * ss + 2, W2);
+        if constexpr (S == 3) stage_w(last ? nxt : cur, !last || more, last ? 1 : 2 * ss + 3, W2);
         if (live) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -318,10 +335,10 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
           for (int j = 0; j < 4; ++j) sw[0][j] = sw[1][j];
         }
       };
-      step(std::integral_constant<int, 0>{}, a0, a1, a3, w0, w1);
-      step(std::integral_constant<int, 1>{}, a1, a2, a0, w1, w1);
-      step(std::integral_constant<int, 2>{}, a2, a3, a1, w1, w0);
-      step(std::integral_constant<int, 3>{}, a3, a0, a2, w0, w0);
+      step(std::integral_constant<int, 0>{}, a0, a1, a3, w0, w0);
+      step(std::integral_constant<int, 1>{}, a1, a2, a0, w1, w0);
+      step(std::integral_constant<int, 2>{}, a2, a3, a1, w1, w1);
+      step(std::integral_constant<int, 3>{}, a3, a0, a2, w0, w1);
       par ^= 1;
     }
 
