@@ -117,7 +117,10 @@ hipError_t launch_mxfp4_quantize(const void* x, int dtype, int64_t rows, int64_t
 // (w4a4_narrow_rb > 0) quantises g.a itself when w4a4_narrow_fused and g.aq is NULL;
 // otherwise g.aq and g.as hold what launch_w4a4_quantize makes: codes [M, K/2] and scales
 // [M, K/32] (narrow), or [ceil(K/128)][M][64] and [ceil(K/512)][M][16] (tiles).
-constexpr int64_t kW4A4NarrowAvg = 32;   // rows per expert on average up to which the narrow kernel runs
+// Rows per expert on average up to which the narrow kernel runs. At 16 it took 40 us, the
+// tiles 48 (E 32, K 2880, N 2880), 64 against 74 (N 5760), 54 against 54 (E 8, K 4096,
+// N 14336), 51 against 47 (E 128, K 2048, N 1536); at 24 46/48, 80/75, 72/54 and 61/49.
+constexpr int64_t kW4A4NarrowAvg = 16;
 constexpr int kMaxLds = 160 << 10;       // LDS of a CU
 struct W4A4Args {
   const uint16_t* a;      // bf16 [M, K]
