@@ -24,8 +24,19 @@
 // that puts the block's largest in [2^14, 2^15): 11 bits for everything within 2^-29 of
 // it, whatever the layer's scale, and a lane's 32 values are one such block, so the
 // scale joins the weight's in the one product per chunk. (fp32 activations against
-// mixed-precision fmas took twice the arithmetic and three times the registers: 714
-// against 92 us for the second kernel of 8 experts of 4096 x 14336, four tokens.)
+// mixed-precision fmas took twice the arithmetic and three times the registers: for the
+// second kernel of 8 experts of 4096 x 14336, four tokens, 714 us against 37 now.)
+//
+// Both kernels together: 8 experts of 4096 x 14336, top 2, four tokens: 90 us for 542 MB
+// (6.0 TB/s, part of it from the last-level cache). 128 experts of 2048 x 768, top 8: one
+// token 13 us (21 MB), 16 tokens 54 us (219 MB); 32 experts of 2880 x 2880, top 4, MXFP4,
+// one token 20 us (53 MB). One token is
+// bound by latency and issue as much as by bytes: of 20 us about 3 pass from a kernel's
+// start until its first weights are asked for (ids, grouping), 2 until they are there and
+// 1.3 between the two kernels; 16 wavefronts pay 16 clocks of a CU for every vector
+// instruction they share. Not kept for one token: units of 32 rows without a grouping,
+// every load of a workgroup begun at its start, 16 or 8 wavefronts (16.9 and 13.4 us for
+// the MXFP4 first kernel against 13.5).
 #include <algorithm>
 
 #include "geg_device.hpp"

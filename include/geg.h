@@ -409,7 +409,7 @@ geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K
  *            and, with more rows than experts, the codes [M, K/2] and their scales
  *   opts: force_path 0 by size, 2 tiles, 4 narrow kernel (1 and 3 are refused);
  *         kernel_events[0..1] bracket the GEMM kernel
- * Batches of at most 32 rows per expert on average stream the weights once per 16 or 32
+ * Batches of at most 16 rows per expert on average stream the weights once per 16 or 32
  * rows (in one launch up to one row per expert); larger ones run 256 x 256 tiles. A
  * row whose activations hold an inf or NaN comes out NaN and flags
  * GEG_DEVERR_NON_FINITE.
