@@ -971,9 +971,9 @@ geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K
   if (dtype < GEG_BF16 || dtype > GEG_F32) return fail(GEG_ERR_BAD_OPTION, "dtype must be GEG_BF16, GEG_F16 or GEG_F32");
   if (rows < 0 || K <= 0 || K % 32) return fail(GEG_ERR_BAD_SHAPE, "need rows >= 0, K > 0, K % 32 == 0");
   if (ld < K) return fail(GEG_ERR_BAD_SHAPE, "the row pitch ld must be at least K");
-  // one thread per 4 values at least, at most 2^31 - 1 workgroups of 256
-  if (K > ((int64_t)1 << 40) || rows > ((int64_t)1 << 40) / K || ld > ((int64_t)1 << 60) / std::max<int64_t>(rows, 1))
-    return fail(GEG_ERR_BAD_SHAPE, "rows * K must not exceed 2^40");
+  // a launch holds fewer than 2^32 threads, of at least 16 values each
+  if (K > ((int64_t)1 << 35) || rows > ((int64_t)1 << 35) / K || ld > ((int64_t)1 << 60) / std::max<int64_t>(rows, 1))
+    return fail(GEG_ERR_BAD_SHAPE, "rows * K must not exceed 2^35");
   if (rows == 0) return GEG_OK;
   if (!x || !blocks || !scales) return fail(GEG_ERR_NULL_POINTER, "x, blocks and scales are required");
   if (!aligned(x, 16) || (rows > 1 && (ld * dtype_bytes(dtype)) % 16) || !aligned(blocks, 4) ||
@@ -992,13 +992,15 @@ geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K
   return GEG_OK;
 }
 
+// One wavefront each, and a launch holds fewer than 2^32 threads.
+static constexpr int64_t kMaxWaves = (int64_t)1 << 25;
+
 static geg_status check_gate(int32_t dtype, int64_t T, int32_t E, int32_t k) {
   if (dtype < GEG_BF16 || dtype > GEG_F32) return fail(GEG_ERR_BAD_OPTION, "dtype must be GEG_BF16, GEG_F16 or GEG_F32");
   if (T < 0 || E <= 0 || k <= 0) return fail(GEG_ERR_BAD_SHAPE, "need T >= 0, E > 0, k > 0");
   if (E > geg::kMaxExperts) return fail(GEG_ERR_BAD_SHAPE, "E exceeds 1024 experts");
   if (k > E || k > 64) return fail(GEG_ERR_BAD_SHAPE, "k must not exceed E or 64");
-  if (T >= (int64_t)INT32_MAX || T * (int64_t)k >= (int64_t)INT32_MAX)
-    return fail(GEG_ERR_BAD_SHAPE, "T * k must be below 2^31");
+  if (T > kMaxWaves) return fail(GEG_ERR_BAD_SHAPE, "T must not exceed 2^25");
   return GEG_OK;
 }
 
@@ -1047,8 +1049,7 @@ geg_status geg_route_combine_grad(const void* dout, const void* y, const int32_t
                                   const float* weights, int64_t T, int32_t k, int64_t N, void* dy, float* dweights,
                                   hipStream_t stream) {
   if (T < 0 || k <= 0 || N <= 0 || N % 8) return fail(GEG_ERR_BAD_SHAPE, "need T >= 0, k > 0, N > 0, N % 8 == 0");
-  if (T >= (int64_t)INT32_MAX || T * (int64_t)k >= (int64_t)INT32_MAX)
-    return fail(GEG_ERR_BAD_SHAPE, "T * k must be below 2^31");
+  if (T > kMaxWaves || T * (int64_t)k > kMaxWaves) return fail(GEG_ERR_BAD_SHAPE, "T * k must not exceed 2^25");
   if (T == 0) return GEG_OK;
   if (!dout || !row_of || !dy || (dweights && !y))
     return fail(GEG_ERR_NULL_POINTER, "dout, row_of, dy and (for dweights) y are required");

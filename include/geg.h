@@ -394,7 +394,7 @@ geg_status gmxfp4_grouped_dgrad_lora(const void* dy, const int32_t* sizes, const
  *   scales  u8 [rows, K/32] out
  *   values  NULL, or dtype [rows, K] out, 16-B aligned: what the codes stand for
  *           (exact in every one of the types)
- *   K % 32 == 0.
+ *   K % 32 == 0, rows * K <= 2^35.
  */
 geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K, int64_t ld, uint8_t* blocks,
                            uint8_t* scales, void* values, hipStream_t stream);
@@ -406,7 +406,7 @@ geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K
  *   out[rows of e, :] = bf16( Q(a_e) . W_e^T ), fp32 accumulation.
  *   a, sizes, blocks, scales, out, M, N, K, E: as gmxfp4_grouped_gemm (K % 32 == 0)
  *   workspace: geg_workspace_bytes(GEG_OP_MXFP4_W4A4, ...) bytes; holds the error word
- *            and, with more rows than experts, the codes [M, K/2] and their scales
+ *            and, with more rows than experts, the activations' codes and scales
  *   opts: force_path 0 by size, 2 tiles, 4 narrow kernel (1 and 3 are refused);
  *         kernel_events[0..1] bracket the GEMM kernel
  * Batches of at most 16 rows per expert on average stream the weights once per 16 or 32
@@ -426,7 +426,7 @@ geg_status gmxfp4_w4a4_grouped_gemm(const void* a, const int32_t* sizes, const u
  * the sum over all E experts, or with renormalize != 0 over the chosen k (the softmax
  * of the chosen logits). fp32 arithmetic. The ids and weights are what geg_route_sort,
  * geg_route_combine and the MoE layer take.
- *   logits   dtype [T, E], E <= 1024
+ *   logits   dtype [T, E], E <= 1024, T <= 2^25
  *   weights  fp32 [T, k] out, ids int32 [T, k] out; 1 <= k <= min(E, 64)
  *   error_word  device uint32 that receives GEG_DEVERR_NON_FINITE when a logit is NaN
  *            (OR-ed in; the caller clears it), or NULL
@@ -452,7 +452,8 @@ geg_status geg_route_topk_grad(const float* dweights, const void* logits, int32_
  *   dy[row_of[t*k + s], :] = bf16( weights[t, s] * dout[t, :] )
  *   dweights[t, s] = sum_n dout[t, n] * y[row_of[t*k + s], n]     (fp32)
  *   dout bf16 [T, N], y bf16 [T*k, N], row_of int32 [T*k] (values in [-1, T*k),
- *   no row twice), weights fp32 [T, k] or NULL for all ones; N % 8 == 0
+ *   no row twice), weights fp32 [T, k] or NULL for all ones; N % 8 == 0,
+ *   T * k <= 2^25
  *   src_of   int32 [T*k] of geg_route_sort, or NULL: with it, rows of dy that no entry
  *            lands on (src_of < 0) are set to 0; without it they are left untouched
  *   dy bf16 [T*k, N] (not y itself), dweights fp32 [T, k] or NULL (then y may be NULL)

@@ -21,6 +21,7 @@ def test_quantize_refusals():
     assert _quant(ld=32) == 2
     assert b"pitch" in L().geg_last_error()
     assert _quant(rows=1 << 40, K=64) == 2 and _quant(K=1 << 41) == 2
+    assert _quant(rows=(1 << 29) + 1) == 2 and _quant(rows=1 << 29) not in (0, 1, 2, 3)
     assert _quant(rows=0, x=None, blocks=None, scales=None) == 0
     assert _quant(x=None) == 1 and _quant(scales=None) == 1
     assert _quant(x=P + 8) == 3 and _quant(values=P + 8) == 3 and _quant(blocks=P + 2) == 3
@@ -49,6 +50,7 @@ def test_gate_refusals():
         assert call(logits=None) == 1 and call(ids=None) == 1 and call(w=None) == 1
         assert call(logits=P + 2) == 3 and call(logits=P + 2, dtype=0) not in (0, 3)
         assert call() not in (0, 1, 2, 3, 8)
+        assert call(T=(1 << 25) + 1) == 2 and call(T=1 << 25) not in (0, 1, 2, 3)
     assert _topk(err=P + 2) == 3
     assert _topk_grad(dl=P) == 8
 
@@ -60,6 +62,8 @@ def _combine_grad(dout=P, y=P, row=P, src=None, w=P, T=4, k=2, N=64, dy=2 * P, d
 def test_combine_gradient_refusals():
     assert _combine_grad(N=60) == 2 and _combine_grad(T=-1) == 2 and _combine_grad(k=0) == 2
     assert _combine_grad(T=1 << 62) == 2
+    # a launch of one wavefront per entry holds fewer than 2^32 threads
+    assert _combine_grad(T=(1 << 24) + 1, k=2) == 2 and _combine_grad(T=1 << 24, k=2) not in (0, 1, 2, 3)
     assert _combine_grad(T=0, dout=None) == 0
     assert _combine_grad(dout=None) == 1 and _combine_grad(y=None) == 1 and _combine_grad(dy=None) == 1
     assert _combine_grad(y=None, dw=None) not in (0, 1)
@@ -112,11 +116,11 @@ def test_w4a4_refusals():
     assert _w4a4(opts=geg.Opts(1, 0)) == 8 and _w4a4(opts=geg.Opts(3, 0)) == 8 and _w4a4(opts=geg.Opts(0, 0, None, -1)) == 8
     assert _w4a4(opts=geg.Opts(4, 0), K=65536, N=64) == 8      # the narrow kernel's rows past LDS
     assert _w4a4() not in (0, 1, 2, 3, 5, 8)
-    # header only up to one row per expert; else codes and scales [ceil(K/512)][M][16]
+    # header only up to one row per expert; else codes [ceil(K/128)][M][64] and scales [ceil(K/512)][M][16]
     op = geg.GEG_OP_MXFP4_W4A4
     assert geg.geg_workspace_bytes(op, 4, 64, 128, 4) == 256
     assert geg.geg_workspace_bytes(op, 5, 64, 128, 4) == 256 + 512 + 256
-    assert geg.geg_workspace_bytes(op, 8192, 5760, 2880, 32) == 256 + 8192 * 1440 + 6 * 8192 * 16
+    assert geg.geg_workspace_bytes(op, 8192, 5760, 2880, 32) == 256 + 23 * 8192 * 64 + 6 * 8192 * 16
     assert geg.geg_workspace_bytes(op, 64, 64, 512, 4, geg.Opts(2, 0)) == 256 + 64 * 256 + 64 * 16
     need = geg.geg_workspace_bytes(op, 8192, 64, 128, 4)
     assert _w4a4(M=8192, nbytes=need - 1) == 5 and _w4a4(M=8192, nbytes=need) not in (0, 1, 2, 3, 5, 8)
