@@ -11,6 +11,7 @@ refused, and a missing library raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -789,18 +790,30 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _outlive(stream, *ts):
-    """Tensors allocated here for a call on another stream than the current one stay
-    allocated until that stream's work is done."""
+_HERE = contextlib.nullcontext()
+
+
+def _allocating(stream):
+    """Context in which a call on `stream` allocates: memory for another stream than the
+    current one comes from that stream's pool, where only its own earlier work (or work
+    that was recorded on it) may still use it."""
     if stream is None:
-        return
+        return _HERE
     import torch
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
-    if stream != torch.cuda.current_stream():
-        for t in ts:
-            if t is not None:
-                t.record_stream(stream)
+    return torch.cuda.stream(stream)
+
+
+def _outlive(stream, *ts):
+    """Results that a call on another stream allocated there stay allocated until the
+    current stream, where they are going to be used, is done with them."""
+    if stream is None:
+        return
+    import torch
+    for t in ts:
+        if t is not None:
+            t.record_stream(torch.cuda.current_stream())
 
 
 _stream_ws = {}
@@ -817,9 +830,11 @@ def _layer_workspace(ws, need, ref, stream, raw):
         key = (ref.device.index, raw)
         ws = _stream_ws.get(key)
         if ws is None:
-            ws = _stream_ws[key] = Workspace(0, ref.device)
+            with _allocating(stream):
+                ws = _stream_ws[key] = Workspace(0, ref.device)
     if ws.buf is None or ws.buf.numel() < need:
-        ws.ensure(max(need, 1 << 20), stream)
+        with _allocating(stream):
+            ws.ensure(max(need, 1 << 20), stream)
     return ws
 
 
@@ -845,9 +860,10 @@ def gmxfp4_quantize(x, values: bool = False, stream=None):
                           f"{list(x.stride())} of shape {list(x.shape)}")
     _on_device(x)
     lead = x.shape[:-1]
-    codes = x.new_empty(lead + (K // 2,), dtype=torch.uint8)
-    scales = codes.new_empty(lead + (K // 32,))
-    vals = x.new_empty(x.shape) if values else None
+    with _allocating(stream):
+        codes = x.new_empty(lead + (K // 2,), dtype=torch.uint8)
+        scales = codes.new_empty(lead + (K // 32,))
+        vals = x.new_empty(x.shape) if values else None
     _check(lib().gmxfp4_quantize(x.data_ptr(), dt, rows, K, ld, codes.data_ptr(), scales.data_ptr(), _addr(vals),
                                  _raw_stream(stream, x)))
     _outlive(stream, codes, scales, vals)
@@ -874,7 +890,8 @@ def gmxfp4_w4a4_grouped_gemm(a, sizes, blocks, scales, out=None, workspace: Work
     _on_device(a, sizes, blocks, scales, out)
     mine = out is None
     if mine:
-        out = a.new_empty((M, N))
+        with _allocating(stream):
+            out = a.new_empty((M, N))
     L, o = lib(), ctypes.byref(opts) if opts else None
     raw = _raw_stream(stream, a)
     ws = _layer_workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a, stream, raw)
@@ -899,8 +916,9 @@ def route_topk(logits, k: int, renormalize: bool = True, error_word=None, stream
     T, E = logits.shape
     _check_tensor(error_word, "error_word", torch.int32, (1,))
     _on_device(logits, error_word)
-    weights = logits.new_empty((T, k), dtype=torch.float32)
-    ids = logits.new_empty((T, k), dtype=torch.int32)
+    with _allocating(stream):
+        weights = logits.new_empty((T, k), dtype=torch.float32)
+        ids = logits.new_empty((T, k), dtype=torch.int32)
     _check(lib().geg_route_topk(logits.data_ptr(), dt, T, E, k, int(renormalize), weights.data_ptr(), ids.data_ptr(),
                                 _addr(error_word), _raw_stream(stream, logits)))
     _outlive(stream, weights, ids)
@@ -920,7 +938,8 @@ def route_topk_grad(dweights, logits, ids, weights, renormalize: bool = True, st
     _check_tensor(weights, "weights", torch.float32, (T, k))
     _check_tensor(dweights, "dweights", torch.float32, (T, k))
     _on_device(logits, ids, weights, dweights)
-    dlogits = logits.new_empty((T, E))
+    with _allocating(stream):
+        dlogits = logits.new_empty((T, E))
     _check(lib().geg_route_topk_grad(dweights.data_ptr(), logits.data_ptr(), dt, ids.data_ptr(), weights.data_ptr(), T,
                                      E, k, int(renormalize), dlogits.data_ptr(), _raw_stream(stream, logits)))
     _outlive(stream, dlogits)
@@ -943,8 +962,9 @@ def route_combine_grad(dout, y, row_of, weights, src_of=None, stream=None):
     _check_tensor(src_of, "src_of", torch.int32, (T * k,))
     _check_tensor(weights, "weights", torch.float32, (T, k))
     _on_device(dout, y, row_of, weights, src_of)
-    dy = y.new_empty((T * k, N))
-    dw = weights.new_empty((T, k))
+    with _allocating(stream):
+        dy = y.new_empty((T * k, N))
+        dw = weights.new_empty((T, k))
     _check(lib().geg_route_combine_grad(dout.data_ptr(), y.data_ptr(), row_of.data_ptr(), _addr(src_of),
                                         weights.data_ptr(), T, k, N, dy.data_ptr(), dw.data_ptr(),
                                         _raw_stream(stream, dout)))
@@ -968,7 +988,8 @@ def _moe_layer(nf4, x, topk_ids, topk_weights, w13, s13, w2, s2, out, workspace,
     _on_device(x, topk_ids, topk_weights, w13, s13, w2, s2, out)
     mine = out is None
     if mine:
-        out = x.new_empty((T, H))
+        with _allocating(stream):
+            out = x.new_empty((T, H))
     L = lib()
     raw = _raw_stream(stream, x)
     ws = _layer_workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x, stream, raw)
@@ -1019,6 +1040,7 @@ def _make_router_gate():
             return weights, ids
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dweights, _):
             logits, ids, weights = ctx.saved_tensors
             return route_topk_grad(dweights.contiguous(), logits, ids, weights, ctx.renormalize), None, None
@@ -1032,13 +1054,18 @@ def _make_dispatch_rows():
     class DispatchRows(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, topk_ids, E):
-            sizes, row_of, src_of, xs = route_sort(topk_ids, E, x)
+            # a workspace per stream and capture: two of these may run at once
+            _on_device(topk_ids, x)
+            need = lib().geg_route_workspace_bytes(topk_ids.shape[0], topk_ids.shape[1], E)
+            ws = _layer_workspace(None, need, topk_ids, None, _raw_stream(None, topk_ids))
+            sizes, row_of, src_of, xs = route_sort(topk_ids, E, x, workspace=ws)
             ctx.save_for_backward(row_of)
             ctx.k = topk_ids.shape[1]
             ctx.mark_non_differentiable(sizes, row_of, src_of)
             return xs, sizes, row_of, src_of
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dxs, *_):
             row_of, = ctx.saved_tensors
             return route_combine(dxs.contiguous(), row_of, None, ctx.k), None, None
@@ -1056,6 +1083,7 @@ def _make_combine_rows():
             return route_combine(y, row_of, weights, weights.shape[1])
 
         @staticmethod
+        @torch.autograd.function.once_differentiable
         def backward(ctx, dout):
             y, weights, row_of, src_of = ctx.saved_tensors
             dy, dw = route_combine_grad(dout.contiguous(), y, row_of, weights, src_of)

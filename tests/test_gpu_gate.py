@@ -207,3 +207,79 @@ def test_a_differentiable_layer_from_logits_to_loss(fmt):
     for got, want, n in ((out, ref, 4), (xg.grad, xd.grad, 7), (lg.grad, ld.grad, 5)):
         got = got.detach().double().cpu()
         assert float((got - want).norm() / want.norm()) <= n * 2.0 ** -8
+
+
+def _pipeline(geg, ops, dout):
+    """Forward and backward of the routing around experts that pass their rows on."""
+    logits, x = ops
+    w, ids = geg.route_topk(logits, 4)
+    xs, sizes, row_of, src_of = geg.dispatch_rows(x, ids, logits.shape[1])
+    out = geg.route_combine(xs, row_of, w, 4)
+    dy, dw = geg.route_combine_grad(dout, xs, row_of, w, src_of)
+    return out, sizes, dy, geg.route_topk_grad(dw, logits, ids, w)
+
+
+def _routing_case(seed, T=300, E=40, H=256):
+    g = torch.Generator().manual_seed(seed)
+    return ((torch.randn(T, E, generator=g).cuda(), torch.randn(T, H, generator=g).to(torch.bfloat16).cuda()),
+            torch.randn(T, H, generator=g).to(torch.bfloat16).cuda())
+
+
+def test_routing_in_two_captured_graphs():
+    import grouped_expert_gemm_amd as geg
+    cases = [_routing_case(s) for s in range(4)]
+    want = [[t.clone() for t in _pipeline(geg, *c)] for c in cases]
+    held = [(tuple(t.clone() for t in c[0]), c[1].clone()) for c in cases[:2]]
+    graphs, outs = [], []
+    for h in held:
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(_pipeline(geg, *h))
+        graphs.append(gr)
+    for turn in range(4):
+        for i in range(2):
+            c = cases[(turn + 2 * i) % 4]
+            for dst, src in zip((*held[i][0], held[i][1]), (*c[0], c[1])):
+                dst.copy_(src)
+            graphs[i].replay()
+        _pipeline(geg, *cases[turn])   # eager work between the replays
+        torch.cuda.synchronize()
+        for i in range(2):
+            for got, w in zip(outs[i], want[(turn + 2 * i) % 4]):
+                assert torch.equal(got, w), (turn, i)
+
+
+def test_routing_on_two_streams():
+    import grouped_expert_gemm_amd as geg
+    cases = [_routing_case(s) for s in (5, 6)]
+    want = [[t.clone() for t in _pipeline(geg, *c)] for c in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        for c, s in zip(cases, streams):
+            with torch.cuda.stream(s):
+                got.append(_pipeline(geg, *c))
+    torch.cuda.synchronize()
+    for i, outs in enumerate(got):
+        assert all(torch.equal(g, w) for g, w in zip(outs, want[i % 2])), i
+    # a stream given by hand: allocated there, usable here after a wait
+    logits, s = cases[0][0][0], streams[0]
+    s.wait_stream(torch.cuda.current_stream())
+    w, ids = geg.route_topk(logits, 4, stream=s)
+    dl = geg.route_topk_grad(torch.ones_like(w), logits, ids, w, stream=s.cuda_stream)
+    torch.cuda.current_stream().wait_stream(s)
+    ref, ref_ids = geg.route_topk(logits, 4)
+    assert torch.equal(w, ref) and torch.equal(ids, ref_ids)
+    # dw = 1 for all: w (1 - sum w) = w (1 - 1 up to four roundings of the sum and the division)
+    assert float(dl.abs().max()) <= 8 * 2.0 ** -24
+
+
+def test_no_second_derivative():
+    import grouped_expert_gemm_amd as geg
+    l = torch.randn(6, 8, device="cuda", requires_grad=True)
+    w, _ = geg.router_gate(l, 2)
+    g, = torch.autograd.grad((w * w).sum(), l, create_graph=True)
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(g.sum(), l)
