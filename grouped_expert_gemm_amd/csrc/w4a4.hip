@@ -157,8 +157,10 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
   const int r16 = lane & 15, grp = lane >> 4;
   const int nss = (KS + 15) / 16;   // pieces of four steps
   const int G = gridDim.x;
-  const int slot = (G % 8 == 0) ? (blockIdx.x % 8) * (G / 8) + blockIdx.x / 8 : blockIdx.x;
-  if (slot >= total) return;
+  const int P = G % 8 == 0 ? 8 : 1, step = G / P, part = blockIdx.x % P;
+  const int32_t end = (int32_t)((int64_t)total * (part + 1) / P);
+  int32_t u = (int32_t)((int64_t)total * part / P) + blockIdx.x / P;
+  if (u >= end) return;
 
   struct Tile {
     int64_t row0, n0, w0;   // first row, first column, first weight row in [E N]
@@ -260,7 +262,6 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
     for (int i = 0; i < 4; ++i) d[i] = *reinterpret_cast<const uint32_t*>(from + at + 256 * i);
   };
 
-  int32_t u = slot;
   Tile cur = tile_of(u);
   bool live = 128 * wm < cur.rows;
   int par = 0;   // scale buffer of the piece at hand
@@ -278,8 +279,8 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
   read_s(sc[0], rd_sa, slo);
 
   for (;;) {
-    const bool more = u + G < total;
-    const Tile nxt = more ? tile_of(u + G) : cur;
+    const bool more = u + step < end;
+    const Tile nxt = more ? tile_of(u + step) : cur;
     const bool nlive = more && 128 * wm < nxt.rows;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -289,7 +290,7 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
       const bool last = ss + 1 == nss;
       // Step S of the piece in buffer `L`, the next one in `L1`. A piece's scales stay in
       // registers; sw alternates between two sets, as the weights' fragments do.
-      auto step = [&](auto Sc, const uint8_t* L, const uint8_t* L1, uint8_t* L3, const uint8_t* W1, uint8_t* W2) {
+      auto one_step = [&](auto Sc, const uint8_t* L, const uint8_t* L1, uint8_t* L3, const uint8_t* W1, uint8_t* W2) {
         constexpr int S = decltype(Sc)::value;
         constexpr int c = S & 1, n = c ^ 1;
         if constexpr (S == 0) load_scales(last ? nxt : cur, !last || more, last ? 0 : ss + 1);
@@ -336,10 +337,10 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
           for (int j = 0; j < 4; ++j) sw[0][j] = sw[1][j];
         }
       };
-      step(std::integral_constant<int, 0>{}, a0, a1, a3, w0, w0);
-      step(std::integral_constant<int, 1>{}, a1, a2, a0, w1, w0);
-      step(std::integral_constant<int, 2>{}, a2, a3, a1, w1, w1);
-      step(std::integral_constant<int, 3>{}, a3, a0, a2, w0, w1);
+      one_step(std::integral_constant<int, 0>{}, a0, a1, a3, w0, w0);
+      one_step(std::integral_constant<int, 1>{}, a1, a2, a0, w1, w0);
+      one_step(std::integral_constant<int, 2>{}, a2, a3, a1, w1, w1);
+      one_step(std::integral_constant<int, 3>{}, a3, a0, a2, w0, w1);
       par ^= 1;
     }
 
@@ -382,7 +383,7 @@ __device__ __forceinline__ void w4a4_tiles(const W4A4Args& g) {
       }
     }
     if (!more) break;
-    u += G;
+    u += step;
     cur = nxt;
     live = nlive;
   }
