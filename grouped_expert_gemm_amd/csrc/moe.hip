@@ -29,14 +29,15 @@
 //
 // Both kernels together: 8 experts of 4096 x 14336, top 2, four tokens: 90 us for 542 MB
 // (6.0 TB/s, part of it from the last-level cache). 128 experts of 2048 x 768, top 8: one
-// token 13 us (21 MB), 16 tokens 54 us (219 MB); 32 experts of 2880 x 2880, top 4, MXFP4,
-// one token 20 us (53 MB). One token is
-// bound by latency and issue as much as by bytes: of 20 us about 3 pass from a kernel's
-// start until its first weights are asked for (ids, grouping), 2 until they are there and
-// 1.3 between the two kernels; 16 wavefronts pay 16 clocks of a CU for every vector
-// instruction they share. Not kept for one token: units of 32 rows without a grouping,
-// every load of a workgroup begun at its start, 16 or 8 wavefronts (16.9 and 13.4 us for
-// the MXFP4 first kernel against 13.5).
+// token 12 us (21 MB), 16 tokens 54 us (219 MB); 32 experts of 2880 x 2880, top 4, MXFP4,
+// one token 19 us (53 MB). One token is bound by latency and issue as much as by bytes:
+// two kernels each ask for their weights two microseconds after their start, wait two more
+// for the first, and lie 1.3 apart; 16 wavefronts pay 16 clocks of a CU for every vector
+// instruction they share. So nothing is grouped for one token (item q is slot q, the ids
+// stay in a register) and no unit costs a division: 21.8 -> 20.1 us in a kernel trace. Not
+// kept: units of 32 rows, and loops unrolled over a ring of loads with all of a workgroup's
+// begun at its start: 12.2 to 17 us for the MXFP4 first kernel against 12.8, the second
+// slower by 1 to 6 (instructions that run once come from memory).
 #include <algorithm>
 
 #include "geg_device.hpp"
@@ -51,7 +52,7 @@ typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 
 constexpr int MG = 4;   // most entries per item
 
-// One token: 16 wavefronts of 4 weight rows and one entry each, so that every load is out
+// One token (k <= 64): 16 wavefronts of 4 weight rows and one entry each, so that every load is out
 // as soon as possible. More: 8 wavefronts of 8 rows and up to four entries (with twice the
 // registers each; 16 would spill). Either way a unit of the first kernel is 64 rows, the
 // 32 values of a block of act.
@@ -370,46 +371,68 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
   u32x4 xp[XP];
   auto put_x = [&](int p, u32x4 v) {
     if (p < pieces) {
-      const int tok = p / (4 * C), q = p % (4 * C);   // piece q of the token: chunk q / 4, piece q % 4
+      const int tok = ONE ? 0 : p / (4 * C), q = ONE ? p : p % (4 * C);   // piece q of the token: chunk q / 4, piece q % 4
       if constexpr (F == NF4) v = bf16x8_to_f16(v, range);
       *reinterpret_cast<u32x4*>(xs + ((4 * tok + (q & 3)) * C + (q >> 2)) * 16) = v;
     }
   };
-  const int my_id = t < n ? g.ids[t] : 0;
+  // one token: every wavefront holds the k <= 64 ids
+  const int my_id = ONE ? g.ids[min(lane, n - 1)] : (t < n ? g.ids[t] : 0);
   if constexpr (XL) {
 #pragma unroll
     for (int i = 0; i < XP; ++i)
       if (t + i * MT < pieces) xp[i] = reinterpret_cast<const u32x4*>(g.x)[t + i * MT];
     for (int p = t + XP * MT; p < pieces; p += MT) put_x(p, reinterpret_cast<const u32x4*>(g.x)[p]);
   }
-  group_entries<MT, MOST>(grp, my_id, n, g.k, g.E, blockIdx.x == 0 ? g.err : nullptr);
-  const int items = grp.items;
-  if (blockIdx.x == 0 && t < kMoeMaxEntries) {
-    if (t == 0) g.plan[0] = items;
-    if (t < items) {
-      g.plan[4 + 2 * t] = grp.expert[t];
-      g.plan[4 + 2 * t + 1] = grp.first[t] | (grp.size[t] << 16);
+  int items = n;
+  if constexpr (ONE) {   // item q is slot q
+    if (blockIdx.x == 0 && t < n && (my_id < 0 || my_id >= g.E)) atomicOr(g.err, kErrBadExpertId);
+  } else {
+    group_entries<MT, MOST>(grp, my_id, n, g.k, g.E, blockIdx.x == 0 ? g.err : nullptr);
+    items = grp.items;
+    if (blockIdx.x == 0 && t < kMoeMaxEntries) {
+      if (t == 0) g.plan[0] = items;
+      if (t < items) {
+        g.plan[4 + 2 * t] = grp.expert[t];
+        g.plan[4 + 2 * t + 1] = grp.first[t] | (grp.size[t] << 16);
+      }
+      if (t < n) g.plan[4 + 2 * kMoeMaxEntries + t] = grp.ent[t];
     }
-    if (t < n) g.plan[4 + 2 * kMoeMaxEntries + t] = grp.ent[t];
   }
   const int gl = lane / LPR, li = lane % LPR;
   const uint32_t lane_off = nf4_byte_lut_lane(lane);
-  const int total = items * CI;
   const __amdgpu_buffer_rsrc_t X = mrsrc(g.x, (int64_t)g.T * H * 2);
   // The passes of this workgroup's units in turn, AHEAD of them with their codes in flight.
   Codes<F, LPR, U> pre[AHEAD];
-  int l_unit = blockIdx.x, l_c0 = 0;   // the next pass to load
+  // Units are stepped through as (item, block of act): every division less counts, as 16
+  // wavefronts make each
+  struct Unit {
+    int q, c;
+  };
+  const Unit stride{(int)gridDim.x / CI, (int)gridDim.x % CI};
+  auto advance = [&](Unit& u) {
+    u.q += stride.q;
+    u.c += stride.c;
+    if (u.c >= CI) {
+      u.c -= CI;
+      ++u.q;
+    }
+  };
+  Unit at{(int)blockIdx.x / CI, (int)blockIdx.x % CI};
+  Unit l = at;   // the next pass to load
+  int l_c0 = 0;
   auto load_next = [&](Codes<F, LPR, U>& w) {
-    if (l_unit >= total) return;
-    const int e = __builtin_amdgcn_readfirstlane(grp.expert[l_unit / CI]);
-    const __amdgpu_buffer_rsrc_t W = mrsrc(g.w13 + (int64_t)e * N * (H >> 1), N * (H >> 1));
-    const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s13, e, N, H), scale_bytes<F>(N, H));
+    if (l.q >= items) return;
+    const int e = ONE ? __builtin_amdgcn_readlane(my_id, l.q) : __builtin_amdgcn_readfirstlane(grp.expert[l.q]);
+    const bool ok = !ONE || (e >= 0 && e < g.E);   // else zeros, without an access
+    const __amdgpu_buffer_rsrc_t W = mrsrc(g.w13 + (int64_t)e * N * (H >> 1), ok ? N * (H >> 1) : 0);
+    const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s13, e, N, H), ok ? scale_bytes<F>(N, H) : 0);
     const int c = l_c0 + li;
     // chunks past the row read as zero: their offsets lie past every buffer
-    w.load(W, S, (int64_t)(l_unit % CI) * 64 + ROWS * wave, gl, H, c, c < C ? 0u : 0xFFFFFFF0u);
+    w.load(W, S, (int64_t)l.c * 64 + ROWS * wave, gl, H, c, c < C ? 0u : 0xFFFFFFF0u);
     if ((l_c0 += LPR) >= C) {
       l_c0 = 0;
-      l_unit += gridDim.x;
+      advance(l);
     }
   };
 #pragma unroll
@@ -422,16 +445,15 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
   }
   lds_barrier();
   int seq = 0;
-  for (int unit = blockIdx.x; unit < total; unit += gridDim.x, ++seq) {
-    const int q = unit / CI;
-    const int first = __builtin_amdgcn_readfirstlane(grp.first[q]);
-    const int cnt = __builtin_amdgcn_readfirstlane(grp.size[q]);
+  for (; at.q < items; advance(at), ++seq) {
+    const int first = ONE ? at.q : __builtin_amdgcn_readfirstlane(grp.first[at.q]);
+    const int cnt = ONE ? 1 : __builtin_amdgcn_readfirstlane(grp.size[at.q]);
     float(*acc)[MOST * ROWS] = lds.accs[seq & 1];
     by_entries<MOST>(cnt, [&](auto rv) {
       constexpr int RV = decltype(rv)::value;
       int tok[RV];
 #pragma unroll
-      for (int m = 0; m < RV; ++m) tok[m] = __builtin_amdgcn_readfirstlane(grp.tok[first + min(m, cnt - 1)]);
+      for (int m = 0; m < RV; ++m) tok[m] = ONE ? 0 : __builtin_amdgcn_readfirstlane(grp.tok[first + min(m, cnt - 1)]);
       float tot[U][RV];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -469,8 +491,8 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
       const uint32_t mx = max32(__float_as_uint(v) & 0x7FFFFFFFu);
       // the block's largest to [2^14, 2^15); 2^ex stays a normal fp32 value
       const int ex = max((int)(mx >> 23) - 127 - 14, -126);
-      const int64_t slot = grp.ent[first + m];
-      const int c = unit % CI;
+      const int64_t slot = ONE ? at.q : grp.ent[first + m];
+      const int c = at.c;
       const _Float16 h = (_Float16)__builtin_ldexpf(v, -ex);
       g.act[slot * g.I + ((i >> 3) * CI + c) * 8 + (i & 7)] = __builtin_bit_cast(uint16_t, h);
       if (i == 0) g.act_scale[slot * CI + c] = __uint_as_float((uint32_t)(ex + 127) << 23);
@@ -505,33 +527,57 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
   const int gl = lane / LPR, li = lane % LPR;
   const uint32_t lane_off = nf4_byte_lut_lane(lane);
   const int RB = g.rb, subs = RB / ROWS;
-  const int items = g.plan[0];
-  for (int i = t; i < 2 * n; i += MT) lds.item[i] = g.plan[4 + i];
-  if (t < n) {
-    // places past the last hold nothing: any entry will do
-    const int f = min((uint32_t)g.plan[4 + 2 * kMoeMaxEntries + t], (uint32_t)(n - 1));
-    lds.ent[t] = f;
-    lds.tok[t] = f / g.k;
-    lds.weight[t] = g.weights[f];
+  int items = n, my_id = 0;
+  float my_weight = 0.f;
+  uint64_t valid = 0;
+  if constexpr (ONE) {   // item q is slot q; every wavefront holds the k <= 64 ids and weights
+    my_id = g.ids[min(lane, n - 1)];
+    my_weight = g.weights[min(lane, n - 1)];
+    valid = __builtin_amdgcn_ballot_w64(my_id >= 0 && my_id < g.E);
+  } else {
+    items = g.plan[0];
+    for (int i = t; i < 2 * n; i += MT) lds.item[i] = g.plan[4 + i];
+    if (t < n) {
+      // places past the last hold nothing: any entry will do
+      const int f = min((uint32_t)g.plan[4 + 2 * kMoeMaxEntries + t], (uint32_t)(n - 1));
+      lds.ent[t] = f;
+      lds.tok[t] = f / g.k;
+      lds.weight[t] = g.weights[f];
+    }
+    lds_barrier();
   }
-  lds_barrier();
   const int64_t blocks = (H + RB - 1) / RB;
   const int works = items * subs;
   // the passes of this wavefront's pieces of work, block by block
   Codes<F, LPR, U> pre[AHEAD];
+  struct Work {
+    int q, sub;   // item, ROWS rows of the block
+  };
+  const Work stride{MW / subs, MW % subs}, w0{wave / subs, wave % subs};
+  auto advance = [&](Work& w) {
+    w.q += stride.q;
+    w.sub += stride.sub;
+    if (w.sub >= subs) {
+      w.sub -= subs;
+      ++w.q;
+    }
+  };
   int64_t l_b = blockIdx.x;
-  int l_wk = wave, l_c0 = 0;
+  Work l = w0;
+  int l_c0 = 0;
   auto load_next = [&](Codes<F, LPR, U>& w) {
     if (l_b >= blocks || wave >= works) return;
-    const int e = __builtin_amdgcn_readfirstlane(lds.item[2 * (l_wk / subs)]);
-    const __amdgpu_buffer_rsrc_t W = mrsrc(g.w2 + (int64_t)e * H * (K >> 1), H * (K >> 1));
-    const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s2, e, H, K), scale_bytes<F>(H, K));
+    const int e = ONE ? __builtin_amdgcn_readlane(my_id, l.q) : __builtin_amdgcn_readfirstlane(lds.item[2 * l.q]);
+    const bool ok = !ONE || (valid >> l.q) & 1;   // else zeros, without an access
+    const __amdgpu_buffer_rsrc_t W = mrsrc(g.w2 + (int64_t)e * H * (K >> 1), ok ? H * (K >> 1) : 0);
+    const __amdgpu_buffer_rsrc_t S = mrsrc(expert_scales<F>(g.s2, e, H, K), ok ? scale_bytes<F>(H, K) : 0);
     const int c = l_c0 + li;
-    w.load(W, S, l_b * RB + (l_wk % subs) * ROWS, gl, K, c, c < C ? 0u : 0xFFFFFFF0u);
+    w.load(W, S, l_b * RB + l.sub * ROWS, gl, K, c, c < C ? 0u : 0xFFFFFFF0u);
     if ((l_c0 += LPR) >= C) {
       l_c0 = 0;
-      if ((l_wk += MW) >= works) {
-        l_wk = wave;
+      advance(l);
+      if (l.q >= items) {
+        l = w0;
         l_b += gridDim.x;
       }
     }
@@ -542,10 +588,10 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
   if constexpr (F == NF4) nf4_byte_lut_fill<64, MT>(blut);
   lds_barrier();
   for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-    for (int wk = wave; wk < works; wk += MW) {
-      const int q = wk / subs, sub = wk % subs;
-      const int fc = __builtin_amdgcn_readfirstlane(lds.item[2 * q + 1]);
-      const int first = fc & 0xFFFF, cnt = fc >> 16;
+    for (Work wk = w0; wk.q < items; advance(wk)) {
+      const int sub = wk.sub;
+      const int fc = ONE ? 0 : __builtin_amdgcn_readfirstlane(lds.item[2 * wk.q + 1]);
+      const int first = ONE ? wk.q : fc & 0xFFFF, cnt = ONE ? (int)((valid >> wk.q) & 1) : fc >> 16;
       by_entries<MOST>(cnt, [&](auto rv) {
         constexpr int RV = decltype(rv)::value;
         float tot[U][RV];
@@ -560,7 +606,7 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
           float xs[RV];
 #pragma unroll
           for (int m = 0; m < RV; ++m) {
-            const int64_t f = __builtin_amdgcn_readfirstlane(lds.ent[first + min(m, cnt - 1)]);
+            const int64_t f = ONE ? first : __builtin_amdgcn_readfirstlane(lds.ent[first + min(m, cnt - 1)]);
             a[m] = reinterpret_cast<const u32x4*>(g.act + f * K);
             xs[m] = g.act_scale[f * C + cc];
           }
@@ -570,8 +616,12 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
           dot_pass<F, NF4>(w, [&](int j, int m) -> u32x4 { return a[m][j * C + cc]; }, xs, blut, lane_off, tot);
         }
         sum_lanes<LPR, U, RV>(tot, lane, [&](int row, int m, float v) {
-          if (m < cnt)
+          if constexpr (ONE) {
+            const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_weight), first));
+            if (cnt) lds.outs[wave][sub * ROWS + row] += w * v;
+          } else if (m < cnt) {
             lds.outs[wave][(sub * ROWS + row) * T + lds.tok[first + m]] += lds.weight[first + m] * v;
+          }
         });
       });
     }
@@ -637,7 +687,7 @@ hipError_t layer(const MoeArgs& g, int cus, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_moe_layer(int fmt, const MoeArgs& g, int cus, hipStream_t s) {
-  if (g.T == 1) return fmt == NF4 ? layer<NF4, true>(g, cus, s) : layer<MXFP4, true>(g, cus, s);
+  if (g.T == 1 && g.k <= 64) return fmt == NF4 ? layer<NF4, true>(g, cus, s) : layer<MXFP4, true>(g, cus, s);
   return fmt == NF4 ? layer<NF4, false>(g, cus, s) : layer<MXFP4, false>(g, cus, s);
 }
 

@@ -131,6 +131,31 @@ def test_ids_outside_the_experts_are_dropped_and_flagged(fmt):
     assert bool((_call(none) == 0).all())
 
 
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 64, 64, 64, 64), (1, 65, 80, 128, 64), (1, 256, 300, 64, 64),
+                                       (1, 8, 1024, 64, 128), (16, 16, 1024, 64, 64), (1, 3, 4, 6208, 4160),
+                                       (1, 1, 1, 71744, 64), (2, 2, 3, 35904, 64)])
+def test_most_entries_experts_and_tokens_past_the_staging(fmt, T, k, E, H, I):
+    _check(_case(fmt, T, k, E, H, I))
+
+
+@pytest.mark.parametrize("k", [5, 70])
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+def test_one_token_with_dropped_ids(fmt, k):
+    import grouped_expert_gemm_amd as geg
+    rng = np.random.default_rng(k)
+    c = _case(fmt, 1, k, 6, 256, 192, ids=[rng.integers(-2, 9, k)])
+    c["ids"][0, :4] = torch.tensor([6, 0, -1, 1 << 30])
+    ws = geg.Workspace(1 << 20)
+    ws.buf[256:] = 255   # act that nobody writes would be NaN
+    got = _call(c, workspace=ws)
+    assert ws.read_error() == geg.DEVERR_BAD_EXPERT_ID
+    ref, tol = _reference(c)
+    assert np.all(np.abs(got.double().cpu().numpy() - ref) <= tol)
+    none = _case(fmt, 1, k, 6, 256, 192, ids=[[-1] * k])
+    assert bool((_call(none, workspace=ws) == 0).all())
+
+
 def test_nf4_fp16_overflow_is_flagged():
     import grouped_expert_gemm_amd as geg
     for H in (256, 4096):                  # tokens staged in LDS, and read from memory
