@@ -254,3 +254,15 @@ def test_gate_and_layer_agree_with_the_large_batch_path(fmt):
     ref = geg.route_combine(block(xs, sizes, *d), row_of, weights, 4).double()
     # that path rounds act and each expert's output to bf16 as well
     assert float((got - ref).norm() / ref.norm()) <= 3 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("T", [1, 5])
+def test_mxfp4_scales_at_any_byte(T):
+    c = _case("mxfp4", T, 2, 4, 288, 96)
+    want = _call(c)
+    for shift in (1, 2, 3):
+        d = dict(c)
+        for name in ("s13", "s2"):
+            s = torch.zeros(c[name].size + shift, dtype=torch.uint8, device="cuda")[shift:].view(c[name].shape)
+            d[name] = s.copy_(torch.tensor(c[name]))
+        assert torch.equal(_call(d), want), shift

@@ -204,3 +204,30 @@ def test_quantised_values_through_the_plain_mxfp4_gemm_agree():
     for path in (0, TILES, NARROW):
         # two roundings to bf16 and the sums of both
         assert np.all(np.abs(_call(c, path).double().cpu().numpy() - ref) <= 2 * tol)
+
+
+@pytest.mark.parametrize("N,K", [(64, 288), (71, 2080), (256, 512)])
+@pytest.mark.parametrize("path", [TILES, NARROW])
+def test_scales_at_any_byte_and_an_output_at_any_pair(path, N, K):
+    import grouped_expert_gemm_amd as geg
+    c = _case([4, 0, 21], N, K)
+    want = _check(c, path)
+    M, n = len(want), c["s"].size
+    for shift in (1, 2, 3, 7):
+        s = torch.zeros(n + shift, dtype=torch.uint8, device="cuda")[shift:].view(c["s"].shape)
+        s.copy_(torch.tensor(c["s"]))
+        buf = torch.full((M * N + 2 * shift + 2,), 5.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[2 * shift:2 * shift + M * N].view(M, N)
+        geg.gmxfp4_w4a4_grouped_gemm(c["a"].cuda(), c["sizes"].cuda(), torch.tensor(c["w"]).cuda(), s, out=out,
+                                     opts=geg.Opts(path, 0))
+        assert np.array_equal(out.double().cpu().numpy(), want), shift
+        assert bool((buf[:2 * shift] == 5).all()) and bool((buf[-2:] == 5).all())
+
+
+@pytest.mark.parametrize("path", [TILES, NARROW])
+def test_many_experts_few_of_them_with_rows(path):
+    sizes = np.zeros(1024, int)
+    sizes[[0, 3, 511, 1023]] = 2, 19, 1, 5
+    c = _case(sizes.tolist(), 40, 320)
+    got = _check(c, path)
+    assert np.array_equal(_call(c, path, cu_limit=1).double().cpu().numpy(), got)
