@@ -30,13 +30,13 @@
 // Both kernels together: 8 experts of 4096 x 14336, top 2, four tokens: 90 us for 542 MB
 // (6.0 TB/s, part of it from the last-level cache). 128 experts of 2048 x 768, top 8: one
 // token 12 us (21 MB), 16 tokens 54 us (219 MB); 32 experts of 2880 x 2880, top 4, MXFP4,
-// one token 19 us (53 MB). One token is bound by latency and issue as much as by bytes:
+// one token 18 us (53 MB). One token is bound by latency and issue as much as by bytes:
 // two kernels each ask for their weights two microseconds after their start, wait two more
 // for the first, and lie 1.3 apart; 16 wavefronts pay 16 clocks of a CU for every vector
 // instruction they share. So nothing is grouped for one token (item q is slot q, the ids
 // stay in a register) and no unit costs a division: 21.8 -> 20.1 us in a kernel trace. Not
 // kept: units of 32 rows, and loops unrolled over a ring of loads with all of a workgroup's
-// begun at its start: 12.2 to 17 us for the MXFP4 first kernel against 12.8, the second
+// begun at its start: 12.2 to 17 us for the MXFP4 first kernel against 12.8 then, the second
 // slower by 1 to 6 (instructions that run once come from memory).
 #include <algorithm>
 
@@ -52,10 +52,9 @@ typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
 
 constexpr int MG = 4;   // most entries per item
 
-// One token (k <= 64): 16 wavefronts of 4 weight rows and one entry each, so that every load is out
-// as soon as possible. More: 8 wavefronts of 8 rows and up to four entries (with twice the
-// registers each; 16 would spill). Either way a unit of the first kernel is 64 rows, the
-// 32 values of a block of act.
+// Workgroups of the second kernel. One token (k <= 64): 16 wavefronts of 4 weight rows and
+// one entry each, so that every load is out as soon as possible. More: 8 wavefronts of 8
+// rows and up to four entries (with twice the registers each; 16 would spill).
 template <bool ONE>
 struct Shape {
   static constexpr int kMT = ONE ? 1024 : 512;   // threads per workgroup
@@ -63,7 +62,20 @@ struct Shape {
   static constexpr int kRows = ONE ? 4 : 8;      // weight rows per wavefront
   static constexpr int kMost = ONE ? 1 : MG;     // entries taken at once
   static constexpr int kAhead = ONE ? 3 : 1;     // passes whose codes are in flight
-  static_assert(kMW * kRows == 64, "a unit makes one block of act");
+};
+// Of the first, whose units are 64 rows, the 32 values of a block of act. The same, but for
+// one token in MXFP4 two workgroups of 8 wavefronts share a CU: a unit past one per CU then
+// runs beside another instead of after it (360 units of 2880: 11.1-11.9 us, 12.7 in workgroups
+// of 16; NF4's table leaves no room for a second: 8.0 against 6.9 for 192 units).
+template <Fmt F, bool ONE>
+struct UpShape {
+  static constexpr bool kTwo = ONE && F == MXFP4;
+  static constexpr int kMT = ONE && !kTwo ? 1024 : 512;
+  static constexpr int kMW = kMT / 64;
+  static constexpr int kRows = 64 / kMW;
+  static constexpr int kMost = ONE ? 1 : MG;
+  static constexpr int kAhead = ONE && !kTwo ? 3 : 1;
+  static constexpr int kWavesPerSimd = kTwo ? 4 : kMT / 256;
 };
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t mrsrc(const void* base, int64_t bytes) {
@@ -332,8 +344,8 @@ __device__ __forceinline__ int64_t scale_bytes(int64_t N, int64_t K) {
 // The staged tokens: chunk c of token t as four 16-byte pieces, piece j at
 // ((4 t + j) C + c) 16 bytes, so that the lanes of a wavefront (consecutive chunks)
 // read consecutive pieces.
-template <Fmt F>
-constexpr int x_lds_bytes() { return F == NF4 ? 64 << 10 : 140 << 10; }
+template <Fmt F, bool ONE>
+constexpr int x_lds_bytes() { return F == NF4 || ONE ? 64 << 10 : 140 << 10; }
 
 // First kernel. Units (item, 64 rows of its gate/up weight = 32 values of act) over a grid
 // of one workgroup per CU; a wavefront's codes of the next unit are
@@ -344,14 +356,14 @@ constexpr int x_lds_bytes() { return F == NF4 ? 64 << 10 : 140 << 10; }
 // ((j (I / 32) + c) 8 + b): the order in which the second kernel's lanes read it).
 // Workgroup 0 also writes the grouping.
 template <Fmt F, int LPR, bool XL, bool ONE>
-__global__ __launch_bounds__(Shape<ONE>::kMT) void moe_up_kernel(MoeArgs g) {
-  constexpr int MT = Shape<ONE>::kMT, MW = Shape<ONE>::kMW, ROWS = Shape<ONE>::kRows, MOST = Shape<ONE>::kMost;
-  constexpr int AHEAD = Shape<ONE>::kAhead;
+__global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPerSimd)) void moe_up_kernel(MoeArgs g) {
+  using Form = UpShape<F, ONE>;
+  constexpr int MT = Form::kMT, MW = Form::kMW, ROWS = Form::kRows, MOST = Form::kMost, AHEAD = Form::kAhead;
   constexpr int G = 64 / LPR, U = ROWS / G;
   // the byte table first: at LDS address 0 a code byte's address needs no base added
   __shared__ struct __attribute__((aligned(16))) {
     uint32_t blut[F == NF4 ? kNf4ByteLutWords : 4];
-    uint8_t xs[XL ? x_lds_bytes<F>() : 16];
+    uint8_t xs[XL ? x_lds_bytes<F, ONE>() : 16];
     Groups grp;
     float accs[2][MW][MOST * ROWS];
   } lds;
@@ -644,8 +656,8 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
 
 template <Fmt F, int LPR, bool ONE>
 hipError_t up(const MoeArgs& g, int cus, hipStream_t s) {
-  const dim3 grid((unsigned)cus), block(Shape<ONE>::kMT);
-  if ((int64_t)g.T * g.H * 2 <= x_lds_bytes<F>())
+  const dim3 grid((unsigned)(UpShape<F, ONE>::kTwo ? 2 * cus : cus)), block(UpShape<F, ONE>::kMT);
+  if ((int64_t)g.T * g.H * 2 <= x_lds_bytes<F, ONE>())
     hipLaunchKernelGGL((moe_up_kernel<F, LPR, true, ONE>), grid, block, 0, s, g);
   else
     hipLaunchKernelGGL((moe_up_kernel<F, LPR, false, ONE>), grid, block, 0, s, g);
@@ -665,23 +677,24 @@ hipError_t down(MoeArgs g, int cus, hipStream_t s) {
   return hipGetLastError();
 }
 
-// f(LPR) with the lanes per weight row for a contraction of K (C chunks): the number that
-// leaves the fewest lanes idle over the row's passes, the larger on a tie (90 chunks: three
-// passes of 32 lanes; two of 64 would idle 38 of 128).
-template <typename Fn>
+// f(LPR) with the lanes per weight row for a contraction of K (C chunks): the number up to
+// MOST that leaves the fewest lanes idle over the row's passes, the larger on a tie (90
+// chunks: three passes of 32 lanes; two of 64 would idle 38 of 128).
+template <int MOST, typename Fn>
 hipError_t by_lanes(int64_t K, Fn f) {
   const int64_t C = K >> 5;
   auto lanes = [&](int64_t l) { return (C + l - 1) / l * l; };
-  if (lanes(64) <= lanes(32) && lanes(64) <= lanes(16)) return f(std::integral_constant<int, 64>{});
+  if constexpr (MOST >= 64)
+    if (lanes(64) <= lanes(32) && lanes(64) <= lanes(16)) return f(std::integral_constant<int, 64>{});
   if (lanes(32) <= lanes(16)) return f(std::integral_constant<int, 32>{});
   return f(std::integral_constant<int, 16>{});
 }
 
 template <Fmt F, bool ONE>
 hipError_t layer(const MoeArgs& g, int cus, hipStream_t s) {
-  const hipError_t e = by_lanes(g.H, [&](auto l) { return up<F, decltype(l)::value, ONE>(g, cus, s); });
+  const hipError_t e = by_lanes<UpShape<F, ONE>::kTwo ? 32 : 64>(g.H, [&](auto l) { return up<F, decltype(l)::value, ONE>(g, cus, s); });
   if (e != hipSuccess) return e;
-  return by_lanes(g.I, [&](auto l) { return down<F, decltype(l)::value, ONE>(g, cus, s); });
+  return by_lanes<64>(g.I, [&](auto l) { return down<F, decltype(l)::value, ONE>(g, cus, s); });
 }
 
 }  // namespace
