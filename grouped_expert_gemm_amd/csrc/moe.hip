@@ -17,8 +17,8 @@
 // row and pass, against the tokens' same 32 values with packed fp32-accumulated dot
 // products. NF4 codes go through the byte table in LDS (two fp16 values per 32-bit
 // read), MXFP4 through the scaled fp4 conversion; the block scale multiplies the
-// chunk's fp32 dot product. One workgroup per CU shares the table, the grouping and the
-// staged tokens.
+// chunk's fp32 dot product. A workgroup shares the table, the grouping and the staged
+// tokens.
 //
 // act goes from one kernel to the other as fp16 with a power-of-two scale per 32 values
 // that puts the block's largest in [2^14, 2^15): 11 bits for everything within 2^-29 of
@@ -348,8 +348,8 @@ template <Fmt F, bool ONE>
 constexpr int x_lds_bytes() { return F == NF4 || ONE ? 64 << 10 : 140 << 10; }
 
 // First kernel. Units (item, 64 rows of its gate/up weight = 32 values of act) over a grid
-// of one workgroup per CU; a wavefront's codes of the next unit are
-// in flight while it works on this one. x is staged in LDS when all tokens fit (XL), as
+// of one or two workgroups per CU; a wavefront's codes of the next pass are in flight
+// while it works on this one. x is staged in LDS when all tokens fit (XL), as
 // fp16 for NF4 (flagged when it overflows; MXFP4 keeps bf16, exact), else each lane loads
 // its slice from memory. The sums meet in LDS, where a half wavefront per entry forms the
 // 32 act values, their scale and their fp16 form (value i = 32 c + 8 j + b of a row at
