@@ -765,15 +765,15 @@ def _on_device(ref, *ts):
     """Every tensor on ref's device, and that the current one: kernels launch on the
     current device's streams."""
     import torch
-    dev = ref.device
-    if dev.type != "cuda":
+    dev = ref.get_device()   # -1 unless on a GPU
+    if dev < 0:
         _require_gpu(ref)
     for t in ts:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != dev:
             _require_gpu(t)
-            raise GegError(4, f"tensors on several devices: {dev} and {t.device}")
-    if dev.index != torch._C._cuda_getDevice():
-        raise GegError(4, f"tensors are on {dev} but the current device is "
+            raise GegError(4, f"tensors on several devices: {ref.device} and {t.device}")
+    if dev != torch._C._cuda_getDevice():
+        raise GegError(4, f"tensors are on {ref.device} but the current device is "
                           f"cuda:{torch.cuda.current_device()}: call under torch.cuda.device(...)")
 
 
@@ -782,7 +782,7 @@ def _raw_stream(stream, ref):
     (read without building a torch.cuda.Stream, which costs as much as a launch)."""
     if stream is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(ref.device.index)
+        return torch._C._cuda_getCurrentRawStream(ref.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -827,7 +827,7 @@ def _layer_workspace(ws, need, ref, stream, raw):
     if ws is None:
         if torch.cuda.is_current_stream_capturing():
             return Workspace(need, ref.device)
-        key = (ref.device.index, raw)
+        key = (ref.get_device(), raw)
         ws = _stream_ws.get(key)
         if ws is None:
             with _allocating(stream):
