@@ -651,7 +651,7 @@ hipError_t launch_w4a4_narrow(const W4A4Args& g, int rb, int cus, hipStream_t s)
   constexpr std::integral_constant<int, 1> one{};
   constexpr std::integral_constant<int, 2> two{};
   if (g.aq) return rb == 2 ? run(two, std::true_type{}) : run(one, std::true_type{});
-  return rb == 2 ? run(two, std::false_type{}) : run(one, std::false_type{});
+  return run(one, std::false_type{});   // no more rows than experts: one block of 16
 }
 
 hipError_t launch_w4a4_quantize(const uint16_t* a, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, uint32_t* err,
