@@ -20,6 +20,10 @@
 // chunk's fp32 dot product. A workgroup shares the table, the grouping and the staged
 // tokens.
 //
+// NF4 multiplies fp16 values: each token is first multiplied by a power of two that puts its
+// largest magnitude in [2^14, 2^15) and the sums by the inverse, both exact, so that no token
+// under- or overflows, whatever its scale. MXFP4 multiplies bf16 as it is.
+//
 // act goes from one kernel to the other as fp16 with a power-of-two scale per 32 values
 // that puts the block's largest in [2^14, 2^15): 11 bits for everything within 2^-29 of
 // it, whatever the layer's scale, and a lane's 32 values are one such block, so the
@@ -119,6 +123,37 @@ __device__ __forceinline__ uint32_t max32(uint32_t v) {
   const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
   const uint32_t x = r[0], y = r[1];
   return max(x, y);
+}
+
+// Largest |x| of 8 bf16 values, as its bits.
+__device__ __forceinline__ uint32_t max_abs8(const u32x4& x) {
+  u16x2 m = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = x[i] & 0x7FFF7FFFu;
+    m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, w));
+  }
+  const uint16_t lo = m[0], hi = m[1];
+  return max((uint32_t)lo, (uint32_t)hi);
+}
+
+// The exponent ex for which bf16 magnitudes of at most `mx` times 2^-ex lie below 2^15, the
+// largest at 2^14 or more; 2^ex and 2^-ex are normal fp32 values. (inf and NaN stay so.)
+__device__ __forceinline__ int fit_exponent(uint32_t mx) { return max((int)(mx >> 7) - 127 - 14, -126); }
+__device__ __forceinline__ float pow2(int ex) { return __uint_as_float((uint32_t)(ex + 127) << 23); }
+constexpr uint32_t kBf16PastF16 = 0x4780;   // 65536, the smallest bf16 magnitude past fp16's range
+
+// 8 bf16 values times m as fp16, natural order.
+__device__ __forceinline__ u32x4 bf16x8_times_to_f16(const u32x4& x, float m) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f16x2 h;
+    h[0] = (_Float16)(__uint_as_float(x[i] << 16) * m);
+    h[1] = (_Float16)(__uint_as_float(x[i] & 0xFFFF0000u) * m);
+    r[i] = __builtin_bit_cast(uint32_t, h);
+  }
+  return r;
 }
 
 // Grouping of the T k entries by expert, in LDS. An entry's place is the number of
@@ -349,12 +384,15 @@ constexpr int x_lds_bytes() { return F == NF4 || ONE ? 64 << 10 : 140 << 10; }
 
 // First kernel. Units (item, 64 rows of its gate/up weight = 32 values of act) over a grid
 // of one or two workgroups per CU; a wavefront's codes of the next pass are in flight
-// while it works on this one. x is staged in LDS when all tokens fit (XL), as
-// fp16 for NF4 (flagged when it overflows; MXFP4 keeps bf16, exact), else each lane loads
-// its slice from memory. The sums meet in LDS, where a half wavefront per entry forms the
-// 32 act values, their scale and their fp16 form (value i = 32 c + 8 j + b of a row at
-// ((j (I / 32) + c) 8 + b): the order in which the second kernel's lanes read it).
-// Workgroup 0 also writes the grouping.
+// while it works on this one. x is staged in LDS when all tokens fit (XL), else each lane loads
+// its slice from memory. For NF4 every workgroup finds the tokens' largest magnitudes before it
+// scales them: from the registers they pass through on their way into LDS (0.4 us for one
+// token, nothing at 16 of 2048, where a second pass over LDS cost 3.7), or in a pass of its
+// own over tokens that are not staged (1.9 us for 16 of 4096). Workgroup 0 flags what plain
+// fp16 could not hold. The sums meet in LDS, where a half wavefront per entry forms the 32 act
+// values, their scale and their fp16 form (value i = 32 c + 8 j + b of a row at
+// ((j (I / 32) + c) 8 + b): the order in which the second kernel's lanes read it). Workgroup 0
+// also writes the grouping.
 template <Fmt F, int LPR, bool XL, bool ONE>
 __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPerSimd)) void moe_up_kernel(MoeArgs g) {
   using Form = UpShape<F, ONE>;
@@ -366,6 +404,7 @@ __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPer
     uint8_t xs[XL ? x_lds_bytes<F, ONE>() : 16];
     Groups grp;
     float accs[2][MW][MOST * ROWS];
+    uint32_t xmax[F == NF4 ? kMoeMaxTokens : 4];   // NF4: the tokens' largest |x|, as bf16 bits
   } lds;
   uint32_t* const blut = lds.blut;
   uint8_t* const xs = lds.xs;
@@ -375,16 +414,19 @@ __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPer
   const int C = (int)(H >> 5), CI = (int)(g.I >> 5);
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  uint32_t range = 0;
+  if constexpr (F == NF4) {
+    if (t < kMoeMaxTokens) lds.xmax[t] = 0;
+    if constexpr (ONE) lds_barrier();   // else the grouping's barriers come before its first use
+  }
   // The tokens' loads go out before the weights' (loads complete in order): the first XP
-  // pieces of 8 values per thread wait in registers, more are stored right away.
-  constexpr int XP = 4;
+  // pieces of 8 values per thread wait in registers (NF4: all), more are stored right away.
+  constexpr int XP = F == NF4 ? x_lds_bytes<F, ONE>() / (16 * MT) : 4;
+  static_assert(F != NF4 || XP * 16 * MT == x_lds_bytes<F, ONE>(), "every staged piece of an NF4 call has a register");
   const int pieces = g.T * 4 * C;
   u32x4 xp[XP];
   auto put_x = [&](int p, u32x4 v) {
     if (p < pieces) {
       const int tok = ONE ? 0 : p / (4 * C), q = ONE ? p : p % (4 * C);   // piece q of the token: chunk q / 4, piece q % 4
-      if constexpr (F == NF4) v = bf16x8_to_f16(v, range);
       *reinterpret_cast<u32x4*>(xs + ((4 * tok + (q & 3)) * C + (q >> 2)) * 16) = v;
     }
   };
@@ -394,7 +436,8 @@ __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPer
 #pragma unroll
     for (int i = 0; i < XP; ++i)
       if (t + i * MT < pieces) xp[i] = reinterpret_cast<const u32x4*>(g.x)[t + i * MT];
-    for (int p = t + XP * MT; p < pieces; p += MT) put_x(p, reinterpret_cast<const u32x4*>(g.x)[p]);
+    if constexpr (F != NF4)
+      for (int p = t + XP * MT; p < pieces; p += MT) put_x(p, reinterpret_cast<const u32x4*>(g.x)[p]);
   }
   int items = n;
   if constexpr (ONE) {   // item q is slot q
@@ -451,21 +494,75 @@ __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPer
   for (int i = 0; i < AHEAD; ++i) load_next(pre[i]);
   // the table and the tokens while the first weights are on their way
   if constexpr (F == NF4) nf4_byte_lut_fill<64, MT>(blut);
-  if constexpr (XL) {
+  if constexpr (XL && F == NF4) {
+    // token and place of each piece; H % 64 == 0, so eight adjacent lanes hold pieces of one token
+    int tok[XP], q[XP];
+    const int dt = ONE ? 0 : MT / (4 * C), dq = MT - dt * 4 * C;
+    tok[0] = ONE ? 0 : t / (4 * C), q[0] = t - tok[0] * 4 * C;
+#pragma unroll
+    for (int i = 1; i < XP; ++i) {
+      const bool over = !ONE && q[i - 1] + dq >= 4 * C;
+      tok[i] = tok[i - 1] + dt + over;
+      q[i] = q[i - 1] + dq - (over ? 4 * C : 0);
+    }
+#pragma unroll
+    for (int i = 0; i < XP; ++i)
+      if (t + i * MT < pieces) {
+        uint32_t mx = max_abs8(xp[i]);
+        mx = max(mx, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mx, 0xB1, 0xF, 0xF, false));    // lane ^ 1
+        mx = max(mx, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mx, 0x4E, 0xF, 0xF, false));    // lane ^ 2
+        mx = max(mx, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mx, 0x141, 0xF, 0xF, false));   // 7 - lane
+        if ((lane & 7) == 0) atomicMax(&lds.xmax[tok[i]], mx);   // a maximum: the same in any order
+      }
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < XP; ++i)
+      if (t + i * MT < pieces)
+        *reinterpret_cast<u32x4*>(xs + ((4 * tok[i] + (q[i] & 3)) * C + (q[i] >> 2)) * 16) =
+            bf16x8_times_to_f16(xp[i], pow2(-fit_exponent(lds.xmax[tok[i]])));
+  } else if constexpr (XL) {
 #pragma unroll
     for (int i = 0; i < XP; ++i) put_x(t + i * MT, xp[i]);
+  } else if constexpr (F == NF4) {
+    constexpr int UN = 8;   // pieces per lane in flight
+    const int runs = (4 * C + 64 * UN - 1) / (64 * UN);
+    for (int r = wave; r < g.T * runs; r += MW) {
+      const int tok = r / runs, p0 = (r - tok * runs) * 64 * UN + lane;
+      u32x4 v[UN];
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        v[i] = u32x4{0, 0, 0, 0};
+        if (p0 + 64 * i < 4 * C) v[i] = reinterpret_cast<const u32x4*>(g.x)[(int64_t)tok * 4 * C + p0 + 64 * i];
+      }
+      uint32_t mx = 0;
+#pragma unroll
+      for (int i = 0; i < UN; ++i) mx = max(mx, max_abs8(v[i]));
+      mx = max32(mx);
+      if ((lane & 31) == 0) atomicMax(&lds.xmax[tok], mx);
+    }
   }
   lds_barrier();
+  if constexpr (F == NF4) {
+    if (blockIdx.x == 0 && t < g.T && lds.xmax[t] >= kBf16PastF16) atomicOr(g.err, kErrFp16Range);
+  }
   int seq = 0;
   for (; at.q < items; advance(at), ++seq) {
     const int first = ONE ? at.q : __builtin_amdgcn_readfirstlane(grp.first[at.q]);
     const int cnt = ONE ? 1 : __builtin_amdgcn_readfirstlane(grp.size[at.q]);
     float(*acc)[MOST * ROWS] = lds.accs[seq & 1];
+    // two wavefronts, others from unit to unit, form the block of act: 32 lanes per entry
+    const int m = ((wave - 2 * seq) & (MW - 1)) * 2 + (lane >> 5), i = lane & 31;
+    float back = 1.f;
+    if constexpr (F == NF4) back = pow2(fit_exponent(lds.xmax[ONE ? 0 : grp.tok[min(first + m, n - 1)]]));
     by_entries<MOST>(cnt, [&](auto rv) {
       constexpr int RV = decltype(rv)::value;
       int tok[RV];
 #pragma unroll
       for (int m = 0; m < RV; ++m) tok[m] = ONE ? 0 : __builtin_amdgcn_readfirstlane(grp.tok[first + min(m, cnt - 1)]);
+      float fit[RV];   // of a token's values that were not staged
+#pragma unroll
+      for (int m = 0; m < RV; ++m)
+        fit[m] = F == NF4 && !XL ? pow2(-fit_exponent(__builtin_amdgcn_readfirstlane(lds.xmax[tok[m]]))) : 1.f;
       float tot[U][RV];
 #pragma unroll
       for (int u = 0; u < U; ++u)
@@ -486,7 +583,7 @@ __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPer
               } else {
                 u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(
                     X, (uint32_t)(((int64_t)tok[m] * H + 32 * c) * 2 + 16 * j) | off_mask, 0, 0);
-                if constexpr (F == NF4) v = bf16x8_to_f16(v, range);
+                if constexpr (F == NF4) v = bf16x8_times_to_f16(v, fit[m]);
                 return v;
               }
             },
@@ -495,11 +592,9 @@ __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPer
       sum_lanes<LPR, U, RV>(tot, lane, [&](int row, int m, float v) { acc[wave][m * ROWS + row] = v; });
     });
     lds_barrier();   // the sums of this unit; the other parity's are free again after the next one
-    // two wavefronts, others from unit to unit, form the block of act: 32 lanes per entry
-    const int m = ((wave - 2 * seq) & (MW - 1)) * 2 + (lane >> 5), i = lane & 31;
     if (m < cnt) {
       const float* a = acc[2 * i / ROWS] + m * ROWS + 2 * i % ROWS;
-      const float v = swiglu(a[0], a[1]);
+      const float v = F == NF4 ? swiglu(a[0] * back, a[1] * back) : swiglu(a[0], a[1]);
       const uint32_t mx = max32(__float_as_uint(v) & 0x7FFFFFFFu);
       // the block's largest to [2^14, 2^15); 2^ex stays a normal fp32 value
       const int ex = max((int)(mx >> 23) - 127 - 14, -126);
@@ -509,9 +604,6 @@ __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPer
       g.act[slot * g.I + ((i >> 3) * CI + c) * 8 + (i & 7)] = __builtin_bit_cast(uint16_t, h);
       if (i == 0) g.act_scale[slot * CI + c] = __uint_as_float((uint32_t)(ex + 127) << 23);
     }
-  }
-  if constexpr (F == NF4) {
-    if ((blockIdx.x == 0 || !XL) && range_overflowed(range)) atomicOr(g.err, kErrFp16Range);
   }
 }
 

@@ -481,9 +481,11 @@ geg_status geg_route_combine_grad(const void* dout, const void* y, const int32_t
  * Entries whose id lies outside [0, E) are dropped and flag GEG_DEVERR_BAD_EXPERT_ID; a
  * token without any valid entry gets zeros. act is held as fp16 with a power of two per
  * 32 values (11 bits for what lies within 2^-29 of the block's largest, whatever its
- * scale); NF4 multiplies x as fp16 (GEG_DEVERR_FP16_RANGE when it overflows) and its
- * table's values as fp16, MXFP4 multiplies x and the codes exactly. Sums in fp32.
- * Deterministic.
+ * scale); NF4 multiplies x as fp16 with a power of two per token, as the tiled path does
+ * (largest magnitude in [2^14, 2^15), undone in the fp32 sums), and its table's values as
+ * fp16, MXFP4 multiplies x and the codes exactly. As on the decode paths an NF4 call flags
+ * GEG_DEVERR_FP16_RANGE for |x| > 65504 or a non-finite x, though finite ones are computed
+ * all the same. Sums in fp32. Deterministic.
  */
 size_t geg_moe_layer_workspace_bytes(int64_t T, int32_t k, int64_t I);
 geg_status gnf4_moe_layer(const void* x, const int32_t* topk_ids, const float* topk_weights, const uint8_t* w13,

@@ -266,3 +266,15 @@ def test_mxfp4_scales_at_any_byte(T):
             s = torch.zeros(c[name].size + shift, dtype=torch.uint8, device="cuda")[shift:].view(c[name].shape)
             d[name] = s.copy_(torch.tensor(c[name]))
         assert torch.equal(_call(d), want), shift
+
+
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+@pytest.mark.parametrize("T,k,E,H,I", [(1, 2, 4, 256, 128), (3, 2, 4, 320, 128), (16, 2, 3, 2112, 64),
+                                       (1, 2, 2, 32832, 64), (5, 8, 8, 64, 64)])
+def test_tokens_of_any_scale(fmt, T, k, E, H, I):
+    """Small and large tokens beside each other, staged (T H <= 32768) or not. What fp16 values
+    under a common power of two lose, 2^-39 of the largest, vanishes in the table's 2^-11."""
+    c = _case(fmt, T, k, E, H, I, seed=7)
+    scale = torch.tensor([1e-8, 1e4, 1e-12, 1.0, 3e-5]).repeat(4)[:T]
+    c["x"] = (c["x"].float() * scale[:, None]).to(torch.bfloat16)
+    _check(c)
