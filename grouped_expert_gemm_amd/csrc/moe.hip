@@ -303,10 +303,11 @@ struct Codes {
 // tot[u][m] += scale[u] xscale[m] (dot product of row group u's chunk with entry m's 32
 // values), for the four quarters j of the chunk in turn: a quarter's values of all row
 // groups are decoded once for all entries. x(j, m): entry m's 8 values of quarter j as
-// fp16 (FT = NF4) or bf16 (MXFP4) pairs.
+// fp16 (FT = NF4) or bf16 (MXFP4) pairs. Lanes past the row (`on` false) hold zero codes and
+// another chunk's values, and add nothing: 0 times an infinity there would be NaN.
 template <Fmt F, int FT, int LPR, int U, int RV, typename X>
-__device__ __forceinline__ void dot_pass(const Codes<F, LPR, U>& w, X x, const float* xscale, const uint32_t* blut,
-                                         uint32_t lane_off, float (&tot)[U][RV]) {
+__device__ __forceinline__ void dot_pass(const Codes<F, LPR, U>& w, X x, const float* xscale, bool on,
+                                         const uint32_t* blut, uint32_t lane_off, float (&tot)[U][RV]) {
   constexpr std::integral_constant<int, FT> ft{};
   float d[U][RV];
   u32x4 xv[2][RV];   // the next quarter's values are fetched ahead
@@ -341,9 +342,10 @@ __device__ __forceinline__ void dot_pass(const Codes<F, LPR, U>& w, X x, const f
       }
     __builtin_amdgcn_sched_barrier(0);
   }
+  if (!on) return;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const float s = w.scale_f32(u);   // 0 for chunks past the row
+    const float s = w.scale_f32(u);
 #pragma unroll
     for (int m = 0; m < RV; ++m) tot[u][m] += d[u][m] * (xscale ? s * xscale[m] : s);
   }
@@ -587,7 +589,7 @@ __global__ __launch_bounds__((UpShape<F, ONE>::kMT), (UpShape<F, ONE>::kWavesPer
                 return v;
               }
             },
-            nullptr, blut, lane_off, tot);
+            nullptr, c < C, blut, lane_off, tot);
       }
       sum_lanes<LPR, U, RV>(tot, lane, [&](int row, int m, float v) { acc[wave][m * ROWS + row] = v; });
     });
@@ -717,7 +719,8 @@ __global__ __launch_bounds__(Shape<ONE>::kMT) void moe_down_kernel(MoeArgs g) {
 #pragma unroll
           for (int i = 0; i + 1 < AHEAD; ++i) pre[i] = pre[i + 1];
           load_next(pre[AHEAD - 1]);
-          dot_pass<F, NF4>(w, [&](int j, int m) -> u32x4 { return a[m][j * C + cc]; }, xs, blut, lane_off, tot);
+          dot_pass<F, NF4>(w, [&](int j, int m) -> u32x4 { return a[m][j * C + cc]; }, xs, c < C, blut, lane_off,
+                           tot);
         }
         sum_lanes<LPR, U, RV>(tot, lane, [&](int row, int m, float v) {
           if constexpr (ONE) {

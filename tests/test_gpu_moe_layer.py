@@ -278,3 +278,15 @@ def test_tokens_of_any_scale(fmt, T, k, E, H, I):
     scale = torch.tensor([1e-8, 1e4, 1e-12, 1.0, 3e-5]).repeat(4)[:T]
     c["x"] = (c["x"].float() * scale[:, None]).to(torch.bfloat16)
     _check(c)
+
+
+@pytest.mark.parametrize("fmt", ["nf4", "mxfp4"])
+@pytest.mark.parametrize("T,H,I", [(1, 192, 192), (3, 192, 192), (1, 64, 64), (3, 32832, 64)])
+def test_an_infinity_in_the_last_block_stays_one(fmt, T, H, I):
+    # every weight is positive, so gate, up, act and the result of that token are +inf; lanes
+    # that have no block of the row must not turn it into NaN
+    c = _case(fmt, T, 2, 4, H, I)
+    c["q13"][:] = c["q2"][:] = 0xFF if fmt == "nf4" else 0x22
+    c["x"][T - 1, H - 1] = float("inf")
+    got = _call(c)
+    assert bool((got[T - 1] == float("inf")).all()) and bool(got[:T - 1].isfinite().all())
