@@ -703,7 +703,7 @@ geg_status gmxfp4_w4a4_grouped_gemm(const void* a, const int32_t* sizes, const u
   const int cus = cu_count();
   hipError_t e = hipSuccess;
   if (p.a16_bytes) {
-    e = geg::launch_w4a4_quantize(g.a, M, K, aq, as, g.err, !p.narrow, cus, stream);
+    e = geg::launch_w4a4_quantize(g, aq, as, !p.narrow, cus, stream);
     if (e != hipSuccess) return hip_fail(e, "activation quantisation launch");
     ++g_launches;
   } else {

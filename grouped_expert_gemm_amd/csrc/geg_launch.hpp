@@ -137,8 +137,7 @@ struct W4A4Args {
 int w4a4_narrow_rb(int64_t M, int64_t K, int32_t E, int force);
 hipError_t launch_w4a4_narrow(const W4A4Args& g, int rb, int cus, hipStream_t s);
 bool w4a4_narrow_fused(int64_t M, int32_t E);
-hipError_t launch_w4a4_quantize(const uint16_t* a, int64_t M, int64_t K, uint8_t* codes, uint8_t* scales, uint32_t* err,
-                                bool tiles, int cus, hipStream_t s);
+hipError_t launch_w4a4_quantize(const W4A4Args& g, uint8_t* codes, uint8_t* scales, bool tiles, int cus, hipStream_t s);
 hipError_t launch_w4a4_tile(const W4A4Args& g, int cus, hipStream_t s);
 // Router gate: top-k of logits [T, E] with softmax weights, its gradient, and the
 // gradient of the weighted combine (see gate.hip).

@@ -412,7 +412,7 @@ geg_status gmxfp4_quantize(const void* x, int32_t dtype, int64_t rows, int64_t K
  * Batches of at most 16 rows per expert on average stream the weights once per 16 or 32
  * rows (in one launch up to one row per expert); larger ones run 256 x 256 tiles. A
  * row whose activations hold an inf or NaN comes out NaN and flags
- * GEG_DEVERR_NON_FINITE.
+ * GEG_DEVERR_NON_FINITE (rows past sum(sizes) may hold anything).
  */
 geg_status gmxfp4_w4a4_grouped_gemm(const void* a, const int32_t* sizes, const uint8_t* blocks,
                                     const uint8_t* scales, void* out, int64_t M, int64_t N, int64_t K,

@@ -231,3 +231,20 @@ def test_many_experts_few_of_them_with_rows(path):
     c = _case(sizes.tolist(), 40, 320)
     got = _check(c, path)
     assert np.array_equal(_call(c, path, cu_limit=1).double().cpu().numpy(), got)
+
+
+@pytest.mark.parametrize("path", [0, TILES, NARROW])
+@pytest.mark.parametrize("sizes,extra", [([20, 3], 5), ([1, 0, 0, 0, 0, 0, 0, 0], 4), ([3, -2, 9], 40)])
+def test_nan_rows_that_no_expert_owns_are_not_flagged(path, sizes, extra):
+    import grouped_expert_gemm_amd as geg
+    c = _case([max(n, 0) for n in sizes], 40, 160, extra=extra)
+    c["sizes"] = torch.tensor(sizes, dtype=torch.int32)
+    negative = geg.DEVERR_NEGATIVE_SIZE if min(sizes) < 0 else 0
+    c["a"][-extra:] = float("nan")
+    ws = geg.Workspace()
+    got = _call(c, path, workspace=ws)
+    rows = len(c["a"]) - extra
+    assert ws.read_error() == negative and bool(got[:rows].isfinite().all())
+    c["a"][rows - 1, 159] = float("inf")      # the last row that one owns
+    got = _call(c, path, workspace=ws)
+    assert ws.read_error() == negative | geg.DEVERR_NON_FINITE and bool(got[rows - 1].isnan().all())
