@@ -821,20 +821,20 @@ _stream_ws = {}
 
 def _layer_workspace(ws, need, ref, stream, raw):
     """The caller's workspace, or one of this library's own for the (device, stream)
-    pair, so that calls on two streams never share one. During a graph capture each
-    call gets its own from the graph's memory pool, which lives as long as the graph."""
+    pair, so that calls on two streams never share one. A call on a stream that is being
+    captured gets one from the graph's memory pool, as that stream's allocation: what takes
+    the memory next in the graph runs on the same stream, behind the call."""
     import torch
-    if ws is None:
-        if torch.cuda.is_current_stream_capturing():
-            return Workspace(need, ref.device)
-        key = (ref.get_device(), raw)
-        ws = _stream_ws.get(key)
+    with _allocating(stream):   # the call's stream is the current one in here
         if ws is None:
-            with _allocating(stream):
+            if torch.cuda.is_current_stream_capturing():
+                return Workspace(need, ref.device)
+            key = (ref.get_device(), raw)
+            ws = _stream_ws.get(key)
+            if ws is None:
                 ws = _stream_ws[key] = Workspace(0, ref.device)
-    if ws.buf is None or ws.buf.numel() < need:
-        with _allocating(stream):
-            ws.ensure(max(need, 1 << 20), stream)
+        if ws.buf is None or ws.buf.numel() < need:
+            ws.ensure(max(need, 1 << 20))
     return ws
 
 

@@ -1,0 +1,84 @@
+"""Workspaces of calls that overlap: branches of one captured graph, streams, host threads."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def _up(*arrays):
+    return [torch.tensor(np.ascontiguousarray(v)).cuda() if isinstance(v, np.ndarray) else v.cuda() for v in arrays]
+
+
+def _calls(name):
+    """(function, two argument lists of different values and sizes) of an operator with scratch."""
+    import grouped_expert_gemm_amd as geg
+    import test_gpu_moe_layer as layer
+    import test_gpu_w4a4 as w4a4
+    if name in ("nf4", "mxfp4"):
+        cases = [layer._case(name, T, k, 8, 512, 256, seed=i) for i, (T, k) in enumerate([(16, 4), (7, 3)])]
+        return (geg.gnf4_moe_layer if name == "nf4" else geg.gmxfp4_moe_layer,
+                [_up(c["x"], c["ids"], c["w"], c["q13"], c["s13"], c["q2"], c["s2"]) for c in cases])
+    cases = [w4a4._case(sizes, 136, 320, seed=i) for i, sizes in enumerate([[20, 3, 9], [0, 41, 200]])]
+    return geg.gmxfp4_w4a4_grouped_gemm, [_up(c["a"], c["sizes"], c["w"], c["s"]) for c in cases]
+
+
+OPERATORS = ["nf4", "mxfp4", "w4a4"]
+
+
+def _as_list(r):
+    return [t for t in r if t is not None] if isinstance(r, tuple) else [r]
+
+
+def _equal(got, want):
+    return all(torch.equal(g, w) for g, w in zip(_as_list(got), _as_list(want)))
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_branches_of_one_graph_with_a_stream_given(name):
+    """Two side streams forked into a capture, each with calls of its own, and allocations that
+    the main branch fills meanwhile."""
+    f, (a, b) = _calls(name)
+    want = f(*a), f(*b)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    outs = []
+    with torch.cuda.graph(g):
+        main = torch.cuda.current_stream()
+        s1.wait_stream(main)
+        s2.wait_stream(main)
+        for _ in range(3):
+            outs.append((f(*a, stream=s1), f(*b, stream=s2)))
+            for n in (1 << 10, 1 << 14, 1 << 18, 1 << 20):
+                torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255)
+        main.wait_stream(s1)
+        main.wait_stream(s2)
+    for turn in range(4):
+        for pair in outs:
+            for r in pair:
+                for t in _as_list(r):
+                    t.zero_()
+        g.replay()
+        f(*a)   # eager work between the replays
+        torch.cuda.synchronize()
+        assert all(_equal(x, want[0]) and _equal(y, want[1]) for x, y in outs), turn
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_a_call_onto_a_stream_that_is_captured(name):
+    """Made while another stream is the current one; eager calls on the same stream follow."""
+    f, (b, a) = _calls(name)
+    want = f(*a), f(*b)
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        with torch.cuda.stream(other):
+            out = f(*a, stream=s)
+    for turn in range(3):
+        assert _equal(f(*b, stream=s), want[1])
+        torch.empty(1 << 20, dtype=torch.uint8, device="cuda").fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert _equal(out, want[0]), turn
