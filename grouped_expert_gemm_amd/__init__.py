@@ -816,12 +816,18 @@ def _outlive(stream, *ts):
             t.record_stream(torch.cuda.current_stream())
 
 
-_stream_ws = {}
+class _PerThread(threading.local):
+    def __init__(self):
+        self.of = {}
+
+
+_stream_ws = _PerThread()
 
 
 def _layer_workspace(ws, need, ref, stream, raw):
-    """The caller's workspace, or one of this library's own for the (device, stream)
-    pair, so that calls on two streams never share one. A call on a stream that is being
+    """The caller's workspace, or one of this library's own for the host thread, device and
+    stream: calls on two streams never share one, nor calls of two threads, whose launches on
+    one stream may come in turns (a call may be several). A call on a stream that is being
     captured gets one from the graph's memory pool, as that stream's allocation: what takes
     the memory next in the graph runs on the same stream, behind the call."""
     import torch
@@ -830,9 +836,9 @@ def _layer_workspace(ws, need, ref, stream, raw):
             if torch.cuda.is_current_stream_capturing():
                 return Workspace(need, ref.device)
             key = (ref.get_device(), raw)
-            ws = _stream_ws.get(key)
+            ws = _stream_ws.of.get(key)
             if ws is None:
-                ws = _stream_ws[key] = Workspace(0, ref.device)
+                ws = _stream_ws.of[key] = Workspace(0, ref.device)
         if ws.buf is None or ws.buf.numel() < need:
             ws.ensure(max(need, 1 << 20))
     return ws

@@ -1,4 +1,6 @@
 """Workspaces of calls that overlap: branches of one captured graph, streams, host threads."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -82,3 +84,30 @@ def test_a_call_onto_a_stream_that_is_captured(name):
         g.replay()
         torch.cuda.synchronize()
         assert _equal(out, want[0]), turn
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_two_host_threads_on_one_stream(name):
+    f, args = _calls(name)
+    want = [f(*a) for a in args]
+    torch.cuda.synchronize()
+    start, outs, failed = threading.Barrier(2), [[], []], []
+
+    def work(i):
+        try:
+            torch.cuda.set_device(0)
+            start.wait(30)
+            for _ in range(60):
+                outs[i].append(f(*args[i]))
+        except Exception as e:   # shown by the assertion below
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    assert not failed, failed
+    for i in range(2):
+        assert len(outs[i]) == 60 and all(_equal(o, want[i]) for o in outs[i])
