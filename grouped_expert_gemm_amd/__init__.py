@@ -672,20 +672,23 @@ def route_sort(topk_ids, E: int, x=None, workspace: Workspace | None = None, str
     _check_tensor(topk_ids, "topk_ids", torch.int32, (T, k))
     if x is not None:
         _check_tensor(x, "x", torch.bfloat16, (T, x.shape[1]))
-    _require_gpu(topk_ids, x)
+    _on_device(topk_ids, x)
     dev = topk_ids.device
-    sizes = torch.empty((E,), dtype=torch.int32, device=dev)
-    row_of = torch.empty((T * k,), dtype=torch.int32, device=dev)
-    src_of = torch.empty((T * k,), dtype=torch.int32, device=dev)
     xs = None
     H = 0
-    if x is not None:
-        H = x.shape[1]
-        xs = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
-    need = lib().geg_route_workspace_bytes(T, k, E)
-    ws = _workspace(workspace, need, dev, stream)
+    with _allocating(stream):
+        sizes = torch.empty((E,), dtype=torch.int32, device=dev)
+        row_of = torch.empty((T * k,), dtype=torch.int32, device=dev)
+        src_of = torch.empty((T * k,), dtype=torch.int32, device=dev)
+        if x is not None:
+            H = x.shape[1]
+            xs = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
+    raw = _raw_stream(stream, topk_ids)
+    # a workspace per thread, stream and capture: two sorts may run at once
+    ws = _layer_workspace(workspace, lib().geg_route_workspace_bytes(T, k, E), topk_ids, stream, raw)
     _check(lib().geg_route_sort(_ptr(topk_ids), T, k, E, _ptr(x), H, _ptr(sizes), _ptr(row_of),
-                                _ptr(src_of), _ptr(xs), _ptr(ws.buf), ws.nbytes, _stream(stream)))
+                                _ptr(src_of), _ptr(xs), _ptr(ws.buf), ws.nbytes, raw))
+    _outlive(stream, sizes, row_of, src_of, xs)
     _check_device_errors(ws, check_errors, stream)
     return sizes, row_of, src_of, xs
 
@@ -1060,11 +1063,7 @@ def _make_dispatch_rows():
     class DispatchRows(torch.autograd.Function):
         @staticmethod
         def forward(ctx, x, topk_ids, E):
-            # a workspace per stream and capture: two of these may run at once
-            _on_device(topk_ids, x)
-            need = lib().geg_route_workspace_bytes(topk_ids.shape[0], topk_ids.shape[1], E)
-            ws = _layer_workspace(None, need, topk_ids, None, _raw_stream(None, topk_ids))
-            sizes, row_of, src_of, xs = route_sort(topk_ids, E, x, workspace=ws)
+            sizes, row_of, src_of, xs = route_sort(topk_ids, E, x)
             ctx.save_for_backward(row_of)
             ctx.k = topk_ids.shape[1]
             ctx.mark_non_differentiable(sizes, row_of, src_of)

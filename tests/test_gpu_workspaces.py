@@ -21,11 +21,16 @@ def _calls(name):
         cases = [layer._case(name, T, k, 8, 512, 256, seed=i) for i, (T, k) in enumerate([(16, 4), (7, 3)])]
         return (geg.gnf4_moe_layer if name == "nf4" else geg.gmxfp4_moe_layer,
                 [_up(c["x"], c["ids"], c["w"], c["q13"], c["s13"], c["q2"], c["s2"]) for c in cases])
+    if name == "sort":
+        rng = np.random.default_rng(3)
+        return geg.route_sort, [(*_up(rng.integers(0, E, (T, k)).astype(np.int32)), E,
+                                 torch.randn(T, 64, device="cuda").to(torch.bfloat16))
+                                for T, k, E in ((6000, 8, 64), (300, 4, 40))]
     cases = [w4a4._case(sizes, 136, 320, seed=i) for i, sizes in enumerate([[20, 3, 9], [0, 41, 200]])]
     return geg.gmxfp4_w4a4_grouped_gemm, [_up(c["a"], c["sizes"], c["w"], c["s"]) for c in cases]
 
 
-OPERATORS = ["nf4", "mxfp4", "w4a4"]
+OPERATORS = ["nf4", "mxfp4", "w4a4", "sort"]
 
 
 def _as_list(r):
@@ -111,3 +116,35 @@ def test_two_host_threads_on_one_stream(name):
     assert not failed, failed
     for i in range(2):
         assert len(outs[i]) == 60 and all(_equal(o, want[i]) for o in outs[i])
+
+
+def test_sorts_on_two_streams_at_once():
+    f, args = _calls("sort")
+    want = [f(*a) for a in args]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(20):
+        for a, s in zip(args, streams):
+            with torch.cuda.stream(s):
+                outs.append(f(*a))
+        outs += [f(*a, stream=s) for a, s in zip(args, streams)]
+    torch.cuda.synchronize()
+    assert all(_equal(o, want[i % 2]) for i, o in enumerate(outs))
+
+
+def test_a_captured_sort_before_a_larger_one():
+    """The larger one must not take away the memory that the graph writes."""
+    f, (large, small) = _calls("sort")
+    large = (large[0].repeat(40, 1), *large[1:2])
+    want = f(*small), f(*large)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = f(*small)
+    for turn in range(4):
+        assert _equal(f(*large), want[1])
+        torch.empty(1 << 24, dtype=torch.uint8, device="cuda").fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert _equal(out, want[0]), turn
