@@ -271,20 +271,44 @@ def geg_workspace_bytes(op, M, N, K, E, opts: Opts | None = None) -> int:
 
 class Workspace:
     """A device workspace (torch-allocated uint8 buffer), zeroed once on creation
-    and grown on demand. One workspace must not be shared by concurrent calls."""
+    and grown on demand. One workspace must not be shared by concurrent calls; calls
+    that are ordered may come on any streams. Memory that growing replaces is not
+    reused before the streams that it was used on are done with it, and what a
+    captured graph uses lives as long as the workspace."""
 
     def __init__(self, nbytes: int = 1 << 20, device=None):
         import torch
-        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
-        self.buf = None
+        self._start(device)
         self.ensure(nbytes)
+        if not torch.cuda.is_current_stream_capturing():   # zeroed, whichever stream the first call comes on
+            torch.cuda.current_stream(self.device).synchronize()
+
+    def _start(self, device):
+        import torch
+        device = torch.device("cuda" if device is None else device)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+        self.buf = None
+        self._users = set()      # streams that the buffer was allocated or used on
+        self._captured = False   # by a graph
+        self._kept = []          # earlier buffers of captured graphs
 
     def ensure(self, nbytes: int, stream=None):
+        """At least nbytes for a call on `stream` (None: the current one)."""
         import torch
         nbytes = max(256, (int(nbytes) + 255) & ~255)
-        if self.buf is None or self.buf.numel() < nbytes:
-            self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-            _check(lib().geg_workspace_init(_ptr(self.buf), nbytes, _stream(stream)))
+        with _allocating(stream):
+            raw = torch._C._cuda_getCurrentRawStream(self.device.index)
+            if self.buf is None or self.buf.numel() < nbytes:
+                if self._captured:
+                    self._kept.append(self.buf)
+                self.buf = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+                self._users, self._captured = {raw}, False
+                _check(lib().geg_workspace_init(_ptr(self.buf), nbytes, ctypes.c_void_p(raw)))
+            elif raw not in self._users:
+                self._users.add(raw)
+                self.buf.record_stream(torch.cuda.current_stream(self.device))
+            if not self._captured:
+                self._captured = torch.cuda.is_current_stream_capturing()
         return self
 
     @property
@@ -298,6 +322,14 @@ class Workspace:
 
     def reset(self, stream=None):
         _check(lib().geg_workspace_init(_ptr(self.buf), self.nbytes, _stream(stream)))
+
+
+class _OwnWorkspace(Workspace):
+    """One of this library's own, for one thread and stream: no memory before the first
+    ensure(), on that stream."""
+
+    def __init__(self, device):
+        self._start(device)
 
 
 _default_ws = {}
@@ -837,13 +869,15 @@ def _layer_workspace(ws, need, ref, stream, raw):
     with _allocating(stream):   # the call's stream is the current one in here
         if ws is None:
             if torch.cuda.is_current_stream_capturing():
-                return Workspace(need, ref.device)
+                return _OwnWorkspace(ref.device).ensure(need)
             key = (ref.get_device(), raw)
             ws = _stream_ws.of.get(key)
             if ws is None:
-                ws = _stream_ws.of[key] = Workspace(0, ref.device)
-        if ws.buf is None or ws.buf.numel() < need:
-            ws.ensure(max(need, 1 << 20))
+                ws = _stream_ws.of[key] = _OwnWorkspace(ref.device)
+            if ws.buf is None or ws.buf.numel() < need:
+                ws.ensure(max(need, 1 << 20))
+        else:
+            ws.ensure(need)
     return ws
 
 

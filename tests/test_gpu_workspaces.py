@@ -148,3 +148,72 @@ def test_a_captured_sort_before_a_larger_one():
         g.replay()
         torch.cuda.synchronize()
         assert _equal(out, want[0]), turn
+
+
+def _busy(stream, seconds=0.02):
+    """Work on `stream` that outlasts what the caller does next."""
+    with torch.cuda.stream(stream):
+        a = torch.randn(4096, 4096, device="cuda")
+        for _ in range(max(1, int(seconds / 1.5e-3))):
+            a = a @ a * 1e-3
+    return a
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_a_workspace_that_grows_on_another_stream(name):
+    """What growing replaces belongs to the stream that the workspace was made on, which goes on
+    allocating while the earlier call still waits for its turn."""
+    import grouped_expert_gemm_amd as geg
+    f, args = _calls(name)
+    args = sorted(args, key=lambda a: a[0].numel())
+    want = [f(*a) for a in args]
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        ws = geg.Workspace(256)
+        f(*args[0], workspace=ws)            # the small call's size
+        torch.cuda.synchronize()
+        n = ws.nbytes
+        _busy(s)
+        small = f(*args[0], workspace=ws, stream=s)
+        large = f(*args[1], workspace=ws, stream=s)
+        assert ws.nbytes > n
+        junk = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255) for _ in range(8)]
+        torch.cuda.synchronize()
+        assert _equal(small, want[0]) and _equal(large, want[1])
+        del junk
+
+
+def test_the_first_call_on_another_stream_keeps_its_flags():
+    import grouped_expert_gemm_amd as geg
+    f, args = _calls("sort")
+    ids = args[1][0].clone()
+    ids[0, 0] = -1
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _busy(torch.cuda.current_stream())
+    ws = geg.Workspace(1 << 20)
+    f(ids, 40, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert ws.read_error() == geg.DEVERR_BAD_EXPERT_ID
+
+
+@pytest.mark.parametrize("name", OPERATORS)
+def test_a_captured_workspace_that_grows_later(name):
+    import grouped_expert_gemm_amd as geg
+    f, args = _calls(name)
+    args = sorted(args, key=lambda a: a[0].numel())
+    want = [f(*a) for a in args]
+    ws = geg.Workspace(256)
+    f(*args[0], workspace=ws)
+    n = ws.nbytes
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = f(*args[0], workspace=ws)
+    for turn in range(3):
+        assert _equal(f(*args[1], workspace=ws), want[1])
+        junk = [torch.empty(n, dtype=torch.uint8, device="cuda").fill_(255) for _ in range(8)]
+        g.replay()
+        torch.cuda.synchronize()
+        assert _equal(out, want[0]) and all(bool((j == 255).all()) for j in junk), turn
+    assert ws.nbytes > n
