@@ -335,13 +335,16 @@ class _OwnWorkspace(Workspace):
 _default_ws = {}
 
 
-def _workspace(ws, need, device, stream):
-    if ws is None:
+def _workspace(ws, need, device, stream, check_errors=False):
+    own = ws is None
+    if own:
         key = device.index
         ws = _default_ws.get(key)
         if ws is None:
             ws = _default_ws[key] = Workspace(max(need, 1 << 20), device)
     ws.ensure(need, stream)
+    if own and check_errors:   # earlier calls may have left its error word set
+        ws.reset(stream)
     return ws
 
 
@@ -357,7 +360,7 @@ def _gemm(fn_name, op, a, sizes, wq, scales, out, workspace, opts, stream, check
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     need = geg_workspace_bytes(op, M, N, K, E, opts)
-    ws = _workspace(workspace, need, a.device, stream)
+    ws = _workspace(workspace, need, a.device, stream, check_errors)
     f = getattr(lib(), fn_name)
     _check(f(_ptr(a), _ptr(sizes), _ptr(wq), _ptr(scales), _ptr(out), M, N, K, E,
              _ptr(ws.buf), ws.nbytes, ctypes.byref(opts) if opts else None, _stream(stream)))
@@ -421,7 +424,7 @@ def _dgrad(fn_name, op, dy, sizes, w, scales, dx, workspace, opts, stream, check
     if dx is None:
         dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
     need = geg_workspace_bytes(op, M, N, K, E, opts)
-    ws = _workspace(workspace, need, dy.device, stream)
+    ws = _workspace(workspace, need, dy.device, stream, check_errors)
     _check(getattr(lib(), fn_name)(_ptr(dy), _ptr(sizes), _ptr(w), _ptr(scales), _ptr(dx), M, N, K, E,
                                    _ptr(ws.buf), ws.nbytes, ctypes.byref(opts) if opts else None,
                                    _stream(stream)))
@@ -493,7 +496,7 @@ def _gemm_lora(fmt, a, sizes, w, scales, lora_a, lora_b, scale, out, u, workspac
     _check_tensor(u, "u", torch.float32, (M, r))
     _require_gpu(a, sizes, w, scales, lora_a, lora_b, out, u)
     op = GEG_OP_NF4_FWD if fmt == "nf4" else GEG_OP_MXFP4_FWD
-    ws = _workspace(workspace, lib().geg_lora_workspace_bytes(op, M, N, K, E, r), a.device, stream)
+    ws = _workspace(workspace, lib().geg_lora_workspace_bytes(op, M, N, K, E, r), a.device, stream, check_errors)
     fn = getattr(lib(), "gnf4_grouped_gemm_lora" if fmt == "nf4" else "gmxfp4_grouped_gemm_lora")
     _check(fn(_ptr(a), _ptr(sizes), _ptr(w), _ptr(scales), _ptr(lora_a), _ptr(lora_b), float(scale), _ptr(out),
               _ptr(u), M, N, K, E, r, _ptr(ws.buf), ws.nbytes, ctypes.byref(opts) if opts else None, _stream(stream)))
@@ -539,7 +542,7 @@ def _dgrad_lora(fmt, dy, sizes, w, scales, x, lora_a, lora_b, u, scale, dx, grad
     _check_tensor(grad_b, "grad_b", torch.float32, (E, N, r))
     _require_gpu(dy, sizes, w, scales, x, lora_a, lora_b, u, dx, grad_a, grad_b)
     op = GEG_OP_NF4_DGRAD if fmt == "nf4" else GEG_OP_MXFP4_DGRAD
-    ws = _workspace(workspace, lib().geg_lora_workspace_bytes(op, M, N, K, E, r), dy.device, stream)
+    ws = _workspace(workspace, lib().geg_lora_workspace_bytes(op, M, N, K, E, r), dy.device, stream, check_errors)
     fn = getattr(lib(), "gnf4_grouped_dgrad_lora" if fmt == "nf4" else "gmxfp4_grouped_dgrad_lora")
     _check(fn(_ptr(dy), _ptr(sizes), _ptr(w), _ptr(scales), _ptr(x), _ptr(lora_a), _ptr(lora_b), _ptr(u),
               float(scale), _ptr(dx), _ptr(grad_a), _ptr(grad_b), M, N, K, E, r, _ptr(ws.buf), ws.nbytes,
@@ -661,7 +664,7 @@ def _block(fn_name, op, a, sizes, w13, s13, w2, s2, out, workspace, opts, stream
     if out is None:
         out = torch.empty((M, H), dtype=torch.bfloat16, device=a.device)
     need = geg_workspace_bytes(op, M, H, I, E, opts)
-    ws = _workspace(workspace, need, a.device, stream)
+    ws = _workspace(workspace, need, a.device, stream, check_errors)
     _check(getattr(lib(), fn_name)(_ptr(a), _ptr(sizes), _ptr(w13), _ptr(s13), _ptr(w2), _ptr(s2),
                                    _ptr(out), M, H, I, E, _ptr(ws.buf), ws.nbytes,
                                    ctypes.byref(opts) if opts else None, _stream(stream)))
@@ -717,7 +720,7 @@ def route_sort(topk_ids, E: int, x=None, workspace: Workspace | None = None, str
             xs = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
     raw = _raw_stream(stream, topk_ids)
     # a workspace per thread, stream and capture: two sorts may run at once
-    ws = _layer_workspace(workspace, lib().geg_route_workspace_bytes(T, k, E), topk_ids, stream, raw)
+    ws = _layer_workspace(workspace, lib().geg_route_workspace_bytes(T, k, E), topk_ids, stream, raw, check_errors)
     _check(lib().geg_route_sort(_ptr(topk_ids), T, k, E, _ptr(x), H, _ptr(sizes), _ptr(row_of),
                                 _ptr(src_of), _ptr(xs), _ptr(ws.buf), ws.nbytes, raw))
     _outlive(stream, sizes, row_of, src_of, xs)
@@ -859,12 +862,13 @@ class _PerThread(threading.local):
 _stream_ws = _PerThread()
 
 
-def _layer_workspace(ws, need, ref, stream, raw):
+def _layer_workspace(ws, need, ref, stream, raw, check_errors=False):
     """The caller's workspace, or one of this library's own for the host thread, device and
     stream: calls on two streams never share one, nor calls of two threads, whose launches on
     one stream may come in turns (a call may be several). A call on a stream that is being
     captured gets one from the graph's memory pool, as that stream's allocation: what takes
-    the memory next in the graph runs on the same stream, behind the call."""
+    the memory next in the graph runs on the same stream, behind the call. With check_errors
+    the error word of an own one is cleared first: earlier calls may have left it set."""
     import torch
     with _allocating(stream):   # the call's stream is the current one in here
         if ws is None:
@@ -876,6 +880,8 @@ def _layer_workspace(ws, need, ref, stream, raw):
                 ws = _stream_ws.of[key] = _OwnWorkspace(ref.device)
             if ws.buf is None or ws.buf.numel() < need:
                 ws.ensure(max(need, 1 << 20))
+            if check_errors:
+                ws.reset()
         else:
             ws.ensure(need)
     return ws
@@ -937,7 +943,7 @@ def gmxfp4_w4a4_grouped_gemm(a, sizes, blocks, scales, out=None, workspace: Work
             out = a.new_empty((M, N))
     L, o = lib(), ctypes.byref(opts) if opts else None
     raw = _raw_stream(stream, a)
-    ws = _layer_workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a, stream, raw)
+    ws = _layer_workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a, stream, raw, check_errors)
     _check(L.gmxfp4_w4a4_grouped_gemm(a.data_ptr(), sizes.data_ptr(), blocks.data_ptr(), scales.data_ptr(),
                                       out.data_ptr(), M, N, K, E, ws.buf.data_ptr(), ws.buf.numel(), o, raw))
     if mine:
@@ -1035,7 +1041,7 @@ def _moe_layer(nf4, x, topk_ids, topk_weights, w13, s13, w2, s2, out, workspace,
             out = x.new_empty((T, H))
     L = lib()
     raw = _raw_stream(stream, x)
-    ws = _layer_workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x, stream, raw)
+    ws = _layer_workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x, stream, raw, check_errors)
     f = L.gnf4_moe_layer if nf4 else L.gmxfp4_moe_layer
     _check(f(x.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
              s2.data_ptr(), out.data_ptr(), T, k, H, I, E, ws.buf.data_ptr(), ws.buf.numel(),

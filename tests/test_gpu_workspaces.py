@@ -217,3 +217,14 @@ def test_a_captured_workspace_that_grows_later(name):
         torch.cuda.synchronize()
         assert _equal(out, want[0]) and all(bool((j == 255).all()) for j in junk), turn
     assert ws.nbytes > n
+
+
+def test_a_checked_call_does_not_raise_for_an_earlier_one():
+    import grouped_expert_gemm_amd as geg
+    f, args = _calls("sort")
+    bad = args[1][0].clone()
+    bad[0, 0] = -1
+    f(bad, 40)                                    # flagged in the library's own workspace, unchecked
+    assert _equal(f(*args[1], check_errors=True), f(*args[1]))
+    with pytest.raises(geg.GegDeviceError):
+        f(bad, 40, check_errors=True)
