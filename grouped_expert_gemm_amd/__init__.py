@@ -331,20 +331,42 @@ class _OwnWorkspace(Workspace):
     def __init__(self, device):
         self._start(device)
 
+    def take(self, nbytes):
+        """Memory of one captured call, whose error word nobody can read: not zeroed."""
+        import torch
+        self.buf = torch.empty(max(256, nbytes), dtype=torch.uint8, device=self.device)
+        return self
 
-_default_ws = {}
+
+class _PerThread(threading.local):
+    def __init__(self):
+        self.of = {}
+
+
+_own_ws = _PerThread()
 
 
 def _workspace(ws, need, device, stream, check_errors=False):
-    own = ws is None
-    if own:
-        key = device.index
-        ws = _default_ws.get(key)
+    """The caller's workspace, or one of this library's own for the host thread, device and
+    stream: calls on two streams never share one, nor calls of two threads, whose launches on
+    one stream may come in turns (a call may be several). A call on a stream that is being
+    captured gets one from the graph's memory pool, as that stream's allocation: what takes
+    the memory next in the graph runs on the same stream, behind the call. With check_errors
+    the error word of an own one is cleared first: earlier calls may have left it set."""
+    import torch
+    with _allocating(stream):   # the call's stream is the current one in here
+        if ws is not None:
+            return ws.ensure(need)
+        if torch.cuda.is_current_stream_capturing():
+            return _OwnWorkspace(device).take(need)
+        key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
+        ws = _own_ws.of.get(key)
         if ws is None:
-            ws = _default_ws[key] = Workspace(max(need, 1 << 20), device)
-    ws.ensure(need, stream)
-    if own and check_errors:   # earlier calls may have left its error word set
-        ws.reset(stream)
+            ws = _own_ws.of[key] = _OwnWorkspace(device)
+        if ws.buf is None or ws.buf.numel() < need:
+            ws.ensure(max(need, 1 << 20))
+        if check_errors:
+            ws.reset()
     return ws
 
 
@@ -719,8 +741,7 @@ def route_sort(topk_ids, E: int, x=None, workspace: Workspace | None = None, str
             H = x.shape[1]
             xs = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
     raw = _raw_stream(stream, topk_ids)
-    # a workspace per thread, stream and capture: two sorts may run at once
-    ws = _layer_workspace(workspace, lib().geg_route_workspace_bytes(T, k, E), topk_ids, stream, raw, check_errors)
+    ws = _workspace(workspace, lib().geg_route_workspace_bytes(T, k, E), dev, stream, check_errors)
     _check(lib().geg_route_sort(_ptr(topk_ids), T, k, E, _ptr(x), H, _ptr(sizes), _ptr(row_of),
                                 _ptr(src_of), _ptr(xs), _ptr(ws.buf), ws.nbytes, raw))
     _outlive(stream, sizes, row_of, src_of, xs)
@@ -854,39 +875,6 @@ def _outlive(stream, *ts):
             t.record_stream(torch.cuda.current_stream())
 
 
-class _PerThread(threading.local):
-    def __init__(self):
-        self.of = {}
-
-
-_stream_ws = _PerThread()
-
-
-def _layer_workspace(ws, need, ref, stream, raw, check_errors=False):
-    """The caller's workspace, or one of this library's own for the host thread, device and
-    stream: calls on two streams never share one, nor calls of two threads, whose launches on
-    one stream may come in turns (a call may be several). A call on a stream that is being
-    captured gets one from the graph's memory pool, as that stream's allocation: what takes
-    the memory next in the graph runs on the same stream, behind the call. With check_errors
-    the error word of an own one is cleared first: earlier calls may have left it set."""
-    import torch
-    with _allocating(stream):   # the call's stream is the current one in here
-        if ws is None:
-            if torch.cuda.is_current_stream_capturing():
-                return _OwnWorkspace(ref.device).ensure(need)
-            key = (ref.get_device(), raw)
-            ws = _stream_ws.of.get(key)
-            if ws is None:
-                ws = _stream_ws.of[key] = _OwnWorkspace(ref.device)
-            if ws.buf is None or ws.buf.numel() < need:
-                ws.ensure(max(need, 1 << 20))
-            if check_errors:
-                ws.reset()
-        else:
-            ws.ensure(need)
-    return ws
-
-
 def gmxfp4_quantize(x, values: bool = False, stream=None):
     """MXFP4-pack x [..., K] (bf16, fp16 or fp32; K % 32 == 0) on the GPU -> (blocks uint8
     [..., K/2], scales uint8 [..., K/32]), with values=True also the values that the
@@ -943,7 +931,7 @@ def gmxfp4_w4a4_grouped_gemm(a, sizes, blocks, scales, out=None, workspace: Work
             out = a.new_empty((M, N))
     L, o = lib(), ctypes.byref(opts) if opts else None
     raw = _raw_stream(stream, a)
-    ws = _layer_workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a, stream, raw, check_errors)
+    ws = _workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a.device, stream, check_errors)
     _check(L.gmxfp4_w4a4_grouped_gemm(a.data_ptr(), sizes.data_ptr(), blocks.data_ptr(), scales.data_ptr(),
                                       out.data_ptr(), M, N, K, E, ws.buf.data_ptr(), ws.buf.numel(), o, raw))
     if mine:
@@ -1041,7 +1029,7 @@ def _moe_layer(nf4, x, topk_ids, topk_weights, w13, s13, w2, s2, out, workspace,
             out = x.new_empty((T, H))
     L = lib()
     raw = _raw_stream(stream, x)
-    ws = _layer_workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x, stream, raw, check_errors)
+    ws = _workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x.device, stream, check_errors)
     f = L.gnf4_moe_layer if nf4 else L.gmxfp4_moe_layer
     _check(f(x.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
              s2.data_ptr(), out.data_ptr(), T, k, H, I, E, ws.buf.data_ptr(), ws.buf.numel(),

@@ -219,6 +219,77 @@ def test_a_captured_workspace_that_grows_later(name):
     assert ws.nbytes > n
 
 
+def _gemm_calls(name):
+    """(function, a large and a small argument list) of the grouped GEMM, its gradient and the block."""
+    import grouped_expert_gemm_amd as geg
+    g = torch.Generator(device="cuda").manual_seed(5)
+    E, N, K = 4, 384, 1024
+
+    def weights(n, k):
+        return (torch.randint(0, 256, (E, n, k // 2), dtype=torch.uint8, generator=g, device="cuda"),
+                0.02 + 0.03 * torch.rand(E, n, k // 64, generator=g, device="cuda"))
+
+    def rows(sizes, k):
+        return (torch.randn(sum(sizes), k, generator=g, device="cuda").to(torch.bfloat16),
+                torch.tensor(sizes, dtype=torch.int32, device="cuda"))
+    sizes = ([700, 300, 0, 500], [90, 70, 3, 200])
+    if name == "gemm":
+        w = weights(N, K)
+        return geg.gnf4_grouped_gemm, [(*rows(n, K), *w) for n in sizes]
+    if name == "dgrad":
+        w = weights(N, K)
+        return geg.gnf4_grouped_dgrad, [(*rows(n, N), *w) for n in sizes]
+    w13, w2 = weights(512, K), weights(K, 256)
+    return geg.gnf4_expert_block, [(*rows(n, K), *w13, *w2) for n in sizes]
+
+
+@pytest.mark.parametrize("name", ["gemm", "dgrad", "block"])
+def test_the_gemms_at_once_on_streams_and_threads(name):
+    f, args = _gemm_calls(name)
+    want = [f(*a) for a in args]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(10):
+        for a, s in zip(args, streams):
+            with torch.cuda.stream(s):
+                outs.append(f(*a))
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want[i % 2]) for i, o in enumerate(outs))
+    threaded = [[], []]
+
+    def work(i):
+        torch.cuda.set_device(0)
+        for _ in range(30):
+            threaded[i].append(f(*args[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(threaded[i]) == 30 and all(torch.equal(o, want[i]) for o in threaded[i])
+
+
+@pytest.mark.parametrize("name", ["gemm", "dgrad", "block"])
+def test_a_captured_gemm_before_a_larger_one(name):
+    f, (large, small) = _gemm_calls(name)
+    large = (large[0].repeat(20, 1), large[1] * 20, *large[2:])
+    want = f(*small), f(*large)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = f(*small)
+    for turn in range(4):
+        assert torch.equal(f(*large), want[1])
+        torch.empty(1 << 26, dtype=torch.uint8, device="cuda").fill_(255)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]), turn
+
+
 def test_a_checked_call_does_not_raise_for_an_earlier_one():
     import grouped_expert_gemm_amd as geg
     f, args = _calls("sort")
@@ -226,5 +297,8 @@ def test_a_checked_call_does_not_raise_for_an_earlier_one():
     bad[0, 0] = -1
     f(bad, 40)                                    # flagged in the library's own workspace, unchecked
     assert _equal(f(*args[1], check_errors=True), f(*args[1]))
+    gemm, calls = _gemm_calls("gemm")
+    f(bad, 40)
+    gemm(*calls[1], check_errors=True)
     with pytest.raises(geg.GegDeviceError):
         f(bad, 40, check_errors=True)
