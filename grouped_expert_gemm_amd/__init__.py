@@ -849,7 +849,7 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-_HERE = contextlib.nullcontext()
+_NO_CHANGE = contextlib.nullcontext()
 
 
 def _allocating(stream):
@@ -857,7 +857,7 @@ def _allocating(stream):
     current one comes from that stream's pool, where only its own earlier work (or work
     that was recorded on it) may still use it."""
     if stream is None:
-        return _HERE
+        return _NO_CHANGE
     import torch
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))

@@ -160,3 +160,8 @@ def test_python_refusals():
                  lambda: geg.gmxfp4_moe_layer(x, ids, w, w13, m13, w2, m2)):
         with pytest.raises(geg.GegError, match="GPU"):
             call()
+
+
+def test_the_packages_paths_stay_paths():
+    import os
+    assert os.path.isdir(geg._HERE) and os.path.dirname(geg.LIB_PATH) == geg._HERE
