@@ -740,8 +740,8 @@ def route_sort(topk_ids, E: int, x=None, workspace: Workspace | None = None, str
         if x is not None:
             H = x.shape[1]
             xs = torch.empty((T * k, H), dtype=torch.bfloat16, device=dev)
+        ws = _workspace(workspace, lib().geg_route_workspace_bytes(T, k, E), dev, None, check_errors)
     raw = _raw_stream(stream, topk_ids)
-    ws = _workspace(workspace, lib().geg_route_workspace_bytes(T, k, E), dev, stream, check_errors)
     _check(lib().geg_route_sort(_ptr(topk_ids), T, k, E, _ptr(x), H, _ptr(sizes), _ptr(row_of),
                                 _ptr(src_of), _ptr(xs), _ptr(ws.buf), ws.nbytes, raw))
     _outlive(stream, sizes, row_of, src_of, xs)
@@ -852,6 +852,25 @@ def _addr(t):
 _NO_CHANGE = contextlib.nullcontext()
 
 
+class _OnStream:
+    """torch.cuda.stream(stream) without its checks, which cost as much as a call."""
+    __slots__ = ("stream", "before")
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        from torch import _C
+        s = self.stream
+        self.before = _C._cuda_getCurrentStream(_C._cuda_getDevice())
+        _C._cuda_setStream(stream_id=s.stream_id, device_index=s.device_index, device_type=s.device_type)
+
+    def __exit__(self, *_):
+        from torch import _C
+        at, index, kind = self.before
+        _C._cuda_setStream(stream_id=at, device_index=index, device_type=kind)
+
+
 def _allocating(stream):
     """Context in which a call on `stream` allocates: memory for another stream than the
     current one comes from that stream's pool, where only its own earlier work (or work
@@ -859,9 +878,9 @@ def _allocating(stream):
     if stream is None:
         return _NO_CHANGE
     import torch
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
-    return torch.cuda.stream(stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return _OnStream(stream)
 
 
 def _outlive(stream, *ts):
@@ -870,9 +889,10 @@ def _outlive(stream, *ts):
     if stream is None:
         return
     import torch
+    here = torch.cuda.current_stream()
     for t in ts:
         if t is not None:
-            t.record_stream(torch.cuda.current_stream())
+            t.record_stream(here)
 
 
 def gmxfp4_quantize(x, values: bool = False, stream=None):
@@ -926,12 +946,12 @@ def gmxfp4_w4a4_grouped_gemm(a, sizes, blocks, scales, out=None, workspace: Work
     _check_tensor(out, "out", torch.bfloat16, (M, N))
     _on_device(a, sizes, blocks, scales, out)
     mine = out is None
-    if mine:
-        with _allocating(stream):
-            out = a.new_empty((M, N))
     L, o = lib(), ctypes.byref(opts) if opts else None
     raw = _raw_stream(stream, a)
-    ws = _workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a.device, stream, check_errors)
+    with _allocating(stream):
+        if mine:
+            out = a.new_empty((M, N))
+        ws = _workspace(workspace, L.geg_workspace_bytes(GEG_OP_MXFP4_W4A4, M, N, K, E, o), a.device, None, check_errors)
     _check(L.gmxfp4_w4a4_grouped_gemm(a.data_ptr(), sizes.data_ptr(), blocks.data_ptr(), scales.data_ptr(),
                                       out.data_ptr(), M, N, K, E, ws.buf.data_ptr(), ws.buf.numel(), o, raw))
     if mine:
@@ -1024,12 +1044,12 @@ def _moe_layer(nf4, x, topk_ids, topk_weights, w13, s13, w2, s2, out, workspace,
     _check_tensor(out, "out", torch.bfloat16, (T, H))
     _on_device(x, topk_ids, topk_weights, w13, s13, w2, s2, out)
     mine = out is None
-    if mine:
-        with _allocating(stream):
-            out = x.new_empty((T, H))
     L = lib()
     raw = _raw_stream(stream, x)
-    ws = _workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x.device, stream, check_errors)
+    with _allocating(stream):
+        if mine:
+            out = x.new_empty((T, H))
+        ws = _workspace(workspace, L.geg_moe_layer_workspace_bytes(T, k, I), x.device, None, check_errors)
     f = L.gnf4_moe_layer if nf4 else L.gmxfp4_moe_layer
     _check(f(x.data_ptr(), topk_ids.data_ptr(), topk_weights.data_ptr(), w13.data_ptr(), s13.data_ptr(), w2.data_ptr(),
              s2.data_ptr(), out.data_ptr(), T, k, H, I, E, ws.buf.data_ptr(), ws.buf.numel(),

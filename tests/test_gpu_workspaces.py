@@ -302,3 +302,19 @@ def test_a_checked_call_does_not_raise_for_an_earlier_one():
     gemm(*calls[1], check_errors=True)
     with pytest.raises(geg.GegDeviceError):
         f(bad, 40, check_errors=True)
+
+
+@pytest.mark.parametrize("name", ["nf4", "w4a4", "sort", "gemm"])
+def test_streams_in_any_form(name):
+    """A torch stream, its handle (0: the null stream) and any object that has one."""
+    from types import SimpleNamespace
+    f, args = _gemm_calls(name) if name == "gemm" else _calls(name)
+    want = f(*args[0])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    here = torch.cuda.current_stream().cuda_stream
+    outs = [f(*args[0], stream=form) for form in (s, s.cuda_stream, SimpleNamespace(cuda_stream=s.cuda_stream), 0,
+                                                  torch.cuda.current_stream())]
+    assert torch.cuda.current_stream().cuda_stream == here
+    torch.cuda.synchronize()
+    assert all(_equal(o, want) for o in outs)
