@@ -31,10 +31,10 @@
 // mixed-precision fmas took twice the arithmetic and three times the registers: for the
 // second kernel of 8 experts of 4096 x 14336, four tokens, 714 us against 37 now.)
 //
-// Both kernels together: 8 experts of 4096 x 14336, top 2, four tokens: 90 us for 542 MB
-// (6.0 TB/s, part of it from the last-level cache). 128 experts of 2048 x 768, top 8: one
-// token 12 us (21 MB), 16 tokens 54 us (219 MB); 32 experts of 2880 x 2880, top 4, MXFP4,
-// one token 18 us (53 MB). One token is bound by latency and issue as much as by bytes:
+// Both kernels together, in a kernel trace: 8 experts of 4096 x 14336, top 2, four tokens:
+// 99 to 103 us for 542 MB (5.4 TB/s). 128 experts of 2048 x 768, top 8: one token 13 us (21
+// MB), 16 tokens 55 us (219 MB); 32 experts of 2880 x 2880, top 4, MXFP4, one token 18.5 us
+// (53 MB), 8 tokens 70. One token is bound by latency and issue as much as by bytes:
 // two kernels each ask for their weights two microseconds after their start, wait two more
 // for the first, and lie 1.3 apart; 16 wavefronts pay 16 clocks of a CU for every vector
 // instruction they share. So nothing is grouped for one token (item q is slot q, the ids
@@ -69,8 +69,11 @@ struct Shape {
 };
 // Of the first, whose units are 64 rows, the 32 values of a block of act. The same, but for
 // one token in MXFP4 two workgroups of 8 wavefronts share a CU: a unit past one per CU then
-// runs beside another instead of after it (360 units of 2880: 11.1-11.9 us, 12.7 in workgroups
-// of 16; NF4's table leaves no room for a second: 8.0 against 6.9 for 192 units).
+// runs beside another instead of after it, and a unit's 8 wavefronts meet sooner than 16. Units
+// of 64 rows, in workgroups of 8 against 16: 48 of 2880 values 6.3 / 7.5-8.4 us, 192 of 2048
+// 5.8 / 6.1, 240 of 2880 7.6-8.8 / 9.5-9.9, 256 of 4096 9.6-10.5 / 11.6-12.0, 360 of 2880
+// 10.8-11.6 / 12.6, 896 of 4096 26.4 / 28.9. NF4's table leaves no room for a second workgroup:
+// with 8 wavefronts it took 8.0 us for 192 units, with 16 6.9.
 template <Fmt F, bool ONE>
 struct UpShape {
   static constexpr bool kTwo = ONE && F == MXFP4;
@@ -759,8 +762,9 @@ hipError_t up(const MoeArgs& g, int cus, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rows of W2 per workgroup: one round of the chip where that stays within the LDS
-// arrays.
+// Rows of W2 per workgroup: no more than one round of the chip where that stays within the
+// LDS arrays. (Fewer than ROWS rows per CU leave CUs idle: neither the items nor the
+// contraction are split.)
 template <Fmt F, int LPR, bool ONE>
 hipError_t down(MoeArgs g, int cus, hipStream_t s) {
   constexpr int ROWS = Shape<ONE>::kRows;
