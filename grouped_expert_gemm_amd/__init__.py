@@ -30,6 +30,7 @@ __all__ = [
     "DEVERR_BAD_EXPERT_ID",
     "gmxfp4_quantize", "gmxfp4_w4a4_grouped_gemm", "GEG_OP_MXFP4_W4A4", "route_topk", "route_topk_grad", "route_combine_grad",
     "gnf4_moe_layer", "gmxfp4_moe_layer", "router_gate", "dispatch_rows", "combine_rows",
+    "grouped_gemm", "grouped_dgrad", "grouped_wgrad", "grouped_matmul",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -139,6 +140,11 @@ def lib() -> ctypes.CDLL:
                 f = getattr(L, name)
                 f.argtypes = [_P, _P, _P, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I32, _P, _SZ, _P, _P]
                 f.restype = ctypes.c_int
+            dense = [_P, _P, _P, _P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _SZ, _P, _P]
+            for name in ("geg_grouped_gemm", "geg_grouped_dgrad", "geg_grouped_wgrad"):
+                f = getattr(L, name)
+                f.argtypes, f.restype = dense, ctypes.c_int
+            L.geg_grouped_wgrad.argtypes = [_P, _P, _P, _P, _I32, _I32, _I64, _I64, _I64, _I32, _P, _SZ, _P, _P]
             L.geg_workspace_bytes.argtypes = [_I32, _I64, _I64, _I64, _I32, _P]
             L.geg_workspace_bytes.restype = _SZ
             L.geg_workspace_init.argtypes, L.geg_workspace_init.restype = [_P, _SZ, _P], ctypes.c_int
@@ -1166,3 +1172,128 @@ def combine_rows(y, weights, row_of, src_of):
     """route_combine as a torch autograd op, differentiable with respect to the expert
     outputs y bf16 [T*k, N] and the router weights fp32 [T, k]."""
     return _CombineRows.apply(y, weights, row_of, src_of)
+
+
+# ----------------------------------------------------------------------------- 16-bit grouped products
+def _dtype16(t, name):
+    code = _dtype(t, name)
+    if code == 2:
+        raise GegError(2, f"{name}: expected a bfloat16 or float16 tensor, got {t.dtype}")
+    return code
+
+
+def _dense(fn_name, x, xname, sizes, w, out, oname, width, zero_rest, workspace, opts, stream, check_errors):
+    """Forward (x = a, out [M, N]) or gradient of the activations (x = dy, out [M, K])."""
+    import torch
+    dt = _dtype16(x, xname)
+    if x.dim() != 2 or w.dim() != 3:
+        raise GegError(2, f"{xname}: expected a 2-D tensor, w [E, N, K]")
+    M = x.shape[0]
+    E, N, K = w.shape
+    _check_tensor(x, xname, x.dtype, (M, N + K - width))
+    _check_tensor(sizes, "sizes", torch.int32, (E,))
+    _check_tensor(w, "w", x.dtype, (E, N, K))
+    _check_tensor(out, oname, x.dtype, (M, width))
+    _on_device(x, sizes, w, out)
+    mine = out is None
+    raw = _raw_stream(stream, x)
+    with _allocating(stream):
+        if mine:
+            out = x.new_empty((M, width))
+        ws = _workspace(workspace, 256, x.device, None, check_errors)
+    _check(getattr(lib(), fn_name)(x.data_ptr(), sizes.data_ptr(), w.data_ptr(), out.data_ptr(), dt, M, N, K, E,
+                                   int(zero_rest), ws.buf.data_ptr(), ws.buf.numel(),
+                                   ctypes.byref(opts) if opts else None, raw))
+    if mine:
+        _outlive(stream, out)
+    _check_device_errors(ws, check_errors, stream)
+    return out
+
+
+def grouped_gemm(a, sizes, w, out=None, zero_rest: bool = False, workspace: Workspace | None = None,
+                 opts: Opts | None = None, stream=None, check_errors: bool = False):
+    """The grouped expert product with 16-bit weights: a [M, K] (bf16 or fp16, rows grouped
+    by expert), sizes int32 [E], w [E, N, K] of a's type -> out [M, N] = a_e W_e^T, summed
+    in fp32. K % 8 == 0. Rows past sum(sizes) stay as they were allocated, or are set to 0
+    with zero_rest."""
+    return _dense("geg_grouped_gemm", a, "a", sizes, w, out, "out", w.shape[1] if w.dim() == 3 else 0, zero_rest,
+                  workspace, opts, stream, check_errors)
+
+
+def grouped_dgrad(dy, sizes, w, dx=None, zero_rest: bool = False, workspace: Workspace | None = None,
+                  opts: Opts | None = None, stream=None, check_errors: bool = False):
+    """Gradient of grouped_gemm's activations: dy [M, N], w [E, N, K] -> dx [M, K] = dy_e W_e.
+    N % 8 == 0 and K % 8 == 0."""
+    return _dense("geg_grouped_dgrad", dy, "dy", sizes, w, dx, "dx", w.shape[2] if w.dim() == 3 else 0, zero_rest,
+                  workspace, opts, stream, check_errors)
+
+
+def grouped_wgrad(dy, a, sizes, dw=None, dtype=None, workspace: Workspace | None = None, opts: Opts | None = None,
+                  stream=None, check_errors: bool = False):
+    """Gradient of grouped_gemm's weights: dy [M, N], a [M, K], sizes int32 [E] -> dw
+    [E, N, K] = dy_e^T a_e (0 for experts without rows), in dtype: a's (None) or
+    torch.float32. N % 8 == 0 and K % 8 == 0."""
+    import torch
+    dt = _dtype16(dy, "dy")
+    if dy.dim() != 2 or a.dim() != 2 or sizes.dim() != 1:
+        raise GegError(2, "dy: expected [M, N], a [M, K], sizes [E]")
+    M, N = dy.shape
+    K, E = a.shape[1], sizes.shape[0]
+    if dtype is None:
+        dtype = dw.dtype if dw is not None else dy.dtype
+    if dtype not in (dy.dtype, torch.float32):
+        raise GegError(2, f"dtype: expected {dy.dtype} or torch.float32, got {dtype}")
+    _check_tensor(dy, "dy", dy.dtype, (M, N))
+    _check_tensor(a, "a", dy.dtype, (M, K))
+    _check_tensor(sizes, "sizes", torch.int32, (E,))
+    _check_tensor(dw, "dw", dtype, (E, N, K))
+    _on_device(dy, a, sizes, dw)
+    mine = dw is None
+    raw = _raw_stream(stream, dy)
+    with _allocating(stream):
+        if mine:
+            dw = dy.new_empty((E, N, K), dtype=dtype)
+        ws = _workspace(workspace, 256, dy.device, None, check_errors)
+    _check(lib().geg_grouped_wgrad(dy.data_ptr(), a.data_ptr(), sizes.data_ptr(), dw.data_ptr(), dt,
+                                   2 if dtype is torch.float32 else dt, M, N, K, E, ws.buf.data_ptr(), ws.buf.numel(),
+                                   ctypes.byref(opts) if opts else None, raw))
+    if mine:
+        _outlive(stream, dw)
+    _check_device_errors(ws, check_errors, stream)
+    return dw
+
+
+def _make_grouped_matmul():
+    import torch
+
+    class GroupedMatmul(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a, sizes, w, check_errors):
+            ctx.save_for_backward(a, sizes, w)
+            ctx.check_errors = check_errors
+            return grouped_gemm(a, sizes, w, zero_rest=True, check_errors=check_errors)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dy):
+            a, sizes, w = ctx.saved_tensors
+            dy = dy.contiguous()
+            da = dw = None
+            if ctx.needs_input_grad[0]:
+                da = grouped_dgrad(dy, sizes, w, zero_rest=True, check_errors=ctx.check_errors)
+            if ctx.needs_input_grad[2]:
+                dw = grouped_wgrad(dy, a, sizes, check_errors=ctx.check_errors)
+            return da, None, dw, None
+
+    return GroupedMatmul
+
+
+_GroupedMatmul = _LazyFn(_make_grouped_matmul)
+
+
+def grouped_matmul(a, sizes, w, check_errors: bool = False):
+    """grouped_gemm as a torch autograd op, differentiable with respect to the activations a
+    [M, K] and the weights w [E, N, K]: training of experts that are not quantised, next to
+    router_gate, dispatch_rows and combine_rows. Rows past sum(sizes) (a padded batch) give
+    0 and get 0."""
+    return _GroupedMatmul.apply(a, sizes, w, bool(check_errors))

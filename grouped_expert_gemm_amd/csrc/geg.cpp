@@ -1153,6 +1153,72 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
                    workspace, workspace_bytes, opts, stream);
 }
 
+// Grouped products with 16-bit weights. p: a or dy; q: w, or a for the weights' gradient.
+static geg_status dense_common(int dir, const void* p, const char* pname, const void* q, const char* qname,
+                               const int32_t* sizes, void* out, const char* oname, int32_t dtype, int32_t out_dtype,
+                               int64_t M, int64_t N, int64_t K, int32_t E, int32_t zero_rest, void* ws, size_t ws_bytes,
+                               const geg_opts* opts, hipStream_t stream) {
+  CuScope cu_scope(opts);
+  if (dtype != GEG_BF16 && dtype != GEG_F16) return fail(GEG_ERR_BAD_OPTION, "dtype must be GEG_BF16 or GEG_F16");
+  if (out_dtype != dtype && out_dtype != GEG_F32)
+    return fail(GEG_ERR_BAD_OPTION, "dw_dtype must be dtype or GEG_F32");
+  const int32_t force = opts ? opts->force_path : 0;
+  if (force != 0 && force != 2 && (force != 4 || dir != geg::kDenseFwd))
+    return fail(GEG_ERR_BAD_OPTION, "16-bit products run on tiles (force_path 2) or, forward, on the narrow kernel (4)");
+  if (opts && opts->cu_limit < 0) return fail(GEG_ERR_BAD_OPTION, "cu_limit must be >= 0");
+  geg_status st;
+  if ((st = check_shape(M, 1, K, E, 8)) != GEG_OK) return st;
+  if (N <= 0 || N > kMaxWindow / 512)
+    return fail(GEG_ERR_BAD_SHAPE, "need N > 0 and 256 rows of N 16-bit values within 0x7FFFFFF0 bytes");
+  if (dir != geg::kDenseFwd && N % 8) return fail(GEG_ERR_BAD_SHAPE, "the gradients need N % 8 == 0");
+  const bool wgrad = dir == geg::kDenseWgrad;
+  if (M == 0 && !wgrad) return GEG_OK;
+  if (!sizes || !out || (M > 0 && !p) || ((M > 0 || !wgrad) && !q))
+    return fail(GEG_ERR_NULL_POINTER, "a required pointer is NULL");
+  if (!ws) return fail(GEG_ERR_WORKSPACE, "workspace is NULL");
+  if (!aligned(p, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(sizes, 4))
+    return fail(GEG_ERR_MISALIGNED, std::string(pname) + ", " + qname + " and " + oname + " must be 16-byte aligned");
+  if (!aligned(ws, 256)) return fail(GEG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < kHeader) return fail(GEG_ERR_WORKSPACE, "workspace smaller than geg_workspace_bytes(): need 256");
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{p, pname}, {sizes, "sizes"}, {q, qname}, {out, oname},
+                           {ws, "workspace"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  geg::DenseArgs g{reinterpret_cast<const uint16_t*>(p), reinterpret_cast<const uint16_t*>(q), sizes, out, M, N, K, E,
+                   zero_rest != 0, reinterpret_cast<uint32_t*>(ws)};
+  const int cus = cu_count();
+  const bool narrow = dir == geg::kDenseFwd && (force == 4 || (force == 0 && M <= geg::kDenseNarrowAvg * (int64_t)E));
+  hipError_t e = record_event(opts, narrow ? 2 : 0, stream);
+  if (e == hipSuccess)
+    e = narrow ? geg::launch_dense_narrow(dtype, g, cus, stream)
+               : geg::launch_dense_tile(dir, dtype, out_dtype == GEG_F32, g, cus, stream);
+  if (e == hipSuccess) e = record_event(opts, narrow ? 3 : 1, stream);
+  if (e != hipSuccess) return hip_fail(e, "16-bit product launch");
+  ++g_launches;
+  return GEG_OK;
+}
+
+geg_status geg_grouped_gemm(const void* a, const int32_t* sizes, const void* w, void* out, int32_t dtype, int64_t M,
+                            int64_t N, int64_t K, int32_t E, int32_t zero_rest, void* workspace, size_t workspace_bytes,
+                            const geg_opts* opts, hipStream_t stream) {
+  return dense_common(geg::kDenseFwd, a, "a", w, "w", sizes, out, "out", dtype, dtype, M, N, K, E, zero_rest, workspace,
+                      workspace_bytes, opts, stream);
+}
+
+geg_status geg_grouped_dgrad(const void* dy, const int32_t* sizes, const void* w, void* dx, int32_t dtype, int64_t M,
+                             int64_t N, int64_t K, int32_t E, int32_t zero_rest, void* workspace,
+                             size_t workspace_bytes, const geg_opts* opts, hipStream_t stream) {
+  return dense_common(geg::kDenseDgrad, dy, "dy", w, "w", sizes, dx, "dx", dtype, dtype, M, N, K, E, zero_rest, workspace,
+                      workspace_bytes, opts, stream);
+}
+
+geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes, void* dw, int32_t dtype,
+                             int32_t dw_dtype, int64_t M, int64_t N, int64_t K, int32_t E, void* workspace,
+                             size_t workspace_bytes, const geg_opts* opts, hipStream_t stream) {
+  return dense_common(geg::kDenseWgrad, dy, "dy", a, "a", sizes, dw, "dw", dtype, dw_dtype, M, N, K, E, 0, workspace,
+                      workspace_bytes, opts, stream);
+}
+
 size_t geg_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E,
                            const geg_opts* opts) {
   if (op < 0 || (op > 6 && op != GEG_OP_MXFP4_W4A4) || M < 0 || N <= 0 || K <= 0 || E <= 0) return 0;

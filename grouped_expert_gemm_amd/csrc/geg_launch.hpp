@@ -139,6 +139,24 @@ hipError_t launch_w4a4_narrow(const W4A4Args& g, int rb, int cus, hipStream_t s)
 bool w4a4_narrow_fused(int64_t M, int32_t E);
 hipError_t launch_w4a4_quantize(const W4A4Args& g, uint8_t* codes, uint8_t* scales, bool tiles, int cus, hipStream_t s);
 hipError_t launch_w4a4_tile(const W4A4Args& g, int cus, hipStream_t s);
+// Grouped products with 16-bit weights (see dense.hip): forward, gradient of the
+// activations, gradient of the weights.
+enum DenseDir : int { kDenseFwd = 0, kDenseDgrad = 1, kDenseWgrad = 2 };
+struct DenseArgs {
+  const uint16_t* p;      // a [M, K] (forward), dy [M, N] (gradients)
+  const uint16_t* q;      // w [E, N, K]; the weights' gradient: a [M, K]
+  const int32_t* sizes;   // [E]
+  void* out;              // [M, N], [M, K] or [E, N, K]
+  int64_t M, N, K;
+  int32_t E;
+  int32_t zero_rest;      // rows past the experts' are set to 0 (else left as they are)
+  uint32_t* err;
+};
+// Rows per expert on average up to which the forward streams its weights once per 16 or 32
+// rows instead of running tiles.
+constexpr int64_t kDenseNarrowAvg = 32;
+hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, const DenseArgs& g, int cus, hipStream_t s);
+hipError_t launch_dense_narrow(int dtype, const DenseArgs& g, int cus, hipStream_t s);
 // Router gate: top-k of logits [T, E] with softmax weights, its gradient, and the
 // gradient of the weighted combine (see gate.hip).
 hipError_t launch_route_topk(const void* logits, int dtype, int64_t T, int32_t E, int32_t k, int renorm,

@@ -497,6 +497,35 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
                             const uint8_t* scales2, void* out, int64_t T, int32_t k, int64_t H, int64_t I, int32_t E,
                             void* workspace, size_t workspace_bytes, const geg_opts* opts, hipStream_t stream);
 
+/*
+ * geg_grouped_gemm / geg_grouped_dgrad / geg_grouped_wgrad — the grouped expert products
+ * with 16-bit weights, for experts that are not quantised: the forward pass, the gradient
+ * of the activations and the gradient of the weights,
+ *   out[rows of e, :] = a[rows of e, :] . W_e^T
+ *   dx[rows of e, :]  = dy[rows of e, :] . W_e
+ *   dW_e              = dy[rows of e, :]^T . a[rows of e, :]
+ *   dtype    GEG_BF16 or GEG_F16, of every 16-bit tensor
+ *   a, dx    [M, K], out, dy [M, N]: rows grouped by expert, sizes int32 [E] as above
+ *   w        [E, N, K]; dw [E, N, K] in dw_dtype: dtype, or GEG_F32
+ *   zero_rest  0: rows past sum(sizes) of out / dx are left untouched; else they are set to 0
+ *   workspace  256 bytes (the error word)
+ *   opts     force_path 0 by size, 2 tiles, 4 (forward) the narrow kernel, which runs with at
+ *            most 32 rows per expert on average; kernel_events as usual
+ * Every tensor 16-byte aligned; K % 8 == 0, for the gradients N % 8 == 0, and 256 rows of N or
+ * K values within 0x7FFFFFF0 bytes (an expert's weights may be larger). Products are exact and
+ * summed in fp32, rounded once to nearest even. dW of an expert without rows is 0, for M == 0
+ * all of it. No tensor may overlap another. Deterministic.
+ */
+geg_status geg_grouped_gemm(const void* a, const int32_t* sizes, const void* w, void* out, int32_t dtype, int64_t M,
+                            int64_t N, int64_t K, int32_t E, int32_t zero_rest, void* workspace, size_t workspace_bytes,
+                            const geg_opts* opts, hipStream_t stream);
+geg_status geg_grouped_dgrad(const void* dy, const int32_t* sizes, const void* w, void* dx, int32_t dtype, int64_t M,
+                             int64_t N, int64_t K, int32_t E, int32_t zero_rest, void* workspace,
+                             size_t workspace_bytes, const geg_opts* opts, hipStream_t stream);
+geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes, void* dw, int32_t dtype,
+                             int32_t dw_dtype, int64_t M, int64_t N, int64_t K, int32_t E, void* workspace,
+                             size_t workspace_bytes, const geg_opts* opts, hipStream_t stream);
+
 /* Workspace bytes needed by one call of operation `op` with these sizes and options. */
 size_t geg_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E,
                            const geg_opts* opts);
