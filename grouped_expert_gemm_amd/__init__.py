@@ -30,7 +30,8 @@ __all__ = [
     "DEVERR_BAD_EXPERT_ID",
     "gmxfp4_quantize", "gmxfp4_w4a4_grouped_gemm", "GEG_OP_MXFP4_W4A4", "route_topk", "route_topk_grad", "route_combine_grad",
     "gnf4_moe_layer", "gmxfp4_moe_layer", "router_gate", "dispatch_rows", "combine_rows",
-    "grouped_gemm", "grouped_dgrad", "grouped_wgrad", "grouped_matmul",
+    "grouped_gemm", "grouped_dgrad", "grouped_wgrad", "grouped_matmul", "request_lora",
+    "philox_dropout", "dropout",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -145,6 +146,20 @@ def lib() -> ctypes.CDLL:
                 f = getattr(L, name)
                 f.argtypes, f.restype = dense, ctypes.c_int
             L.geg_grouped_wgrad.argtypes = [_P, _P, _P, _P, _I32, _I32, _I64, _I64, _I64, _I32, _P, _SZ, _P, _P]
+            L.geg_request_lora.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I64, _I32, _I32,
+                                           _P, _SZ, _P]
+            L.geg_request_lora.restype = ctypes.c_int
+            L.geg_request_lora_workspace_bytes.argtypes = [_I64, _I64, _I32]
+            L.geg_request_lora_workspace_bytes.restype = _SZ
+            L.geg_lora_dropout_workspace_bytes.argtypes = [_I32, _I64, _I64, _I64, _I32, _I32]
+            L.geg_lora_dropout_workspace_bytes.restype = _SZ
+            drop = [ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, _P]
+            for fmt in ("gnf4", "gmxfp4"):
+                for way, after in (("gemm", 7), ("dgrad", 9)):   # p, seed, offset, rng behind the scale
+                    f, plain = getattr(L, f"{fmt}_grouped_{way}_lora_dropout"), getattr(L, f"{fmt}_grouped_{way}_lora").argtypes
+                    f.argtypes, f.restype = [*plain[:after], *drop, *plain[after:]], ctypes.c_int
+            L.geg_dropout.argtypes = [_P, _P, _P, _I32, _I64, ctypes.c_double, ctypes.c_uint64, ctypes.c_uint64, _P, _P]
+            L.geg_dropout.restype = ctypes.c_int
             L.geg_workspace_bytes.argtypes = [_I32, _I64, _I64, _I64, _I32, _P]
             L.geg_workspace_bytes.restype = _SZ
             L.geg_workspace_init.argtypes, L.geg_workspace_init.restype = [_P, _SZ, _P], ctypes.c_int
@@ -511,8 +526,18 @@ def _check_lora(x, sizes, lora_a, lora_b):
     return M, N, K, E, r
 
 
+def _lora_call(name, dropout):
+    """The entry point of an adapter call and what dropout = (p, seed, offset) adds to its arguments."""
+    if dropout is None:
+        return getattr(lib(), name), lib().geg_lora_workspace_bytes, ()
+    p, seed, offset = dropout
+    seed, offset, rng = _seed(seed, offset)
+    _require_gpu(rng)
+    return (getattr(lib(), name + "_dropout"), lib().geg_lora_dropout_workspace_bytes, (float(p), seed, offset, _ptr(rng)))
+
+
 def _gemm_lora(fmt, a, sizes, w, scales, lora_a, lora_b, scale, out, u, workspace, opts, stream,
-               check_errors=False):
+               check_errors=False, dropout=None):
     import torch
     M, N, K, E, r = _check_lora(a, sizes, lora_a, lora_b)
     _check_packed(fmt == "nf4", w, scales, E, N, K, "weights", "scales")
@@ -524,9 +549,9 @@ def _gemm_lora(fmt, a, sizes, w, scales, lora_a, lora_b, scale, out, u, workspac
     _check_tensor(u, "u", torch.float32, (M, r))
     _require_gpu(a, sizes, w, scales, lora_a, lora_b, out, u)
     op = GEG_OP_NF4_FWD if fmt == "nf4" else GEG_OP_MXFP4_FWD
-    ws = _workspace(workspace, lib().geg_lora_workspace_bytes(op, M, N, K, E, r), a.device, stream, check_errors)
-    fn = getattr(lib(), "gnf4_grouped_gemm_lora" if fmt == "nf4" else "gmxfp4_grouped_gemm_lora")
-    _check(fn(_ptr(a), _ptr(sizes), _ptr(w), _ptr(scales), _ptr(lora_a), _ptr(lora_b), float(scale), _ptr(out),
+    fn, need, drop = _lora_call("gnf4_grouped_gemm_lora" if fmt == "nf4" else "gmxfp4_grouped_gemm_lora", dropout)
+    ws = _workspace(workspace, need(op, M, N, K, E, r), a.device, stream, check_errors)
+    _check(fn(_ptr(a), _ptr(sizes), _ptr(w), _ptr(scales), _ptr(lora_a), _ptr(lora_b), float(scale), *drop, _ptr(out),
               _ptr(u), M, N, K, E, r, _ptr(ws.buf), ws.nbytes, ctypes.byref(opts) if opts else None, _stream(stream)))
     _check_device_errors(ws, check_errors, stream)
     return out, u
@@ -553,7 +578,7 @@ def gmxfp4_grouped_gemm_lora(a, sizes, blocks, scales, lora_a, lora_b, scale: fl
 
 
 def _dgrad_lora(fmt, dy, sizes, w, scales, x, lora_a, lora_b, u, scale, dx, grad_a, grad_b, workspace, opts,
-                stream, check_errors=False):
+                stream, check_errors=False, dropout=None):
     import torch
     M, N, K, E, r = _check_lora(x, sizes, lora_a, lora_b)
     _check_packed(fmt == "nf4", w, scales, E, N, K, "weights", "scales")
@@ -570,10 +595,10 @@ def _dgrad_lora(fmt, dy, sizes, w, scales, x, lora_a, lora_b, u, scale, dx, grad
     _check_tensor(grad_b, "grad_b", torch.float32, (E, N, r))
     _require_gpu(dy, sizes, w, scales, x, lora_a, lora_b, u, dx, grad_a, grad_b)
     op = GEG_OP_NF4_DGRAD if fmt == "nf4" else GEG_OP_MXFP4_DGRAD
-    ws = _workspace(workspace, lib().geg_lora_workspace_bytes(op, M, N, K, E, r), dy.device, stream, check_errors)
-    fn = getattr(lib(), "gnf4_grouped_dgrad_lora" if fmt == "nf4" else "gmxfp4_grouped_dgrad_lora")
+    fn, need, drop = _lora_call("gnf4_grouped_dgrad_lora" if fmt == "nf4" else "gmxfp4_grouped_dgrad_lora", dropout)
+    ws = _workspace(workspace, need(op, M, N, K, E, r), dy.device, stream, check_errors)
     _check(fn(_ptr(dy), _ptr(sizes), _ptr(w), _ptr(scales), _ptr(x), _ptr(lora_a), _ptr(lora_b), _ptr(u),
-              float(scale), _ptr(dx), _ptr(grad_a), _ptr(grad_b), M, N, K, E, r, _ptr(ws.buf), ws.nbytes,
+              float(scale), *drop, _ptr(dx), _ptr(grad_a), _ptr(grad_b), M, N, K, E, r, _ptr(ws.buf), ws.nbytes,
               ctypes.byref(opts) if opts else None, _stream(stream)))
     _check_device_errors(ws, check_errors, stream)
     return dx, grad_a, grad_b
@@ -599,14 +624,23 @@ def gmxfp4_grouped_dgrad_lora(dy, sizes, blocks, scales, x, lora_a, lora_b, u, s
 
 
 def grouped_linear_lora(a, sizes, w, scales, lora_a, lora_b, scale: float, fmt: str = "nf4",
-                        check_errors: bool = False):
+                        check_errors: bool = False, dropout: float = 0.0, seed=None, offset: int = 0):
     """The grouped 4-bit projection with a trainable low-rank delta at the
     pre-activation point, as a torch autograd op: out = a_e W_e^T + scale *
     (a_e A_e^T) B_e^T per expert. Backward: dA (through the dgrad kernel and the
     adapter kernels), d lora_a, d lora_b (fp32); the 4-bit weights are frozen.
     check_errors=True makes both directions raise GegDeviceError on a flagged
-    device condition (see gnf4_grouped_gemm)."""
-    return _GroupedLinearLora.apply(a, sizes, w, scales, lora_a, lora_b, float(scale), fmt, bool(check_errors))
+    device condition (see gnf4_grouped_gemm). dropout > 0 drops values of the adapter's
+    input (the projection's stays whole) by philox_dropout's mask for seed and offset over
+    a, which both directions draw anew; seed as in dropout()."""
+    if dropout:
+        if seed is None:
+            raise GegError(8, "dropout needs a seed: an int, or a device int64 tensor {seed, offset}")
+        import torch
+        rng = seed if isinstance(seed, torch.Tensor) else None
+        return _GroupedLinearLora.apply(a, sizes, w, scales, lora_a, lora_b, float(scale), fmt, bool(check_errors),
+                                        (float(dropout), None if rng is not None else seed, int(offset)), rng)
+    return _GroupedLinearLora.apply(a, sizes, w, scales, lora_a, lora_b, float(scale), fmt, bool(check_errors), None, None)
 
 
 def grouped_linear(a, sizes, w, scales, fmt: str = "nf4", check_errors: bool = False):
@@ -645,20 +679,25 @@ def _make_grouped_linear_lora():
 
     class GroupedLinearLora(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, a, sizes, w, scales, lora_a, lora_b, scale, fmt, check_errors):
-            fn = gnf4_grouped_gemm_lora if fmt == "nf4" else gmxfp4_grouped_gemm_lora
-            out, u = fn(a, sizes, w, scales, lora_a, lora_b, scale, check_errors=check_errors)
-            ctx.save_for_backward(a, sizes, w, scales, lora_a, lora_b, u)
+        def forward(ctx, a, sizes, w, scales, lora_a, lora_b, scale, fmt, check_errors, dropout, rng):
+            if dropout is not None and rng is not None:
+                dropout = (dropout[0], rng, dropout[2])
+            out, u = _gemm_lora(fmt, a, sizes, w, scales, lora_a, lora_b, scale, None, None, None, None, None,
+                                check_errors, dropout)
+            ctx.save_for_backward(a, sizes, w, scales, lora_a, lora_b, u, *(() if rng is None else (rng,)))
             ctx.fmt, ctx.scale, ctx.check_errors = fmt, scale, check_errors
+            ctx.dropout = None if dropout is None else (dropout[0], None if rng is not None else dropout[1], dropout[2])
             return out
 
         @staticmethod
         def backward(ctx, grad_out):
-            a, sizes, w, scales, lora_a, lora_b, u = ctx.saved_tensors
-            fn = gnf4_grouped_dgrad_lora if ctx.fmt == "nf4" else gmxfp4_grouped_dgrad_lora
-            da, ga, gb = fn(grad_out.contiguous(), sizes, w, scales, a, lora_a, lora_b, u, ctx.scale,
-                            check_errors=ctx.check_errors)
-            return (da if ctx.needs_input_grad[0] else None), None, None, None, ga, gb, None, None, None
+            a, sizes, w, scales, lora_a, lora_b, u, *rng = ctx.saved_tensors
+            dropout = ctx.dropout
+            if rng:
+                dropout = (dropout[0], rng[0], dropout[2])
+            da, ga, gb = _dgrad_lora(ctx.fmt, grad_out.contiguous(), sizes, w, scales, a, lora_a, lora_b, u, ctx.scale,
+                                     None, None, None, None, None, None, ctx.check_errors, dropout)
+            return ((da if ctx.needs_input_grad[0] else None), None, None, None, ga, gb, None, None, None, None, None)
 
     return GroupedLinearLora
 
@@ -1297,3 +1336,123 @@ def grouped_matmul(a, sizes, w, check_errors: bool = False):
     router_gate, dispatch_rows and combine_rows. Rows past sum(sizes) (a padded batch) give
     0 and get 0."""
     return _GroupedMatmul.apply(a, sizes, w, bool(check_errors))
+
+
+# ----------------------------------------------------------------------------- adapters of many requests
+def _pitch(t, name, dtype, shape):
+    """Row pitch of a 2-D tensor of contiguous rows (a slice of columns, say)."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or (shape[1] > 1 and t.stride(1) != 1) or \
+            (shape[0] > 1 and t.stride(0) < shape[1]):
+        raise GegError(2, f"{name}: expected a {dtype} tensor of shape {list(shape)} with contiguous rows, got "
+                          f"{t.dtype} {list(t.shape)} of strides {list(t.stride())}")
+    return t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def request_lora(y, x, ids, lora_a, lora_b, scales=None, out=None, workspace: Workspace | None = None, stream=None,
+                 check_errors: bool = False):
+    """Low-rank adapters of many requests beside a projection that they share: out [M, N] =
+    y + scales[i] (x A_i^T) B_i^T with each row's own adapter i = ids[t], ids int32 [M] in any
+    order (negative: none). y [M, N] (what the projection gave; None for zeros), x [M, K],
+    lora_a [L, r, K] and lora_b [L, N, r] of one type, bf16 or fp16; scales fp32 [L] or None;
+    r 8, 16, ..., 128. out=y adds in place. x, y and out may be slices of columns (rows that
+    start at multiples of 16 bytes). For rows routed to experts with adapters of their own:
+    ids = adapter * E + expert over lora_a [adapters * E, r, K]."""
+    import torch
+    dt = _dtype16(x, "x")
+    if x.dim() != 2 or lora_a.dim() != 3 or lora_b.dim() != 3:
+        raise GegError(2, "x: expected [M, K], lora_a [L, r, K], lora_b [L, N, r]")
+    M, K = x.shape
+    L, r = lora_a.shape[0], lora_a.shape[1]
+    N = lora_b.shape[1]
+    ldx = _pitch(x, "x", x.dtype, (M, K))
+    ldy = 0 if y is None else _pitch(y, "y", x.dtype, (M, N))
+    _check_tensor(ids, "ids", torch.int32, (M,))
+    _check_tensor(lora_a, "lora_a", x.dtype, (L, r, K))
+    _check_tensor(lora_b, "lora_b", x.dtype, (L, N, r))
+    _check_tensor(scales, "scales", torch.float32, (L,))
+    ldo = N if out is None else _pitch(out, "out", x.dtype, (M, N))
+    _on_device(x, y, ids, lora_a, lora_b, scales, out)
+    mine = out is None
+    raw = _raw_stream(stream, x)
+    lib_ = lib()
+    with _allocating(stream):
+        if mine:
+            out = x.new_empty((M, N))
+        ws = _workspace(workspace, lib_.geg_request_lora_workspace_bytes(M, K, r), x.device, None, check_errors)
+    _check(lib_.geg_request_lora(_addr(y), ldy, x.data_ptr(), ldx, ids.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(),
+                                 _addr(scales), out.data_ptr(), ldo, dt, M, N, K, L, r, ws.buf.data_ptr(), ws.buf.numel(),
+                                 raw))
+    if mine:
+        _outlive(stream, out)
+    _check_device_errors(ws, check_errors, stream)
+    return out
+
+
+# ----------------------------------------------------------------------------- dropout
+def _seed(seed, offset):
+    """(seed, offset, rng tensor or None) of a seed given as an int or as a device int64 tensor
+    {seed, offset}, whose offset the given one is added to."""
+    import torch
+    if isinstance(seed, torch.Tensor):
+        _check_tensor(seed, "seed", torch.int64, (2,))
+        return 0, int(offset) & 0xFFFFFFFFFFFFFFFF, seed
+    return int(seed) & 0xFFFFFFFFFFFFFFFF, int(offset) & 0xFFFFFFFFFFFFFFFF, None
+
+
+def philox_dropout(x, p: float, seed, offset: int = 0, residual=None, out=None, stream=None):
+    """Dropout from a counter-based generator (Philox4x32-10), its mask never stored: out =
+    [residual +] x / (1 - p) where value i's 16 random bits are at least round(65536 p), else
+    [residual +] 0 (1 - p as those bits have it). The mask follows from seed, offset and i
+    alone: the same call over a gradient drops the same values. seed: an int, or an int64
+    tensor {seed, offset} on the device, whose offset `offset` is added to and which a captured
+    call reads anew on every replay. bf16, fp16 or fp32; out may be x or residual."""
+    dt = _dtype(x, "x")
+    seed, offset, rng = _seed(seed, offset)
+    if not x.is_contiguous():
+        raise GegError(2, f"x: expected a contiguous tensor, got strides {list(x.stride())} of shape {list(x.shape)}")
+    _check_tensor(residual, "residual", x.dtype, x.shape)
+    _check_tensor(out, "out", x.dtype, x.shape)
+    _on_device(x, residual, out, rng)
+    mine = out is None
+    if mine:
+        with _allocating(stream):
+            out = x.new_empty(x.shape)
+    _check(lib().geg_dropout(x.data_ptr(), _addr(residual), out.data_ptr(), dt, x.numel(), float(p), seed, offset,
+                             _addr(rng), _raw_stream(stream, x)))
+    if mine:
+        _outlive(stream, out)
+    return out
+
+
+def _make_dropout():
+    import torch
+
+    class Dropout(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, p, seed, offset, residual):
+            ctx.p, ctx.offset = p, offset
+            ctx.seed = None if isinstance(seed, torch.Tensor) else seed
+            ctx.save_for_backward(*(() if ctx.seed is not None else (seed,)))
+            return philox_dropout(x, p, seed, offset, residual)
+
+        @staticmethod
+        @torch.autograd.function.once_differentiable
+        def backward(ctx, dout):
+            seed = ctx.seed if ctx.seed is not None else ctx.saved_tensors[0]
+            dx = None
+            if ctx.needs_input_grad[0]:
+                dx = philox_dropout(dout.contiguous(), ctx.p, seed, ctx.offset)
+            return dx, None, None, None, dout if ctx.needs_input_grad[4] else None
+
+    return Dropout
+
+
+_Dropout = _LazyFn(_make_dropout)
+
+
+def dropout(x, p: float, seed, offset: int = 0, residual=None):
+    """philox_dropout as a torch autograd op, differentiable with respect to x and the
+    residual. A seed given as a tensor must keep its values until the backward pass is done
+    (torch refuses the backward pass of one changed in place): layers of one step take
+    different offsets, the next step's values are set after the backward pass."""
+    return _Dropout.apply(x, float(p), seed, int(offset), residual)

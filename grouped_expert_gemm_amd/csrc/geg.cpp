@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdio>
 #include <cstring>
 #include <functional>
@@ -281,6 +282,7 @@ struct LoraIn {
   const float* q = nullptr;
   int32_t r = 0;
   float s = 0.f;
+  const geg::DropoutArgs* drop = nullptr;   // dgrad: masks the delta
   std::function<hipError_t()> pre;
   std::function<hipError_t()> post;
 };
@@ -353,6 +355,7 @@ geg_status gemm_common(int fmt, const void* a, const int32_t* sizes, const uint8
   g.lora_q = lora.q;
   g.lora_r = lora.r;
   g.lora_s = lora.s;
+  g.lora_drop = 0;
   if (lora.pre) {
     hipError_t e = lora.pre();
     if (e != hipSuccess) return hip_fail(e, "adapter launch");
@@ -509,6 +512,8 @@ geg_status dgrad_common(int fmt, const void* dy, const int32_t* sizes, const uin
   g.lora_q = lora.q;
   g.lora_r = lora.r;
   g.lora_s = lora.s;
+  g.lora_drop = lora.drop != nullptr;
+  if (lora.drop) g.drop = *lora.drop;
   g.split = 1;
   g.glu = 0;
   g.tail_part = p.tail_bytes ? reinterpret_cast<float*>(wsb + p.tail_off) : nullptr;
@@ -735,6 +740,13 @@ geg_status gmxfp8_quantize(const void* a, uint8_t* codes, uint8_t* scales, int64
   return GEG_OK;
 }
 
+size_t geg_lora_dropout_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r) {
+  const size_t plain = geg_lora_workspace_bytes(op, M, N, K, E, r);
+  // the backward's masked activations
+  const bool back = op == GEG_OP_NF4_DGRAD || op == GEG_OP_MXFP4_DGRAD;
+  return plain && back ? plain + round256((size_t)M * (size_t)K * 2) : plain;
+}
+
 size_t geg_lora_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r) {
   if (M < 0 || N <= 0 || K <= 0 || E <= 0 || r <= 0) return 0;
   Plan p;
@@ -766,7 +778,7 @@ geg_status lora_args(int32_t r, const float* lora_a, const float* lora_b) {
 geg_status gemm_lora(int fmt, const void* a, const int32_t* sizes, const uint8_t* w, const void* scales,
                      const float* lora_a, const float* lora_b, float scale, void* out, void* u, int64_t M, int64_t N,
                      int64_t K, int32_t E, int32_t r, void* workspace, size_t workspace_bytes, const geg_opts* opts,
-                     hipStream_t stream) {
+                     hipStream_t stream, const geg::DropoutArgs* drop = nullptr) {
   CuScope cu_scope(opts);
   geg_status st = check_shape(M, N, K, E, fmt == geg::NF4 ? 64 : 32);
   if (st != GEG_OK) return st;
@@ -779,13 +791,13 @@ geg_status gemm_lora(int fmt, const void* a, const int32_t* sizes, const uint8_t
   L.u = reinterpret_cast<const float*>(u);
   L.q = lora_b;
   L.r = r;
-  L.s = scale;
+  L.s = drop ? scale * drop->scale : scale;
   // u = x A_e^T first; the tiled kernel's epilogue then adds s u B_e^T
   L.pre = [=]() -> hipError_t {
     ++g_launches;
     return geg::launch_lora_down(reinterpret_cast<const uint16_t*>(a), lora_a, sizes, E, M, K, r, 1.0f,
                                  reinterpret_cast<float*>(u), reinterpret_cast<uint32_t*>(workspace), cu_count(),
-                                 stream);
+                                 stream, drop);
   };
   return gemm_common(fmt, a, sizes, w, scales, out, M, N, K, E, workspace, workspace_bytes, opts, stream, 0, L);
 }
@@ -793,7 +805,8 @@ geg_status gemm_lora(int fmt, const void* a, const int32_t* sizes, const uint8_t
 geg_status dgrad_lora(int fmt, const void* dy, const int32_t* sizes, const uint8_t* w, const void* scales,
                       const void* x, const float* lora_a, const float* lora_b, const void* u, float scale, void* dx,
                       float* grad_a, float* grad_b, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r,
-                      void* workspace, size_t workspace_bytes, const geg_opts* opts, hipStream_t stream) {
+                      void* workspace, size_t workspace_bytes, const geg_opts* opts, hipStream_t stream,
+                      const geg::DropoutArgs* drop = nullptr) {
   CuScope cu_scope(opts);
   geg_status st = check_shape(M, N, K, E, fmt == geg::NF4 ? 64 : 32);
   if (st != GEG_OK) return st;
@@ -805,9 +818,13 @@ geg_status dgrad_lora(int fmt, const void* dy, const int32_t* sizes, const uint8
   if (M > 0 && (!aligned(x, 16) || !aligned(u, 16))) return fail(GEG_ERR_MISALIGNED, "x and u must be 16-byte aligned");
   if (!workspace) return fail(GEG_ERR_WORKSPACE, "workspace is NULL");
   if (!aligned(workspace, 256)) return fail(GEG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  const size_t need = geg_lora_workspace_bytes(fmt == geg::NF4 ? GEG_OP_NF4_DGRAD : GEG_OP_MXFP4_DGRAD, M, N, K, E, r);
+  const int32_t op = fmt == geg::NF4 ? GEG_OP_NF4_DGRAD : GEG_OP_MXFP4_DGRAD;
+  const size_t plain = geg_lora_workspace_bytes(op, M, N, K, E, r);
+  const size_t need = drop ? geg_lora_dropout_workspace_bytes(op, M, N, K, E, r) : plain;
   if (workspace_bytes < need)
-    return fail(GEG_ERR_WORKSPACE, "workspace smaller than geg_lora_workspace_bytes(): need " + std::to_string(need));
+    return fail(GEG_ERR_WORKSPACE, std::string("workspace smaller than ") +
+                                       (drop ? "geg_lora_dropout_workspace_bytes" : "geg_lora_workspace_bytes") +
+                                       "(): need " + std::to_string(need));
   if ((st = check_device()) != GEG_OK) return st;
   for (auto [ptr, name] : {std::pair<const void*, const char*>{grad_a, "grad_a"}, {grad_b, "grad_b"},
                            {sizes, "sizes"}, {workspace, "workspace"}})
@@ -828,13 +845,21 @@ geg_status dgrad_lora(int fmt, const void* dy, const int32_t* sizes, const uint8
                                       round256((size_t)E * K * r * 4));              // [M, r]
   const int cus = cu_count();
   const uint16_t* dy16 = reinterpret_cast<const uint16_t*>(dy);
+  if (drop) scale *= drop->scale;
+  const uint16_t* x16 = reinterpret_cast<const uint16_t*>(x);
+  uint16_t* xm = drop ? reinterpret_cast<uint16_t*>(wsb + plain) : nullptr;   // the masked activations
+  geg::DropoutArgs mask = drop ? *drop : geg::DropoutArgs{};
+  mask.scale = 1.0f;
   // adapter gradients (zeros for experts without rows, and for M == 0)
   auto grads = [=]() -> hipError_t {
     hipError_t e = geg::launch_lora_grad(dy16, reinterpret_cast<const float*>(u), sizes, E, M, N, r, scale, grad_b,
                                          false, err, cus, stream);
+    if (e == hipSuccess && xm && M > 0) {
+      e = geg::launch_dropout(x16, nullptr, xm, geg::kBF16, M * K, mask, cus, stream);
+      ++g_launches;
+    }
     if (e == hipSuccess)
-      e = geg::launch_lora_grad(reinterpret_cast<const uint16_t*>(x), g, sizes, E, M, K, r, 1.0f, grad_a, true, err,
-                                cus, stream);
+      e = geg::launch_lora_grad(xm ? xm : x16, g, sizes, E, M, K, r, 1.0f, grad_a, true, err, cus, stream);
     g_launches += 2;
     return e;
   };
@@ -846,6 +871,7 @@ geg_status dgrad_lora(int fmt, const void* dy, const int32_t* sizes, const uint8
   L.u = g;
   L.q = At;
   L.r = r;
+  L.drop = drop;
   L.s = 1.0f;
   // g = s dy B_e (from a transposed copy of B) and a transposed copy of A first;
   // the dgrad epilogue adds g A_e; the gradients after
@@ -1217,6 +1243,155 @@ geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes
                              size_t workspace_bytes, const geg_opts* opts, hipStream_t stream) {
   return dense_common(geg::kDenseWgrad, dy, "dy", a, "a", sizes, dw, "dw", dtype, dw_dtype, M, N, K, E, 0, workspace,
                       workspace_bytes, opts, stream);
+}
+
+size_t geg_request_lora_workspace_bytes(int64_t M, int64_t K, int32_t r) {
+  if (M < 0 || K <= 0 || r <= 0 || r > geg::kRequestMaxRank || M >= (int64_t)INT32_MAX) return 0;
+  return kHeader + round256((size_t)geg::request_splits(M, K, r) * (size_t)M * (size_t)r * 4);
+}
+
+geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t ldx, const int32_t* ids,
+                            const void* lora_a, const void* lora_b, const float* scales, void* out, int64_t ldo,
+                            int32_t dtype, int64_t M, int64_t N, int64_t K, int32_t L, int32_t r, void* ws,
+                            size_t ws_bytes, hipStream_t stream) {
+  if (dtype != GEG_BF16 && dtype != GEG_F16) return fail(GEG_ERR_BAD_OPTION, "dtype must be GEG_BF16 or GEG_F16");
+  if (M < 0 || N <= 0 || K <= 0 || L <= 0) return fail(GEG_ERR_BAD_SHAPE, "need M >= 0, N > 0, K > 0, L > 0");
+  if (M >= (int64_t)INT32_MAX) return fail(GEG_ERR_BAD_SHAPE, "M must be below 2^31");
+  if (N % 8 || K % 8) return fail(GEG_ERR_BAD_SHAPE, "N and K must be multiples of 8");
+  if (r < 8 || r > geg::kRequestMaxRank || r % 8)
+    return fail(GEG_ERR_BAD_SHAPE, "the adapters' rank r must be 8, 16, ..., 128");
+  if ((y && ldy < N) || ldx < K || ldo < N) return fail(GEG_ERR_BAD_SHAPE, "a row pitch must be at least the row's width");
+  if (std::max({N, K, y ? ldy : N, ldx, ldo}) > kMaxWindow / 512)
+    return fail(GEG_ERR_BAD_SHAPE, "256 rows of 16-bit values, pitch included, must fit in 0x7FFFFFF0 bytes");
+  // a launch holds fewer than 2^32 threads: a workgroup of 256 per 32 rows, a wavefront per 32 rows and 64 columns
+  if ((M + 15) / 16 * ((N + 63) / 64) > (int64_t)1 << 24)
+    return fail(GEG_ERR_BAD_SHAPE, "ceil(M / 16) * ceil(N / 64) must not exceed 2^24");
+  if (M == 0) return GEG_OK;
+  if (!x || !ids || !lora_a || !lora_b || !out) return fail(GEG_ERR_NULL_POINTER, "a required pointer is NULL");
+  if (!ws) return fail(GEG_ERR_WORKSPACE, "workspace is NULL");
+  if (out == x) return fail(GEG_ERR_BAD_OPTION, "out may not be x");
+  if (y && y == out && M > 1 && ldy != ldo) return fail(GEG_ERR_BAD_OPTION, "in place, y and out have one row pitch");
+  if (!aligned(y, 16) || !aligned(x, 16) || !aligned(lora_a, 16) || !aligned(lora_b, 16) || !aligned(out, 16) ||
+      (M > 1 && ((y && ldy % 8) || ldx % 8 || ldo % 8)) || !aligned(ids, 4) || !aligned(scales, 4))
+    return fail(GEG_ERR_MISALIGNED, "y, x, lora_a, lora_b, out and their row pitches must be 16-byte aligned");
+  if (!aligned(ws, 256)) return fail(GEG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  const size_t need = geg_request_lora_workspace_bytes(M, K, r);
+  if (ws_bytes < need)
+    return fail(GEG_ERR_WORKSPACE, "workspace smaller than geg_request_lora_workspace_bytes(): need " + std::to_string(need));
+  geg_status st;
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{y, "y"}, {x, "x"}, {ids, "ids"}, {lora_a, "lora_a"},
+                           {lora_b, "lora_b"}, {scales, "scales"}, {out, "out"}, {ws, "workspace"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  uint8_t* wsb = reinterpret_cast<uint8_t*>(ws);
+  geg::RequestArgs g{reinterpret_cast<const uint16_t*>(y), reinterpret_cast<const uint16_t*>(x), ids,
+                     reinterpret_cast<const uint16_t*>(lora_a), reinterpret_cast<const uint16_t*>(lora_b), scales,
+                     reinterpret_cast<uint16_t*>(out), reinterpret_cast<float*>(wsb + kHeader),
+                     // a single row has no pitch
+                     M == 1 ? N : ldy, M == 1 ? K : ldx, M == 1 ? N : ldo, M, N, K, L, r,
+                     geg::request_splits(M, K, r), reinterpret_cast<uint32_t*>(wsb)};
+  hipError_t e = geg::launch_request_lora(g, dtype, stream);
+  if (e != hipSuccess) return hip_fail(e, "request adapter launch");
+  g_launches += 2;
+  return GEG_OK;
+}
+
+// The threshold of 16 random bits for the drop probability p, and what kept values are multiplied by.
+static geg_status dropout_args(double p, uint64_t seed, uint64_t offset, const uint64_t* rng, geg::DropoutArgs& d) {
+  if (!(p >= 0.0 && p <= 1.0)) return fail(GEG_ERR_BAD_OPTION, "p must lie in [0, 1]");
+  if (!aligned(rng, 8)) return fail(GEG_ERR_MISALIGNED, "rng must be 8-byte aligned");
+  d.seed = seed;
+  d.offset = offset;
+  d.dev = rng;
+  d.threshold = (uint32_t)std::nearbyint(p * 65536.0);
+  d.scale = d.threshold < 65536 ? (float)(65536.0 / (65536.0 - d.threshold)) : 0.f;
+  return GEG_OK;
+}
+
+geg_status geg_dropout(const void* x, const void* residual, void* out, int32_t dtype, int64_t n, double p, uint64_t seed,
+                       uint64_t offset, const uint64_t* rng, hipStream_t stream) {
+  if (dtype < GEG_BF16 || dtype > GEG_F32) return fail(GEG_ERR_BAD_OPTION, "dtype must be GEG_BF16, GEG_F16 or GEG_F32");
+  if (n < 0 || n > (int64_t)1 << 48) return fail(GEG_ERR_BAD_SHAPE, "need 0 <= n <= 2^48");
+  geg::DropoutArgs d;
+  geg_status st;
+  if ((st = dropout_args(p, seed, offset, rng, d)) != GEG_OK) return st;
+  if (n == 0) return GEG_OK;
+  if (!x || !out) return fail(GEG_ERR_NULL_POINTER, "x and out are required");
+  const size_t size = dtype_bytes(dtype);
+  if (!aligned(x, size) || !aligned(residual, size) || !aligned(out, size))
+    return fail(GEG_ERR_MISALIGNED, "x, residual and out must be aligned to their elements");
+  if ((st = check_device()) != GEG_OK) return st;
+  for (auto [ptr, name] : {std::pair<const void*, const char*>{x, "x"}, {residual, "residual"}, {out, "out"}, {rng, "rng"}})
+    if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
+  hipError_t e = geg::launch_dropout(x, residual, out, dtype, n, d, cu_count(), stream);
+  if (e != hipSuccess) return hip_fail(e, "dropout launch");
+  ++g_launches;
+  return GEG_OK;
+}
+
+static geg_status gemm_lora_dropout(int fmt, const void* a, const int32_t* sizes, const uint8_t* w, const void* scales,
+                                    const float* lora_a, const float* lora_b, float scale, double p, uint64_t seed,
+                                    uint64_t offset, const uint64_t* rng, void* out, void* u, int64_t M, int64_t N,
+                                    int64_t K, int32_t E, int32_t r, void* workspace, size_t workspace_bytes,
+                                    const geg_opts* opts, hipStream_t stream) {
+  geg::DropoutArgs d;
+  geg_status st;
+  if ((st = dropout_args(p, seed, offset, rng, d)) != GEG_OK) return st;
+  if ((st = check_device_ptr(rng, "rng")) != GEG_OK) return st;
+  return gemm_lora(fmt, a, sizes, w, scales, lora_a, lora_b, scale, out, u, M, N, K, E, r, workspace, workspace_bytes, opts,
+                   stream, &d);
+}
+
+static geg_status dgrad_lora_dropout(int fmt, const void* dy, const int32_t* sizes, const uint8_t* w, const void* scales,
+                                     const void* x, const float* lora_a, const float* lora_b, const void* u, float scale,
+                                     double p, uint64_t seed, uint64_t offset, const uint64_t* rng, void* dx,
+                                     float* grad_a, float* grad_b, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r,
+                                     void* workspace, size_t workspace_bytes, const geg_opts* opts, hipStream_t stream) {
+  geg::DropoutArgs d;
+  geg_status st;
+  if ((st = dropout_args(p, seed, offset, rng, d)) != GEG_OK) return st;
+  if ((st = check_device_ptr(rng, "rng")) != GEG_OK) return st;
+  return dgrad_lora(fmt, dy, sizes, w, scales, x, lora_a, lora_b, u, scale, dx, grad_a, grad_b, M, N, K, E, r, workspace,
+                    workspace_bytes, opts, stream, &d);
+}
+
+geg_status gnf4_grouped_gemm_lora_dropout(const void* a, const int32_t* sizes, const uint8_t* w, const float* absmax,
+                                          const float* lora_a, const float* lora_b, float scale, double p, uint64_t seed,
+                                          uint64_t offset, const uint64_t* rng, void* out, void* u, int64_t M, int64_t N,
+                                          int64_t K, int32_t E, int32_t r, void* workspace, size_t workspace_bytes,
+                                          const geg_opts* opts, hipStream_t stream) {
+  return gemm_lora_dropout(geg::NF4, a, sizes, w, absmax, lora_a, lora_b, scale, p, seed, offset, rng, out, u, M, N, K, E,
+                           r, workspace, workspace_bytes, opts, stream);
+}
+
+geg_status gmxfp4_grouped_gemm_lora_dropout(const void* a, const int32_t* sizes, const uint8_t* blocks,
+                                            const uint8_t* scales, const float* lora_a, const float* lora_b, float scale,
+                                            double p, uint64_t seed, uint64_t offset, const uint64_t* rng, void* out,
+                                            void* u, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r,
+                                            void* workspace, size_t workspace_bytes, const geg_opts* opts,
+                                            hipStream_t stream) {
+  return gemm_lora_dropout(geg::MXFP4, a, sizes, blocks, scales, lora_a, lora_b, scale, p, seed, offset, rng, out, u, M, N,
+                           K, E, r, workspace, workspace_bytes, opts, stream);
+}
+
+geg_status gnf4_grouped_dgrad_lora_dropout(const void* dy, const int32_t* sizes, const uint8_t* w, const float* absmax,
+                                           const void* x, const float* lora_a, const float* lora_b, const void* u,
+                                           float scale, double p, uint64_t seed, uint64_t offset, const uint64_t* rng,
+                                           void* dx, float* grad_a, float* grad_b, int64_t M, int64_t N, int64_t K,
+                                           int32_t E, int32_t r, void* workspace, size_t workspace_bytes,
+                                           const geg_opts* opts, hipStream_t stream) {
+  return dgrad_lora_dropout(geg::NF4, dy, sizes, w, absmax, x, lora_a, lora_b, u, scale, p, seed, offset, rng, dx, grad_a,
+                            grad_b, M, N, K, E, r, workspace, workspace_bytes, opts, stream);
+}
+
+geg_status gmxfp4_grouped_dgrad_lora_dropout(const void* dy, const int32_t* sizes, const uint8_t* blocks,
+                                             const uint8_t* scales, const void* x, const float* lora_a,
+                                             const float* lora_b, const void* u, float scale, double p, uint64_t seed,
+                                             uint64_t offset, const uint64_t* rng, void* dx, float* grad_a, float* grad_b,
+                                             int64_t M, int64_t N, int64_t K, int32_t E, int32_t r, void* workspace,
+                                             size_t workspace_bytes, const geg_opts* opts, hipStream_t stream) {
+  return dgrad_lora_dropout(geg::MXFP4, dy, sizes, blocks, scales, x, lora_a, lora_b, u, scale, p, seed, offset, rng, dx,
+                            grad_a, grad_b, M, N, K, E, r, workspace, workspace_bytes, opts, stream);
 }
 
 size_t geg_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E,

@@ -39,6 +39,15 @@ constexpr int64_t kVecOneRowM = 8;   // batches up to this many rows: one row pe
 constexpr int kTileM = 256;
 constexpr int kTileN = 256;
 
+// A dropout mask (philox.hpp). With `dev` the key and the offset's base come from there (uint64
+// {seed, offset}), so that a captured graph draws new masks on every replay.
+struct DropoutArgs {
+  uint64_t seed, offset;
+  const uint64_t* dev;
+  uint32_t threshold;   // a value is dropped where its 16 bits are below; 65536: every one
+  float scale;          // 1 / (1 - threshold / 65536); 0 if every value is dropped
+};
+
 struct GemmArgs {
   const uint16_t* a;      // bf16 [M, K]
   const uint16_t* a16;    // NF4 tile path: the activations as fp16 in NF4 slot order, each
@@ -74,6 +83,8 @@ struct GemmArgs {
   const float* lora_q;
   int32_t lora_r;
   float lora_s;
+  int32_t lora_drop;      // 1 (dgrad): the delta is masked by `drop` over [M, output width]
+  DropoutArgs drop;
 };
 
 // Each launcher returns the hipError_t of its launch.
@@ -157,6 +168,26 @@ struct DenseArgs {
 constexpr int64_t kDenseNarrowAvg = 32;
 hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, const DenseArgs& g, int cus, hipStream_t s);
 hipError_t launch_dense_narrow(int dtype, const DenseArgs& g, int cus, hipStream_t s);
+// Low-rank adapters of many requests beside a shared projection (see request.hip).
+constexpr int kRequestMaxRank = 128;
+struct RequestArgs {
+  const uint16_t* y;      // [M, N], rows ldy apart, or NULL: zeros
+  const uint16_t* x;      // [M, K], rows ldx apart
+  const int32_t* ids;     // [M]: each row's adapter; negative: none
+  const uint16_t* a;      // [L, r, K]
+  const uint16_t* b;      // [L, N, r]
+  const float* scales;    // [L] or NULL: ones
+  uint16_t* out;          // [M, N], rows ldo apart; may be y
+  float* u;               // workspace: partial x A^T [splits, M, r]
+  int64_t ldy, ldx, ldo, M, N, K;
+  int32_t L, r, splits;
+  uint32_t* err;
+};
+int request_splits(int64_t M, int64_t K, int32_t r);
+hipError_t launch_request_lora(const RequestArgs& g, int dtype, hipStream_t s);
+// Dropout: out = [res +] keep ? x * scale : 0 for n values (see dropout.hip, philox.hpp).
+hipError_t launch_dropout(const void* x, const void* res, void* out, int dtype, int64_t n, const DropoutArgs& d, int cus,
+                          hipStream_t s);
 // Router gate: top-k of logits [T, E] with softmax weights, its gradient, and the
 // gradient of the weighted combine (see gate.hip).
 hipError_t launch_route_topk(const void* logits, int dtype, int64_t T, int32_t E, int32_t k, int renorm,
@@ -195,7 +226,8 @@ hipError_t launch_moe_layer(int fmt, const MoeArgs& g, int cus, hipStream_t s);
 // for fp32 [E, P, Qd]. The delta U Q^T itself is added in the tiled kernel's
 // epilogue (GemmArgs::lora_*).
 hipError_t launch_lora_down(const uint16_t* X, const float* T, const int32_t* sizes, int32_t E, int64_t M, int64_t C,
-                            int32_t r, float s, float* U, uint32_t* err, int cus, hipStream_t st);
+                            int32_t r, float s, float* U, uint32_t* err, int cus, hipStream_t st,
+                            const DropoutArgs* drop = nullptr);   // X with a dropout mask (unscaled)
 hipError_t launch_lora_grad(const uint16_t* Wd, const float* Nw, const int32_t* sizes, int32_t E, int64_t M,
                             int64_t Wc, int32_t r, float s, float* G, bool jc, uint32_t* err, int cus, hipStream_t st);
 hipError_t launch_lora_transpose(const float* in, int64_t E, int64_t P, int64_t Qd, float* out, int cus,

@@ -15,10 +15,20 @@
 // backward gets that from transposed fp32 copies of A and B. The reductions
 // over rows for the adapter gradients run on the vector ALUs, one thread per
 // column of the wide operand.
+//
+// Dropout of the adapter's input (the projection's stays whole): with the mask m of philox.hpp
+// over x's M K values and s' = s / (1 - p),
+//   forward   u = (m x) A_e^T;  y += s' u B_e^T
+//   backward  g = s' dy B_e;  dx += m (g A_e);  dB_e = s' sum_rows dy^T u;
+//             dA_e = sum_rows g^T (m x)
+// Masking x is exact, the factor stays in fp32, and the tiled kernel masks the delta in its
+// epilogue, so dx is rounded once. A lane of the x A^T pass loads just the 8 values that one
+// generator call covers.
 #include <algorithm>
 
 #include "geg_device.hpp"
 #include "geg_launch.hpp"
+#include "philox.hpp"
 
 namespace geg {
 
@@ -62,11 +72,12 @@ __device__ __forceinline__ Split8x3 load8_split3(const __amdgpu_buffer_rsrc_t& R
 // partial when r % 16 == 8); its four wavefronts take interleaved batches of the
 // contraction and are summed through LDS in wave order (deterministic).
 // C % 8 == 0; rows past the expert read zeros.
-template <int NCB>
+// DROP: X with the mask of `drop`.
+template <int NCB, bool DROP>
 __global__ __launch_bounds__(kThreads) void lora_down_kernel(const uint16_t* __restrict__ X, const float* __restrict__ T,
                                                              const int32_t* __restrict__ sizes, int32_t E, int64_t M,
                                                              int64_t C, int32_t r, float s, float* __restrict__ U,
-                                                             uint32_t* err) {
+                                                             uint32_t* err, DropoutArgs drop) {
   __shared__ Plan plan;
   __shared__ f32x4 red[3][NCB][64];
   const int32_t total = build_plan(plan, sizes, E, M, err, [](int32_t n) -> int32_t { return (n + 15) / 16; });
@@ -99,6 +110,14 @@ __global__ __launch_bounds__(kThreads) void lora_down_kernel(const uint16_t* __r
       }
 #pragma unroll
       for (int q = 0; q < kU; ++q) {
+        if constexpr (DROP) {
+          uint32_t w[4];
+          PhiloxState(drop).bits((uint64_t)((row0 + r16) * C + c00 + 32 * q + 8 * g) >> 3, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            a[q][i] &= (philox_kept(w, 2 * i, drop.threshold) ? 0xFFFFu : 0u) |
+                       (philox_kept(w, 2 * i + 1, drop.threshold) ? 0xFFFF0000u : 0u);
+        }
 #pragma unroll
         for (int cb = 0; cb < NCB; ++cb) {
           acc[cb] = mfma16<MXFP4>(a[q], b[q][cb].hi, acc[cb]);
@@ -221,18 +240,29 @@ __global__ __launch_bounds__(kThreads) void lora_transpose_kernel(const float* _
 
 }  // namespace
 
+template <int NCB>
+hipError_t launch_down(const uint16_t* X, const float* T, const int32_t* sizes, int32_t E, int64_t M, int64_t C, int32_t r,
+                       float s, float* U, uint32_t* err, int64_t grid, const DropoutArgs* drop, hipStream_t st) {
+  if (drop)
+    hipLaunchKernelGGL((lora_down_kernel<NCB, true>), dim3((unsigned)grid), dim3(kThreads), 0, st, X, T, sizes, E, M, C, r,
+                       s, U, err, *drop);
+  else
+    hipLaunchKernelGGL((lora_down_kernel<NCB, false>), dim3((unsigned)grid), dim3(kThreads), 0, st, X, T, sizes, E, M, C,
+                       r, s, U, err, DropoutArgs{});
+  return hipGetLastError();
+}
+
 hipError_t launch_lora_down(const uint16_t* X, const float* T, const int32_t* sizes, int32_t E, int64_t M, int64_t C,
-                            int32_t r, float s, float* U, uint32_t* err, int cus, hipStream_t st) {
+                            int32_t r, float s, float* U, uint32_t* err, int cus, hipStream_t st, const DropoutArgs* drop) {
   const int64_t units = (M + 15) / 16 + std::min<int64_t>(E, M);
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(units, (int64_t)cus * 16));
   switch ((r + 15) / 16) {
-    case 1: hipLaunchKernelGGL(lora_down_kernel<1>, dim3((unsigned)grid), dim3(kThreads), 0, st, X, T, sizes, E, M, C, r, s, U, err); break;
-    case 2: hipLaunchKernelGGL(lora_down_kernel<2>, dim3((unsigned)grid), dim3(kThreads), 0, st, X, T, sizes, E, M, C, r, s, U, err); break;
-    case 3: hipLaunchKernelGGL(lora_down_kernel<3>, dim3((unsigned)grid), dim3(kThreads), 0, st, X, T, sizes, E, M, C, r, s, U, err); break;
-    case 4: hipLaunchKernelGGL(lora_down_kernel<4>, dim3((unsigned)grid), dim3(kThreads), 0, st, X, T, sizes, E, M, C, r, s, U, err); break;
+    case 1: return launch_down<1>(X, T, sizes, E, M, C, r, s, U, err, grid, drop, st);
+    case 2: return launch_down<2>(X, T, sizes, E, M, C, r, s, U, err, grid, drop, st);
+    case 3: return launch_down<3>(X, T, sizes, E, M, C, r, s, U, err, grid, drop, st);
+    case 4: return launch_down<4>(X, T, sizes, E, M, C, r, s, U, err, grid, drop, st);
     default: return hipErrorInvalidValue;
   }
-  return hipGetLastError();
 }
 
 template <bool JC>

@@ -28,6 +28,7 @@
 
 #include "geg_device.hpp"
 #include "geg_launch.hpp"
+#include "philox.hpp"
 
 namespace geg {
 
@@ -572,7 +573,24 @@ __device__ __forceinline__ TailPlan tail_plan(int32_t total0, int32_t total1, in
   return S > 1 ? TailPlan{total1 - r, S} : none;
 }
 
-template <Fmt F, bool DG, bool TAIL>
+// acc += a 16 x 16 block of the adapter delta over 32 of the rank (hi x hi + lo x hi + hi x lo),
+// in the main loop's operand order, so that the layouts agree.
+template <bool TR>
+__device__ __forceinline__ void lora_block(const Split8& u, const Split8& q, f32x4& acc) {
+  if constexpr (TR) {
+    acc = mfma16<MXFP4>(q.hi, u.hi, acc);
+    acc = mfma16<MXFP4>(q.lo, u.hi, acc);
+    acc = mfma16<MXFP4>(q.hi, u.lo, acc);
+  } else {
+    acc = mfma16<MXFP4>(u.hi, q.hi, acc);
+    acc = mfma16<MXFP4>(u.hi, q.lo, acc);
+    acc = mfma16<MXFP4>(u.lo, q.hi, acc);
+  }
+}
+
+// DROP (dgrad): the adapter delta is masked by g.drop. An instantiation of its own: the others
+// keep their registers.
+template <Fmt F, bool DG, bool TAIL, bool DROP>
 __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(GemmArgs g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
   __shared__ int32_t p_u0[kMaxExperts + 1];
@@ -750,17 +768,32 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(GemmArgs g) {
         for (int i = 0; i < 8; ++i) {
           const Split8 au = load8_split(RU, (uint32_t)((16 * i + r16) * r + jj), ok, g.lora_s,
                                         -rowexp(16 * i + r16));
+          if constexpr (!DROP) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            // the same operand order as the main loop, so the layouts agree
-            if constexpr (kTr<F, DG>) {
-              acc[i][j] = mfma16<MXFP4>(bq[j].hi, au.hi, acc[i][j]);
-              acc[i][j] = mfma16<MXFP4>(bq[j].lo, au.hi, acc[i][j]);
-              acc[i][j] = mfma16<MXFP4>(bq[j].hi, au.lo, acc[i][j]);
-            } else {
-              acc[i][j] = mfma16<MXFP4>(au.hi, bq[j].hi, acc[i][j]);
-              acc[i][j] = mfma16<MXFP4>(au.hi, bq[j].lo, acc[i][j]);
-              acc[i][j] = mfma16<MXFP4>(au.lo, bq[j].hi, acc[i][j]);
+            for (int j = 0; j < 4; ++j) lora_block<kTr<F, DG>>(au, bq[j], acc[i][j]);
+          } else {
+            // Two column blocks at a time: lane (r16, kg) draws the 8 bits of row 16 i + r16 and
+            // columns 32 p + 8 kg .., the lanes that hold those results fetch them.
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+              uint32_t w[4];
+              const int64_t at = (row0 + 128 * wm + 16 * i + r16) * O + n0 + 64 * wn + 32 * p + 8 * kg;
+              PhiloxState(g.drop).bits((uint64_t)at >> 3, w);
+              int kept = 0;
+#pragma unroll
+              for (int b = 0; b < 8; ++b) kept |= (int)philox_kept(w, b, g.drop.threshold) << b;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                f32x4 d = {0.f, 0.f, 0.f, 0.f};
+                lora_block<kTr<F, DG>>(au, bq[2 * p + j], d);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  // this result's row and column in the 16 x 16 block
+                  const int rr = kTr<F, DG> ? r16 : 4 * kg + q, cc = kTr<F, DG> ? 4 * kg + q : dg_col(r16);
+                  const int bits = __shfl(kept, rr + 16 * (2 * j + (cc >> 3)));
+                  if ((bits >> (cc & 7)) & 1) acc[i][2 * p + j][q] += d[q];
+                }
+              }
             }
           }
         }
@@ -976,7 +1009,13 @@ hipError_t launch_tile_fixup(const GemmArgs& g, bool dgrad, int tile_grid, hipSt
 
 template <Fmt F, bool DG, bool TAIL>
 hipError_t launch_tile_t(const GemmArgs& g, int grid, hipStream_t s) {
-  hipLaunchKernelGGL((tile_kernel<F, DG, TAIL>), dim3(grid), dim3(kTileThreads), 0, s, g);
+  if constexpr (DG) {
+    if (g.lora_drop) {
+      hipLaunchKernelGGL((tile_kernel<F, DG, TAIL, true>), dim3(grid), dim3(kTileThreads), 0, s, g);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((tile_kernel<F, DG, TAIL, false>), dim3(grid), dim3(kTileThreads), 0, s, g);
   return hipGetLastError();
 }
 

@@ -526,6 +526,85 @@ geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes
                              int32_t dw_dtype, int64_t M, int64_t N, int64_t K, int32_t E, void* workspace,
                              size_t workspace_bytes, const geg_opts* opts, hipStream_t stream);
 
+/*
+ * geg_request_lora — low-rank adapters of many requests in one batch, added to what a
+ * projection that they share gave (any of the products above, with E = 1 or grouped):
+ *   out[t, :] = y[t, :] + scales[i] * (x[t, :] . A_i^T) . B_i^T,   i = ids[t]
+ *   dtype    GEG_BF16 or GEG_F16, of y, x, the adapters and out
+ *   y        [M, N], rows ldy values apart, or NULL for zeros (then ldy is ignored)
+ *   x        [M, K], rows ldx apart; ids int32 [M], in any order; a negative id: no adapter,
+ *            out is y there; an id >= L likewise, and flags GEG_DEVERR_BAD_EXPERT_ID
+ *   lora_a   [L, r, K], lora_b [L, N, r]; r 8, 16, ..., 128; adapters of lower rank are
+ *            filled up with zeros
+ *   scales   fp32 [L], or NULL for ones
+ *   out      [M, N], rows ldo apart; may be y itself (same pitch), not x
+ *   workspace: geg_request_lora_workspace_bytes(M, K, r) bytes
+ * N, K and the pitches are multiples of 8, every tensor is 16-byte aligned. Sums run in fp32;
+ * x A^T keeps at least 16 significant bits on its way into the second product; one rounding.
+ * An adapter's values reach only the rows that name it. Rows routed to experts with
+ * an adapter each have ids = adapter * E + expert over lora_a [adapters * E, r, K].
+ */
+size_t geg_request_lora_workspace_bytes(int64_t M, int64_t K, int32_t r);
+geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t ldx, const int32_t* ids,
+                            const void* lora_a, const void* lora_b, const float* scales, void* out, int64_t ldo,
+                            int32_t dtype, int64_t M, int64_t N, int64_t K, int32_t L, int32_t r, void* workspace,
+                            size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * geg_dropout — dropout from a counter-based generator, with a mask that is never stored:
+ *   out[i] = [residual[i] +] (bits_i >= threshold ? x[i] * scale : 0)
+ *   threshold = round(p * 65536), scale = 65536 / (65536 - threshold) (p = 1: all dropped)
+ * bits_i are 16 of the 128 bits that Philox4x32-10 (Salmon et al. 2011) gives for the counter
+ * (low word of i / 8, high word, low word of offset, high word) and the key (low word of seed,
+ * high word): half i % 8 of its four words, low halves first. A pass with the same seed and
+ * offset over n values of another tensor (the gradient, a recomputed forward) drops the same
+ * ones; other passes take another offset.
+ *   x, out    dtype [n], contiguous; out may be x or residual
+ *   residual  dtype [n] or NULL
+ *   rng       NULL, or device uint64 {seed, offset}: used instead of `seed`, and added to
+ *             `offset`; a captured call then draws what the words hold on each replay
+ * A dropped value leaves 0 whatever it was. fp32 arithmetic, one rounding. Tensors are aligned
+ * to their elements (at 16 bytes it is faster).
+ */
+geg_status geg_dropout(const void* x, const void* residual, void* out, int32_t dtype, int64_t n, double p, uint64_t seed,
+                       uint64_t offset, const uint64_t* rng, hipStream_t stream);
+
+/*
+ * g*_grouped_gemm_lora_dropout / g*_grouped_dgrad_lora_dropout — the adapter entry points above
+ * with dropout of the adapter's input (the frozen projection's stays whole): with the mask m
+ * that geg_dropout draws for p, seed, offset and rng over the M * K values of x, and
+ * s' = scale / (1 - p),
+ *   out = a_e W_e^T + s' ((m a_e) A_e^T) B_e^T          (u = (m a_e) A_e^T)
+ *   dx  = dy_e W_e + m (s' (dy_e B_e) A_e),  grad_a = sum (s' dy_e B_e)^T (m a_e),
+ *   grad_b = s' sum dy_e^T u
+ * The backward takes the forward's p, seed, offset and rng words. Workspace:
+ * geg_lora_dropout_workspace_bytes.
+ */
+size_t geg_lora_dropout_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r);
+geg_status gnf4_grouped_gemm_lora_dropout(const void* a, const int32_t* sizes, const uint8_t* w, const float* absmax,
+                                          const float* lora_a, const float* lora_b, float scale, double p, uint64_t seed,
+                                          uint64_t offset, const uint64_t* rng, void* out, void* u, int64_t M, int64_t N,
+                                          int64_t K, int32_t E, int32_t r, void* workspace, size_t workspace_bytes,
+                                          const geg_opts* opts, hipStream_t stream);
+geg_status gmxfp4_grouped_gemm_lora_dropout(const void* a, const int32_t* sizes, const uint8_t* blocks,
+                                            const uint8_t* scales, const float* lora_a, const float* lora_b, float scale,
+                                            double p, uint64_t seed, uint64_t offset, const uint64_t* rng, void* out,
+                                            void* u, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r,
+                                            void* workspace, size_t workspace_bytes, const geg_opts* opts,
+                                            hipStream_t stream);
+geg_status gnf4_grouped_dgrad_lora_dropout(const void* dy, const int32_t* sizes, const uint8_t* w, const float* absmax,
+                                           const void* x, const float* lora_a, const float* lora_b, const void* u,
+                                           float scale, double p, uint64_t seed, uint64_t offset, const uint64_t* rng,
+                                           void* dx, float* grad_a, float* grad_b, int64_t M, int64_t N, int64_t K,
+                                           int32_t E, int32_t r, void* workspace, size_t workspace_bytes,
+                                           const geg_opts* opts, hipStream_t stream);
+geg_status gmxfp4_grouped_dgrad_lora_dropout(const void* dy, const int32_t* sizes, const uint8_t* blocks,
+                                             const uint8_t* scales, const void* x, const float* lora_a,
+                                             const float* lora_b, const void* u, float scale, double p, uint64_t seed,
+                                             uint64_t offset, const uint64_t* rng, void* dx, float* grad_a, float* grad_b,
+                                             int64_t M, int64_t N, int64_t K, int32_t E, int32_t r, void* workspace,
+                                             size_t workspace_bytes, const geg_opts* opts, hipStream_t stream);
+
 /* Workspace bytes needed by one call of operation `op` with these sizes and options. */
 size_t geg_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E,
                            const geg_opts* opts);

@@ -56,6 +56,7 @@ from .route import route_sort_ref, gather_ref, combine_ref, brute_force_route
 from .lora import lora_delta_ref, lora_forward_ref, lora_backward_ref, brute_force_lora
 from .w4a8 import (E4M3_TABLE, e4m3_value, e4m3_round, mxfp8_scale_bytes, quantize_mxfp8,
                    dequant_mxfp8, w4a8_grouped_ref, sampled_w4a8_ref, brute_force_w4a8)
+from .philox import philox4x32, dropout_bits, dropout_threshold, dropout_keep, dropout_scale
 
 PARITY = {
     "NF4_TABLE_F32": "pinned: published decimal values and closed-form quantiles",
@@ -87,6 +88,7 @@ PARITY = {
     "lora_forward_ref / lora_backward_ref": "pinned: torch fp64 autograd of the same "
                         "forward (independent derivatives), pure-Python brute force, "
                         "s = 0 reduction, linearity in s",
+    "philox4x32": "pinned: the published known answers of the generator",
 }
 
 __all__ = [n for n in dir() if not n.startswith("_")]

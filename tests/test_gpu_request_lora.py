@@ -1,0 +1,253 @@
+"""Adapters of many requests (request_lora) against fp64.
+
+Tolerance per element, with U = sum |x| |A| of the first product: u is summed over K (at most
+32 additions inside a matrix instruction, K / 32 between them, and 40 across wavefronts and
+ranges), each off by at most 2^-23 of U; it enters the second product with 16 significant bits
+at least (2^-17 of |u|, or 2^-34 of its row's largest); that one's r products again (r / 8 + 32
+additions of both parts); the result is rounded once, finfo.eps / 2 of its value or half a
+subnormal step."""
+import pytest
+
+from gpu_util import log
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def geg():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import grouped_expert_gemm_amd as g
+    g.lib()
+    return g
+
+
+def _types():
+    import torch
+    return {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def _case(dtype, M, K, N, L, r, seed, mixed=True):
+    import torch
+    t = _types()[dtype]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, y = rand(M, K).to(t), rand(M, N).to(t)
+    A, B = (rand(L, r, K) * K ** -0.5).to(t), rand(L, N, r).to(t)
+    scales = torch.rand(L, generator=g, device="cuda") + 0.5
+    ids = torch.randint(-1, L, (M,), generator=g, device="cuda").to(torch.int32)
+    return y, x, ids if mixed else torch.sort(ids).values, A, B, scales
+
+
+def _ref(y, x, ids, A, B, scales):
+    """(result, tolerance) in fp64."""
+    import torch
+    K, r = x.shape[1], A.shape[1]
+    out = torch.zeros(x.shape[0], B.shape[1], dtype=torch.float64, device="cuda") if y is None else y.double()
+    tol = 2.0 ** -23 * out.abs()
+    for i in sorted(set(ids.tolist())):
+        if i < 0 or i >= A.shape[0]:
+            continue
+        rows = torch.nonzero(ids == i).flatten()
+        s = 1.0 if scales is None else scales[i].double()
+        X, At, Bt = x[rows].double(), A[i].double().t().contiguous(), B[i].double().t().contiguous()
+        u, U = X @ At, X.abs() @ At.abs()
+        du = (K / 32 + 72) * 2.0 ** -23 * U + 2.0 ** -17 * u.abs() + 2.0 ** -34 * u.abs().amax(1, keepdim=True)
+        out[rows] += s * (u @ Bt)
+        tol[rows] += s * (du @ Bt.abs() + (r / 8 + 34) * 2.0 ** -23 * (u.abs() @ Bt.abs()))
+    info = torch.finfo(x.dtype)
+    return out, tol + info.eps / 2 * (out.abs() + tol) + info.smallest_normal * info.eps / 2
+
+
+def _check(got, ref, tol, what):
+    over = ((got.double() - ref).abs() / tol).max().item() if ref.numel() else 0.0
+    log(f"  {what}: largest error {over:.3f} of its bound")
+    assert got.isfinite().all() and over <= 1.0, what
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,K,N,L,r,mixed", [
+    (1, 8, 8, 1, 8, True), (1, 2048, 1024, 8, 16, True), (5, 264, 72, 3, 24, True), (17, 4096, 200, 40, 64, True),
+    (96, 1000, 520, 32, 128, True), (300, 512, 64, 7, 40, False), (513, 136, 264, 5, 16, False), (700, 72, 136, 300, 32, True),
+    (1025, 320, 328, 6, 104, False), (640, 256, 96, 4, 72, True)])
+def test_shapes(geg, dtype, M, K, N, L, r, mixed):
+    log(f"case: request adapters {dtype} M={M} K={K} N={N} L={L} r={r} mixed={mixed}")
+    args = _case(dtype, M, K, N, L, r, seed=M + K + N, mixed=mixed)
+    _check(geg.request_lora(*args, check_errors=True), *_ref(*args), "out")
+    y, x, ids, A, B, _ = args
+    _check(geg.request_lora(None, x, ids, A, B), *_ref(None, x, ids, A, B, None), "without y and scales")
+
+
+def test_rows_without_an_adapter_and_in_place(geg):
+    import torch
+    log("case: request adapters, rows without one")
+    for M in (40, 600):
+        y, x, ids, A, B, scales = _case("bf16", M, 128, 264, 4, 16, seed=1)
+        y[ids < 0] = float("nan")
+        bits = y[ids < 0].view(torch.int16).clone()
+        out = geg.request_lora(y, x, ids, A, B, scales)
+        assert torch.equal(out[ids < 0].view(torch.int16), bits)
+        z = y.clone()
+        assert geg.request_lora(z, x, ids, A, B, scales, out=z) is z
+        assert torch.equal(z.view(torch.int16), out.view(torch.int16))
+        none = torch.full_like(ids, -5)
+        assert torch.equal(geg.request_lora(z, x, none, A, B, scales).view(torch.int16), z.view(torch.int16))
+        assert (geg.request_lora(None, x, none, A, B, scales) == 0).all()
+
+
+def test_ids_out_of_range(geg):
+    import torch
+    log("case: request adapters, ids past L")
+    y, x, ids, A, B, scales = _case("bf16", 33, 64, 64, 3, 8, seed=2)
+    ids[20] = 3
+    with pytest.raises(geg.GegDeviceError) as e:
+        geg.request_lora(y, x, ids, A, B, scales, check_errors=True)
+    assert e.value.bits == geg.DEVERR_BAD_EXPERT_ID
+    out = geg.request_lora(y, x, ids, A, B, scales)
+    assert torch.equal(out[20], y[20])
+    _check(out, *_ref(y, x, ids, A, B, scales), "the other rows")
+
+
+def test_slices_of_wider_tensors(geg):
+    import torch
+    log("case: request adapters on slices of columns")
+    for M in (1, 50, 700):
+        y, x, ids, A, B, scales = _case("fp16", M, 72, 136, 6, 16, seed=3)
+        wide_y, wide_x, wide_o = (torch.full((M, 400), 3.0, dtype=torch.float16, device="cuda") for _ in range(3))
+        wide_y[:, 8:144], wide_x[:, 320:392] = y, x
+        out = geg.request_lora(wide_y[:, 8:144], wide_x[:, 320:392], ids, A, B, scales, out=wide_o[:, 200:336])
+        want = geg.request_lora(y, x, ids, A, B, scales)
+        assert torch.equal(out, want)
+        assert (wide_o[:, :200] == 3).all() and (wide_o[:, 336:] == 3).all()
+        geg.request_lora(wide_y[:, 8:144], x, ids, A, B, scales, out=wide_y[:, 8:144])
+        assert torch.equal(wide_y[:, 8:144], want) and (wide_y[:, :8] == 3).all() and (wide_y[:, 144:] == 3).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_values_stay_with_their_rows(geg, dtype):
+    import torch
+    log(f"case: request adapters {dtype} with infinities and NaN")
+    for M in (30, 530):
+        y, x, ids, A, B, scales = _case(dtype, M, 72, 72, 4, 8, seed=4)
+        plain = geg.request_lora(y, x, ids, A, B, scales)
+        x2 = x.clone()
+        row = int(torch.nonzero(ids >= 0)[3])
+        x2[row, 70] = float("nan")
+        got = geg.request_lora(y, x2, ids, A, B, scales)
+        assert got[row].isnan().all()
+        got[row] = plain[row]
+        assert torch.equal(got, plain)
+        bad = int(ids[row])
+        A2, B2 = A.clone(), B.clone()
+        A2[bad, 7], B2[bad, 71] = float("inf"), float("nan")
+        for a, b in ((A2, B), (A, B2)):
+            got = geg.request_lora(y, x, ids, a, b, scales)
+            assert not got[ids == bad][:, -1].isfinite().any()
+            assert torch.equal(got[ids != bad], plain[ids != bad])
+
+
+def test_scales_of_any_size_in_fp16(geg):
+    """u far outside fp16's range, and far below it."""
+    import torch
+    log("case: request adapters, fp16 with large and small u")
+    for factor, back in ((2.0 ** 9, 2.0 ** -14), (2.0 ** -11, 2.0 ** 10)):
+        y, x, ids, A, B, scales = _case("fp16", 40, 512, 64, 3, 16, seed=5)
+        x, A, B = x * factor, A * factor, B * back
+        _check(geg.request_lora(y, x, ids, A, B, scales), *_ref(y, x, ids, A, B, scales), f"factor {factor}")
+
+
+def test_offsets_past_2_31(geg):
+    import torch
+    log("case: request adapters with more than 2^31 elements of y and of the adapters")
+    t = torch.bfloat16
+    M, N, K = 70000, 32768, 64
+    y = torch.zeros(M, N, dtype=t, device="cuda")
+    x = torch.randn(M, K, device="cuda").to(t)
+    A, B = torch.randn(2, 8, K, device="cuda").to(t), torch.randn(2, N, 8, device="cuda").to(t)
+    ids = (torch.arange(M, device="cuda") >= M - 100).to(torch.int32)
+    geg.request_lora(y, x, ids, A, B, out=y)
+    at = torch.tensor([0, M - 101, M - 100, M - 1], device="cuda")
+    ref, tol = _ref(None, x[at], ids[at], A, B, None)
+    _check(y[at], ref, tol, "rows at both ends")
+    del y
+    L, r = 2100, 64
+    A = torch.zeros(L, r, 16384, dtype=t, device="cuda")
+    B = torch.zeros(L, 16384, r, dtype=t, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(6)
+    A[L - 1] = torch.randn(r, 16384, generator=g, device="cuda") / 128
+    B[L - 1] = torch.randn(16384, r, generator=g, device="cuda")
+    x = torch.randn(3, 16384, generator=g, device="cuda").to(t)
+    ids = torch.full((3,), L - 1, dtype=torch.int32, device="cuda")
+    out = geg.request_lora(None, x, ids, A, B)
+    _check(out, *_ref(None, x, torch.zeros_like(ids), A[L - 1:], B[L - 1:], None), "the last adapter")
+
+
+def test_captured_and_on_streams(geg):
+    import torch
+    log("case: request adapters captured and on another stream")
+    for M in (24, 600):
+        args = _case("bf16", M, 256, 264, 5, 16, seed=7)
+        geg.request_lora(*args)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = geg.request_lora(*args)
+        for seed in range(3):
+            for old, new in zip(args, _case("bf16", M, 256, 264, 5, 16, seed=10 + seed)):
+                old.copy_(new)
+            want = geg.request_lora(*args)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(got, want)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        out = geg.request_lora(*args, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        assert torch.equal(out, want)
+
+
+def test_two_streams_at_once(geg):
+    import torch
+    log("case: request adapters on two streams at once")
+    cases = [_case("bf16", 200, 2048, 512, 6, 32, seed=20 + i) for i in range(2)]
+    want = [geg.request_lora(*c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(geg.request_lora(*cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+def test_beside_quantised_experts(geg):
+    """A decode batch through a quantised projection and through quantised experts, each request
+    with its adapter, one per expert: the calls as a server makes them."""
+    import torch
+    log("case: request adapters beside quantised projections")
+    T, k, E, H, N, P, r = 12, 2, 6, 128, 192, 3, 16
+    g = torch.Generator(device="cuda").manual_seed(8)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x = rand(T, H).bfloat16()
+    owner = torch.randint(-1, P, (T,), generator=g, device="cuda").to(torch.int32)
+    # shared projection, E = 1
+    w, am = geg.gnf4_quantize((rand(1, N, H) * 0.05))
+    sizes1 = torch.tensor([T], dtype=torch.int32, device="cuda")
+    A1, B1 = (rand(P, r, H) * H ** -0.5).bfloat16(), rand(P, N, r).bfloat16()
+    y = geg.gnf4_grouped_gemm(x, sizes1, w, am)
+    _check(geg.request_lora(y, x, owner, A1, B1), *_ref(y, x, owner, A1, B1, None), "shared projection")
+    # routed experts: row r of the sorted rows belongs to token src_of[r] // k and its expert
+    wE, amE = geg.gnf4_quantize((rand(E, N, H) * 0.05))
+    weights, ids = geg.route_topk(rand(T, E), k)
+    sizes, row_of, src_of, xs = geg.route_sort(ids, E, x)
+    h = geg.gnf4_grouped_gemm(xs, sizes, wE, amE)
+    expert = ids.flatten()[src_of.long()]
+    own = owner[(src_of // k).long()]
+    rows = torch.where(own < 0, -1, own * E + expert).to(torch.int32)
+    AE, BE = (rand(P * E, r, H) * H ** -0.5).bfloat16(), rand(P * E, N, r).bfloat16()
+    _check(geg.request_lora(h, xs, rows, AE, BE), *_ref(h, xs, rows, AE, BE, None), "routed experts")
