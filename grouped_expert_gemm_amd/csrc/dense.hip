@@ -64,14 +64,15 @@ __device__ __forceinline__ void zero_rows(uint16_t* out, int64_t row0, int64_t M
 
 // ------------------------------------------------------------------ tiles
 constexpr int TM = 256, TN = 256, TK = 64;
-constexpr int TThreads = 512;            // 8 wavefronts: 2 (rows of 128) x 4 (columns of 64)
-constexpr int kStage = 256 * TK * 2;     // bytes of one operand per stage
+constexpr int TThreads = 512;            // 8 wavefronts: per quadrant 2 (rows of 64) x 4 (columns of 32)
+constexpr int kHalf = 128 * TK * 2;      // bytes of half an operand per stage
 
-// A stage of an operand held along its rows: 256 rows of 128 bytes, 16-byte chunk c of row r
-// at c ^ (r % 8). Held across: 64 contraction rows of 512 bytes, 32-byte unit u of row r at
-// u ^ h(r), h(r) = r % 4 + 4 (r / 8 % 2): the eight rows that 32 lanes of a transposing read
-// touch at once (4 of lane group g, 4 of g + 1) then lie in different banks.
-template <int D, int T>
+// Half an operand's stage, 128 rows (columns) of the tile by 64 of the contraction. Held along
+// its rows: 128 rows of 128 bytes, 16-byte chunk c of row r at c ^ (r % 8). Held across: 64
+// contraction rows of 256 bytes, 32-byte unit u of row r at u ^ h(r), h(r) = r % 4 + 4 (r / 8 %
+// 2): the eight rows that 32 lanes of a transposing read touch at once (4 of lane group g, 4 of
+// g + 1) then lie in different banks. Neither meets a bank conflict.
+template <int D>
 struct Tiles {
   static constexpr bool kPAlong = D != kDenseWgrad, kQAlong = D == kDenseFwd;
 
@@ -104,8 +105,8 @@ struct Tiles {
       x.q = g.q + (int64_t)o0 * g.K + k0;
       x.row0 = (int64_t)e * g.N + n0;
       x.c0 = k0;
-      x.rows = (int)min<int64_t>(TM, g.N - n0);
-      x.cols = (int)min<int64_t>(TN, g.K - k0);
+      x.rows = min(TM, (int)(g.N - n0));
+      x.cols = min(TN, (int)(g.K - k0));
       x.n = o1 - o0;
     } else {
       const int e = __builtin_amdgcn_readfirstlane(find_expert(p_u, g.E, u));
@@ -114,9 +115,9 @@ struct Tiles {
       const int rblocks = (o1 - o0 + TM - 1) / TM;
       const int ct = lu / rblocks, rt = lu - ct * rblocks;
       x.row0 = o0 + (int64_t)rt * TM;
-      x.rows = (int)min<int64_t>(TM, o1 - x.row0);
+      x.rows = min(TM, o1 - o0 - rt * TM);
       x.c0 = (int64_t)ct * TN;
-      x.cols = (int)min<int64_t>(TN, O - x.c0);
+      x.cols = min(TN, (int)(O - x.c0));
       x.p = g.p + x.row0 * C;
       x.q = D == kDenseFwd ? g.q + ((int64_t)e * g.N + x.c0) * g.K : g.q + (int64_t)e * g.N * g.K + x.c0;
       x.n0 = 0;
@@ -126,54 +127,65 @@ struct Tiles {
     return x;
   }
 
-  // Loads of a stage straight into LDS: 16 bytes per lane, 1 KB (8 rows along, 2 across) per
-  // instruction, four per wavefront and operand; what lies past the tile's rows or the
+  // The place of the loads: the memory of P's and Q's next stage and what is left of it.
+  struct Cursor {
+    const uint8_t* p;
+    const uint8_t* q;
+    int64_t left_p, left_q;
+    int rest;            // contraction left
+    int st, stages;
+  };
+  __device__ __forceinline__ void aim(Cursor& c, const Tile& x, bool any) const {
+    c.p = reinterpret_cast<const uint8_t*>(x.p);
+    c.left_p = !any ? 0 : (kPAlong ? x.rows * C : x.n * g.N - x.n0) * 2;
+    c.q = reinterpret_cast<const uint8_t*>(x.q);
+    c.left_q = !any ? 0 : (kQAlong ? x.cols * g.K : x.n * g.K - x.c0) * 2;
+    c.rest = x.n;
+    c.st = 0;
+    c.stages = x.stages;
+  }
+  __device__ __forceinline__ void next(Cursor& c) const {
+    const int64_t dp = kPAlong ? TK * 2 : TK * g.N * 2, dq = kQAlong ? TK * 2 : TK * g.K * 2;
+    c.p += dp;
+    c.left_p -= dp;
+    c.q += dq;
+    c.left_q -= dq;
+    c.rest -= TK;
+    ++c.st;
+  }
+
+  // Loads of half an operand's stage straight into LDS: 16 bytes per lane, 1 KB (8 rows along,
+  // 4 across) per instruction, two per wavefront; what lies past the tile's rows or the
   // contraction reads as zeros, columns past an across operand's as anything (they meet only
   // results that are not stored).
-  __device__ __forceinline__ void along(const uint16_t* base, int rows, int64_t pitch, int n, int st, uint8_t* L) const {
-    const int chunk = (lane & 7) ^ (lane >> 3);
-    const __amdgpu_buffer_rsrc_t R = window(base + (int64_t)st * TK, (rows * pitch - (int64_t)st * TK) * 2);
-    const uint32_t at = (uint32_t)((8 * wave + (lane >> 3)) * (uint32_t)pitch * 2 + 16 * chunk), next = 128 * (uint32_t)pitch;
-    const uint32_t off = oob_unless(st * TK + 8 * chunk < n, at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(R, (lds_ptr_t)(L + (wave + 8 * i) * 1024), 16, off + i * next, 0, 0, 0);
+  static __device__ __forceinline__ uint32_t lane_at(bool along, int lane, int wave, int64_t pitch) {
+    if (along) return (uint32_t)((8 * wave + (lane >> 3)) * (uint32_t)pitch * 2 + 16 * ((lane & 7) ^ (lane >> 3)));
+    const int r = 4 * wave + (lane >> 4), h = (r & 3) | ((r >> 1) & 4);
+    return (uint32_t)(r * (uint32_t)pitch * 2 + 16 * ((lane & 15) ^ (2 * h)));
   }
-  __device__ __forceinline__ void across(const uint16_t* base, int64_t col0, int64_t pitch, int n, int st,
-                                         uint8_t* L) const {
-    const int r = 2 * wave + (lane >> 5);
-    const int h = (r & 3) | ((r >> 1) & 4);
-    const int chunk = (lane & 31) ^ (2 * h);
-    const int rows = min(TK, n - st * TK);
-    const __amdgpu_buffer_rsrc_t R = window(base + (int64_t)st * TK * pitch, rows > 0 ? (rows * pitch - col0) * 2 : 0);
-    const uint32_t off = (uint32_t)(r * (uint32_t)pitch * 2 + 16 * chunk), next = 32 * (uint32_t)pitch;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(R, (lds_ptr_t)(L + (wave + 8 * i) * 1024), 16, off + i * next, 0, 0, 0);
-  }
-  __device__ __forceinline__ void load(const Tile& x, bool any, int st, uint8_t* P, uint8_t* Q) const {
-    if constexpr (kPAlong)
-      along(x.p, any ? x.rows : 0, C, x.n, st, P);
-    else
-      across(x.p, x.n0, g.N, any ? x.n : 0, st, P);
-    if constexpr (kQAlong)
-      along(x.q, any ? x.cols : 0, g.K, x.n, st, Q);
-    else
-      across(x.q, x.c0, g.K, any ? x.n : 0, st, Q);
+  // Instruction i of half h.
+  template <bool ALONG>
+  __device__ __forceinline__ void load(const uint8_t* base, int64_t left, int rest, uint32_t at, int64_t pitch, int h, int i,
+                                       uint8_t* L) const {
+    const int64_t skip = h * (ALONG ? 256 * pitch : 256);
+    const __amdgpu_buffer_rsrc_t R = window(base + skip, left - skip);
+    if constexpr (ALONG) at = oob_unless(8 * ((lane & 7) ^ (lane >> 3)) < rest, at);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(R, (lds_ptr_t)(L + (wave + 8 * i) * 1024), 16,
+                                             at + i * ((ALONG ? 128 : 64) * (uint32_t)pitch), 0, 0, 0);
   }
 };
 
 template <bool ALONG>
 struct Frag {
   uint32_t at;
-  // block0: the first of the operand's 16-wide blocks that the wavefront reads
+  // block0: the first of the half's 16-wide blocks that the wavefront reads
   __device__ __forceinline__ Frag(int lane, int block0) {
     const int r16 = lane & 15, grp = lane >> 4;
     if constexpr (ALONG) {
       at = (uint32_t)((16 * block0 + r16) * 128 + ((grp ^ (r16 & 7)) << 4));
     } else {
       const int j = r16 >> 2, h = j | ((grp & 1) << 2);
-      at = (uint32_t)((8 * grp + j) * 512 + ((block0 ^ h) << 5) + ((r16 & 3) << 3));
+      at = (uint32_t)((8 * grp + j) * 256 + ((block0 ^ h) << 5) + ((r16 & 3) << 3));
     }
   }
   // Block i (of the wavefront's), 32-wide substep q of the stage.
@@ -181,8 +193,8 @@ struct Frag {
     if constexpr (ALONG) {
       return *reinterpret_cast<const u32x4*>(L + (at ^ (64 * q)) + 2048 * i);
     } else {
-      const uint8_t* p = L + (at ^ (32 * i)) + 16384 * q;
-      const u32x2 lo = tr(p), hi = tr(p + 2048);
+      const uint8_t* p = L + (at ^ (32 * i)) + 8192 * q;
+      const u32x2 lo = tr(p), hi = tr(p + 1024);
       return u32x4{lo[0], lo[1], hi[0], hi[1]};
     }
   }
@@ -192,25 +204,31 @@ struct Frag {
   }
 };
 
+// One workgroup per CU, persistent over tiles. A stage is four quadrants of 128 x 128 results,
+// P half h by Q half v, in the order (0, 0), (0, 1), (1, 0), (1, 1), of 16 instructions per
+// wavefront each (64 x 32 results). Fragments are read a little ahead of their products, so a
+// half of an operand is needed in LDS for half a stage only; its buffer then takes the stage
+// after the next, and the loads have one and a half stages to land. Reads and loads stand between
+// the products, four at a time. The loads run on across tiles, at their own place in the list.
 template <int D, int T, bool F32>
 __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
   __shared__ int32_t p_u[kMaxExperts + 1];
-  __shared__ __attribute__((aligned(16))) uint8_t pa[kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t pb[kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t qa[kStage];
-  __shared__ __attribute__((aligned(16))) uint8_t qb[kStage];
+  // distinct objects, named at compile time: the compiler then adds no wait for loads that fill
+  // the others
+  __shared__ __attribute__((aligned(16))) uint8_t pa0[kHalf], pa1[kHalf], pb0[kHalf], pb1[kHalf];
+  __shared__ __attribute__((aligned(16))) uint8_t qa0[kHalf], qa1[kHalf], qb0[kHalf], qb1[kHalf];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave >> 2, wn = wave & 3;
   const int r16 = lane & 15, grp = lane >> 4;
-  using W = Tiles<D, T>;
+  using W = Tiles<D>;
   const int64_t O = D == kDenseFwd ? g.N : g.K;
   const int blocks_n = (int)((g.N + TM - 1) / TM), blocks_k = (int)((g.K + TN - 1) / TN);
   const int c_tiles = (int)((O + TN - 1) / TN);
   int32_t total = build_plan(p_off, p_u, g.sizes, g.E, g.M, g.err,
                              [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : (s + TM - 1) / TM * c_tiles; });
-  if constexpr (D == kDenseWgrad) total = g.E * blocks_n * blocks_k;
+  total = D == kDenseWgrad ? g.E * blocks_n * blocks_k : __builtin_amdgcn_readfirstlane(total);
   if constexpr (D != kDenseWgrad) {
     if (g.zero_rest) zero_rows((uint16_t*)g.out, p_off[g.E], g.M, O);
   }
@@ -222,122 +240,175 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   int32_t u = (int32_t)((int64_t)total * part / parts) + blockIdx.x / parts;
   if (u >= end) return;
 
-  const Frag<W::kPAlong> fp(lane, 8 * wm);
-  const Frag<W::kQAlong> fq(lane, 4 * wn);
-  u32x4 q[2][4], plo[4], phi[4];
-  f32x4 acc[8][4];
-  auto read_q = [&](const uint8_t* L, int s, u32x4* d) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = fq.read(L, j, s);
-  };
-  auto read_p = [&](const uint8_t* L, int i0, int s, u32x4* d) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = fp.read(L, i0 + i, s);
-  };
+  const Frag<W::kPAlong> fp(lane, 4 * wm);
+  const Frag<W::kQAlong> fq(lane, 2 * wn);
+  u32x4 p[2][4], q0[2][2], q1[2][2];   // [substep][block] of one P half and of both Q halves
+  f32x4 acc[2][2][4][2];
 
-  // The loads run two stages ahead of the products, across tiles: their own place in the list.
-  typename W::Tile lt = w.tile_of(u), cur = lt;
+  typename W::Tile cur = w.tile_of(u);   // of the products
+  typename W::Cursor lc;                 // of the loads
+  w.aim(lc, cur, true);
   int32_t lu = u;
-  int lst = 0;
-  bool lany = true;
-  auto load_next = [&](uint8_t* P, uint8_t* Q) {
-    w.load(lt, lany, lst, P, Q);
-    if (++lst == lt.stages) {
-      lst = 0;
+  int st = 0;
+  const int64_t pitch_p = W::kPAlong ? w.C : g.N;
+  const uint32_t at_p = W::lane_at(W::kPAlong, lane, wave, pitch_p), at_q = W::lane_at(W::kQAlong, lane, wave, g.K);
+  auto load_p = [&](int h, int i, uint8_t* L) {
+    w.template load<W::kPAlong>(lc.p, lc.left_p, lc.rest, at_p, pitch_p, h, i, L);
+  };
+  auto load_q = [&](int h, int i, uint8_t* L) {
+    w.template load<W::kQAlong>(lc.q, lc.left_q, lc.rest, at_q, g.K, h, i, L);
+  };
+  auto advance = [&]() {
+    w.next(lc);
+    if (lc.st == lc.stages) {
       lu += step;
-      lany = lu < end;
-      if (lany) lt = w.tile_of(lu);
+      const bool any = lu < end;
+      w.aim(lc, any ? w.tile_of(lu) : cur, any);
     }
   };
-  load_next(pa, qa);
-  load_next(pb, qb);
-  step_barrier<8>();
-  read_q(qa, 0, q[0]);
-  read_p(pa, 0, 0, plo);
-
-  int st = 0;
-  bool lo, hi;
-  auto begin = [&]() {
-    lo = 128 * wm < cur.rows && 64 * wn < cur.cols;
-    hi = 128 * wm + 64 < cur.rows && 64 * wn < cur.cols;
+  auto load_all = [&](uint8_t* P0, uint8_t* P1, uint8_t* Q0, uint8_t* Q1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 2; ++i) load_p(0, i, P0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < 2; ++i) load_q(0, i, Q0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_q(1, i, Q1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_p(1, i, P1);
+    advance();
   };
-  auto multiply = [&](int i0, const u32x4* p, const u32x4* qq) {
+  load_all(pa0, pa1, qa0, qa1);
+  load_all(pb0, pb1, qb0, qb1);
+  step_barrier<10>();
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+  for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i0 + i][j] = mfma<T>(qq[j], p[i], acc[i0 + i][j]);
+    for (int j = 0; j < 2; ++j) q0[s][j] = fq.read(qa0, j, s);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[0][i] = fp.read(pa0, i, 0);
+
+  int on[2][2];   // whether a quadrant has results of this wavefront's
+  auto begin = [&]() {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        on[h][v] = __builtin_amdgcn_readfirstlane(128 * h + 64 * wm < cur.rows && 128 * v + 32 * wn < cur.cols);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[h][v][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+  };
+  // A quadrant: 16 products, four at a time (two rows of a substep), if they are wanted; due(k)
+  // goes before the four, so that reads and loads stand between the products. `on` is made
+  // opaque: otherwise paths with and without products each get a copy of what stands between.
+  auto quadrant = [&](int h, int v, const u32x4 (&q)[2][2], auto due) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      due(k);
+      asm volatile("" : "+s"(on[h][v]));
+      if (on[h][v]) {
+#pragma unroll
+        for (int i = 2 * (k & 1); i < 2 * (k & 1) + 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) acc[h][v][i][j] = mfma<T>(q[k >> 1][j], p[k >> 1][i], acc[h][v][i][j]);
+      }
+    }
   };
   auto store = [&]() {
-    if (!lo) return;
-    if constexpr (F32) {
-      float* dst = reinterpret_cast<float*>(g.out) + (cur.row0 + 128 * wm + r16) * O + cur.c0 + 64 * wn + 4 * grp;
-      const int rows = cur.rows - 128 * wm - r16, left = cur.cols - 64 * wn - 4 * grp;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (16 * i < rows && 16 * j < left) *reinterpret_cast<f32x4*>(dst + (int64_t)(16 * i) * O + 16 * j) = acc[i][j];
-    } else {
-      // lane groups 0, 2 end up with columns 0-7, 8-15 of block j, groups 1, 3 of block j + 1
-      const bool wide = (O & 7) == 0;
-      const int col = 16 * (grp & 1) + 8 * (grp >> 1);
-      uint16_t* dst = reinterpret_cast<uint16_t*>(g.out) + (cur.row0 + 128 * wm + r16) * O + cur.c0 + 64 * wn + col;
-      const int rows = cur.rows - 128 * wm - r16, left = cur.cols - 64 * wn - col;
+      for (int v = 0; v < 2; ++v) {
+        if (!on[h][v]) continue;
+        const int rows = cur.rows - 128 * h - 64 * wm - r16, c0 = 128 * v + 32 * wn;
+        const int64_t at = (cur.row0 + 128 * h + 64 * wm + r16) * O + cur.c0 + c0;
+        if constexpr (F32) {
+          float* dst = reinterpret_cast<float*>(g.out) + at + 4 * grp;
+          const int left = cur.cols - c0 - 4 * grp;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-          u32x4 v;
+            for (int j = 0; j < 2; ++j)
+              if (16 * i < rows && 16 * j < left)
+                *reinterpret_cast<f32x4*>(dst + (int64_t)(16 * i) * O + 16 * j) = acc[h][v][i][j];
+        } else {
+          // rows of 16 lanes of the two column blocks trade places: 8 adjacent columns per lane
+          const int col = 16 * (grp & 1) + 8 * (grp >> 1), left = cur.cols - c0 - col;
+          uint16_t* dst = reinterpret_cast<uint16_t*>(g.out) + at + col;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = pack2<T>(acc[i][j][2 * h], acc[i][j][2 * h + 1]);
-            const uint32_t y = pack2<T>(acc[i][j + 1][2 * h], acc[i][j + 1][2 * h + 1]);
-            const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-            v[h] = r[0];
-            v[2 + h] = r[1];
-          }
-          if (16 * i < rows && 16 * j < left) {
-            uint16_t* d = dst + (int64_t)(16 * i) * O + 16 * j;
-            if (wide) {
-              *reinterpret_cast<u32x4*>(d) = v;
-            } else {
+          for (int i = 0; i < 4; ++i) {
+            u32x4 o;
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const uint32_t x = pack2<T>(acc[h][v][i][0][2 * b], acc[h][v][i][0][2 * b + 1]);
+              const uint32_t y = pack2<T>(acc[h][v][i][1][2 * b], acc[h][v][i][1][2 * b + 1]);
+              const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
+              o[b] = r[0];
+              o[2 + b] = r[1];
+            }
+            if (16 * i < rows && left > 0) {
+              uint16_t* d = dst + (int64_t)(16 * i) * O;
+              if ((O & 7) == 0) {
+                *reinterpret_cast<u32x4*>(d) = o;
+              } else {
 #pragma clang loop unroll(disable)
-              for (int b = 0; b < min(8, left - 16 * j); ++b) {
-                const uint32_t x = b < 4 ? (b < 2 ? v[0] : v[1]) : (b < 6 ? v[2] : v[3]);
-                d[b] = (uint16_t)(x >> (16 * (b & 1)));
+                for (int b = 0; b < min(8, left); ++b) {
+                  const uint32_t x = b < 4 ? (b < 2 ? o[0] : o[1]) : (b < 6 ? o[2] : o[3]);
+                  d[b] = (uint16_t)(x >> (16 * (b & 1)));
+                }
               }
             }
           }
         }
       }
-    }
   };
-  // One stage from buffers P, Q, the next one's in P1, Q1. Behind the last tile an odd one out
-  // runs without products: a way out between the two copies of this body would, to the
-  // compiler, lead back to the first, which then waits for all loads.
+  auto read_p = [&](const uint8_t* L, int s, int k) {   // two blocks
+#pragma unroll
+    for (int i = 2 * k; i < 2 * k + 2; ++i) p[s][i] = fp.read(L, i, s);
+  };
+  auto read_q = [&](const uint8_t* L, int s, u32x4 (&d)[2][2]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) d[s][j] = fq.read(L, j, s);
+  };
+  // One stage from the buffers of P and Q, the next one's first halves in N0 and M0. Behind the
+  // last tile an odd stage runs without products: a way out between the two copies of this body
+  // would, to the compiler, lead back to the first, which then waits for all loads.
+  auto stage = [&](uint8_t* P0, uint8_t* P1, uint8_t* Q0, uint8_t* Q1, const uint8_t* N0, const uint8_t* M0) {
+    quadrant(0, 0, q0, [&](int k) {
+      if (k < 2)
+        read_p(P0, 1, k);
+      else
+        read_q(Q1, k - 2, q1);
+    });
+    step_barrier<8>();   // P0, Q0 and Q1 are read; P1 has landed
+    quadrant(0, 1, q1, [&](int k) {
+      if (k >= 2) read_p(P1, 0, k - 2);   // over what the first substep's products are done with
+    });
+    quadrant(1, 0, q0, [&](int k) {
+      if (k < 2) read_p(P1, 1, k);
+      if (k == 1) {
+        load_p(0, 0, P0);
+        load_p(0, 1, P0);
+      } else if (k >= 2) {
+        load_q(k - 2, 0, k == 2 ? Q0 : Q1);
+        load_q(k - 2, 1, k == 2 ? Q0 : Q1);
+      }
+    });
+    step_barrier<8>();   // P1 is read; the next N0 and both halves of the next Q have landed
+    quadrant(1, 1, q1, [&](int k) {
+      if (k < 2) {
+        load_p(1, k, P1);
+        read_q(M0, k, q0);
+      } else {
+        read_p(N0, 0, k - 2);
+      }
+    });
+  };
   bool more = true;
-  auto stage = [&](uint8_t* P, uint8_t* Q, const uint8_t* P1, const uint8_t* Q1) {
-    read_p(P, 4, 0, phi);
-    if (lo) multiply(0, plo, q[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    read_q(Q, 1, q[1]);
-    read_p(P, 0, 1, plo);
-    if (hi) multiply(4, phi, q[0]);
-    __builtin_amdgcn_sched_barrier(0);
-    read_p(P, 4, 1, phi);
-    if (lo) multiply(0, plo, q[1]);
-    __builtin_amdgcn_sched_barrier(0);
-    // every read of this stage is done and the next one's loads have landed
-    step_barrier<0>();
-    read_q(Q1, 0, q[0]);
-    read_p(P1, 0, 0, plo);
-    load_next(P, Q);
-    if (hi) multiply(4, phi, q[1]);
-    __builtin_amdgcn_sched_barrier(0);
+  auto finish = [&]() {   // of a stage
+    advance();
     if (++st == cur.stages) {
       store();
       u += step;
@@ -354,8 +425,10 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   };
   begin();
   do {
-    stage(pa, qa, pb, qb);
-    stage(pb, qb, pa, qa);
+    stage(pa0, pa1, qa0, qa1, pb0, qb0);
+    finish();
+    stage(pb0, pb1, qb0, qb1, pa0, qa0);
+    finish();
   } while (more);
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no load into LDS outlives the workgroup
 }
@@ -372,9 +445,8 @@ __global__ __launch_bounds__(NThreads) void dense_narrow_kernel(DenseArgs g) {
   __shared__ int32_t p_u[kMaxExperts + 1];
   const int64_t K = g.K, N = g.N;
   const int nblk = (int)((N + 15) / 16);
-  const int32_t total = build_plan(p_off, p_u, g.sizes, g.E, g.M, g.err, [&](int32_t s) -> int32_t {
-    return (s + 16 * RB - 1) / (16 * RB) * nblk;
-  });
+  const int32_t total = __builtin_amdgcn_readfirstlane(build_plan(
+      p_off, p_u, g.sizes, g.E, g.M, g.err, [&](int32_t s) -> int32_t { return (s + 16 * RB - 1) / (16 * RB) * nblk; }));
   if (g.zero_rest) zero_rows((uint16_t*)g.out, p_off[g.E], g.M, N);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
