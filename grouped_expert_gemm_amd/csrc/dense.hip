@@ -55,6 +55,14 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("s_barrier" ::: "memory");
 }
 
+// The lane's number, worked out where it is used: kept in a register over a tile's stages, it (and
+// what follows from it) would cost registers that they need.
+__device__ __forceinline__ int fresh_lane() {
+  int l = __builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
 // Rows [row0, M) of a 16-bit matrix set to zero by the whole grid.
 __device__ __forceinline__ void zero_rows(uint16_t* out, int64_t row0, int64_t M, int64_t width) {
   const int64_t n = (M - row0) * width, stride = (int64_t)gridDim.x * blockDim.x;
@@ -64,7 +72,7 @@ __device__ __forceinline__ void zero_rows(uint16_t* out, int64_t row0, int64_t M
 
 // ------------------------------------------------------------------ tiles
 constexpr int TM = 256, TN = 256, TK = 64;
-constexpr int TThreads = 512;            // 8 wavefronts: per quadrant 2 (rows of 64) x 4 (columns of 32)
+constexpr int TThreads = 512;            // 8 wavefronts: per quadrant 4 (rows of 32) x 2 (columns of 64)
 constexpr int kHalf = 128 * TK * 2;      // bytes of half an operand per stage
 
 // Half an operand's stage, 128 rows (columns) of the tile by 64 of the contraction. Held along
@@ -90,14 +98,15 @@ struct Tiles {
     int64_t n0;          // wgrad: first column of dy
     int rows, cols;      // valid
     int n;               // contraction length
-    int stages;
+    int stages;          // an even number: both sets of buffers
   };
 
   __device__ __forceinline__ Tile tile_of(int32_t u) const {
     Tile x;
     if constexpr (D == kDenseWgrad) {
-      const int e = u / (pb * qb), lu = u - e * (pb * qb);
-      const int qi = lu / pb, pi = lu - qi * pb;
+      // (divisions run on the vector ALUs)
+      const int e = __builtin_amdgcn_readfirstlane(u / (pb * qb)), lu = u - e * (pb * qb);
+      const int qi = __builtin_amdgcn_readfirstlane(lu / pb), pi = lu - qi * pb;
       const int32_t o0 = __builtin_amdgcn_readfirstlane(p_off[e]), o1 = __builtin_amdgcn_readfirstlane(p_off[e + 1]);
       const int64_t n0 = (int64_t)pi * TM, k0 = (int64_t)qi * TN;
       x.n0 = n0;
@@ -109,11 +118,11 @@ struct Tiles {
       x.cols = min(TN, (int)(g.K - k0));
       x.n = o1 - o0;
     } else {
-      const int e = __builtin_amdgcn_readfirstlane(find_expert(p_u, g.E, u));
+      const int e = __builtin_amdgcn_readfirstlane(find_expert(p_u, g.E, u, fresh_lane()));
       const int32_t lu = u - __builtin_amdgcn_readfirstlane(p_u[e]);
       const int32_t o0 = __builtin_amdgcn_readfirstlane(p_off[e]), o1 = __builtin_amdgcn_readfirstlane(p_off[e + 1]);
       const int rblocks = (o1 - o0 + TM - 1) / TM;
-      const int ct = lu / rblocks, rt = lu - ct * rblocks;
+      const int ct = __builtin_amdgcn_readfirstlane(lu / rblocks), rt = lu - ct * rblocks;   // (vector ALUs)
       x.row0 = o0 + (int64_t)rt * TM;
       x.rows = min(TM, o1 - o0 - rt * TM);
       x.c0 = (int64_t)ct * TN;
@@ -123,7 +132,7 @@ struct Tiles {
       x.n0 = 0;
       x.n = (int)C;
     }
-    x.stages = max(1, (x.n + TK - 1) / TK);
+    x.stages = max(2, 2 * ((x.n + 2 * TK - 1) / (2 * TK)));
     return x;
   }
 
@@ -205,22 +214,31 @@ struct Frag {
 };
 
 // One workgroup per CU, persistent over tiles. A stage is four quadrants of 128 x 128 results,
-// P half h by Q half v, in the order (0, 0), (0, 1), (1, 0), (1, 1), of 16 instructions per
-// wavefront each (64 x 32 results). Fragments are read a little ahead of their products, so a
+// P half h by Q half v, in the order (0, 0), (1, 0), (0, 1), (1, 1), of 16 instructions per
+// wavefront each (32 x 64 results). Fragments are read a little ahead of their products, so a
 // half of an operand is needed in LDS for half a stage only; its buffer then takes the stage
 // after the next, and the loads have one and a half stages to land. Reads and loads stand between
 // the products, four at a time. The loads run on across tiles, at their own place in the list.
-template <int D, int T, bool F32>
+// Cache policy of the tiles' stores: streamed past the XCD's L2, where they would displace the
+// operands that its tiles share (non-temporal, system scope). Backward of 16384 rows over 64
+// experts of 2048 x 2048, weights' gradient: 277 us without, 216 with.
+constexpr int kStream = 18;
+
+// How results are stored: 16 bits in rows of whole 16-byte pieces, fp32, or 16 bits in rows of any
+// width, value by value (forward).
+enum Out : int { kWide = 0, kF32Out = 1, kAnyWidth = 2 };
+template <int D, int T, int OUT>
 __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
   __shared__ int32_t p_u[kMaxExperts + 1];
   // distinct objects, named at compile time: the compiler then adds no wait for loads that fill
   // the others
-  __shared__ __attribute__((aligned(16))) uint8_t pa0[kHalf], pa1[kHalf], pb0[kHalf], pb1[kHalf];
-  __shared__ __attribute__((aligned(16))) uint8_t qa0[kHalf], qa1[kHalf], qb0[kHalf], qb1[kHalf];
+  // (placed by alignment: each operand's 64 KB together, within reach of one address register)
+  __shared__ __attribute__((aligned(128))) uint8_t qa0[kHalf], qa1[kHalf], qb0[kHalf], qb1[kHalf];
+  __shared__ __attribute__((aligned(64))) uint8_t pa0[kHalf], pa1[kHalf], pb0[kHalf], pb1[kHalf];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave >> 1, wn = wave & 1;
   const int r16 = lane & 15, grp = lane >> 4;
   using W = Tiles<D>;
   const int64_t O = D == kDenseFwd ? g.N : g.K;
@@ -240,16 +258,15 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   int32_t u = (int32_t)((int64_t)total * part / parts) + blockIdx.x / parts;
   if (u >= end) return;
 
-  const Frag<W::kPAlong> fp(lane, 4 * wm);
-  const Frag<W::kQAlong> fq(lane, 2 * wn);
-  u32x4 p[2][4], q0[2][2], q1[2][2];   // [substep][block] of one P half and of both Q halves
-  f32x4 acc[2][2][4][2];
+  const Frag<W::kPAlong> fp(lane, 2 * wm);
+  const Frag<W::kQAlong> fq(lane, 4 * wn);
+  u32x4 q[2][4], p0[2][2], p1[2][2];   // [substep][block] of one Q half and of both P halves
+  f32x4 acc[2][2][2][4];
 
   typename W::Tile cur = w.tile_of(u);   // of the products
   typename W::Cursor lc;                 // of the loads
   w.aim(lc, cur, true);
   int32_t lu = u;
-  int st = 0;
   const int64_t pitch_p = W::kPAlong ? w.C : g.N;
   const uint32_t at_p = W::lane_at(W::kPAlong, lane, wave, pitch_p), at_q = W::lane_at(W::kQAlong, lane, wave, g.K);
   auto load_p = [&](int h, int i, uint8_t* L) {
@@ -268,13 +285,13 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   };
   auto load_all = [&](uint8_t* P0, uint8_t* P1, uint8_t* Q0, uint8_t* Q1) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) load_p(0, i, P0);
-#pragma unroll
     for (int i = 0; i < 2; ++i) load_q(0, i, Q0);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) load_q(1, i, Q1);
+    for (int i = 0; i < 2; ++i) load_p(0, i, P0);
 #pragma unroll
     for (int i = 0; i < 2; ++i) load_p(1, i, P1);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) load_q(1, i, Q1);
     advance();
   };
   load_all(pa0, pa1, qa0, qa1);
@@ -283,153 +300,187 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) q0[s][j] = fq.read(qa0, j, s);
+    for (int i = 0; i < 2; ++i) p0[s][i] = fp.read(pa0, i, s);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) p[0][i] = fp.read(pa0, i, 0);
+  for (int j = 0; j < 4; ++j) q[0][j] = fq.read(qa0, j, 0);
 
-  int on[2][2];   // whether a quadrant has results of this wavefront's
+  int on;   // bit 2 h + v: the quadrant has results of this wavefront's
   auto begin = [&]() {
+    on = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
-        on[h][v] = __builtin_amdgcn_readfirstlane(128 * h + 64 * wm < cur.rows && 128 * v + 32 * wn < cur.cols);
+        on |= (int)(128 * h + 32 * wm < cur.rows && 128 * v + 64 * wn < cur.cols) << (2 * h + v);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[h][v][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < 4; ++j) acc[h][v][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
+    on = __builtin_amdgcn_readfirstlane(on);
   };
-  // A quadrant: 16 products, four at a time (two rows of a substep), if they are wanted; due(k)
+  // A quadrant: 16 products, four at a time (two columns of a substep), if they are wanted; due(k)
   // goes before the four, so that reads and loads stand between the products. `on` is made
   // opaque: otherwise paths with and without products each get a copy of what stands between.
-  auto quadrant = [&](int h, int v, const u32x4 (&q)[2][2], auto due) {
+  auto quadrant = [&](int h, int v, const u32x4 (&p)[2][2], auto due) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       due(k);
-      asm volatile("" : "+s"(on[h][v]));
-      if (on[h][v]) {
+      asm volatile("" : "+s"(on));
+      if (on & (1 << (2 * h + v))) {
 #pragma unroll
-        for (int i = 2 * (k & 1); i < 2 * (k & 1) + 2; ++i)
+        for (int j = 2 * (k & 1); j < 2 * (k & 1) + 2; ++j)
 #pragma unroll
-          for (int j = 0; j < 2; ++j) acc[h][v][i][j] = mfma<T>(q[k >> 1][j], p[k >> 1][i], acc[h][v][i][j]);
+          for (int i = 0; i < 2; ++i) acc[h][v][i][j] = mfma<T>(q[k >> 1][j], p[k >> 1][i], acc[h][v][i][j]);
       }
     }
   };
+  // A tile's stores: always kStores of them, so that the waits behind them can count (what lies
+  // past the rows and columns is dropped by the window); value by value, none is left in flight.
+  constexpr bool F32 = OUT == kF32Out;
+  constexpr int kStores = OUT == kAnyWidth ? 0 : F32 ? 32 : 16;
   auto store = [&]() {
+    if constexpr (OUT == kAnyWidth) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        if (!on[h][v]) continue;
-        const int rows = cur.rows - 128 * h - 64 * wm - r16, c0 = 128 * v + 32 * wn;
-        const int64_t at = (cur.row0 + 128 * h + 64 * wm + r16) * O + cur.c0 + c0;
-        if constexpr (F32) {
-          float* dst = reinterpret_cast<float*>(g.out) + at + 4 * grp;
-          const int left = cur.cols - c0 - 4 * grp;
+        for (int v = 0; v < 2; ++v) {
+          const int rows = cur.rows - 128 * h - 32 * wm - r16, c0 = 128 * v + 64 * wn + 4 * grp;
+          uint16_t* dst = reinterpret_cast<uint16_t*>(g.out) + (cur.row0 + 128 * h + 32 * wm + r16) * O + cur.c0 + c0;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+          for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-              if (16 * i < rows && 16 * j < left)
-                *reinterpret_cast<f32x4*>(dst + (int64_t)(16 * i) * O + 16 * j) = acc[h][v][i][j];
-        } else {
-          // rows of 16 lanes of the two column blocks trade places: 8 adjacent columns per lane
-          const int col = 16 * (grp & 1) + 8 * (grp >> 1), left = cur.cols - c0 - col;
-          uint16_t* dst = reinterpret_cast<uint16_t*>(g.out) + at + col;
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            u32x4 o;
+              for (int b = 0; b < 4; ++b)
+                if (16 * i < rows && 16 * j + b < cur.cols - c0)
+                  dst[(int64_t)(16 * i) * O + 16 * j + b] = (uint16_t)pack2<T>(acc[h][v][i][j][b], 0.f);
+        }
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+      return;
+    }
+    // Whole 128-byte lines: a lane has 16 bytes of its row in each of two 64-byte halves (16
+    // bits: of two pairs of column blocks, whose rows of 16 lanes have traded places); the lanes of
+    // rows 8-15 and 0-7 of the block trade a half, and a store then writes 8 rows of 128 bytes.
+    constexpr int size = F32 ? 4 : 2;
+    const int l = fresh_lane();
+    const int r16 = l & 15, grp = l >> 4;
+    const bool low = r16 < 8;
+    const int col = (F32 ? 4 * grp : 16 * (grp & 1) + 8 * (grp >> 1)) + (low ? 0 : F32 ? 16 : 32);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const uint32_t x = pack2<T>(acc[h][v][i][0][2 * b], acc[h][v][i][0][2 * b + 1]);
-              const uint32_t y = pack2<T>(acc[h][v][i][1][2 * b], acc[h][v][i][1][2 * b + 1]);
-              const auto r = __builtin_amdgcn_permlane16_swap(x, y, false, false);
-              o[b] = r[0];
-              o[2 + b] = r[1];
-            }
-            if (16 * i < rows && left > 0) {
-              uint16_t* d = dst + (int64_t)(16 * i) * O;
-              if ((O & 7) == 0) {
-                *reinterpret_cast<u32x4*>(d) = o;
-              } else {
-#pragma clang loop unroll(disable)
-                for (int b = 0; b < min(8, left); ++b) {
-                  const uint32_t x = b < 4 ? (b < 2 ? o[0] : o[1]) : (b < 6 ? o[2] : o[3]);
-                  d[b] = (uint16_t)(x >> (16 * (b & 1)));
-                }
+    for (int h = 0; h < 2; ++h) {
+      const int rows = cur.rows - 128 * h;
+      const __amdgpu_buffer_rsrc_t R = window(reinterpret_cast<uint8_t*>(g.out) + ((cur.row0 + 128 * h) * O + cur.c0) * size,
+                                              rows > 0 ? (rows * O - cur.c0) * size : 0);
+      const uint32_t row = (uint32_t)(32 * wm + (r16 & 7)) * (uint32_t)O * size;
+#pragma unroll
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; j += F32 ? 2 : 4) {
+            u32x4 a, b;
+            if constexpr (F32) {
+              a = __builtin_bit_cast(u32x4, acc[h][v][i][j]);
+              b = __builtin_bit_cast(u32x4, acc[h][v][i][j + 1]);
+            } else {
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                auto two = [&](int jj) { return pack2<T>(acc[h][v][i][jj][2 * x], acc[h][v][i][jj][2 * x + 1]); };
+                const auto r = __builtin_amdgcn_permlane16_swap(two(0), two(1), false, false);
+                const auto s = __builtin_amdgcn_permlane16_swap(two(2), two(3), false, false);
+                a[x] = r[0];
+                a[2 + x] = r[1];
+                b[x] = s[0];
+                b[2 + x] = s[1];
               }
             }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t give = low ? b[x] : a[x];
+              const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, true);   // row_ror:8
+              a[x] = low ? a[x] : got;
+              b[x] = low ? got : b[x];
+            }
+            const int c = 128 * v + 64 * wn + 16 * j + col;
+            const uint32_t at = row + (uint32_t)(16 * i) * (uint32_t)O * size + c * size;
+            __builtin_amdgcn_raw_buffer_store_b128(a, R, oob_unless(c < cur.cols, at), 0, kStream);
+            __builtin_amdgcn_raw_buffer_store_b128(b, R, oob_unless(c < cur.cols, at + 8 * (uint32_t)O * size), 0, kStream);
           }
-        }
-      }
-  };
-  auto read_p = [&](const uint8_t* L, int s, int k) {   // two blocks
-#pragma unroll
-    for (int i = 2 * k; i < 2 * k + 2; ++i) p[s][i] = fp.read(L, i, s);
-  };
-  auto read_q = [&](const uint8_t* L, int s, u32x4 (&d)[2][2]) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) d[s][j] = fq.read(L, j, s);
-  };
-  // One stage from the buffers of P and Q, the next one's first halves in N0 and M0. Behind the
-  // last tile an odd stage runs without products: a way out between the two copies of this body
-  // would, to the compiler, lead back to the first, which then waits for all loads.
-  auto stage = [&](uint8_t* P0, uint8_t* P1, uint8_t* Q0, uint8_t* Q1, const uint8_t* N0, const uint8_t* M0) {
-    quadrant(0, 0, q0, [&](int k) {
-      if (k < 2)
-        read_p(P0, 1, k);
-      else
-        read_q(Q1, k - 2, q1);
-    });
-    step_barrier<8>();   // P0, Q0 and Q1 are read; P1 has landed
-    quadrant(0, 1, q1, [&](int k) {
-      if (k >= 2) read_p(P1, 0, k - 2);   // over what the first substep's products are done with
-    });
-    quadrant(1, 0, q0, [&](int k) {
-      if (k < 2) read_p(P1, 1, k);
-      if (k == 1) {
-        load_p(0, 0, P0);
-        load_p(0, 1, P0);
-      } else if (k >= 2) {
-        load_q(k - 2, 0, k == 2 ? Q0 : Q1);
-        load_q(k - 2, 1, k == 2 ? Q0 : Q1);
-      }
-    });
-    step_barrier<8>();   // P1 is read; the next N0 and both halves of the next Q have landed
-    quadrant(1, 1, q1, [&](int k) {
-      if (k < 2) {
-        load_p(1, k, P1);
-        read_q(M0, k, q0);
-      } else {
-        read_p(N0, 0, k - 2);
-      }
-    });
-  };
-  bool more = true;
-  auto finish = [&]() {   // of a stage
-    advance();
-    if (++st == cur.stages) {
-      store();
-      u += step;
-      st = 0;
-      more = u < end;
-      if (more) {
-        cur = w.tile_of(u);
-      } else {
-        cur.rows = 0;
-        cur.stages = 2;
-      }
-      begin();
     }
   };
-  begin();
-  do {
-    stage(pa0, pa1, qa0, qa1, pb0, qb0);
-    finish();
-    stage(pb0, pb1, qb0, qb1, pa0, qa0);
-    finish();
-  } while (more);
+  auto read_q = [&](const uint8_t* L, int s, int k) {   // two blocks
+#pragma unroll
+    for (int j = 2 * k; j < 2 * k + 2; ++j) q[s][j] = fq.read(L, j, s);
+  };
+  auto read_p = [&](const uint8_t* L, int s, u32x4 (&d)[2][2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) d[s][i] = fp.read(L, i, s);
+  };
+  // One stage from the buffers of P and Q, the next one's first halves in N0 and M0. S: stores of
+  // the tile before that may be in flight behind the loads which are waited for.
+  auto stage = [&](auto behind, uint8_t* P0, uint8_t* P1, uint8_t* Q0, uint8_t* Q1, const uint8_t* N0, const uint8_t* M0) {
+    constexpr int S = decltype(behind)::value;
+    quadrant(0, 0, p0, [&](int k) {
+      if (k < 2)
+        read_q(Q0, 1, k);
+      else
+        read_p(P1, k - 2, p1);
+    });
+    step_barrier<8 + S>();   // Q0, P0 and P1 are read; Q1 has landed
+    quadrant(1, 0, p1, [&](int k) {
+      if (k >= 2) read_q(Q1, 0, k - 2);   // over what the first substep's products are done with
+    });
+    quadrant(0, 1, p0, [&](int k) {
+      if (k < 2) read_q(Q1, 1, k);
+      if (k == 1) {
+        load_q(0, 0, Q0);
+        load_q(0, 1, Q0);
+      } else if (k >= 2) {
+        load_p(k - 2, 0, k == 2 ? P0 : P1);
+        load_p(k - 2, 1, k == 2 ? P0 : P1);
+      }
+    });
+    step_barrier<8 + S>();   // Q1 is read; the next M0 and both halves of the next P have landed
+    quadrant(1, 1, p1, [&](int k) {
+      if (k < 2) {
+        load_q(1, k, Q1);
+        read_p(N0, k, p0);
+      } else {
+        read_q(M0, 0, k - 2);
+      }
+    });
+    advance();
+  };
+  // A tile's first stage stands behind the stores of the tile before (for the first tile: as many
+  // that store nothing). Its place in the program is its own, so that on every way to a wait the
+  // number of memory operations in flight is the same: the compiler, which checks each read of
+  // LDS against the loads, then adds no wait. A tile's odd last stage has no products.
+  constexpr std::integral_constant<int, 0> none{};
+  constexpr std::integral_constant<int, kStores> some{};
+#pragma unroll
+  for (int i = 0; i < kStores; ++i)   // at places of their own, or the compiler keeps one of them
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, window(g.out, 0), 16 * i, 0, 0);
+  for (;;) {
+    begin();
+    int real = (cur.n + TK - 1) / TK;
+    auto second = [&]() {   // the products of the pair's second stage
+      real -= 2;
+      on = __builtin_amdgcn_readfirstlane(real < 0 ? 0 : on);
+    };
+    stage(some, pa0, pa1, qa0, qa1, pb0, qb0);
+    second();
+    stage(none, pb0, pb1, qb0, qb1, pa0, qa0);
+    for (int st = 2; st < cur.stages; st += 2) {
+      stage(none, pa0, pa1, qa0, qa1, pb0, qb0);
+      second();
+      stage(none, pb0, pb1, qb0, qb1, pa0, qa0);
+    }
+    store();
+    u += step;
+    if (u >= end) break;
+    cur = w.tile_of(u);
+  }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no load into LDS outlives the workgroup
 }
 
@@ -529,25 +580,27 @@ hipError_t narrow_one(const DenseArgs& g, int cus, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int D, int T, bool F32>
+template <int D, int T, int OUT>
 hipError_t tile_one(const DenseArgs& g, int cus, hipStream_t s) {
   const int64_t bn = (g.N + TM - 1) / TM, bk = (g.K + TN - 1) / TN;
   const int64_t bound = D == kDenseWgrad ? g.E * bn * bk
                                          : ((g.M + TM - 1) / TM + std::min<int64_t>(g.E, g.M)) * (D == kDenseFwd ? bn : bk);
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(bound, (int64_t)cus));
-  hipLaunchKernelGGL((dense_tile_kernel<D, T, F32>), dim3((unsigned)grid), dim3(TThreads), 0, s, g);
+  hipLaunchKernelGGL((dense_tile_kernel<D, T, OUT>), dim3((unsigned)grid), dim3(TThreads), 0, s, g);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, const DenseArgs& g, int cus, hipStream_t s) {
-  const bool b = dtype == kBF16;
-  if (dir == kDenseFwd) return b ? tile_one<kDenseFwd, kBF16, false>(g, cus, s) : tile_one<kDenseFwd, kF16, false>(g, cus, s);
-  if (dir == kDenseDgrad)
-    return b ? tile_one<kDenseDgrad, kBF16, false>(g, cus, s) : tile_one<kDenseDgrad, kF16, false>(g, cus, s);
-  if (f32_out) return b ? tile_one<kDenseWgrad, kBF16, true>(g, cus, s) : tile_one<kDenseWgrad, kF16, true>(g, cus, s);
-  return b ? tile_one<kDenseWgrad, kBF16, false>(g, cus, s) : tile_one<kDenseWgrad, kF16, false>(g, cus, s);
+  auto run = [&](auto t) {
+    constexpr int T = decltype(t)::value;
+    if (dir == kDenseDgrad) return tile_one<kDenseDgrad, T, kWide>(g, cus, s);
+    if (dir == kDenseWgrad)
+      return f32_out ? tile_one<kDenseWgrad, T, kF32Out>(g, cus, s) : tile_one<kDenseWgrad, T, kWide>(g, cus, s);
+    return g.N % 8 ? tile_one<kDenseFwd, T, kAnyWidth>(g, cus, s) : tile_one<kDenseFwd, T, kWide>(g, cus, s);
+  };
+  return dtype == kBF16 ? run(std::integral_constant<int, kBF16>{}) : run(std::integral_constant<int, kF16>{});
 }
 
 hipError_t launch_dense_narrow(int dtype, const DenseArgs& g, int cus, hipStream_t s) {

@@ -531,8 +531,7 @@ __device__ int32_t build_plan(Plan& p, const int32_t* __restrict__ sizes, int E,
 // the largest e with upre[e] <= u. upre is nondecreasing with upre[0] = 0, so
 // that e is the number of e' in [1, E) with upre[e'] <= u, counted 64 experts per
 // ballot (experts with no units share the next expert's upre and are passed).
-__device__ __forceinline__ int find_expert(const int32_t* upre, int E, int32_t u) {
-  const int lane = threadIdx.x & 63;
+__device__ __forceinline__ int find_expert(const int32_t* upre, int E, int32_t u, int lane) {
   int cnt = 0;
   for (int base = 1; base < E; base += 64) {
     const int e = base + lane;
@@ -542,6 +541,10 @@ __device__ __forceinline__ int find_expert(const int32_t* upre, int E, int32_t u
     if (b != ~0ull) break;   // the rest lie past u
   }
   return cnt;
+}
+
+__device__ __forceinline__ int find_expert(const int32_t* upre, int E, int32_t u) {
+  return find_expert(upre, E, u, threadIdx.x & 63);
 }
 
 __device__ __forceinline__ int find_expert(const Plan& p, int E, int32_t u) { return find_expert(p.upre, E, u); }
