@@ -149,7 +149,7 @@ def lib() -> ctypes.CDLL:
             L.geg_request_lora.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I64, _I32, _I32,
                                            _P, _SZ, _P]
             L.geg_request_lora.restype = ctypes.c_int
-            L.geg_request_lora_workspace_bytes.argtypes = [_I64, _I64, _I32]
+            L.geg_request_lora_workspace_bytes.argtypes = [_I64, _I64, _I32, _I32]
             L.geg_request_lora_workspace_bytes.restype = _SZ
             L.geg_lora_dropout_workspace_bytes.argtypes = [_I32, _I64, _I64, _I64, _I32, _I32]
             L.geg_lora_dropout_workspace_bytes.restype = _SZ
@@ -1378,7 +1378,7 @@ def request_lora(y, x, ids, lora_a, lora_b, scales=None, out=None, workspace: Wo
     with _allocating(stream):
         if mine:
             out = x.new_empty((M, N))
-        ws = _workspace(workspace, lib_.geg_request_lora_workspace_bytes(M, K, r), x.device, None, check_errors)
+        ws = _workspace(workspace, lib_.geg_request_lora_workspace_bytes(M, K, L, r), x.device, None, check_errors)
     _check(lib_.geg_request_lora(_addr(y), ldy, x.data_ptr(), ldx, ids.data_ptr(), lora_a.data_ptr(), lora_b.data_ptr(),
                                  _addr(scales), out.data_ptr(), ldo, dt, M, N, K, L, r, ws.buf.data_ptr(), ws.buf.numel(),
                                  raw))

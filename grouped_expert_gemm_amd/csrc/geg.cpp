@@ -1245,9 +1245,27 @@ geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes
                       workspace_bytes, opts, stream);
 }
 
-size_t geg_request_lora_workspace_bytes(int64_t M, int64_t K, int32_t r) {
-  if (M < 0 || K <= 0 || r <= 0 || r > geg::kRequestMaxRank || M >= (int64_t)INT32_MAX) return 0;
-  return kHeader + round256((size_t)geg::request_splits(M, K, r) * (size_t)M * (size_t)r * 4);
+// Workspace of the request adapters: the header, the units and the rows in their order (batches past
+// kRequestScan), x A^T.
+struct RequestLayout {
+  size_t units, rows, u, total;
+};
+static RequestLayout request_layout(int64_t M, int64_t K, int32_t L, int32_t r) {
+  RequestLayout w{};
+  w.units = w.rows = w.u = kHeader;
+  if (M > geg::kRequestScan) {
+    w.rows = w.units + round256((size_t)(geg::request_units(M, L, r) + 1) * 16);   // (their number first)
+    w.u = w.rows + round256((size_t)M * 4);
+  }
+  w.total = w.u + round256((size_t)geg::request_splits(M, K, r) * (size_t)M * (size_t)r * 4);
+  return w;
+}
+
+size_t geg_request_lora_workspace_bytes(int64_t M, int64_t K, int32_t L, int32_t r) {
+  if (M < 0 || K <= 0 || L <= 0 || L > geg::kRequestMaxAdapters || r <= 0 || r > geg::kRequestMaxRank ||
+      M >= (int64_t)INT32_MAX)
+    return 0;
+  return request_layout(M, K, L, r).total;
 }
 
 geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t ldx, const int32_t* ids,
@@ -1257,15 +1275,18 @@ geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t l
   if (dtype != GEG_BF16 && dtype != GEG_F16) return fail(GEG_ERR_BAD_OPTION, "dtype must be GEG_BF16 or GEG_F16");
   if (M < 0 || N <= 0 || K <= 0 || L <= 0) return fail(GEG_ERR_BAD_SHAPE, "need M >= 0, N > 0, K > 0, L > 0");
   if (M >= (int64_t)INT32_MAX) return fail(GEG_ERR_BAD_SHAPE, "M must be below 2^31");
+  if (L > geg::kRequestMaxAdapters) return fail(GEG_ERR_BAD_SHAPE, "L exceeds 32768 adapters");
   if (N % 8 || K % 8) return fail(GEG_ERR_BAD_SHAPE, "N and K must be multiples of 8");
   if (r < 8 || r > geg::kRequestMaxRank || r % 8)
     return fail(GEG_ERR_BAD_SHAPE, "the adapters' rank r must be 8, 16, ..., 128");
   if ((y && ldy < N) || ldx < K || ldo < N) return fail(GEG_ERR_BAD_SHAPE, "a row pitch must be at least the row's width");
   if (std::max({N, K, y ? ldy : N, ldx, ldo}) > kMaxWindow / 512)
     return fail(GEG_ERR_BAD_SHAPE, "256 rows of 16-bit values, pitch included, must fit in 0x7FFFFFF0 bytes");
-  // a launch holds fewer than 2^32 threads: a workgroup of 256 per 32 rows, a wavefront per 32 rows and 64 columns
-  if ((M + 15) / 16 * ((N + 63) / 64) > (int64_t)1 << 24)
-    return fail(GEG_ERR_BAD_SHAPE, "ceil(M / 16) * ceil(N / 64) must not exceed 2^24");
+  // a launch holds fewer than 2^32 threads: a workgroup of 256 per unit and at most 16 ranges of K, or
+  // per unit and four to 32 chunks of 64 columns
+  const int64_t units = geg::request_units(M, L, r);
+  if (units > (int64_t)1 << 19 || units * ((N + 255) / 256) > (int64_t)1 << 23)
+    return fail(GEG_ERR_BAD_SHAPE, "ceil(M / 32) + L must not exceed 2^19, times ceil(N / 256) 2^23");
   if (M == 0) return GEG_OK;
   if (!x || !ids || !lora_a || !lora_b || !out) return fail(GEG_ERR_NULL_POINTER, "a required pointer is NULL");
   if (!ws) return fail(GEG_ERR_WORKSPACE, "workspace is NULL");
@@ -1275,9 +1296,9 @@ geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t l
       (M > 1 && ((y && ldy % 8) || ldx % 8 || ldo % 8)) || !aligned(ids, 4) || !aligned(scales, 4))
     return fail(GEG_ERR_MISALIGNED, "y, x, lora_a, lora_b, out and their row pitches must be 16-byte aligned");
   if (!aligned(ws, 256)) return fail(GEG_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  const size_t need = geg_request_lora_workspace_bytes(M, K, r);
-  if (ws_bytes < need)
-    return fail(GEG_ERR_WORKSPACE, "workspace smaller than geg_request_lora_workspace_bytes(): need " + std::to_string(need));
+  const RequestLayout w = request_layout(M, K, L, r);
+  if (ws_bytes < w.total)
+    return fail(GEG_ERR_WORKSPACE, "workspace smaller than geg_request_lora_workspace_bytes(): need " + std::to_string(w.total));
   geg_status st;
   if ((st = check_device()) != GEG_OK) return st;
   for (auto [ptr, name] : {std::pair<const void*, const char*>{y, "y"}, {x, "x"}, {ids, "ids"}, {lora_a, "lora_a"},
@@ -1286,13 +1307,15 @@ geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t l
   uint8_t* wsb = reinterpret_cast<uint8_t*>(ws);
   geg::RequestArgs g{reinterpret_cast<const uint16_t*>(y), reinterpret_cast<const uint16_t*>(x), ids,
                      reinterpret_cast<const uint16_t*>(lora_a), reinterpret_cast<const uint16_t*>(lora_b), scales,
-                     reinterpret_cast<uint16_t*>(out), reinterpret_cast<float*>(wsb + kHeader),
+                     reinterpret_cast<uint16_t*>(out), reinterpret_cast<float*>(wsb + w.u),
+                     M > geg::kRequestScan ? reinterpret_cast<int32_t*>(wsb + w.units) + 4 : nullptr,
+                     reinterpret_cast<int32_t*>(wsb + w.units), reinterpret_cast<int32_t*>(wsb + w.rows),
                      // a single row has no pitch
                      M == 1 ? N : ldy, M == 1 ? K : ldx, M == 1 ? N : ldo, M, N, K, L, r,
                      geg::request_splits(M, K, r), reinterpret_cast<uint32_t*>(wsb)};
   hipError_t e = geg::launch_request_lora(g, dtype, stream);
   if (e != hipSuccess) return hip_fail(e, "request adapter launch");
-  g_launches += 2;
+  g_launches += g.units ? 3 : 2;
   return GEG_OK;
 }
 

@@ -170,6 +170,8 @@ hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, const DenseArgs& 
 hipError_t launch_dense_narrow(int dtype, const DenseArgs& g, int cus, hipStream_t s);
 // Low-rank adapters of many requests beside a shared projection (see request.hip).
 constexpr int kRequestMaxRank = 128;
+constexpr int kRequestMaxAdapters = 32768;   // counters in LDS
+constexpr int kRequestScan = 128;   // rows up to which the units come from the ids directly
 struct RequestArgs {
   const uint16_t* y;      // [M, N], rows ldy apart, or NULL: zeros
   const uint16_t* x;      // [M, K], rows ldx apart
@@ -179,11 +181,15 @@ struct RequestArgs {
   const float* scales;    // [L] or NULL: ones
   uint16_t* out;          // [M, N], rows ldo apart; may be y
   float* u;               // workspace: partial x A^T [splits, M, r]
+  int32_t* units;         // workspace: {adapter, first, rows, -} of each unit (NULL: from the ids),
+  int32_t* n_units;       // their number,
+  int32_t* rows;          // and the rows in the units' order [M]
   int64_t ldy, ldx, ldo, M, N, K;
   int32_t L, r, splits;
   uint32_t* err;
 };
 int request_splits(int64_t M, int64_t K, int32_t r);
+int64_t request_units(int64_t M, int32_t L, int32_t r);
 hipError_t launch_request_lora(const RequestArgs& g, int dtype, hipStream_t s);
 // Dropout: out = [res +] keep ? x * scale : 0 for n values (see dropout.hip, philox.hpp).
 hipError_t launch_dropout(const void* x, const void* res, void* out, int dtype, int64_t n, const DropoutArgs& d, int cus,

@@ -535,16 +535,16 @@ geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes
  *   x        [M, K], rows ldx apart; ids int32 [M], in any order; a negative id: no adapter,
  *            out is y there; an id >= L likewise, and flags GEG_DEVERR_BAD_EXPERT_ID
  *   lora_a   [L, r, K], lora_b [L, N, r]; r 8, 16, ..., 128; adapters of lower rank are
- *            filled up with zeros
+ *            filled up with zeros; L <= 32768
  *   scales   fp32 [L], or NULL for ones
  *   out      [M, N], rows ldo apart; may be y itself (same pitch), not x
- *   workspace: geg_request_lora_workspace_bytes(M, K, r) bytes
+ *   workspace: geg_request_lora_workspace_bytes(M, K, L, r) bytes
  * N, K and the pitches are multiples of 8, every tensor is 16-byte aligned. Sums run in fp32;
  * x A^T keeps at least 16 significant bits on its way into the second product; one rounding.
  * An adapter's values reach only the rows that name it. Rows routed to experts with
  * an adapter each have ids = adapter * E + expert over lora_a [adapters * E, r, K].
  */
-size_t geg_request_lora_workspace_bytes(int64_t M, int64_t K, int32_t r);
+size_t geg_request_lora_workspace_bytes(int64_t M, int64_t K, int32_t L, int32_t r);
 geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t ldx, const int32_t* ids,
                             const void* lora_a, const void* lora_b, const float* scales, void* out, int64_t ldo,
                             int32_t dtype, int64_t M, int64_t N, int64_t K, int32_t L, int32_t r, void* workspace,

@@ -26,7 +26,8 @@ def test_request_refusals():
     assert _req(r=0) == 2 and _req(r=12) == 2 and _req(r=136) == 2 and _req(r=128) not in passes
     assert _req(ldy=56) == 2 and _req(ldx=120) == 2 and _req(ldo=56) == 2
     assert _req(N=1 << 62, ldy=1 << 62, ldo=1 << 62) == 2 and _req(ldx=1 << 40) == 2
-    assert _req(M=1 << 29, N=64) == 2 and _req(M=1 << 30) == 2    # more than 2^24 units
+    assert _req(M=1 << 30) == 2 and _req(M=1 << 24, N=65536, ldy=65536, ldo=65536) == 2    # more workgroups than a launch holds
+    assert _req(L_=32769) == 2 and _req(L_=32768) not in passes
     assert _req(M=0, x=None, ws=None) == 0
     for p in ("x", "ids", "a", "b", "out"):
         assert _req(**{p: None}) == 1, p
@@ -38,10 +39,12 @@ def test_request_refusals():
     assert _req(out=2 * P) == 8                                     # out is x
     assert _req(out=P, ldo=72) == 8 and _req(out=P) not in passes  # in place: one pitch
     assert _req(ws=None) == 5 and _req(ws=P + 16) == 5
-    need = L().geg_request_lora_workspace_bytes(4, 128, 16)
+    need = L().geg_request_lora_workspace_bytes(4, 128, 3, 16)
     assert need == 256 + 256      # one range of the contraction
     assert _req(nbytes=need - 1) == 5 and _req(nbytes=need) not in passes
-    assert L().geg_request_lora_workspace_bytes(4, 128, 136) == 0
+    assert L().geg_request_lora_workspace_bytes(4, 128, 3, 136) == 0
+    # past 128 rows: 5 units at most and their number, and the rows in the units' order
+    assert L().geg_request_lora_workspace_bytes(200, 128, 1, 16) == 256 + 256 + 1024 + 200 * 64
 
 
 def _drop(x=P, res=None, out=P, dtype=0, n=100, p=0.5, seed=1, offset=0, rng=None):
