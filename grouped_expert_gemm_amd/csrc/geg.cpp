@@ -1313,7 +1313,7 @@ geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t l
                      // a single row has no pitch
                      M == 1 ? N : ldy, M == 1 ? K : ldx, M == 1 ? N : ldo, M, N, K, L, r,
                      geg::request_splits(M, K, r), reinterpret_cast<uint32_t*>(wsb)};
-  hipError_t e = geg::launch_request_lora(g, dtype, stream);
+  hipError_t e = geg::launch_request_lora(g, dtype, cu_count(), stream);
   if (e != hipSuccess) return hip_fail(e, "request adapter launch");
   g_launches += g.units ? 3 : 2;
   return GEG_OK;

@@ -190,7 +190,7 @@ struct RequestArgs {
 };
 int request_splits(int64_t M, int64_t K, int32_t r);
 int64_t request_units(int64_t M, int32_t L, int32_t r);
-hipError_t launch_request_lora(const RequestArgs& g, int dtype, hipStream_t s);
+hipError_t launch_request_lora(const RequestArgs& g, int dtype, int cus, hipStream_t s);
 // Dropout: out = [res +] keep ? x * scale : 0 for n values (see dropout.hip, philox.hpp).
 hipError_t launch_dropout(const void* x, const void* res, void* out, int dtype, int64_t n, const DropoutArgs& d, int cus,
                           hipStream_t s);

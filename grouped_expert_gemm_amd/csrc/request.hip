@@ -58,7 +58,7 @@ __device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b) {
 __device__ __forceinline__ int named(int id, int L) { return id >= 0 && id < L ? id : -1; }
 
 // ------------------------------------------------------------------ the units
-// One workgroup lists a batch's units: rows counted by adapter (key L: none), offsets and unit
+// One workgroup lists a batch's units (8000 rows: 9 us, two reads of the ids): rows counted by adapter (key L: none), offsets and unit
 // numbers by a scan over the keys, rows dealt to their places (in no fixed order: a row's result
 // does not depend on its place).
 constexpr int kPlanThreads = 1024;
@@ -206,7 +206,9 @@ struct Unit {
 
 // ------------------------------------------------------------------ u = x A^T
 // U[split][t, j] = sum over the split's k of x[t, k] A_i[j, k]. A workgroup has one unit and one
-// range of 32-wide steps, dealt to its wavefronts in turn; they are added in wavefront order.
+// range of 32-wide steps, dealt to its wavefronts in turn; they are added in wavefront order. Bound by
+// x (8000 x 4096: 65.5 MB in 21 us where x is in the last cache, 28 where not), a small batch by
+// latency; loads a step ahead of the products gained nothing (28 to 32 us).
 template <int T, int RB, int NCB>
 __global__ __launch_bounds__(kThreads) void request_down_kernel(RequestArgs g) {
   __shared__ f32x4 red[kWaves - 1][RB][NCB][64];
@@ -272,176 +274,293 @@ __global__ __launch_bounds__(kThreads) void request_down_kernel(RequestArgs g) {
 }
 
 // ------------------------------------------------------------------ out = y + s u B^T
-// out[t, n] = y[t, n] + sum_j (s_i u[t, j]) B_i[n, j]. A workgroup has one unit, its wavefronts
-// `per` chunks of 64 columns each. u enters the matrix instructions in two 16-bit parts, high and
-// rest (together 16 bits of it in bf16, 22 in fp16), laid side by side along the contraction: slot
-// group q (8 wide) of the 2 r / 8 holds part q / (r / 8) of j = 8 (q % (r / 8)) .., against the
-// same B. fp16 has too few exponents for that: a row of u is scaled by a power of two that brings
-// its largest value to [2^10, 2^11), undone in the fp32 sums. The parts are made once per
-// workgroup, in LDS.
-template <int T, int RB, int NM>
-__global__ __launch_bounds__(kThreads) void request_up_kernel(RequestArgs g, int per) {
-  __shared__ u32x4 parts[RB][NM][64];
+// out[t, n] = y[t, n] + sum_j (s_i u[t, j]) B_i[n, j]. The work is (unit, 4 chunks of 64 columns, one
+// per wavefront): one of these to a workgroup for batches of kRequestScan rows, equal runs of them to
+// two workgroups per CU for others, so that a unit's start (its rows, the parts of u) is paid once per
+// run and no second round of workgroups is half empty. Bound by y and out: 8000 rows of 14336
+// columns, fp16, rank 64, read and write 459 MB in 117 to 121 us, 3.8 TB/s (a copy of 1 GiB: 5.2);
+// both pass the L2 by, 160 -> 152 us with the launches before. u enters the matrix instructions in two 16-bit parts, high and
+// rest (together 16 bits of it in bf16, 22 in fp16): for r <= 16 (PACK) side by side in one
+// instruction's contraction (slot group q, 8 wide, holds part q / (r / 8) of j = 8 (q % (r / 8)) ..),
+// else NB blocks of 32 of either against the same B. fp16 has too few exponents for that: a row of u
+// is scaled by a power of two that brings its largest value to [2^10, 2^11), undone in the fp32
+// sums. The parts are made once per workgroup, in LDS.
+template <int T, int RB, int NB, bool PACK>
+__global__ __launch_bounds__(kThreads, 2) void request_up_kernel(RequestArgs g, int units) {
+  static_assert(!PACK || NB == 1, "two parts in one block");
+  constexpr int kParts = PACK ? 1 : 2 * NB;
+  __shared__ u32x4 parts[RB][kParts][64];
   __shared__ int32_t pick[16 * RB], power[16 * RB];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r16 = lane & 15, grp = lane >> 4;
-  const int chunks = (int)((g.N + 63) / 64), groups = (chunks + kWaves * per - 1) / (kWaves * per);
-  const int unit = blockIdx.x / groups;
-  const Unit<RB> u(g, unit, pick, false);
-  if (u.n == 0 || (u.id < 0 && g.out == g.y)) return;
+  const int chunks = (int)((g.N + 63) / 64), groups = (chunks + kWaves - 1) / kWaves;
   const int pr = g.r / 8;   // slot groups of a part
-  int ex[RB];
+  // slot group q of block m, here: its j / 8, or past the end
+  auto slot = [&](int m) {
+    const int q = 4 * m + grp;
+    if constexpr (PACK) return q < pr ? q : (q < 2 * pr ? q - pr : 16);
+    return q < pr ? q : 16;
+  };
+  auto run = [&](const Unit<RB>& u, int g0, int g1) {
+    int ex[RB];
 #pragma unroll
-  for (int b = 0; b < RB; ++b) ex[b] = 0;
-  if (u.id >= 0) {
-    const float s = g.scales ? g.scales[u.id] : 1.0f;
+    for (int b = 0; b < RB; ++b) ex[b] = 0;
+    if (u.id >= 0) {
+      const float s = g.scales ? g.scales[u.id] : 1.0f;
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      if (RB > 1 && b % kWaves != wave) continue;   // (one block: every wavefront, so that none waits)
-      float v[NM][8];
-      float top = 0.f;
+      for (int b = 0; b < RB; ++b) {
+        if (RB > 1 && b % kWaves != wave) continue;   // (one block: every wavefront, so that none waits)
+        float v[NB][8];
+        float top = 0.f;
 #pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        const int q = 4 * m + grp;
+        for (int m = 0; m < NB; ++m) {
+          const int q = slot(m);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[m][i] = 0.f;
-        if (q < 2 * pr && 16 * b + r16 < u.n) {
-          const float* U = g.u + u.row[b] * (int64_t)g.r + 8 * (q < pr ? q : q - pr);
-          for (int k = 0; k < g.splits; ++k, U += g.M * g.r) {
-            const f32x4 lo = *reinterpret_cast<const f32x4*>(U), hi = *reinterpret_cast<const f32x4*>(U + 4);
+          for (int i = 0; i < 8; ++i) v[m][i] = 0.f;
+          if (q < 16 && 16 * b + r16 < u.n) {
+            const float* U = g.u + u.row[b] * (int64_t)g.r + 8 * q;
+#pragma unroll 4
+            for (int k = 0; k < g.splits; ++k, U += g.M * g.r) {
+              const f32x4 lo = *reinterpret_cast<const f32x4*>(U), hi = *reinterpret_cast<const f32x4*>(U + 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[m][i] += lo[i];
-              v[m][4 + i] += hi[i];
+              for (int i = 0; i < 4; ++i) {
+                v[m][i] += lo[i];
+                v[m][4 + i] += hi[i];
+              }
             }
           }
-        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[m][i] *= s;
-          top = fmaxf(top, fabsf(v[m][i]));
-        }
-      }
-      int e = 0;
-      if constexpr (T == kF16) {
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (top > 0.f && top < __builtin_inff()) e = (int)__builtin_amdgcn_frexp_expf(top) - 11;
-        if (grp == 0) power[16 * b + r16] = e;
-      }
-#pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        const bool rest = 4 * m + grp >= pr;
-        u32x4 w;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float a = v[m][2 * i], c = v[m][2 * i + 1];
-          if constexpr (T == kF16) {
-            a = __builtin_amdgcn_ldexpf(a, -e);
-            c = __builtin_amdgcn_ldexpf(c, -e);
+          for (int i = 0; i < 8; ++i) {
+            v[m][i] *= s;
+            top = fmaxf(top, fabsf(v[m][i]));
           }
-          uint32_t h = pack2<T>(a, c);
-          if (rest) {
+        }
+        int e = 0;
+        if constexpr (T == kF16) {
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          if (top > 0.f && top < __builtin_inff()) e = (int)__builtin_amdgcn_frexp_expf(top) - 11;
+          if (grp == 0) power[16 * b + r16] = e;
+        }
+#pragma unroll
+        for (int m = 0; m < NB; ++m) {
+          u32x4 high, rest;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float a = v[m][2 * i], c = v[m][2 * i + 1];
+            if constexpr (T == kF16) {
+              a = __builtin_amdgcn_ldexpf(a, -e);
+              c = __builtin_amdgcn_ldexpf(c, -e);
+            }
+            high[i] = pack2<T>(a, c);
             float ha, hc;
-            unpack2<T>(h, ha, hc);
+            unpack2<T>(high[i], ha, hc);
             // (an infinity has no rest)
-            h = pack2<T>(fabsf(ha) < __builtin_inff() ? a - ha : 0.f, fabsf(hc) < __builtin_inff() ? c - hc : 0.f);
+            rest[i] = pack2<T>(fabsf(ha) < __builtin_inff() ? a - ha : 0.f, fabsf(hc) < __builtin_inff() ? c - hc : 0.f);
           }
-          w[i] = h;
+          if constexpr (PACK) {
+            parts[b][0][lane] = grp < pr ? high : rest;
+          } else {
+            parts[b][m][lane] = high;
+            parts[b][NB + m][lane] = rest;
+          }
         }
-        parts[b][m][lane] = w;
       }
     }
-  }
-  __syncthreads();
-  if constexpr (T == kF16) {
-    if (u.id >= 0) {
+    __syncthreads();
+    if constexpr (T == kF16) {
+      if (u.id >= 0) {
 #pragma unroll
-      for (int b = 0; b < RB; ++b) ex[b] = power[16 * b + r16];
+        for (int b = 0; b < RB; ++b) ex[b] = power[16 * b + r16];
+      }
     }
-  }
-  // a lane has 8 adjacent columns of each row block and pair of column blocks
-  const int col = 16 * (grp & 1) + 8 * (grp >> 1);
-  const int c0 = (blockIdx.x % groups) * kWaves * per + wave;
-  for (int ch = c0; ch < min(chunks, c0 + kWaves * per); ch += kWaves) {
-    const int64_t n0 = 64 * (int64_t)ch;
-    const int cols = (int)min<int64_t>(64, g.N - n0);
-    u32x4 y[RB][2];
+    // The matrix instructions leave a lane 8 adjacent columns of one row in each half chunk; its loads of
+    // y and its stores are of whole 128-byte lines, 8 rows an instruction: rows 8 h + r16 % 8.
+    const bool low = r16 < 8;
+    const int col = 32 * (r16 >> 3) + 16 * (grp & 1) + 8 * (grp >> 1);
+    int row[RB][2];
+    uint32_t live = 0;
 #pragma unroll
     for (int b = 0; b < RB; ++b)
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        y[b][p] = u32x4{0, 0, 0, 0};
-        if (g.y && 16 * b + r16 < u.n && 32 * p + col < cols)
-          y[b][p] = *reinterpret_cast<const u32x4*>(g.y + u.row[b] * g.ldy + n0 + 32 * p + col);
+      for (int h = 0; h < 2; ++h) {
+        const int i = 8 * h + (r16 & 7);
+        row[b][h] = __shfl(u.row[b], i);
+        live |= (uint32_t)(16 * b + i < u.n) << (2 * b + h);
       }
-    f32x4 acc[RB][4] = {};
-    if (u.id >= 0) {
-      const __amdgpu_buffer_rsrc_t B = window(g.b + ((int64_t)u.id * g.N + n0) * g.r, (int64_t)cols * g.r * 2);
+    const int c0 = g0 * kWaves + wave, c1 = min(chunks, g1 * kWaves);
+    uint32_t bat[NB];
 #pragma unroll
-      for (int m = 0; m < NM; ++m) {
-        const int q = 4 * m + grp;
-        u32x4 bf[4];
+    for (int m = 0; m < NB; ++m) bat[m] = oob_unless(slot(m) < 16, (uint32_t)((r16 * g.r + 8 * slot(m)) * 2));
+    auto load_b = [&](int ch, u32x4 (&bf)[NB][4]) {
+      const int64_t n0 = 64 * (int64_t)ch;
+      const __amdgpu_buffer_rsrc_t B =
+          window(g.b + ((int64_t)u.id * g.N + n0) * g.r, std::min<int64_t>(64, g.N - n0) * g.r * 2);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          bf[j] = __builtin_amdgcn_raw_buffer_load_b128(
-              B, oob_unless(q < 2 * pr, (uint32_t)(((16 * j + r16) * g.r + 8 * (q < pr ? q : q - pr)) * 2)), 0, 0);
+      for (int m = 0; m < NB; ++m)
 #pragma unroll
-        for (int b = 0; b < RB; ++b) {
-          if (b > 0 && 16 * b >= u.n) continue;
-          const u32x4 uf = parts[b][m][lane];
+        for (int j = 0; j < 4; ++j) bf[m][j] = __builtin_amdgcn_raw_buffer_load_b128(B, bat[m] + 32 * j * (uint32_t)g.r, 0, 0);
+    };
+    // Loads of y are unconditional (rows and columns past the end: some that are there).
+    auto load_y = [&](int ch, int b, u32x4 (&y)[RB][2]) {
+      const int64_t n = std::min<int64_t>(64 * (int64_t)ch + col, g.N - 8);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[b][j] = mfma<T>(bf[j], uf, acc[b][j]);
+      for (int h = 0; h < 2; ++h)
+        y[b][h] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(g.y + row[b][h] * g.ldy + n));
+    };
+    auto store = [&](int ch, int b, int h, u32x4 o, bool all) {
+      const int64_t n = 64 * (int64_t)ch + col;
+      if (all || (((live >> (2 * b + h)) & 1) && n < g.N))
+        __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(g.out + row[b][h] * g.ldo + n));
+    };
+    auto product = [&](const u32x4 (&bf)[NB][4], int b, float (&d)[2][8]) {
+      f32x4 acc[4] = {};
+#pragma unroll
+      for (int m = 0; m < NB; ++m) {
+        const u32x4 high = parts[b][m][lane];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] = mfma<T>(bf[m][j], high, acc[j]);
+        if constexpr (!PACK) {
+          const u32x4 rest = parts[b][NB + m][lane];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] = mfma<T>(bf[m][j], rest, acc[j]);
         }
       }
-    }
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      if (b > 0 && 16 * b >= u.n) continue;
 #pragma unroll
       for (int p = 0; p < 2; ++p) {
         // rows of 16 lanes of two neighbouring column blocks trade places
-        float d[8];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float lo = acc[b][2 * p][i], hi = acc[b][2 * p + 1][i];
+          float lo = acc[2 * p][i], hi = acc[2 * p + 1][i];
           if constexpr (T == kF16) {
             lo = __builtin_amdgcn_ldexpf(lo, ex[b]);
             hi = __builtin_amdgcn_ldexpf(hi, ex[b]);
           }
           const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(lo), __float_as_uint(hi), false, false);
-          d[i] = __uint_as_float(x[0]);
-          d[4 + i] = __uint_as_float(x[1]);
-        }
-        if (16 * b + r16 < u.n && 32 * p + col < cols) {
-          u32x4 o = y[b][p];   // (without an adapter: the same bits)
-          if (u.id >= 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              float a, e;
-              unpack2<T>(y[b][p][i], a, e);
-              o[i] = pack2<T>(a + d[2 * i], e + d[2 * i + 1]);
-            }
-          }
-          *reinterpret_cast<u32x4*>(g.out + u.row[b] * g.ldo + n0 + 32 * p + col) = o;
+          d[p][i] = __uint_as_float(x[0]);
+          d[p][4 + i] = __uint_as_float(x[1]);
         }
       }
+      // and the second half of a low row with the first of the row 8 below
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int give = __float_as_int(low ? d[1][i] : d[0][i]);
+        const float got = __int_as_float(__builtin_amdgcn_update_dpp(0, give, 0x128, 0xF, 0xF, false));   // row_ror:8
+        d[0][i] = low ? d[0][i] : got;
+        d[1][i] = low ? got : d[1][i];
+      }
+    };
+    auto add = [&](const u32x4& y, const float (&d)[8]) {
+      u32x4 o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float a, e;
+        unpack2<T>(y[i], a, e);
+        o[i] = pack2<T>(a + d[2 * i], e + d[2 * i + 1]);
+      }
+      return o;
+    };
+    if (u.id < 0) {
+      for (int ch = c0; ch < c1; ch += kWaves) {
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          u32x4 y[RB][2] = {};
+          if (g.y) load_y(ch, b, y);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) store(ch, b, h, y[b][h], false);   // the same bits
+        }
+      }
+    } else if (RB == 1 || !g.y) {
+      for (int ch = c0; ch < c1; ch += kWaves) {
+        u32x4 bf[NB][4], y[RB][2] = {};
+        load_b(ch, bf);
+        if (g.y) {
+#pragma unroll
+          for (int b = 0; b < RB; ++b) load_y(ch, b, y);
+        }
+#pragma unroll
+        for (int b = 0; b < RB; ++b) {
+          if (b > 0 && 16 * b >= u.n) continue;
+          float d[2][8];
+          product(bf, b, d);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) store(ch, b, h, add(y[b][h], d[h]), false);
+        }
+      }
+    } else if (c0 < c1) {
+      // The next chunk's B is asked for before this one's products, its y of a row block as soon as this
+      // chunk's is used.
+      auto walk = [&](int lo, int hi, auto all) {
+        if (lo >= hi) return;
+        u32x4 bf[NB][4], y[RB][2];
+        load_b(lo, bf);
+#pragma unroll
+        for (int b = 0; b < RB; ++b) load_y(lo, b, y);
+#pragma unroll 1
+        for (int ch = lo; ch < hi; ch += kWaves) {
+          const int next = ch + kWaves < hi ? ch + kWaves : ch;
+          // (row * pitch anew for every chunk: 64-bit addresses would take 32 registers)
+#pragma unroll
+          for (int b = 0; b < RB; ++b) asm volatile("" : "+v"(row[b][0]), "+v"(row[b][1]));
+          u32x4 nf[NB][4];
+          if constexpr (NB <= 2) load_b(next, nf);
+#pragma unroll
+          for (int b = 0; b < RB; ++b) {
+            float d[2][8];
+            product(bf, b, d);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) store(ch, b, h, add(y[b][h], d[h]), decltype(all)::value);
+            load_y(next, b, y);
+          }
+          if constexpr (NB <= 2) {
+#pragma unroll
+            for (int m = 0; m < NB; ++m)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) bf[m][j] = nf[m][j];
+          } else {
+            load_b(next, bf);
+          }
+        }
+      };
+      if (u.n == 16 * RB && 64 * (int64_t)c1 <= g.N)
+        walk(c0, c1, std::true_type{});
+      else
+        walk(c0, c1, std::false_type{});
     }
+  };
+  if constexpr (RB == 1) {
+    const int unit = blockIdx.x / groups, g0 = blockIdx.x % groups;
+    const Unit<RB> u(g, unit, pick, false);
+    if (u.n > 0 && (u.id >= 0 || g.out != g.y)) run(u, g0, g0 + 1);
+    return;
+  }
+  if (g.units) units = __builtin_amdgcn_readfirstlane(*g.n_units);
+  // neighbouring ranges on one XCD, whose L2 then holds their adapters
+  const int W = gridDim.x, xcd = blockIdx.x % 8, w = xcd * (W / 8) + min(xcd, W % 8) + blockIdx.x / 8;
+  const int64_t items = (int64_t)units * groups;
+  int64_t item = items * w / W;
+  const int64_t end = items * (w + 1) / W;
+  while (item < end) {
+    const int unit = __builtin_amdgcn_readfirstlane((int)(item / groups));
+    const int g0 = __builtin_amdgcn_readfirstlane((int)(item - (int64_t)unit * groups));
+    const int g1 = __builtin_amdgcn_readfirstlane((int)min((int64_t)groups, g0 + end - item));
+    item += g1 - g0;
+    const Unit<RB> u(g, unit, pick, false);
+    if (u.n > 0 && (u.id >= 0 || g.out != g.y)) run(u, g0, g1);
+    __syncthreads();
   }
 }
 
-template <int T, int RB, int NCB>
-hipError_t request_one(const RequestArgs& g, hipStream_t s) {
+template <int T, int RB, int NCB, int NB, bool PACK>
+hipError_t request_one(const RequestArgs& g, int cus, hipStream_t s) {
   const int64_t units = request_units(g.M, g.L, g.r);
   hipLaunchKernelGGL((request_down_kernel<T, RB, NCB>), dim3((unsigned)(units * g.splits)), dim3(kThreads), 0, s, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  // chunks of 64 columns per wavefront: one while that gives at most about 16 wavefronts per CU
-  const int64_t chunks = (g.N + 63) / 64;
-  const int64_t per = std::max<int64_t>(1, std::min<int64_t>(8, units * chunks / 4096));
-  const int64_t groups = (chunks + kWaves * per - 1) / (kWaves * per);
-  hipLaunchKernelGGL((request_up_kernel<T, RB, NCB>), dim3((unsigned)(units * groups)), dim3(kThreads), 0, s, g, (int)per);
+  const int64_t items = units * ((g.N + 64 * kWaves - 1) / (64 * kWaves));
+  const int64_t grid = RB == 1 ? items : std::min<int64_t>(items, 2 * (int64_t)cus);
+  hipLaunchKernelGGL((request_up_kernel<T, RB, NB, PACK>), dim3((unsigned)grid), dim3(kThreads), 0, s, g, (int)units);
   return hipGetLastError();
 }
 
@@ -459,15 +578,16 @@ int64_t request_units(int64_t M, int32_t L, int32_t r) {
 }
 
 // Ranges that the first product's contraction is cut into, by the sizes alone (the sums, so the
-// results, do not depend on the device): about two workgroups per CU, each of at least two steps
-// per wavefront.
+// results, do not depend on the device): about two workgroups per CU, each of at least eight steps
+// per wavefront, for the second product reads every range's sums again (96 rows, 4096 x 4096,
+// rank 16: 16, 8, 4 ranges 4.5 + 8.6, 4.9 + 6.8, 5.1 + 5.6 us).
 int request_splits(int64_t M, int64_t K, int32_t r) {
   const int rows = 16 * request_rows(M, r);
   const int64_t blocks = (M + rows - 1) / rows, steps = (K + 31) / 32;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(blocks, 1), steps / (2 * kWaves), 16}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(blocks, 1), steps / (8 * kWaves), 16}));
 }
 
-hipError_t launch_request_lora(const RequestArgs& g, int dtype, hipStream_t s) {
+hipError_t launch_request_lora(const RequestArgs& g, int dtype, int cus, hipStream_t s) {
   const int rb = request_rows(g.M, g.r), ncb = (g.r + 15) / 16;
   if (g.units) {
     const size_t bytes = ((size_t)g.L + 1) * 4;
@@ -481,9 +601,9 @@ hipError_t launch_request_lora(const RequestArgs& g, int dtype, hipStream_t s) {
     if (e != hipSuccess) return e;
   }
   auto run = [&](auto t, auto n) {
-    constexpr int T = decltype(t)::value, NCB = decltype(n)::value;
-    if (rb == 1) return request_one<T, 1, NCB>(g, s);
-    return request_one<T, NCB <= 4 ? 4 : 2, NCB>(g, s);
+    constexpr int T = decltype(t)::value, NCB = decltype(n)::value, NB = NCB <= 2 ? 1 : NCB / 2;
+    if (rb == 1) return request_one<T, 1, NCB, NB, NCB == 1>(g, cus, s);
+    return request_one<T, NCB <= 4 ? 4 : 2, NCB, NB, NCB == 1>(g, cus, s);
   };
   auto by_rank = [&](auto t) {
     if (ncb == 1) return run(t, std::integral_constant<int, 1>{});
