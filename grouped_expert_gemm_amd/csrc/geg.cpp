@@ -1213,7 +1213,7 @@ static geg_status dense_common(int dir, const void* p, const char* pname, const 
   geg::DenseArgs g{reinterpret_cast<const uint16_t*>(p), reinterpret_cast<const uint16_t*>(q), sizes, out, M, N, K, E,
                    zero_rest != 0, reinterpret_cast<uint32_t*>(ws)};
   const int cus = cu_count();
-  const bool narrow = dir == geg::kDenseFwd && (force == 4 || (force == 0 && M <= geg::kDenseNarrowAvg * (int64_t)E));
+  const bool narrow = dir == geg::kDenseFwd && (force == 4 || (force == 0 && geg::dense_narrow(M, N, E)));
   hipError_t e = record_event(opts, narrow ? 2 : 0, stream);
   if (e == hipSuccess)
     e = narrow ? geg::launch_dense_narrow(dtype, g, cus, stream)

@@ -163,9 +163,13 @@ struct DenseArgs {
   int32_t zero_rest;      // rows past the experts' are set to 0 (else left as they are)
   uint32_t* err;
 };
-// Rows per expert on average up to which the forward streams its weights once per 16 or 32
-// rows instead of running tiles.
-constexpr int64_t kDenseNarrowAvg = 32;
+// Whether the forward streams its weights once per 16 rows instead of running tiles: with few rows
+// per expert, or few tiles to fill the card with. Measured (us, E x N x K, rows per expert, all
+// equal; narrow, tiles): 64 x 2048 x 2048: 1 103, 124; 4 106, 124; 8 114, 124; 16 136, 125, where
+// the sizes differ by the square of a uniform draw 4 90, 107; 8 112, 105; 128 x 1536 x 2048: 1 155, 143;
+// 4 160, 145; 8 172, 146; with 128 tiles, 32 x 1024 x 2048: 4 25, 33; 8 27, 34; 16 32, 34 (drawn 50, 31);
+// with 32, 8 x 1024 x 4096: 16 31, 54; 32 32, 55; 40 59, 55; with 16, 1 x 4096 x 4096: 64 31, 56.
+inline bool dense_narrow(int64_t M, int64_t N, int64_t E) { return M <= 4 * E || M * ((N + 255) / 256) <= 1024; }
 hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, const DenseArgs& g, int cus, hipStream_t s);
 hipError_t launch_dense_narrow(int dtype, const DenseArgs& g, int cus, hipStream_t s);
 // Low-rank adapters of many requests beside a shared projection (see request.hip).

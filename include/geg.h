@@ -510,7 +510,7 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
  *   zero_rest  0: rows past sum(sizes) of out / dx are left untouched; else they are set to 0
  *   workspace  256 bytes (the error word)
  *   opts     force_path 0 by size, 2 tiles, 4 (forward) the narrow kernel, which runs with at
- *            most 32 rows per expert on average; kernel_events as usual
+ *            most 4 rows per expert on average or M * ceil(N / 256) <= 1024; kernel_events as usual
  * Every tensor 16-byte aligned; K % 8 == 0, for the gradients N % 8 == 0, and 256 rows of N or
  * K values within 0x7FFFFFF0 bytes (an expert's weights may be larger). Products are exact and
  * summed in fp32, rounded once to nearest even. dW of an expert without rows is 0, for M == 0
