@@ -5,7 +5,7 @@
 // for the rows of each expert e, grouped by `sizes`; products of 16-bit values are exact in
 // fp32, sums run in fp32 and are rounded once.
 //
-// Each is a product D[r, c] = sum_k P[r, k] Q[c, k] of 256 x 256 tiles, and differs in how
+// Each is a product D[r, c] = sum_k P[r, k] Q[c, k] in tiles of 256 x 256 or 128 x 128, and differs in how
 // memory holds the operands: with the contraction along a row (a, dy of the dgrad, W of the
 // forward: "along") or with a row per contraction index (W of the dgrad, both of the wgrad:
 // "across").
@@ -71,8 +71,8 @@ __device__ __forceinline__ void zero_rows(uint16_t* out, int64_t row0, int64_t M
 }
 
 // ------------------------------------------------------------------ tiles
-constexpr int TM = 256, TN = 256, TK = 64;
-constexpr int TThreads = 512;            // 8 wavefronts: per quadrant 4 (rows of 32) x 2 (columns of 64)
+constexpr int TK = 64;
+constexpr int TThreads = 512;            // 8 wavefronts: per 128 x 128 results 4 (rows of 32) x 2 (columns of 64)
 constexpr int kHalf = 128 * TK * 2;      // bytes of half an operand per stage
 
 // Half an operand's stage, 128 rows (columns) of the tile by 64 of the contraction. Held along
@@ -80,8 +80,10 @@ constexpr int kHalf = 128 * TK * 2;      // bytes of half an operand per stage
 // contraction rows of 256 bytes, 32-byte unit u of row r at u ^ h(r), h(r) = r % 4 + 4 (r / 8 %
 // 2): the eight rows that 32 lanes of a transposing read touch at once (4 of lane group g, 4 of
 // g + 1) then lie in different banks. Neither meets a bank conflict.
-template <int D>
+template <int D, int S>
 struct Tiles {
+  static constexpr int TM = S, TN = S;
+  static constexpr int kRing = S == 256 ? 2 : 4;   // sets of buffers
   static constexpr bool kPAlong = D != kDenseWgrad, kQAlong = D == kDenseFwd;
 
   const DenseArgs& g;
@@ -98,7 +100,7 @@ struct Tiles {
     int64_t n0;          // wgrad: first column of dy
     int rows, cols;      // valid
     int n;               // contraction length
-    int stages;          // an even number: both sets of buffers
+    int stages;          // a multiple of the sets of buffers
   };
 
   __device__ __forceinline__ Tile tile_of(int32_t u) const {
@@ -132,7 +134,7 @@ struct Tiles {
       x.n0 = 0;
       x.n = (int)C;
     }
-    x.stages = max(2, 2 * ((x.n + 2 * TK - 1) / (2 * TK)));
+    x.stages = max(kRing, kRing * ((x.n + kRing * TK - 1) / (kRing * TK)));
     return x;
   }
 
@@ -213,12 +215,6 @@ struct Frag {
   }
 };
 
-// One workgroup per CU, persistent over tiles. A stage is four quadrants of 128 x 128 results,
-// P half h by Q half v, in the order (0, 0), (1, 0), (0, 1), (1, 1), of 16 instructions per
-// wavefront each (32 x 64 results). Fragments are read a little ahead of their products, so a
-// half of an operand is needed in LDS for half a stage only; its buffer then takes the stage
-// after the next, and the loads have one and a half stages to land. Reads and loads stand between
-// the products, four at a time. The loads run on across tiles, at their own place in the list.
 // Cache policy of the tiles' stores: streamed past the XCD's L2, where they would displace the
 // operands that its tiles share (non-temporal, system scope). Backward of 16384 rows over 64
 // experts of 2048 x 2048, weights' gradient: 277 us without, 216 with.
@@ -227,6 +223,81 @@ constexpr int kStream = 18;
 // How results are stored: 16 bits in rows of whole 16-byte pieces, fp32, or 16 bits in rows of any
 // width, value by value (forward).
 enum Out : int { kWide = 0, kF32Out = 1, kAnyWidth = 2 };
+// Stores per wavefront of 128 x 128 results (what lies past the rows and columns is dropped by the
+// window); value by value, none is left in flight.
+template <int OUT>
+constexpr int kQuadrantStores = OUT == kAnyWidth ? 0 : OUT == kF32Out ? 8 : 4;
+
+// A wavefront's 32 x 64 of 128 x 128 results: output rows from row0 (rows of them valid), columns
+// from c0 + cv, of cols from c0.
+template <int T, int OUT>
+__device__ __forceinline__ void store_quadrant(void* out, int64_t O, int64_t row0, int64_t c0, int rows, int cv, int cols, int wm,
+                                               int wn, const f32x4 (&acc)[2][4]) {
+  constexpr bool F32 = OUT == kF32Out;
+  const int l = fresh_lane();
+  const int r16 = l & 15, grp = l >> 4;
+  if constexpr (OUT == kAnyWidth) {
+    const int left = rows - 32 * wm - r16, c = cv + 64 * wn + 4 * grp;
+    uint16_t* dst = reinterpret_cast<uint16_t*>(out) + (row0 + 32 * wm + r16) * O + c0 + c;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (16 * i < left && 16 * j + b < cols - c)
+            dst[(int64_t)(16 * i) * O + 16 * j + b] = (uint16_t)pack2<T>(acc[i][j][b], 0.f);
+    return;
+  }
+  // Whole 128-byte lines: a lane has 16 bytes of its row in each of two 64-byte halves (16
+  // bits: of two pairs of column blocks, whose rows of 16 lanes have traded places); the lanes of
+  // rows 8-15 and 0-7 of the block trade a half, and a store then writes 8 rows of 128 bytes.
+  constexpr int size = F32 ? 4 : 2;
+  const bool low = r16 < 8;
+  const int col = (F32 ? 4 * grp : 16 * (grp & 1) + 8 * (grp >> 1)) + (low ? 0 : F32 ? 16 : 32);
+  const __amdgpu_buffer_rsrc_t R =
+      window(reinterpret_cast<uint8_t*>(out) + (row0 * O + c0) * size, rows > 0 ? (rows * O - c0) * size : 0);
+  const uint32_t row = (uint32_t)(32 * wm + (r16 & 7)) * (uint32_t)O * size;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; j += F32 ? 2 : 4) {
+      u32x4 a, b;
+      if constexpr (F32) {
+        a = __builtin_bit_cast(u32x4, acc[i][j]);
+        b = __builtin_bit_cast(u32x4, acc[i][j + 1]);
+      } else {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          auto two = [&](int jj) { return pack2<T>(acc[i][jj][2 * x], acc[i][jj][2 * x + 1]); };
+          const auto r = __builtin_amdgcn_permlane16_swap(two(0), two(1), false, false);
+          const auto s = __builtin_amdgcn_permlane16_swap(two(2), two(3), false, false);
+          a[x] = r[0];
+          a[2 + x] = r[1];
+          b[x] = s[0];
+          b[2 + x] = s[1];
+        }
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const uint32_t give = low ? b[x] : a[x];
+        const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, true);   // row_ror:8
+        a[x] = low ? a[x] : got;
+        b[x] = low ? got : b[x];
+      }
+      const int c = cv + 64 * wn + 16 * j + col;
+      const uint32_t at = row + (uint32_t)(16 * i) * (uint32_t)O * size + c * size;
+      __builtin_amdgcn_raw_buffer_store_b128(a, R, oob_unless(c < cols, at), 0, kStream);
+      __builtin_amdgcn_raw_buffer_store_b128(b, R, oob_unless(c < cols, at + 8 * (uint32_t)O * size), 0, kStream);
+    }
+}
+
+// One workgroup per CU, persistent over tiles. A stage is four quadrants of 128 x 128 results,
+// P half h by Q half v, in the order (0, 0), (1, 0), (0, 1), (1, 1), of 16 instructions per
+// wavefront each (32 x 64 results). Fragments are read a little ahead of their products, so a
+// half of an operand is needed in LDS for half a stage only; its buffer then takes the stage
+// after the next, and the loads have one and a half stages to land. Reads and loads stand between
+// the products, four at a time. The loads run on across tiles, at their own place in the list.
 template <int D, int T, int OUT>
 __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
@@ -240,7 +311,8 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave >> 1, wn = wave & 1;
   const int r16 = lane & 15, grp = lane >> 4;
-  using W = Tiles<D>;
+  using W = Tiles<D, 256>;
+  constexpr int TM = W::TM, TN = W::TN;
   const int64_t O = D == kDenseFwd ? g.N : g.K;
   const int blocks_n = (int)((g.N + TM - 1) / TM), blocks_k = (int)((g.K + TN - 1) / TN);
   const int c_tiles = (int)((O + TN - 1) / TN);
@@ -335,79 +407,15 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
       }
     }
   };
-  // A tile's stores: always kStores of them, so that the waits behind them can count (what lies
-  // past the rows and columns is dropped by the window); value by value, none is left in flight.
-  constexpr bool F32 = OUT == kF32Out;
-  constexpr int kStores = OUT == kAnyWidth ? 0 : F32 ? 32 : 16;
+  // A tile's stores: always kStores of them, so that the waits behind them can count.
+  constexpr int kStores = 4 * kQuadrantStores<OUT>;
   auto store = [&]() {
-    if constexpr (OUT == kAnyWidth) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-          const int rows = cur.rows - 128 * h - 32 * wm - r16, c0 = 128 * v + 64 * wn + 4 * grp;
-          uint16_t* dst = reinterpret_cast<uint16_t*>(g.out) + (cur.row0 + 128 * h + 32 * wm + r16) * O + cur.c0 + c0;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int b = 0; b < 4; ++b)
-                if (16 * i < rows && 16 * j + b < cur.cols - c0)
-                  dst[(int64_t)(16 * i) * O + 16 * j + b] = (uint16_t)pack2<T>(acc[h][v][i][j][b], 0.f);
-        }
-      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
-      return;
-    }
-    // Whole 128-byte lines: a lane has 16 bytes of its row in each of two 64-byte halves (16
-    // bits: of two pairs of column blocks, whose rows of 16 lanes have traded places); the lanes of
-    // rows 8-15 and 0-7 of the block trade a half, and a store then writes 8 rows of 128 bytes.
-    constexpr int size = F32 ? 4 : 2;
-    const int l = fresh_lane();
-    const int r16 = l & 15, grp = l >> 4;
-    const bool low = r16 < 8;
-    const int col = (F32 ? 4 * grp : 16 * (grp & 1) + 8 * (grp >> 1)) + (low ? 0 : F32 ? 16 : 32);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int rows = cur.rows - 128 * h;
-      const __amdgpu_buffer_rsrc_t R = window(reinterpret_cast<uint8_t*>(g.out) + ((cur.row0 + 128 * h) * O + cur.c0) * size,
-                                              rows > 0 ? (rows * O - cur.c0) * size : 0);
-      const uint32_t row = (uint32_t)(32 * wm + (r16 & 7)) * (uint32_t)O * size;
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int v = 0; v < 2; ++v)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; j += F32 ? 2 : 4) {
-            u32x4 a, b;
-            if constexpr (F32) {
-              a = __builtin_bit_cast(u32x4, acc[h][v][i][j]);
-              b = __builtin_bit_cast(u32x4, acc[h][v][i][j + 1]);
-            } else {
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                auto two = [&](int jj) { return pack2<T>(acc[h][v][i][jj][2 * x], acc[h][v][i][jj][2 * x + 1]); };
-                const auto r = __builtin_amdgcn_permlane16_swap(two(0), two(1), false, false);
-                const auto s = __builtin_amdgcn_permlane16_swap(two(2), two(3), false, false);
-                a[x] = r[0];
-                a[2 + x] = r[1];
-                b[x] = s[0];
-                b[2 + x] = s[1];
-              }
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t give = low ? b[x] : a[x];
-              const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, true);   // row_ror:8
-              a[x] = low ? a[x] : got;
-              b[x] = low ? got : b[x];
-            }
-            const int c = 128 * v + 64 * wn + 16 * j + col;
-            const uint32_t at = row + (uint32_t)(16 * i) * (uint32_t)O * size + c * size;
-            __builtin_amdgcn_raw_buffer_store_b128(a, R, oob_unless(c < cur.cols, at), 0, kStream);
-            __builtin_amdgcn_raw_buffer_store_b128(b, R, oob_unless(c < cur.cols, at + 8 * (uint32_t)O * size), 0, kStream);
-          }
-    }
+        store_quadrant<T, OUT>(g.out, O, cur.row0 + 128 * h, cur.c0, cur.rows - 128 * h, 128 * v, cur.cols, wm, wn, acc[h][v]);
+    if constexpr (OUT == kAnyWidth) __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
   };
   auto read_q = [&](const uint8_t* L, int s, int k) {   // two blocks
 #pragma unroll
@@ -477,6 +485,134 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
       stage(none, pb0, pb1, qb0, qb1, pa0, qa0);
     }
     store();
+    u += step;
+    if (u >= end) break;
+    cur = w.tile_of(u);
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no load into LDS outlives the workgroup
+}
+
+// ------------------------------------------------------------------ tiles of 128 x 128
+// For few tiles, and few rows per expert (the rule and both sides' times: dense_small()). A stage is
+// one quadrant of the above, in a ring of four sets of buffers, three under way while one is used;
+// one barrier per stage. Alone on its CU it is bound by the loads' latency, 0.4 us per stage of 64
+// (a stage of 256 x 256: 0.86, the matrix rate), with many tiles by the weights: 128 experts of
+// 1536 x 2048, one row each, 805 MB in 134 us, 6.0 TB/s.
+template <int D, int T, int OUT>
+__global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
+  __shared__ int32_t p_off[kMaxExperts + 1];
+  __shared__ int32_t p_u[kMaxExperts + 1];
+  __shared__ __attribute__((aligned(128))) uint8_t qa[kHalf], qb[kHalf], qc[kHalf], qd[kHalf];
+  __shared__ __attribute__((aligned(64))) uint8_t pa[kHalf], pb[kHalf], pc[kHalf], pd[kHalf];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  using W = Tiles<D, 128>;
+  constexpr int TM = W::TM, TN = W::TN;
+  const int64_t O = D == kDenseFwd ? g.N : g.K;
+  const int blocks_n = (int)((g.N + TM - 1) / TM), blocks_k = (int)((g.K + TN - 1) / TN);
+  const int c_tiles = (int)((O + TN - 1) / TN);
+  int32_t total = build_plan(p_off, p_u, g.sizes, g.E, g.M, g.err,
+                             [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : (s + TM - 1) / TM * c_tiles; });
+  total = D == kDenseWgrad ? g.E * blocks_n * blocks_k : __builtin_amdgcn_readfirstlane(total);
+  if constexpr (D != kDenseWgrad) {
+    if (g.zero_rest) zero_rows((uint16_t*)g.out, p_off[g.E], g.M, O);
+  }
+  const W w{g, lane, wave, p_off, p_u, D == kDenseDgrad ? g.N : g.K, O, blocks_n, blocks_k};
+  const int G = gridDim.x;
+  const int parts = G % 8 == 0 ? 8 : 1, step = G / parts, part = blockIdx.x % parts;
+  const int32_t end = (int32_t)((int64_t)total * (part + 1) / parts);
+  int32_t u = (int32_t)((int64_t)total * part / parts) + blockIdx.x / parts;
+  if (u >= end) return;
+
+  const Frag<W::kPAlong> fp(lane, 2 * wm);
+  const Frag<W::kQAlong> fq(lane, 4 * wn);
+  f32x4 acc[2][4];
+  typename W::Tile cur = w.tile_of(u);   // of the products
+  typename W::Cursor lc;                 // of the loads
+  w.aim(lc, cur, true);
+  int32_t lu = u;
+  const int64_t pitch_p = W::kPAlong ? w.C : g.N;
+  const uint32_t at_p = W::lane_at(W::kPAlong, lane, wave, pitch_p), at_q = W::lane_at(W::kQAlong, lane, wave, g.K);
+  auto load = [&](uint8_t* P, uint8_t* Q) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      w.template load<W::kQAlong>(lc.q, lc.left_q, lc.rest, at_q, g.K, 0, i, Q);
+      w.template load<W::kPAlong>(lc.p, lc.left_p, lc.rest, at_p, pitch_p, 0, i, P);
+    }
+    w.next(lc);
+    if (lc.st == lc.stages) {
+      lu += step;
+      const bool any = lu < end;
+      w.aim(lc, any ? w.tile_of(lu) : cur, any);
+    }
+  };
+  int on;   // the wavefront has results
+  // One stage from P and Q; the one after the next two is asked for into NP and NQ, which the stage
+  // before has used. S: stores of the tile before that may be in flight.
+  auto stage = [&](auto behind, const uint8_t* P, const uint8_t* Q, uint8_t* NP, uint8_t* NQ) {
+    constexpr int S = decltype(behind)::value;
+    step_barrier<8 + S>();   // P and Q have landed; every wavefront has read the stage before
+    u32x4 p[2][2], q[2][4];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) p[s][i] = fp.read(P, i, s);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) q[s][j] = fq.read(Q, j, s);
+    }
+    load(NP, NQ);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      asm volatile("" : "+s"(on));
+      if (on) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) acc[i][j] = mfma<T>(q[s][j], p[s][i], acc[i][j]);
+      }
+    }
+  };
+  constexpr int kStores = kQuadrantStores<OUT>;
+  constexpr std::integral_constant<int, 0> none{};
+  constexpr std::integral_constant<int, kStores> some{};
+  load(pa, qa);
+  load(pb, qb);
+  load(pc, qc);
+#pragma unroll
+  for (int i = 0; i < kStores; ++i)   // (see dense_tile_kernel)
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, window(g.out, 0), 16 * i, 0, 0);
+  for (;;) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    const int want = __builtin_amdgcn_readfirstlane((int)(32 * wm < cur.rows && 64 * wn < cur.cols));
+    int real = (cur.n + TK - 1) / TK;   // stages with products
+    auto due = [&]() {
+      on = __builtin_amdgcn_readfirstlane(real > 0 ? want : 0);
+      --real;
+    };
+    due();
+    stage(some, pa, qa, pd, qd);
+    due();
+    stage(some, pb, qb, pa, qa);
+    due();
+    stage(some, pc, qc, pb, qb);
+    due();
+    stage(none, pd, qd, pc, qc);
+    for (int st = 4; st < cur.stages; st += 4) {
+      due();
+      stage(none, pa, qa, pd, qd);
+      due();
+      stage(none, pb, qb, pa, qa);
+      due();
+      stage(none, pc, qc, pb, qb);
+      due();
+      stage(none, pd, qd, pc, qc);
+    }
+    store_quadrant<T, OUT>(g.out, O, cur.row0, cur.c0, cur.rows, 0, cur.cols, wm, wn, acc);
+    if constexpr (OUT == kAnyWidth) __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
     u += step;
     if (u >= end) break;
     cur = w.tile_of(u);
@@ -575,24 +711,24 @@ hipError_t narrow_one(const DenseArgs& g, int cus, hipStream_t s) {
 }
 
 template <int D, int T, int OUT>
-hipError_t tile_one(const DenseArgs& g, int cus, hipStream_t s) {
-  const int64_t bn = (g.N + TM - 1) / TM, bk = (g.K + TN - 1) / TN;
-  const int64_t bound = D == kDenseWgrad ? g.E * bn * bk
-                                         : ((g.M + TM - 1) / TM + std::min<int64_t>(g.E, g.M)) * (D == kDenseFwd ? bn : bk);
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(bound, (int64_t)cus));
-  hipLaunchKernelGGL((dense_tile_kernel<D, T, OUT>), dim3((unsigned)grid), dim3(TThreads), 0, s, g);
+hipError_t tile_one(const DenseArgs& g, bool small, int cus, hipStream_t s) {
+  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(dense_tiles(D, g.M, g.N, g.K, g.E, small ? 128 : 256), cus));
+  if (small)
+    hipLaunchKernelGGL((dense_small_kernel<D, T, OUT>), dim3((unsigned)grid), dim3(TThreads), 0, s, g);
+  else
+    hipLaunchKernelGGL((dense_tile_kernel<D, T, OUT>), dim3((unsigned)grid), dim3(TThreads), 0, s, g);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, const DenseArgs& g, int cus, hipStream_t s) {
+hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, bool small, const DenseArgs& g, int cus, hipStream_t s) {
   auto run = [&](auto t) {
     constexpr int T = decltype(t)::value;
-    if (dir == kDenseDgrad) return tile_one<kDenseDgrad, T, kWide>(g, cus, s);
+    if (dir == kDenseDgrad) return tile_one<kDenseDgrad, T, kWide>(g, small, cus, s);
     if (dir == kDenseWgrad)
-      return f32_out ? tile_one<kDenseWgrad, T, kF32Out>(g, cus, s) : tile_one<kDenseWgrad, T, kWide>(g, cus, s);
-    return g.N % 8 ? tile_one<kDenseFwd, T, kAnyWidth>(g, cus, s) : tile_one<kDenseFwd, T, kWide>(g, cus, s);
+      return f32_out ? tile_one<kDenseWgrad, T, kF32Out>(g, small, cus, s) : tile_one<kDenseWgrad, T, kWide>(g, small, cus, s);
+    return g.N % 8 ? tile_one<kDenseFwd, T, kAnyWidth>(g, small, cus, s) : tile_one<kDenseFwd, T, kWide>(g, small, cus, s);
   };
   return dtype == kBF16 ? run(std::integral_constant<int, kBF16>{}) : run(std::integral_constant<int, kF16>{});
 }

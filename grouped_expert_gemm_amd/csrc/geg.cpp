@@ -1189,8 +1189,8 @@ static geg_status dense_common(int dir, const void* p, const char* pname, const 
   if (out_dtype != dtype && out_dtype != GEG_F32)
     return fail(GEG_ERR_BAD_OPTION, "dw_dtype must be dtype or GEG_F32");
   const int32_t force = opts ? opts->force_path : 0;
-  if (force != 0 && force != 2 && (force != 4 || dir != geg::kDenseFwd))
-    return fail(GEG_ERR_BAD_OPTION, "16-bit products run on tiles (force_path 2) or, forward, on the narrow kernel (4)");
+  if (force != 0 && force != 2 && force != 5 && (force != 4 || dir != geg::kDenseFwd))
+    return fail(GEG_ERR_BAD_OPTION, "16-bit products run on tiles (force_path 2 or 5) or, forward, on the narrow kernel (4)");
   if (opts && opts->cu_limit < 0) return fail(GEG_ERR_BAD_OPTION, "cu_limit must be >= 0");
   geg_status st;
   if ((st = check_shape(M, 1, K, E, 8)) != GEG_OK) return st;
@@ -1214,10 +1214,11 @@ static geg_status dense_common(int dir, const void* p, const char* pname, const 
                    zero_rest != 0, reinterpret_cast<uint32_t*>(ws)};
   const int cus = cu_count();
   const bool narrow = dir == geg::kDenseFwd && (force == 4 || (force == 0 && geg::dense_narrow(M, N, E)));
+  const bool small = force == 5 || (force == 0 && geg::dense_small(dir, M, N, K, E));
   hipError_t e = record_event(opts, narrow ? 2 : 0, stream);
   if (e == hipSuccess)
     e = narrow ? geg::launch_dense_narrow(dtype, g, cus, stream)
-               : geg::launch_dense_tile(dir, dtype, out_dtype == GEG_F32, g, cus, stream);
+               : geg::launch_dense_tile(dir, dtype, out_dtype == GEG_F32, small, g, cus, stream);
   if (e == hipSuccess) e = record_event(opts, narrow ? 3 : 1, stream);
   if (e != hipSuccess) return hip_fail(e, "16-bit product launch");
   ++g_launches;

@@ -163,14 +163,32 @@ struct DenseArgs {
   int32_t zero_rest;      // rows past the experts' are set to 0 (else left as they are)
   uint32_t* err;
 };
-// Whether the forward streams its weights once per 16 rows instead of running tiles: with few rows
-// per expert, or few tiles to fill the card with. Measured (us, E x N x K, rows per expert, all
-// equal; narrow, tiles): 64 x 2048 x 2048: 1 103, 124; 4 106, 124; 8 114, 124; 16 136, 125, where
-// the sizes differ by the square of a uniform draw 4 90, 107; 8 112, 105; 128 x 1536 x 2048: 1 155, 143;
-// 4 160, 145; 8 172, 146; with 128 tiles, 32 x 1024 x 2048: 4 25, 33; 8 27, 34; 16 32, 34 (drawn 50, 31);
-// with 32, 8 x 1024 x 4096: 16 31, 54; 32 32, 55; 40 59, 55; with 16, 1 x 4096 x 4096: 64 31, 56.
-inline bool dense_narrow(int64_t M, int64_t N, int64_t E) { return M <= 4 * E || M * ((N + 255) / 256) <= 1024; }
-hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, const DenseArgs& g, int cus, hipStream_t s);
+// An upper bound of a product's tiles of S x S results.
+inline int64_t dense_tiles(int dir, int64_t M, int64_t N, int64_t K, int64_t E, int S) {
+  const int64_t bn = (N + S - 1) / S, bk = (K + S - 1) / S;
+  if (dir == kDenseWgrad) return E * bn * bk;
+  return ((M + S - 1) / S + (E < M ? E : M)) * (dir == kDenseFwd ? bn : bk);
+}
+// Which kernel runs. Measured in us, sizes E x N x K, rows per expert (all equal; "drawn": by the
+// square of a uniform draw):
+// The narrow kernel streams an expert's weights once per 16 rows, at 5.2 TB/s whatever the sizes;
+// tiles of 128 need rounds to come to speed (narrow, 128): 1 x 4096 x 4096: 1 20, 26; 8 26, 26;
+// 16 31, 26; 8 x 8192 x 4096: 1 102, 107; 4 105, 108; 16 128, 108; 64 x 2048 x 2048: 1 102, 102; 4 104,
+// 104; 128 x 2048 x 2048: 1 200, 175; 128 x 1536 x 2048: 1 154, 134; 32 x 8192 x 2048: 4 202, 174.
+inline bool dense_narrow(int64_t M, int64_t N, int64_t E) {
+  return M <= 4 * E && (E < M ? E : M) * ((N + 127) / 128) <= 1024;
+}
+// Tiles of 128 x 128 are four times as many and meet few rows with less waste; tiles of 256 x 256 read
+// less per product (256, 128). Up to two rounds of 256 workgroups (tiles of 128 in parentheses): forward
+// 8 x 1024 x 4096, 256 rows in all (80): 56, 27; 8 x 2048 x 2048, 1024 (256): 37, 21; 2048 (384): 46, 38;
+// 4096 (640): 47, 54; 16 x 2048 x 2048, 2048 (512): 39, 38; gradient of 1 x 1024 x 4096's weights (256), 4096
+// rows: 83, 39; of 16 x 1024 x 1024's (1024), 8192: 24, 31. With many tiles and few rows per expert: 128 x
+// 1536 x 2048: 1 144, 134; 16 148, 143; drawn 4 126, 107; 128 157, 156; 256 205, 278; 32 x 5760 x 2880: 4
+// 184, 181; drawn 16 181, 185; 64 194, 199; 96 202, 217.
+inline bool dense_small(int dir, int64_t M, int64_t N, int64_t K, int64_t E) {
+  return dense_tiles(dir, M, N, K, E, 128) <= 512 || (dir != kDenseWgrad && M <= 16 * E);
+}
+hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, bool small, const DenseArgs& g, int cus, hipStream_t s);
 hipError_t launch_dense_narrow(int dtype, const DenseArgs& g, int cus, hipStream_t s);
 // Low-rank adapters of many requests beside a shared projection (see request.hip).
 constexpr int kRequestMaxRank = 128;

@@ -509,8 +509,8 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
  *   w        [E, N, K]; dw [E, N, K] in dw_dtype: dtype, or GEG_F32
  *   zero_rest  0: rows past sum(sizes) of out / dx are left untouched; else they are set to 0
  *   workspace  256 bytes (the error word)
- *   opts     force_path 0 by size, 2 tiles, 4 (forward) the narrow kernel, which runs with at
- *            most 4 rows per expert on average or M * ceil(N / 256) <= 1024; kernel_events as usual
+ *   opts     force_path 0 by size, 2 tiles of 256 x 256 results, 5 tiles of 128 x 128, 4 (forward)
+ *            the narrow kernel; kernel_events as usual
  * Every tensor 16-byte aligned; K % 8 == 0, for the gradients N % 8 == 0, and 256 rows of N or
  * K values within 0x7FFFFFF0 bytes (an expert's weights may be larger). Products are exact and
  * summed in fp32, rounded once to nearest even. dW of an expert without rows is 0, for M == 0

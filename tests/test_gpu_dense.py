@@ -91,15 +91,18 @@ def test_each_direction(geg, dtype, sizes, N, K):
     log(f"case: 16-bit products {dtype} sizes={sizes} N={N} K={K}")
     a, dy, w, sz = _case(dtype, sizes, N, K, seed=N + K)
     ref, mag = _ref(a, w, sizes, "forward")
-    for path in (0, 2, 4):
+    for path in (0, 2, 4, 5):
         _check(geg.grouped_gemm(a, sz, w, opts=geg.Opts(path, 0), check_errors=True), ref, mag, K, f"forward path {path}")
-    _check(geg.grouped_dgrad(dy, sz, w, check_errors=True), *_ref(dy, w, sizes, "dgrad"), N, "dgrad")
+    ref, mag = _ref(dy, w, sizes, "dgrad")
+    for path in (0, 2, 5):
+        _check(geg.grouped_dgrad(dy, sz, w, opts=geg.Opts(path, 0), check_errors=True), ref, mag, N, f"dgrad path {path}")
     ref, mag = _ref(dy, a, sizes, "wgrad")
-    for out in (None, torch.float32):
-        dw = geg.grouped_wgrad(dy, a, sz, dtype=out, check_errors=True)
-        assert dw.dtype == (out or a.dtype)
-        _check(dw, ref, mag, max(sizes), f"wgrad {dw.dtype}")
-    assert (dw[sz == 0] == 0).all()
+    for path in (0, 2, 5):
+        for out in (None, torch.float32):
+            dw = geg.grouped_wgrad(dy, a, sz, dtype=out, opts=geg.Opts(path, 0), check_errors=True)
+            assert dw.dtype == (out or a.dtype)
+            _check(dw, ref, mag, max(sizes), f"wgrad {dw.dtype} path {path}")
+        assert (dw[sz == 0] == 0).all()
 
 
 @pytest.mark.parametrize("N", [1, 7, 257, 1023])
@@ -108,7 +111,7 @@ def test_forward_odd_widths(geg, N):
     sizes = [3, 0, 290]
     a, _, w, sz = _case("bf16", sizes, N, 136, seed=N)
     ref, mag = _ref(a, w, sizes, "forward")
-    for path in (2, 4):
+    for path in (2, 4, 5):
         _check(geg.grouped_gemm(a, sz, w, opts=geg.Opts(path, 0)), ref, mag, 136, f"path {path}")
 
 
@@ -118,12 +121,13 @@ def test_many_rounds_per_workgroup(geg):
     sizes, N, K = [300, 0, 77, 513, 1, 256, 90], 776, 584
     a, dy, w, sz = _case("bf16", sizes, N, K, seed=3)
     for limit in (1, 3, 8):
-        for path in (2, 4):
+        for path in (2, 4, 5):
             o = geg.Opts(path, 0, None, limit)
             assert torch.equal(geg.grouped_gemm(a, sz, w, opts=o), geg.grouped_gemm(a, sz, w, opts=geg.Opts(path, 0)))
-        o = geg.Opts(0, 0, None, limit)
-        assert torch.equal(geg.grouped_dgrad(dy, sz, w, opts=o), geg.grouped_dgrad(dy, sz, w))
-        assert torch.equal(geg.grouped_wgrad(dy, a, sz, opts=o), geg.grouped_wgrad(dy, a, sz))
+        for path in (2, 5):
+            o, free = geg.Opts(path, 0, None, limit), geg.Opts(path, 0)
+            assert torch.equal(geg.grouped_dgrad(dy, sz, w, opts=o), geg.grouped_dgrad(dy, sz, w, opts=free))
+            assert torch.equal(geg.grouped_wgrad(dy, a, sz, opts=o), geg.grouped_wgrad(dy, a, sz, opts=free))
 
 
 def test_1024_experts(geg):
@@ -131,13 +135,15 @@ def test_1024_experts(geg):
     sizes = [(7 * e) % 5 if e % 3 else 0 for e in range(1024)]
     a, dy, w, sz = _case("fp16", sizes, 48, 40, seed=4)
     ref, mag = _ref(a, w, sizes, "forward")
-    for path in (2, 4):
+    for path in (2, 4, 5):
         _check(geg.grouped_gemm(a, sz, w, opts=geg.Opts(path, 0)), ref, mag, 40, f"path {path}")
-    _check(geg.grouped_dgrad(dy, sz, w), *_ref(dy, w, sizes, "dgrad"), 48, "dgrad")
-    _check(geg.grouped_wgrad(dy, a, sz), *_ref(dy, a, sizes, "wgrad"), max(sizes), "wgrad")
+    for path in (2, 5):
+        o = geg.Opts(path, 0)
+        _check(geg.grouped_dgrad(dy, sz, w, opts=o), *_ref(dy, w, sizes, "dgrad"), 48, f"dgrad path {path}")
+        _check(geg.grouped_wgrad(dy, a, sz, opts=o), *_ref(dy, a, sizes, "wgrad"), max(sizes), f"wgrad path {path}")
 
 
-@pytest.mark.parametrize("path", [2, 4])
+@pytest.mark.parametrize("path", [2, 4, 5])
 def test_rows_past_the_experts(geg, path):
     import torch
     log(f"case: 16-bit products, rows past the experts, path {path}")
@@ -150,14 +156,14 @@ def test_rows_past_the_experts(geg, path):
     assert (out[29:] == 7).all() and out[:29].isfinite().all()
     out = geg.grouped_gemm(a, sz, w, out=out, opts=o, zero_rest=True)
     assert (out[29:] == 0).all()
-    if path == 2:
+    if path != 4:
         dy, w = dy[:, :40].contiguous(), w[:, :40].contiguous()
         dy[29:] = float("nan")
         dx = torch.full((329, K), 7.0, dtype=a.dtype, device="cuda")
-        geg.grouped_dgrad(dy, sz, w, dx=dx)
+        geg.grouped_dgrad(dy, sz, w, dx=dx, opts=o)
         assert (dx[29:] == 7).all() and dx[:29].isfinite().all()
-        assert (geg.grouped_dgrad(dy, sz, w, dx=dx, zero_rest=True)[29:] == 0).all()
-        dw = geg.grouped_wgrad(dy, a, sz)
+        assert (geg.grouped_dgrad(dy, sz, w, dx=dx, zero_rest=True, opts=o)[29:] == 0).all()
+        dw = geg.grouped_wgrad(dy, a, sz, opts=o)
         assert dw.isfinite().all() and (dw[1] == 0).all()
 
 
@@ -182,29 +188,31 @@ def test_a_value_stays_in_its_row(geg, bad):
     log(f"case: 16-bit products with {bad}")
     sizes, N, K = [30, 5, 40], 72, 72   # contraction tails of 8 past a whole stage
     a, dy, w, sz = _case("bf16", sizes, N, K, seed=7)
-    plain = [geg.grouped_gemm(a, sz, w, opts=geg.Opts(p, 0)) for p in (2, 4)] + [geg.grouped_dgrad(dy, sz, w)]
-    dw = geg.grouped_wgrad(dy, a, sz)
+    plain = [geg.grouped_gemm(a, sz, w, opts=geg.Opts(p, 0)) for p in (2, 4, 5)] + [geg.grouped_dgrad(dy, sz, w, opts=geg.Opts(p, 0)) for p in (2, 5)]
     row = 31
     a2, dy2 = a.clone(), dy.clone()
     a2[row], dy2[row] = bad, bad
-    got = [geg.grouped_gemm(a2, sz, w, opts=geg.Opts(p, 0)) for p in (2, 4)] + [geg.grouped_dgrad(dy2, sz, w)]
+    got = [geg.grouped_gemm(a2, sz, w, opts=geg.Opts(p, 0)) for p in (2, 4, 5)] + [geg.grouped_dgrad(dy2, sz, w, opts=geg.Opts(p, 0)) for p in (2, 5)]
     for p, q in zip(plain, got):
         assert not q[row].isfinite().any()
         q[row] = p[row]
         assert torch.equal(p, q)
     # a column of dy reaches its row of dW alone, a column of a its column, in their expert
-    dy2 = dy.clone()
-    dy2[row, 70] = bad
-    got = geg.grouped_wgrad(dy2, a, sz)
-    assert not got[1, 70].isfinite().any()
-    got[1, 70] = dw[1, 70]
-    assert torch.equal(got, dw)
-    a2 = a.clone()
-    a2[row, 3] = bad
-    got = geg.grouped_wgrad(dy, a2, sz)
-    assert not got[1, :, 3].isfinite().any()
-    got[1, :, 3] = dw[1, :, 3]
-    assert torch.equal(got, dw)
+    for path in (2, 5):
+        o = geg.Opts(path, 0)
+        dw = geg.grouped_wgrad(dy, a, sz, opts=o)
+        dy2 = dy.clone()
+        dy2[row, 70] = bad
+        got = geg.grouped_wgrad(dy2, a, sz, opts=o)
+        assert not got[1, 70].isfinite().any()
+        got[1, 70] = dw[1, 70]
+        assert torch.equal(got, dw)
+        a2 = a.clone()
+        a2[row, 3] = bad
+        got = geg.grouped_wgrad(dy, a2, sz, opts=o)
+        assert not got[1, :, 3].isfinite().any()
+        got[1, :, 3] = dw[1, :, 3]
+        assert torch.equal(got, dw)
 
 
 def test_overflow_to_inf_in_fp16(geg):
@@ -212,7 +220,7 @@ def test_overflow_to_inf_in_fp16(geg):
     log("case: fp16 results past 65504")
     sz = torch.tensor([4], dtype=torch.int32, device="cuda")
     a, w = torch.full((4, 64), 200.0, dtype=torch.float16, device="cuda"), torch.full((1, 8, 64), 100.0, dtype=torch.float16, device="cuda")
-    for p in (2, 4):
+    for p in (2, 4, 5):
         assert (geg.grouped_gemm(a, sz, w, opts=geg.Opts(p, 0)) == float("inf")).all()
     assert (geg.grouped_wgrad(a, a, sz) == float("inf")).all()
     assert (geg.grouped_wgrad(a, a, sz, dtype=torch.float32) == 160000.0).all()
@@ -255,9 +263,10 @@ def test_offsets_past_2_31(geg):
     w[E - 1].fill_diagonal_(2.0)
     sz = torch.tensor([0] * (E - 1) + [40], dtype=torch.int32, device="cuda")
     a = torch.randn(40, K, device="cuda").to(t)
-    for p in (2, 4):
+    for p in (2, 4, 5):
         assert torch.equal(geg.grouped_gemm(a, sz, w, opts=geg.Opts(p, 0)), 2 * a)
-    assert torch.equal(geg.grouped_dgrad(a, sz, w), 2 * a)
+    for p in (2, 5):
+        assert torch.equal(geg.grouped_dgrad(a, sz, w, opts=geg.Opts(p, 0)), 2 * a)
 
 
 def test_autograd_op_and_differences(geg):
