@@ -228,11 +228,11 @@ enum Out : int { kWide = 0, kF32Out = 1, kAnyWidth = 2 };
 template <int OUT>
 constexpr int kQuadrantStores = OUT == kAnyWidth ? 0 : OUT == kF32Out ? 8 : 4;
 
-// A wavefront's 32 x 64 of 128 x 128 results: output rows from row0 (rows of them valid), columns
-// from c0 + cv, of cols from c0.
+// 16 of a wavefront's 32 x 64 of 128 x 128 results, row block i: output rows from row0 (rows of them
+// valid), columns from c0 + cv, of cols from c0.
 template <int T, int OUT>
-__device__ __forceinline__ void store_quadrant(void* out, int64_t O, int64_t row0, int64_t c0, int rows, int cv, int cols, int wm,
-                                               int wn, const f32x4 (&acc)[2][4]) {
+__device__ __forceinline__ void store_block(void* out, int64_t O, int64_t row0, int64_t c0, int rows, int cv, int cols, int wm,
+                                            int wn, int i, const f32x4 (&acc)[4]) {
   constexpr bool F32 = OUT == kF32Out;
   const int l = fresh_lane();
   const int r16 = l & 15, grp = l >> 4;
@@ -240,13 +240,11 @@ __device__ __forceinline__ void store_quadrant(void* out, int64_t O, int64_t row
     const int left = rows - 32 * wm - r16, c = cv + 64 * wn + 4 * grp;
     uint16_t* dst = reinterpret_cast<uint16_t*>(out) + (row0 + 32 * wm + r16) * O + c0 + c;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-          if (16 * i < left && 16 * j + b < cols - c)
-            dst[(int64_t)(16 * i) * O + 16 * j + b] = (uint16_t)pack2<T>(acc[i][j][b], 0.f);
+      for (int b = 0; b < 4; ++b)
+        if (16 * i < left && 16 * j + b < cols - c)
+          dst[(int64_t)(16 * i) * O + 16 * j + b] = (uint16_t)pack2<T>(acc[j][b], 0.f);
     return;
   }
   // Whole 128-byte lines: a lane has 16 bytes of its row in each of two 64-byte halves (16
@@ -259,37 +257,42 @@ __device__ __forceinline__ void store_quadrant(void* out, int64_t O, int64_t row
       window(reinterpret_cast<uint8_t*>(out) + (row0 * O + c0) * size, rows > 0 ? (rows * O - c0) * size : 0);
   const uint32_t row = (uint32_t)(32 * wm + (r16 & 7)) * (uint32_t)O * size;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int j = 0; j < 4; j += F32 ? 2 : 4) {
+    u32x4 a, b;
+    if constexpr (F32) {
+      a = __builtin_bit_cast(u32x4, acc[j]);
+      b = __builtin_bit_cast(u32x4, acc[j + 1]);
+    } else {
 #pragma unroll
-    for (int j = 0; j < 4; j += F32 ? 2 : 4) {
-      u32x4 a, b;
-      if constexpr (F32) {
-        a = __builtin_bit_cast(u32x4, acc[i][j]);
-        b = __builtin_bit_cast(u32x4, acc[i][j + 1]);
-      } else {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          auto two = [&](int jj) { return pack2<T>(acc[i][jj][2 * x], acc[i][jj][2 * x + 1]); };
-          const auto r = __builtin_amdgcn_permlane16_swap(two(0), two(1), false, false);
-          const auto s = __builtin_amdgcn_permlane16_swap(two(2), two(3), false, false);
-          a[x] = r[0];
-          a[2 + x] = r[1];
-          b[x] = s[0];
-          b[2 + x] = s[1];
-        }
+      for (int x = 0; x < 2; ++x) {
+        auto two = [&](int jj) { return pack2<T>(acc[jj][2 * x], acc[jj][2 * x + 1]); };
+        const auto r = __builtin_amdgcn_permlane16_swap(two(0), two(1), false, false);
+        const auto s = __builtin_amdgcn_permlane16_swap(two(2), two(3), false, false);
+        a[x] = r[0];
+        a[2 + x] = r[1];
+        b[x] = s[0];
+        b[2 + x] = s[1];
       }
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint32_t give = low ? b[x] : a[x];
-        const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, true);   // row_ror:8
-        a[x] = low ? a[x] : got;
-        b[x] = low ? got : b[x];
-      }
-      const int c = cv + 64 * wn + 16 * j + col;
-      const uint32_t at = row + (uint32_t)(16 * i) * (uint32_t)O * size + c * size;
-      __builtin_amdgcn_raw_buffer_store_b128(a, R, oob_unless(c < cols, at), 0, kStream);
-      __builtin_amdgcn_raw_buffer_store_b128(b, R, oob_unless(c < cols, at + 8 * (uint32_t)O * size), 0, kStream);
     }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t give = low ? b[x] : a[x];
+      const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x128, 0xF, 0xF, true);   // row_ror:8
+      a[x] = low ? a[x] : got;
+      b[x] = low ? got : b[x];
+    }
+    const int c = cv + 64 * wn + 16 * j + col;
+    const uint32_t at = row + (uint32_t)(16 * i) * (uint32_t)O * size + c * size;
+    __builtin_amdgcn_raw_buffer_store_b128(a, R, oob_unless(c < cols, at), 0, kStream);
+    __builtin_amdgcn_raw_buffer_store_b128(b, R, oob_unless(c < cols, at + 8 * (uint32_t)O * size), 0, kStream);
+  }
+}
+
+template <int T, int OUT>
+__device__ __forceinline__ void store_quadrant(void* out, int64_t O, int64_t row0, int64_t c0, int rows, int cv, int cols, int wm,
+                                               int wn, const f32x4 (&acc)[2][4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) store_block<T, OUT>(out, O, row0, c0, rows, cv, cols, wm, wn, i, acc[i]);
 }
 
 // One workgroup per CU, persistent over tiles. A stage is four quadrants of 128 x 128 results,
@@ -382,13 +385,8 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
+      for (int v = 0; v < 2; ++v)
         on |= (int)(128 * h + 32 * wm < cur.rows && 128 * v + 64 * wn < cur.cols) << (2 * h + v);
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[h][v][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
     on = __builtin_amdgcn_readfirstlane(on);
   };
   // A quadrant: 16 products, four at a time (two columns of a substep), if they are wanted; due(k)
@@ -407,15 +405,12 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
       }
     }
   };
-  // A tile's stores: always kStores of them, so that the waits behind them can count.
-  constexpr int kStores = 4 * kQuadrantStores<OUT>;
-  auto store = [&]() {
+  // Stores of row block i of a quadrant, which then starts over.
+  constexpr int kStores = kQuadrantStores<OUT>;
+  auto store = [&](int h, int v, int i) {
+    store_block<T, OUT>(g.out, O, cur.row0 + 128 * h, cur.c0, cur.rows - 128 * h, 128 * v, cur.cols, wm, wn, i, acc[h][v][i]);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int v = 0; v < 2; ++v)
-        store_quadrant<T, OUT>(g.out, O, cur.row0 + 128 * h, cur.c0, cur.rows - 128 * h, 128 * v, cur.cols, wm, wn, acc[h][v]);
-    if constexpr (OUT == kAnyWidth) __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    for (int j = 0; j < 4; ++j) acc[h][v][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   };
   auto read_q = [&](const uint8_t* L, int s, int k) {   // two blocks
 #pragma unroll
@@ -425,21 +420,29 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) d[s][i] = fp.read(L, i, s);
   };
-  // One stage from the buffers of P and Q, the next one's first halves in N0 and M0. S: stores of
-  // the tile before that may be in flight behind the loads which are waited for.
-  auto stage = [&](auto behind, uint8_t* P0, uint8_t* P1, uint8_t* Q0, uint8_t* Q1, const uint8_t* N0, const uint8_t* M0) {
-    constexpr int S = decltype(behind)::value;
+  // One stage from the buffers of P and Q, the next one's first halves in N0 and M0. A, B: stores that
+  // may be in flight behind the loads which the first and second barrier wait for. FIN: a tile's last
+  // stage, which stores each quadrant during the products of the next.
+  auto stage = [&](auto sa, auto sb, auto fin, uint8_t* P0, uint8_t* P1, uint8_t* Q0, uint8_t* Q1, const uint8_t* N0,
+                   const uint8_t* M0) {
+    constexpr int A = decltype(sa)::value, B = decltype(sb)::value;
+    constexpr bool FIN = decltype(fin)::value && OUT != kAnyWidth;
     quadrant(0, 0, p0, [&](int k) {
       if (k < 2)
         read_q(Q0, 1, k);
       else
         read_p(P1, k - 2, p1);
     });
-    step_barrier<8 + S>();   // Q0, P0 and P1 are read; Q1 has landed
+    step_barrier<8 + A>();   // Q0, P0 and P1 are read; Q1 has landed
     quadrant(1, 0, p1, [&](int k) {
+      if (FIN && k < 2) store(0, 0, k);
       if (k >= 2) read_q(Q1, 0, k - 2);   // over what the first substep's products are done with
     });
     quadrant(0, 1, p0, [&](int k) {
+      if (FIN && k == 0) {
+        store(1, 0, 0);
+        store(1, 0, 1);
+      }
       if (k < 2) read_q(Q1, 1, k);
       if (k == 1) {
         load_q(0, 0, Q0);
@@ -449,15 +452,20 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
         load_p(k - 2, 1, k == 2 ? P0 : P1);
       }
     });
-    step_barrier<8 + S>();   // Q1 is read; the next M0 and both halves of the next P have landed
+    step_barrier<8 + B>();   // Q1 is read; the next M0 and both halves of the next P have landed
     quadrant(1, 1, p1, [&](int k) {
       if (k < 2) {
         load_q(1, k, Q1);
         read_p(N0, k, p0);
       } else {
+        if (FIN) store(0, 1, k - 2);
         read_q(M0, 0, k - 2);
       }
     });
+    if (FIN) {
+      store(1, 1, 0);
+      store(1, 1, 1);
+    }
     advance();
   };
   // A tile's first stage stands behind the stores of the tile before (for the first tile: as many
@@ -465,26 +473,45 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   // number of memory operations in flight is the same: the compiler, which checks each read of
   // LDS against the loads, then adds no wait. A tile's odd last stage has no products.
   constexpr std::integral_constant<int, 0> none{};
-  constexpr std::integral_constant<int, kStores> some{};
+  constexpr std::integral_constant<int, 2 * kStores> half{};
+  constexpr std::integral_constant<int, 4 * kStores> whole{};
+  constexpr std::false_type more{};
+  constexpr std::true_type last{};
 #pragma unroll
-  for (int i = 0; i < kStores; ++i)   // at places of their own, or the compiler keeps one of them
+  for (int i = 0; i < 4 * kStores; ++i)   // at places of their own, or the compiler keeps one of them
     __builtin_amdgcn_raw_buffer_store_b128(u32x4{0, 0, 0, 0}, window(g.out, 0), 16 * i, 0, 0);
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[h][v][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (;;) {
     begin();
     int real = (cur.n + TK - 1) / TK;
-    auto second = [&]() {   // the products of the pair's second stage
+    auto second = [&]() {   // the products of a pair's second stage
       real -= 2;
       on = __builtin_amdgcn_readfirstlane(real < 0 ? 0 : on);
     };
-    stage(some, pa0, pa1, qa0, qa1, pb0, qb0);
+    stage(whole, half, more, pa0, pa1, qa0, qa1, pb0, qb0);
     second();
-    stage(none, pb0, pb1, qb0, qb1, pa0, qa0);
     for (int st = 2; st < cur.stages; st += 2) {
-      stage(none, pa0, pa1, qa0, qa1, pb0, qb0);
+      stage(none, none, more, pb0, pb1, qb0, qb1, pa0, qa0);
+      stage(none, none, more, pa0, pa1, qa0, qa1, pb0, qb0);
       second();
-      stage(none, pb0, pb1, qb0, qb1, pa0, qa0);
     }
-    store();
+    stage(none, half, last, pb0, pb1, qb0, qb1, pa0, qa0);
+    if constexpr (OUT == kAnyWidth) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int v = 0; v < 2; ++v)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) store(h, v, i);
+      __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    }
     u += step;
     if (u >= end) break;
     cur = w.tile_of(u);
