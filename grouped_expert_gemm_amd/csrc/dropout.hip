@@ -64,8 +64,9 @@ __device__ __forceinline__ void put_one(void* p, int64_t i, float v) {
 // One block of 8 values per thread at a time; WIDE: 16-byte accesses, the tensors aligned. Bound by
 // memory: 16384 x 4096 bf16 with a residual 403 MB in 78 us (5.2 TB/s), its gradient 268 MB in 44 us; the
 // ten rounds per 8 values hide behind that. 64 x 2048: 2.5 us.
-template <int T, bool RES, bool WIDE>
-__global__ __launch_bounds__(kThreads) void dropout_kernel(const void* x, const void* res, void* out, int64_t n,
+// BITS: the mask is written too.
+template <int T, bool RES, bool WIDE, bool BITS = false>
+__global__ __launch_bounds__(kThreads) void dropout_kernel(const void* x, const void* res, void* out, uint8_t* bits, int64_t n,
                                                            DropoutArgs d) {
   const PhiloxState g(d);
   const int64_t whole = n / 8, stride = (int64_t)gridDim.x * kThreads;
@@ -77,6 +78,12 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const void* x, const 
       v.load(x, b);
       if constexpr (RES) r.load(res, b);
       g.bits((uint64_t)b, w);
+      if constexpr (BITS) {
+        int kept = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) kept |= (int)philox_kept(w, i, d.threshold) << i;
+        bits[b] = (uint8_t)kept;
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float o[2];
@@ -91,8 +98,8 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const void* x, const 
     } else {
       g.bits((uint64_t)b, w);
       for (int i = 0; i < 8 && 8 * b + i < n; ++i) {
-        const uint32_t bits = i < 4 ? (i < 2 ? w[0] : w[1]) : (i < 6 ? w[2] : w[3]);
-        float o = ((bits >> (16 * (i & 1))) & 0xFFFFu) >= d.threshold ? one<T>(x, 8 * b + i) * d.scale : 0.f;
+        const uint32_t half = i < 4 ? (i < 2 ? w[0] : w[1]) : (i < 6 ? w[2] : w[3]);
+        float o = ((half >> (16 * (i & 1))) & 0xFFFFu) >= d.threshold ? one<T>(x, 8 * b + i) * d.scale : 0.f;
         if constexpr (RES) o = one<T>(res, 8 * b + i) + o;
         put_one<T>(out, 8 * b + i, o);
       }
@@ -102,23 +109,27 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const void* x, const 
 
 }  // namespace
 
-hipError_t launch_dropout(const void* x, const void* res, void* out, int dtype, int64_t n, const DropoutArgs& d, int cus,
-                          hipStream_t s) {
+hipError_t launch_dropout(const void* x, const void* res, void* out, uint8_t* bits, int dtype, int64_t n, const DropoutArgs& d,
+                          int cus, hipStream_t s) {
   const bool wide = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(res) | reinterpret_cast<uintptr_t>(out)) & 15) == 0;
   const int64_t blocks = ((n + 7) / 8 + kThreads - 1) / kThreads;
   const dim3 grid((unsigned)std::max<int64_t>(1, std::min<int64_t>(blocks, (int64_t)cus * 32)));
+  if (bits) {
+    hipLaunchKernelGGL((dropout_kernel<kBF16, false, true, true>), grid, dim3(kThreads), 0, s, x, res, out, bits, n, d);
+    return hipGetLastError();
+  }
   auto run = [&](auto t) {
     constexpr int T = decltype(t)::value;
     if (res) {
       if (wide)
-        hipLaunchKernelGGL((dropout_kernel<T, true, true>), grid, dim3(kThreads), 0, s, x, res, out, n, d);
+        hipLaunchKernelGGL((dropout_kernel<T, true, true>), grid, dim3(kThreads), 0, s, x, res, out, bits, n, d);
       else
-        hipLaunchKernelGGL((dropout_kernel<T, true, false>), grid, dim3(kThreads), 0, s, x, res, out, n, d);
+        hipLaunchKernelGGL((dropout_kernel<T, true, false>), grid, dim3(kThreads), 0, s, x, res, out, bits, n, d);
     } else {
       if (wide)
-        hipLaunchKernelGGL((dropout_kernel<T, false, true>), grid, dim3(kThreads), 0, s, x, res, out, n, d);
+        hipLaunchKernelGGL((dropout_kernel<T, false, true>), grid, dim3(kThreads), 0, s, x, res, out, bits, n, d);
       else
-        hipLaunchKernelGGL((dropout_kernel<T, false, false>), grid, dim3(kThreads), 0, s, x, res, out, n, d);
+        hipLaunchKernelGGL((dropout_kernel<T, false, false>), grid, dim3(kThreads), 0, s, x, res, out, bits, n, d);
     }
   };
   if (dtype == kBF16)

@@ -282,7 +282,7 @@ struct LoraIn {
   const float* q = nullptr;
   int32_t r = 0;
   float s = 0.f;
-  const geg::DropoutArgs* drop = nullptr;   // dgrad: masks the delta
+  const uint8_t* mask = nullptr;   // dgrad: the delta's, a bit per value of dx
   std::function<hipError_t()> pre;
   std::function<hipError_t()> post;
 };
@@ -355,7 +355,7 @@ geg_status gemm_common(int fmt, const void* a, const int32_t* sizes, const uint8
   g.lora_q = lora.q;
   g.lora_r = lora.r;
   g.lora_s = lora.s;
-  g.lora_drop = 0;
+  g.lora_mask = nullptr;
   if (lora.pre) {
     hipError_t e = lora.pre();
     if (e != hipSuccess) return hip_fail(e, "adapter launch");
@@ -512,8 +512,7 @@ geg_status dgrad_common(int fmt, const void* dy, const int32_t* sizes, const uin
   g.lora_q = lora.q;
   g.lora_r = lora.r;
   g.lora_s = lora.s;
-  g.lora_drop = lora.drop != nullptr;
-  if (lora.drop) g.drop = *lora.drop;
+  g.lora_mask = lora.mask;
   g.split = 1;
   g.glu = 0;
   g.tail_part = p.tail_bytes ? reinterpret_cast<float*>(wsb + p.tail_off) : nullptr;
@@ -742,9 +741,9 @@ geg_status gmxfp8_quantize(const void* a, uint8_t* codes, uint8_t* scales, int64
 
 size_t geg_lora_dropout_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r) {
   const size_t plain = geg_lora_workspace_bytes(op, M, N, K, E, r);
-  // the backward's masked activations
+  // the backward's masked activations and their mask
   const bool back = op == GEG_OP_NF4_DGRAD || op == GEG_OP_MXFP4_DGRAD;
-  return plain && back ? plain + round256((size_t)M * (size_t)K * 2) : plain;
+  return plain && back ? plain + round256((size_t)M * (size_t)K * 2) + round256((size_t)M * (size_t)K / 8) : plain;
 }
 
 size_t geg_lora_workspace_bytes(int32_t op, int64_t M, int64_t N, int64_t K, int32_t E, int32_t r) {
@@ -847,17 +846,15 @@ geg_status dgrad_lora(int fmt, const void* dy, const int32_t* sizes, const uint8
   const uint16_t* dy16 = reinterpret_cast<const uint16_t*>(dy);
   if (drop) scale *= drop->scale;
   const uint16_t* x16 = reinterpret_cast<const uint16_t*>(x);
-  uint16_t* xm = drop ? reinterpret_cast<uint16_t*>(wsb + plain) : nullptr;   // the masked activations
+  // the masked activations and their mask
+  uint16_t* xm = drop ? reinterpret_cast<uint16_t*>(wsb + plain) : nullptr;
+  uint8_t* bits = drop ? wsb + plain + round256((size_t)M * (size_t)K * 2) : nullptr;
   geg::DropoutArgs mask = drop ? *drop : geg::DropoutArgs{};
   mask.scale = 1.0f;
   // adapter gradients (zeros for experts without rows, and for M == 0)
   auto grads = [=]() -> hipError_t {
     hipError_t e = geg::launch_lora_grad(dy16, reinterpret_cast<const float*>(u), sizes, E, M, N, r, scale, grad_b,
                                          false, err, cus, stream);
-    if (e == hipSuccess && xm && M > 0) {
-      e = geg::launch_dropout(x16, nullptr, xm, geg::kBF16, M * K, mask, cus, stream);
-      ++g_launches;
-    }
     if (e == hipSuccess)
       e = geg::launch_lora_grad(xm ? xm : x16, g, sizes, E, M, K, r, 1.0f, grad_a, true, err, cus, stream);
     g_launches += 2;
@@ -871,12 +868,17 @@ geg_status dgrad_lora(int fmt, const void* dy, const int32_t* sizes, const uint8
   L.u = g;
   L.q = At;
   L.r = r;
-  L.drop = drop;
+  L.mask = bits;
   L.s = 1.0f;
   // g = s dy B_e (from a transposed copy of B) and a transposed copy of A first;
   // the dgrad epilogue adds g A_e; the gradients after
   L.pre = [=]() -> hipError_t {
-    hipError_t e = geg::launch_lora_transpose(lora_b, E, N, r, Bt, cus, stream);
+    hipError_t e = hipSuccess;
+    if (xm) {
+      e = geg::launch_dropout(x16, nullptr, xm, bits, geg::kBF16, M * K, mask, cus, stream);
+      ++g_launches;
+    }
+    if (e == hipSuccess) e = geg::launch_lora_transpose(lora_b, E, N, r, Bt, cus, stream);
     if (e == hipSuccess) e = geg::launch_lora_down(dy16, Bt, sizes, E, M, N, r, scale, g, err, cus, stream);
     if (e == hipSuccess) e = geg::launch_lora_transpose(lora_a, E, r, K, At, cus, stream);
     g_launches += 3;
@@ -1347,7 +1349,7 @@ geg_status geg_dropout(const void* x, const void* residual, void* out, int32_t d
   if ((st = check_device()) != GEG_OK) return st;
   for (auto [ptr, name] : {std::pair<const void*, const char*>{x, "x"}, {residual, "residual"}, {out, "out"}, {rng, "rng"}})
     if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
-  hipError_t e = geg::launch_dropout(x, residual, out, dtype, n, d, cu_count(), stream);
+  hipError_t e = geg::launch_dropout(x, residual, out, nullptr, dtype, n, d, cu_count(), stream);
   if (e != hipSuccess) return hip_fail(e, "dropout launch");
   ++g_launches;
   return GEG_OK;

@@ -83,8 +83,7 @@ struct GemmArgs {
   const float* lora_q;
   int32_t lora_r;
   float lora_s;
-  int32_t lora_drop;      // 1 (dgrad): the delta is masked by `drop` over [M, output width]
-  DropoutArgs drop;
+  const uint8_t* lora_mask;   // dgrad: the delta's mask [M, output width], a bit each, or NULL
 };
 
 // Each launcher returns the hipError_t of its launch.
@@ -214,7 +213,8 @@ int request_splits(int64_t M, int64_t K, int32_t r);
 int64_t request_units(int64_t M, int32_t L, int32_t r);
 hipError_t launch_request_lora(const RequestArgs& g, int dtype, int cus, hipStream_t s);
 // Dropout: out = [res +] keep ? x * scale : 0 for n values (see dropout.hip, philox.hpp).
-hipError_t launch_dropout(const void* x, const void* res, void* out, int dtype, int64_t n, const DropoutArgs& d, int cus,
+// bits: the mask [n / 8] too, a bit per value (bf16, n % 8 == 0, no residual, aligned), or NULL.
+hipError_t launch_dropout(const void* x, const void* res, void* out, uint8_t* bits, int dtype, int64_t n, const DropoutArgs& d, int cus,
                           hipStream_t s);
 // Router gate: top-k of logits [T, E] with softmax weights, its gradient, and the
 // gradient of the weighted combine (see gate.hip).

@@ -28,7 +28,6 @@
 
 #include "geg_device.hpp"
 #include "geg_launch.hpp"
-#include "philox.hpp"
 
 namespace geg {
 
@@ -588,7 +587,7 @@ __device__ __forceinline__ void lora_block(const Split8& u, const Split8& q, f32
   }
 }
 
-// DROP (dgrad): the adapter delta is masked by g.drop. An instantiation of its own: the others
+// DROP (dgrad): the adapter delta is masked by g.lora_mask. An instantiation of its own: the others
 // keep their registers.
 template <Fmt F, bool DG, bool TAIL, bool DROP>
 __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(GemmArgs g) {
@@ -756,6 +755,17 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(GemmArgs g) {
       const __amdgpu_buffer_rsrc_t RQ = __builtin_amdgcn_make_buffer_rsrc(
           const_cast<float*>(g.lora_q + ((int64_t)e * O + n0 + 64 * wn) * r), (short)0,
           (int32_t)(qcols > 0 ? qcols * r * 4 : 0), 0x00020000);
+      // DROP: lane (r16, kg) holds the mask of row 32 ii + 16 (kg / 2) + r16 and columns 32 (kg % 2) ..
+      uint32_t mask[4];
+      if constexpr (DROP) {
+        const int64_t at = (row0 + 128 * wm) * O;
+        const __amdgpu_buffer_rsrc_t RM = __builtin_amdgcn_make_buffer_rsrc(
+            const_cast<uint8_t*>(g.lora_mask + (at >> 3)), (short)0, (int32_t)((rows - 128 * wm) * O >> 3), 0x00020000);
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii)
+          mask[ii] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(
+              RM, (int)(((32 * ii + 16 * (kg >> 1) + r16) * O + n0 + 64 * wn + 32 * (kg & 1)) >> 3), 0, 0);
+      }
       for (int j0 = 0; j0 < r; j0 += 32) {
         const int jj = j0 + 8 * kg;
         const bool ok = jj < r;
@@ -772,16 +782,10 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(GemmArgs g) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) lora_block<kTr<F, DG>>(au, bq[j], acc[i][j]);
           } else {
-            // Two column blocks at a time: lane (r16, kg) draws the 8 bits of row 16 i + r16 and
-            // columns 32 p + 8 kg .., the lanes that hold those results fetch them.
+            // 32 columns of 16 rows are a word in each of 16 lanes (see `mask`); the lanes that hold
+            // these results fetch them.
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-              uint32_t w[4];
-              const int64_t at = (row0 + 128 * wm + 16 * i + r16) * O + n0 + 64 * wn + 32 * p + 8 * kg;
-              PhiloxState(g.drop).bits((uint64_t)at >> 3, w);
-              int kept = 0;
-#pragma unroll
-              for (int b = 0; b < 8; ++b) kept |= (int)philox_kept(w, b, g.drop.threshold) << b;
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 f32x4 d = {0.f, 0.f, 0.f, 0.f};
@@ -790,8 +794,8 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(GemmArgs g) {
                 for (int q = 0; q < 4; ++q) {
                   // this result's row and column in the 16 x 16 block
                   const int rr = kTr<F, DG> ? r16 : 4 * kg + q, cc = kTr<F, DG> ? 4 * kg + q : dg_col(r16);
-                  const int bits = __shfl(kept, rr + 16 * (2 * j + (cc >> 3)));
-                  if ((bits >> (cc & 7)) & 1) acc[i][2 * p + j][q] += d[q];
+                  const uint32_t word = (uint32_t)__shfl((int)mask[i >> 1], rr + 16 * (p + 2 * (i & 1)));
+                  acc[i][2 * p + j][q] += ((word >> (16 * j + cc)) & 1) ? d[q] : 0.f;
                 }
               }
             }
@@ -1010,7 +1014,7 @@ hipError_t launch_tile_fixup(const GemmArgs& g, bool dgrad, int tile_grid, hipSt
 template <Fmt F, bool DG, bool TAIL>
 hipError_t launch_tile_t(const GemmArgs& g, int grid, hipStream_t s) {
   if constexpr (DG) {
-    if (g.lora_drop) {
+    if (g.lora_mask) {
       hipLaunchKernelGGL((tile_kernel<F, DG, TAIL, true>), dim3(grid), dim3(kTileThreads), 0, s, g);
       return hipGetLastError();
     }

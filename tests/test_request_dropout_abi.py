@@ -74,7 +74,7 @@ def test_adapter_dropout_refusals():
         assert back(p=-1.0) == 8 and back(N=60) == 2
     op = geg.GEG_OP_MXFP4_DGRAD
     plain, drop = L().geg_lora_workspace_bytes(op, 4, 64, 128, 2, 16), L().geg_lora_dropout_workspace_bytes(op, 4, 64, 128, 2, 16)
-    assert drop == plain + 4 * 128 * 2
+    assert drop == plain + 4 * 128 * 2 + 256   # the masked activations and their mask
     assert L().geg_lora_dropout_workspace_bytes(geg.GEG_OP_NF4_FWD, 4, 64, 128, 2, 16) == \
         L().geg_lora_workspace_bytes(geg.GEG_OP_NF4_FWD, 4, 64, 128, 2, 16)
 
