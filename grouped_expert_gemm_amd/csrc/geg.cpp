@@ -1204,6 +1204,8 @@ static geg_status dense_common(int dir, const void* p, const char* pname, const 
   if (!sizes || !out || (M > 0 && !p) || ((M > 0 || !wgrad) && !q))
     return fail(GEG_ERR_NULL_POINTER, "a required pointer is NULL");
   if (!ws) return fail(GEG_ERR_WORKSPACE, "workspace is NULL");
+  if (out == p || out == q)
+    return fail(GEG_ERR_BAD_OPTION, std::string(oname) + " may not be " + pname + " or " + qname);
   if (!aligned(p, 16) || !aligned(q, 16) || !aligned(out, 16) || !aligned(sizes, 4))
     return fail(GEG_ERR_MISALIGNED, std::string(pname) + ", " + qname + " and " + oname + " must be 16-byte aligned");
   if (!aligned(ws, 256)) return fail(GEG_ERR_WORKSPACE, "workspace must be 256-byte aligned");

@@ -36,6 +36,7 @@ def test_refusals(name):
     for p in ("p", "q", "out"):
         assert c(**{p: P + 8}) == 3, p
     assert c(sizes=P + 2) == 3
+    assert c(out=P) == 8 and c(q=2 * P) == 8
     assert c(ws=None) == 5 and c(ws=P + 16) == 5 and c(nbytes=255) == 5
     assert c(opts=geg.Opts(1, 0)) == 8 and c(opts=geg.Opts(3, 0)) == 8 and c(opts=geg.Opts(0, 0, None, -1)) == 8
     assert c(opts=geg.Opts(4, 0)) == (8 if name != NAMES[0] else c())

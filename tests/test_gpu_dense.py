@@ -300,6 +300,47 @@ def test_autograd_op_and_differences(geg):
     assert (diff - slope).abs() <= bound
 
 
+def test_captured_training_step(geg):
+    """Two products with dropout between them and on the way into the residual, forward and both
+    backward passes in one graph; inputs, sizes and the dropout's words change between replays."""
+    import torch
+    log("case: captured training step")
+    E, K, I, M = 4, 64, 136, 300
+    g = torch.Generator(device="cuda").manual_seed(13)
+    draw = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()
+    x, w1, w2, dout = draw(M, K).requires_grad_(True), draw(E, I, K).requires_grad_(True), draw(E, K, I).requires_grad_(True), draw(M, K)
+    sz = torch.tensor([100, 0, 190, 7], dtype=torch.int32, device="cuda")
+    words = torch.tensor([5, 0], device="cuda")
+
+    def step():
+        h = geg.dropout(geg.grouped_matmul(x, sz, w1), 0.25, words, 0)
+        out = geg.dropout(geg.grouped_matmul(h, sz, w2), 0.25, words, 1, residual=x)
+        return (out, *torch.autograd.grad(out, (x, w1, w2), dout))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [t.detach() for t in step()]
+    seen = []
+    for n in range(3):
+        with torch.no_grad():
+            x.copy_(draw(M, K)), w1.copy_(draw(E, I, K)), w2.copy_(draw(E, K, I))
+        words[1] += 2
+        sz.copy_(torch.tensor([100 - n, n, 190, 7], dtype=torch.int32))
+        want = [t.detach().clone() for t in step()]
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        seen.append((got[0] == x.detach()).float().mean().item())
+    # values whose delta was dropped: 0.25 of all, 4 standard deviations of a binomial of 300 * 64
+    assert all(abs(v - 0.25) < 4 * (0.25 * 0.75 / (M * K)) ** 0.5 + 3 / M for v in seen), seen
+
+
 def test_only_one_gradient(geg):
     import torch
     a, dy, w, sz = _case("fp16", [4, 9], 16, 24, seed=10)

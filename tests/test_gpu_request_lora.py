@@ -201,15 +201,15 @@ def test_offsets_past_2_31(geg):
 def test_captured_and_on_streams(geg):
     import torch
     log("case: request adapters captured and on another stream")
-    for M in (24, 600):
-        args = _case("bf16", M, 256, 264, 5, 16, seed=7)
+    for M, L, r in ((24, 5, 16), (600, 5, 16), (300, 13000, 8)):
+        args = _case("bf16", M, 256, 264, L, r, seed=7)
         geg.request_lora(*args)
         torch.cuda.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             got = geg.request_lora(*args)
         for seed in range(3):
-            for old, new in zip(args, _case("bf16", M, 256, 264, 5, 16, seed=10 + seed)):
+            for old, new in zip(args, _case("bf16", M, 256, 264, L, r, seed=10 + seed)):
                 old.copy_(new)
             want = geg.request_lora(*args)
             graph.replay()
