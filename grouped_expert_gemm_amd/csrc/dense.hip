@@ -301,13 +301,19 @@ __device__ __forceinline__ void store_quadrant(void* out, int64_t O, int64_t row
 // wavefront each (32 x 64 results). Fragments are read a little ahead of their products, so a
 // half of an operand is needed in LDS for half a stage only; its buffer then takes the stage
 // after the next, and the loads have one and a half stages to land. Reads and loads stand between
-// the products, four at a time. The loads run on across tiles, at their own place in the list.
-// Measured: 8192 rows over 8 experts of 28672 x 4096 1.67-1.72 ms, 1.12-1.15 PFLOP/s (a library product of
-// that many rows by one such expert: 1.33); the matrix pipes are busy 0.57 of the clocks, at 1.8 GHz, and
-// an expert's last row block costs as much time as half a whole one. 3108 rows over 32 of 5760 x 2880 222
-// us, 1.1 GB at 5.0 TB/s. 16384 rows over 64 of 2048 x 2048, activations' gradient 184 us (0.68 GB), then
-// the weights' 284 (0.67 GB; 196 with its inputs in the last cache): tiles of four stages, whose bursts of
-// stores the next tile's loads wait behind (184 with the stores dropped).
+// the products, four at a time. A load into LDS takes 16 clocks of the CU's one path from the L2 and
+// holds its wavefront up while that is busy, so there is at most one per wavefront between four products
+// and the next four (in twos and threes: 4% slower with all CUs at work, 10% with half). The loads run on
+// across tiles, at their own place in the list.
+// Measured: 8192 rows over 8 experts of 28672 x 4096 1.47 ms with 1024 each, 1.31 PFLOP/s, 1.63 ms with the
+// sizes that a router gives (a library product of that many rows by one such expert: 1.33 to 1.48): an
+// expert's last row block of 6 rows costs 0.4 of a whole one. LDS is as busy as the matrix pipes: 192 KB of
+// fragments and 64 KB of loads per stage, 2048 clocks, as 2048 of products; a stage takes 1.24 us on
+// one CU in eight at 2.4 GHz and 1.7 on all at 1.8. (Four wavefronts of 128 x 128 read a third less
+// and were slower, 1.36 and 1.9: alone on its SIMD a wavefront's loads hold its products up.) 3108 rows
+// over 32 experts of 5760 x 2880 215 us, 1.1 GB at 5.2 TB/s. 16384 rows over 64 of 2048 x 2048, both gradients one after
+// the other, 415 us: tiles of four stages in the weights', whose bursts of stores the next tile's loads wait
+// behind (with the stores dropped it takes 184 of its 270).
 template <int D, int T, int OUT>
 __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
@@ -444,6 +450,8 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
     quadrant(1, 0, p1, [&](int k) {
       if (FIN && k < 2) store(0, 0, k);
       if (k >= 2) read_q(Q1, 0, k - 2);   // over what the first substep's products are done with
+      if (k == 0 || k == 1) load_q(0, k, Q0);
+      if (k == 3) load_p(0, 0, P0);
     });
     quadrant(0, 1, p0, [&](int k) {
       if (FIN && k == 0) {
@@ -451,23 +459,18 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
         store(1, 0, 1);
       }
       if (k < 2) read_q(Q1, 1, k);
-      if (k == 1) {
-        load_q(0, 0, Q0);
-        load_q(0, 1, Q0);
-      } else if (k >= 2) {
-        load_p(k - 2, 0, k == 2 ? P0 : P1);
-        load_p(k - 2, 1, k == 2 ? P0 : P1);
-      }
+      if (k == 1) load_p(0, 1, P0);
+      if (k >= 2) load_p(1, k - 2, P1);
     });
     step_barrier<8 + B>();   // Q1 is read; the next M0 and both halves of the next P have landed
     quadrant(1, 1, p1, [&](int k) {
       if (k < 2) {
-        load_q(1, k, Q1);
         read_p(N0, k, p0);
       } else {
         if (FIN) store(0, 1, k - 2);
         read_q(M0, 0, k - 2);
       }
+      if (k & 1) load_q(1, k >> 1, Q1);
     });
     if (FIN) {
       store(1, 1, 0);
