@@ -149,6 +149,8 @@ def lib() -> ctypes.CDLL:
             L.geg_request_lora.argtypes = [_P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _I32, _I64, _I64, _I64, _I32, _I32,
                                            _P, _SZ, _P]
             L.geg_request_lora.restype = ctypes.c_int
+            L.geg_grouped_workspace_bytes.argtypes = [_I32, _I64, _I64, _I64, _I32]
+            L.geg_grouped_workspace_bytes.restype = _SZ
             L.geg_request_lora_workspace_bytes.argtypes = [_I64, _I64, _I32, _I32]
             L.geg_request_lora_workspace_bytes.restype = _SZ
             L.geg_lora_dropout_workspace_bytes.argtypes = [_I32, _I64, _I64, _I64, _I32, _I32]
@@ -1239,7 +1241,8 @@ def _dense(fn_name, x, xname, sizes, w, out, oname, width, zero_rest, workspace,
     with _allocating(stream):
         if mine:
             out = x.new_empty((M, width))
-        ws = _workspace(workspace, 256, x.device, None, check_errors)
+        ws = _workspace(workspace, lib().geg_grouped_workspace_bytes(int(fn_name == "geg_grouped_dgrad"), M, N, K, E), x.device,
+                        None, check_errors)
     _check(getattr(lib(), fn_name)(x.data_ptr(), sizes.data_ptr(), w.data_ptr(), out.data_ptr(), dt, M, N, K, E,
                                    int(zero_rest), ws.buf.data_ptr(), ws.buf.numel(),
                                    ctypes.byref(opts) if opts else None, raw))
@@ -1292,7 +1295,7 @@ def grouped_wgrad(dy, a, sizes, dw=None, dtype=None, workspace: Workspace | None
     with _allocating(stream):
         if mine:
             dw = dy.new_empty((E, N, K), dtype=dtype)
-        ws = _workspace(workspace, 256, dy.device, None, check_errors)
+        ws = _workspace(workspace, lib().geg_grouped_workspace_bytes(2, M, N, K, E), dy.device, None, check_errors)
     _check(lib().geg_grouped_wgrad(dy.data_ptr(), a.data_ptr(), sizes.data_ptr(), dw.data_ptr(), dt,
                                    2 if dtype is torch.float32 else dt, M, N, K, E, ws.buf.data_ptr(), ws.buf.numel(),
                                    ctypes.byref(opts) if opts else None, raw))

@@ -100,6 +100,7 @@ struct Tiles {
     int64_t n0;          // wgrad: first column of dy
     int rows, cols;      // valid
     int n;               // contraction length
+    int k0;              // where the contraction starts (a piece of it)
     int stages;          // a multiple of the sets of buffers
   };
 
@@ -134,7 +135,22 @@ struct Tiles {
       x.n0 = 0;
       x.n = (int)C;
     }
-    x.stages = max(kRing, kRing * ((x.n + kRing * TK - 1) / (kRing * TK)));
+    x.k0 = 0;
+    x.stages = stages_of(x.n);
+    return x;
+  }
+  static __device__ __forceinline__ int stages_of(int n) { return max(kRing, kRing * ((n + kRing * TK - 1) / (kRing * TK))); }
+  // Piece `i` of `split` of a tile's contraction, in whole stages.
+  __device__ __forceinline__ Tile piece_of(int32_t u, int split) const {
+    const int32_t t = __builtin_amdgcn_readfirstlane(u / split);   // (vector ALUs)
+    const int i = u - t * split;
+    Tile x = tile_of(t);
+    const int len = __builtin_amdgcn_readfirstlane(((x.n + TK - 1) / TK + split - 1) / split) * TK;
+    x.k0 = min(i * len, x.n);
+    x.n = min(len, x.n - x.k0);
+    x.p += x.k0 * (kPAlong ? 1 : g.N);
+    x.q += x.k0 * (kQAlong ? 1 : g.K);
+    x.stages = stages_of(x.n);
     return x;
   }
 
@@ -148,9 +164,9 @@ struct Tiles {
   };
   __device__ __forceinline__ void aim(Cursor& c, const Tile& x, bool any) const {
     c.p = reinterpret_cast<const uint8_t*>(x.p);
-    c.left_p = !any ? 0 : (kPAlong ? x.rows * C : x.n * g.N - x.n0) * 2;
+    c.left_p = !any ? 0 : (kPAlong ? x.rows * C - x.k0 : x.n * g.N - x.n0) * 2;
     c.q = reinterpret_cast<const uint8_t*>(x.q);
-    c.left_q = !any ? 0 : (kQAlong ? x.cols * g.K : x.n * g.K - x.c0) * 2;
+    c.left_q = !any ? 0 : (kQAlong ? x.cols * g.K - x.k0 : x.n * g.K - x.c0) * 2;
     c.rest = x.n;
     c.st = 0;
     c.stages = x.stages;
@@ -535,7 +551,11 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
 // one barrier per stage. Alone on its CU it is bound by the loads' latency, 0.4 us per stage of 64
 // (a stage of 256 x 256: 0.86, the matrix rate), with many tiles by the weights: 128 experts of
 // 1536 x 2048, one row each, 805 MB in 134 us, 6.0 TB/s.
-template <int D, int T, int OUT>
+// SPLIT: so few tiles that each tile's contraction is cut into g.split pieces for workgroups of their own; the
+// fp32 sums go to the workspace, in the order that the lanes hold them, and a second launch adds the
+// pieces in their order.
+constexpr int64_t kPart = 128 * 128 * 4;   // bytes of a piece's sums
+template <int D, int T, int OUT, bool SPLIT>
 __global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
   __shared__ int32_t p_u[kMaxExperts + 1];
@@ -555,7 +575,9 @@ __global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
   if constexpr (D != kDenseWgrad) {
     if (g.zero_rest) zero_rows((uint16_t*)g.out, p_off[g.E], g.M, O);
   }
+  if constexpr (SPLIT) total *= g.split;
   const W w{g, lane, wave, p_off, p_u, D == kDenseDgrad ? g.N : g.K, O, blocks_n, blocks_k};
+  auto unit_of = [&](int32_t v) { return SPLIT ? w.piece_of(v, g.split) : w.tile_of(v); };
   const int G = gridDim.x;
   const int parts = G % 8 == 0 ? 8 : 1, step = G / parts, part = blockIdx.x % parts;
   const int32_t end = (int32_t)((int64_t)total * (part + 1) / parts);
@@ -565,7 +587,7 @@ __global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
   const Frag<W::kPAlong> fp(lane, 2 * wm);
   const Frag<W::kQAlong> fq(lane, 4 * wn);
   f32x4 acc[2][4];
-  typename W::Tile cur = w.tile_of(u);   // of the products
+  typename W::Tile cur = unit_of(u);     // of the products
   typename W::Cursor lc;                 // of the loads
   w.aim(lc, cur, true);
   int32_t lu = u;
@@ -581,7 +603,7 @@ __global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
     if (lc.st == lc.stages) {
       lu += step;
       const bool any = lu < end;
-      w.aim(lc, any ? w.tile_of(lu) : cur, any);
+      w.aim(lc, any ? unit_of(lu) : cur, any);
     }
   };
   int on;   // the wavefront has results
@@ -610,7 +632,7 @@ __global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
       }
     }
   };
-  constexpr int kStores = kQuadrantStores<OUT>;
+  constexpr int kStores = SPLIT ? 8 : kQuadrantStores<OUT>;
   constexpr std::integral_constant<int, 0> none{};
   constexpr std::integral_constant<int, kStores> some{};
   load(pa, qa);
@@ -648,13 +670,53 @@ __global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
       due();
       stage(none, pd, qd, pc, qc);
     }
-    store_quadrant<T, OUT>(g.out, O, cur.row0, cur.c0, cur.rows, 0, cur.cols, wm, wn, acc);
-    if constexpr (OUT == kAnyWidth) __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    if constexpr (SPLIT) {
+      const __amdgpu_buffer_rsrc_t R = window(g.parts + (int64_t)u * kPart, kPart);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), R,
+                                                 (uint32_t)(((wave * 2 + i) * 4 + j) * 1024 + lane * 16), 0, 0);
+    } else {
+      store_quadrant<T, OUT>(g.out, O, cur.row0, cur.c0, cur.rows, 0, cur.cols, wm, wn, acc);
+      if constexpr (OUT == kAnyWidth) __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0)
+    }
     u += step;
     if (u >= end) break;
-    cur = w.tile_of(u);
+    cur = unit_of(u);
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0): no load into LDS outlives the workgroup
+}
+
+// The pieces of a tile added in their order, rounded and stored.
+template <int D, int T, int OUT>
+__global__ __launch_bounds__(TThreads) void dense_join_kernel(DenseArgs g) {
+  __shared__ int32_t p_off[kMaxExperts + 1];
+  __shared__ int32_t p_u[kMaxExperts + 1];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  using W = Tiles<D, 128>;
+  constexpr int TM = W::TM, TN = W::TN;
+  const int64_t O = D == kDenseFwd ? g.N : g.K;
+  const int blocks_n = (int)((g.N + TM - 1) / TM), blocks_k = (int)((g.K + TN - 1) / TN);
+  const int c_tiles = (int)((O + TN - 1) / TN);
+  int32_t total = build_plan(p_off, p_u, g.sizes, g.E, g.M, g.err,
+                             [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : (s + TM - 1) / TM * c_tiles; });
+  total = D == kDenseWgrad ? g.E * blocks_n * blocks_k : __builtin_amdgcn_readfirstlane(total);
+  const W w{g, lane, wave, p_off, p_u, D == kDenseDgrad ? g.N : g.K, O, blocks_n, blocks_k};
+  for (int32_t u = blockIdx.x; u < total; u += gridDim.x) {
+    const typename W::Tile x = w.tile_of(u);
+    f32x4 acc[2][4] = {};
+    const uint8_t* from = g.parts + (int64_t)u * g.split * kPart + wave * 8192 + lane * 16;
+#pragma unroll 4
+    for (int p = 0; p < g.split; ++p, from += kPart)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] += *reinterpret_cast<const f32x4*>(from + (i * 4 + j) * 1024);
+    store_quadrant<T, OUT>(g.out, O, x.row0, x.c0, x.rows, 0, x.cols, wave >> 1, wave & 1, acc);
+  }
 }
 
 // ------------------------------------------------------------------ forward, few rows
@@ -749,11 +811,18 @@ hipError_t narrow_one(const DenseArgs& g, int cus, hipStream_t s) {
 
 template <int D, int T, int OUT>
 hipError_t tile_one(const DenseArgs& g, bool small, int cus, hipStream_t s) {
-  const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(dense_tiles(D, g.M, g.N, g.K, g.E, small ? 128 : 256), cus));
-  if (small)
-    hipLaunchKernelGGL((dense_small_kernel<D, T, OUT>), dim3((unsigned)grid), dim3(TThreads), 0, s, g);
-  else
-    hipLaunchKernelGGL((dense_tile_kernel<D, T, OUT>), dim3((unsigned)grid), dim3(TThreads), 0, s, g);
+  const int64_t tiles = std::max<int64_t>(1, dense_tiles(D, g.M, g.N, g.K, g.E, small ? 128 : 256));
+  const dim3 grid((unsigned)std::min<int64_t>(tiles * (small ? g.split : 1), cus));
+  if (!small) {
+    hipLaunchKernelGGL((dense_tile_kernel<D, T, OUT>), grid, dim3(TThreads), 0, s, g);
+  } else if (g.split == 1) {
+    hipLaunchKernelGGL((dense_small_kernel<D, T, OUT, false>), grid, dim3(TThreads), 0, s, g);
+  } else {
+    hipLaunchKernelGGL((dense_small_kernel<D, T, kWide, true>), grid, dim3(TThreads), 0, s, g);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((dense_join_kernel<D, T, OUT>), dim3((unsigned)std::min<int64_t>(tiles, cus)), dim3(TThreads), 0, s, g);
+  }
   return hipGetLastError();
 }
 

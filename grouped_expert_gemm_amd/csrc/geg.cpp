@@ -1181,6 +1181,14 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
                    workspace, workspace_bytes, opts, stream);
 }
 
+size_t geg_grouped_workspace_bytes(int32_t direction, int64_t M, int64_t N, int64_t K, int32_t E) {
+  if (direction < 0 || direction > geg::kDenseWgrad || M < 0 || N <= 0 || K <= 0 || E <= 0 || M >= (int64_t)INT32_MAX ||
+      N > kMaxWindow / 512 || K > kMaxWindow / 512)
+    return 0;
+  const int split = geg::dense_split(direction, M, N, K, E);
+  return split == 1 ? kHeader : kHeader + (size_t)geg::dense_tiles(direction, M, N, K, E, 128) * split * (128 * 128 * 4);
+}
+
 // Grouped products with 16-bit weights. p: a or dy; q: w, or a for the weights' gradient.
 static geg_status dense_common(int dir, const void* p, const char* pname, const void* q, const char* qname,
                                const int32_t* sizes, void* out, const char* oname, int32_t dtype, int32_t out_dtype,
@@ -1215,17 +1223,20 @@ static geg_status dense_common(int dir, const void* p, const char* pname, const 
                            {ws, "workspace"}})
     if ((st = check_device_ptr(ptr, name)) != GEG_OK) return st;
   geg::DenseArgs g{reinterpret_cast<const uint16_t*>(p), reinterpret_cast<const uint16_t*>(q), sizes, out, M, N, K, E,
-                   zero_rest != 0, reinterpret_cast<uint32_t*>(ws)};
+                   zero_rest != 0, reinterpret_cast<uint32_t*>(ws), 1, reinterpret_cast<uint8_t*>(ws) + kHeader};
   const int cus = cu_count();
-  const bool narrow = dir == geg::kDenseFwd && (force == 4 || (force == 0 && geg::dense_narrow(M, N, E)));
+  // a workspace without room for the pieces: whole tiles
+  const int split = ws_bytes < geg_grouped_workspace_bytes(dir, M, N, K, E) ? 1 : geg::dense_split(dir, M, N, K, E);
+  const bool narrow = dir == geg::kDenseFwd && (force == 4 || (force == 0 && split < 4 && geg::dense_narrow(M, N, E)));
   const bool small = force == 5 || (force == 0 && geg::dense_small(dir, M, N, K, E));
+  if (small && !narrow) g.split = split;
   hipError_t e = record_event(opts, narrow ? 2 : 0, stream);
   if (e == hipSuccess)
     e = narrow ? geg::launch_dense_narrow(dtype, g, cus, stream)
                : geg::launch_dense_tile(dir, dtype, out_dtype == GEG_F32, small, g, cus, stream);
   if (e == hipSuccess) e = record_event(opts, narrow ? 3 : 1, stream);
   if (e != hipSuccess) return hip_fail(e, "16-bit product launch");
-  ++g_launches;
+  g_launches += g.split > 1 ? 2 : 1;
   return GEG_OK;
 }
 

@@ -161,6 +161,8 @@ struct DenseArgs {
   int32_t E;
   int32_t zero_rest;      // rows past the experts' are set to 0 (else left as they are)
   uint32_t* err;
+  int32_t split;          // tiles of 128: pieces of a tile's contraction (1: whole)
+  uint8_t* parts;         // their sums [tiles * split][64 KB]
 };
 // An upper bound of a product's tiles of S x S results.
 inline int64_t dense_tiles(int dir, int64_t M, int64_t N, int64_t K, int64_t E, int S) {
@@ -174,6 +176,7 @@ inline int64_t dense_tiles(int dir, int64_t M, int64_t N, int64_t K, int64_t E, 
 // tiles of 128 need rounds to come to speed (narrow, 128): 1 x 4096 x 4096: 1 20, 26; 8 26, 26;
 // 16 31, 26; 8 x 8192 x 4096: 1 102, 107; 4 105, 108; 16 128, 108; 64 x 2048 x 2048: 1 102, 102; 4 104,
 // 104; 128 x 2048 x 2048: 1 200, 175; 128 x 1536 x 2048: 1 154, 134; 32 x 8192 x 2048: 4 202, 174.
+// Tiles of 128 whose contraction is cut into four pieces or more are ahead (1 x 4096 x 4096, 16 rows: 31, 17).
 inline bool dense_narrow(int64_t M, int64_t N, int64_t E) {
   return M <= 4 * E && (E < M ? E : M) * ((N + 127) / 128) <= 1024;
 }
@@ -186,6 +189,19 @@ inline bool dense_narrow(int64_t M, int64_t N, int64_t E) {
 // 184, 181; drawn 16 181, 185; 64 194, 199; 96 202, 217.
 inline bool dense_small(int dir, int64_t M, int64_t N, int64_t K, int64_t E) {
   return dense_tiles(dir, M, N, K, E, 128) <= 512 || (dir != kDenseWgrad && M <= 16 * E);
+}
+// Pieces that a tile's contraction is cut into where there are fewer than 128 tiles (a bound, from the
+// sizes): up to one per CU, each of at least 8 stages, of contractions (the weights' gradient: an
+// expert's share of the rows) of 2048 and more; less does not pay for the second launch. Measured (us,
+// whole, pieces): forward 1 x 1024 x 4096, 512 rows: 34, 20; 2 x 512 x 2048, 64: 15.3, 12.2; 1 x 447 x 1840,
+// 25: 15.3, 14.3; 4 x 1024 x 1024, 256: 9.8, 13.1; 1 x 256 x 16384, 64: 93, 24; activations' gradient of 9 x
+// 8104 x 216, 410: 55, 22; weights' gradient of 1 x 512 x 512, 4096: 35, 20.
+inline int dense_split(int dir, int64_t M, int64_t N, int64_t K, int64_t E) {
+  if (!dense_small(dir, M, N, K, E)) return 1;
+  const int64_t tiles = dense_tiles(dir, M, N, K, E, 128), c = dir == kDenseFwd ? K : dir == kDenseDgrad ? N : M / E;
+  if (tiles == 0 || c < 2048) return 1;
+  const int64_t s = 256 / tiles < c / 512 ? 256 / tiles : c / 512;
+  return (int)(s < 1 ? 1 : s > 8 ? 8 : s);
 }
 hipError_t launch_dense_tile(int dir, int dtype, bool f32_out, bool small, const DenseArgs& g, int cus, hipStream_t s);
 hipError_t launch_dense_narrow(int dtype, const DenseArgs& g, int cus, hipStream_t s);

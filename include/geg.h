@@ -508,7 +508,9 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
  *   a, dx    [M, K], out, dy [M, N]: rows grouped by expert, sizes int32 [E] as above
  *   w        [E, N, K]; dw [E, N, K] in dw_dtype: dtype, or GEG_F32
  *   zero_rest  0: rows past sum(sizes) of out / dx are left untouched; else they are set to 0
- *   workspace  256 bytes (the error word)
+ *   workspace  256 bytes (the error word); with geg_grouped_workspace_bytes(), where it is more,
+ *            products of few tiles and a long contraction cut it into pieces (fp32 sums in
+ *            there, added in a fixed order): direction 0 forward, 1 dgrad, 2 wgrad
  *   opts     force_path 0 by size, 2 tiles of 256 x 256 results, 5 tiles of 128 x 128, 4 (forward)
  *            the narrow kernel; kernel_events as usual
  * Every tensor 16-byte aligned; K % 8 == 0, for the gradients N % 8 == 0, and 256 rows of N or
@@ -516,6 +518,7 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
  * summed in fp32, rounded once to nearest even. dW of an expert without rows is 0, for M == 0
  * all of it. No tensor may overlap another. Deterministic.
  */
+size_t geg_grouped_workspace_bytes(int32_t direction, int64_t M, int64_t N, int64_t K, int32_t E);
 geg_status geg_grouped_gemm(const void* a, const int32_t* sizes, const void* w, void* out, int32_t dtype, int64_t M,
                             int64_t N, int64_t K, int32_t E, int32_t zero_rest, void* workspace, size_t workspace_bytes,
                             const geg_opts* opts, hipStream_t stream);

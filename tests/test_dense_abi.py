@@ -45,6 +45,16 @@ def test_refusals(name):
     assert c(N=65536, K=65536) not in passes
 
 
+def test_workspace_bytes():
+    need = L().geg_grouped_workspace_bytes
+    assert need(0, 8192, 2048, 4096, 8) == 256 and need(2, 100, 64, 64, 4) == 256
+    # 3 tiles at most, the contraction in 8 pieces
+    assert need(0, 100, 128, 4096, 2) == 256 + 3 * 8 * 65536 and need(1, 100, 4096, 128, 2) == 256 + 3 * 8 * 65536
+    assert need(2, 2100, 128, 256, 1) == 256 + 2 * 4 * 65536
+    assert need(3, 1, 1, 8, 1) == 0 and need(-1, 1, 1, 8, 1) == 0 and need(0, -1, 8, 8, 1) == 0 and need(0, 1, 8, 8, 0) == 0
+    assert need(0, 1 << 31, 8, 8, 1) == 0 and need(0, 1, 1 << 40, 8, 1) == 0 and need(0, 0, 8, 4096, 1) == 256
+
+
 def test_empty_batches():
     for name in NAMES[:2]:
         assert _call(name, M=0, p=None, q=None, sizes=None, out=None, ws=None) == 0

@@ -115,6 +115,34 @@ def test_forward_odd_widths(geg, N):
         _check(geg.grouped_gemm(a, sz, w, opts=geg.Opts(path, 0)), ref, mag, 136, f"path {path}")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_contraction_in_pieces(geg, dtype):
+    import torch
+    log(f"case: 16-bit products {dtype}, few tiles and a long contraction")
+    o, few = geg.Opts(5, 0), geg.Opts(5, 0, None, 8)
+    for sizes, N, K in (([100, 0, 130], 200, 4104), ([1, 2], 257, 8200), ([5, 300, 0, 1], 72, 2104), ([140], 8, 2048)):
+        a, _, w, sz = _case(dtype, sizes, N, K, seed=N + K, extra=3)
+        assert geg.lib().geg_grouped_workspace_bytes(0, sum(sizes) + 3, N, K, len(sizes)) > 256
+        a[sum(sizes):] = float("nan")
+        got = geg.grouped_gemm(a, sz, w, opts=o, zero_rest=True, check_errors=True)
+        assert (got[sum(sizes):] == 0).all()
+        _check(got[:sum(sizes)], *_ref(a[:sum(sizes)], w, sizes, "forward"), K, f"forward {sizes}")
+        assert torch.equal(geg.grouped_gemm(a, sz, w, opts=few, zero_rest=True), got)
+    for sizes, N, K in (([100, 0, 130], 4104, 200), ([1, 2], 8200, 264), ([5, 300, 0, 1], 2104, 72)):
+        _, dy, w, sz = _case(dtype, sizes, N, K, seed=N + K)
+        assert geg.lib().geg_grouped_workspace_bytes(1, sum(sizes), N, K, len(sizes)) > 256
+        got = geg.grouped_dgrad(dy, sz, w, opts=o)
+        _check(got, *_ref(dy, w, sizes, "dgrad"), N, f"dgrad {sizes}")
+        assert torch.equal(geg.grouped_dgrad(dy, sz, w, opts=few), got)
+    for sizes, N, K in (([6100, 0, 300], 264, 136), ([2030, 2200], 8, 520), ([5001], 128, 256)):
+        a, dy, _, sz = _case(dtype, sizes, N, K, seed=N + K)
+        assert geg.lib().geg_grouped_workspace_bytes(2, sum(sizes), N, K, len(sizes)) > 256
+        for out in (None, torch.float32):
+            got = geg.grouped_wgrad(dy, a, sz, dtype=out, opts=o)
+            _check(got, *_ref(dy, a, sizes, "wgrad"), max(sizes), f"wgrad {sizes}")
+            assert torch.equal(geg.grouped_wgrad(dy, a, sz, dtype=out, opts=few), got)
+
+
 def test_many_rounds_per_workgroup(geg):
     import torch
     log("case: 16-bit products on 8 compute units")
