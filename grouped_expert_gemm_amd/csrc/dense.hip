@@ -549,7 +549,7 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
 // For few tiles, and few rows per expert (the rule and both sides' times: dense_small()). A stage is
 // one quadrant of the above, in a ring of four sets of buffers, three under way while one is used;
 // one barrier per stage. Alone on its CU it is bound by the loads' latency, 0.4 us per stage of 64
-// (a stage of 256 x 256: 0.86, the matrix rate), with many tiles by the weights: 128 experts of
+// (a stage of 256 x 256: 1.24), with many tiles by the weights: 128 experts of
 // 1536 x 2048, one row each, 805 MB in 134 us, 6.0 TB/s.
 // SPLIT: so few tiles that each tile's contraction is cut into g.split pieces for workgroups of their own; the
 // fp32 sums go to the workspace, in the order that the lanes hold them, and a second launch adds the
