@@ -510,7 +510,8 @@ geg_status gmxfp4_moe_layer(const void* x, const int32_t* topk_ids, const float*
  *   zero_rest  0: rows past sum(sizes) of out / dx are left untouched; else they are set to 0
  *   workspace  256 bytes (the error word); with geg_grouped_workspace_bytes(), where it is more,
  *            products of few tiles and a long contraction cut it into pieces (fp32 sums in
- *            there, added in a fixed order): direction 0 forward, 1 dgrad, 2 wgrad
+ *            there, added in a fixed order; the last bit may differ from that of a call
+ *            with less): direction 0 forward, 1 dgrad, 2 wgrad
  *   opts     force_path 0 by size, 2 tiles of 256 x 256 results, 5 tiles of 128 x 128, 4 (forward)
  *            the narrow kernel; kernel_events as usual
  * Every tensor 16-byte aligned; K % 8 == 0, for the gradients N % 8 == 0, and 256 rows of N or
@@ -541,7 +542,8 @@ geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes
  *            filled up with zeros; L <= 32768
  *   scales   fp32 [L], or NULL for ones
  *   out      [M, N], rows ldo apart; may be y itself (same pitch), not x
- *   workspace: geg_request_lora_workspace_bytes(M, K, L, r) bytes
+ *   workspace: geg_request_lora_workspace_bytes(M, K, L, r) bytes (its first 256: the error word)
+ * ceil(M / 32) + L at most 2^19, times ceil(N / 256) at most 2^23.
  * N, K and the pitches are multiples of 8, every tensor is 16-byte aligned. Sums run in fp32;
  * x A^T keeps at least 16 significant bits on its way into the second product; one rounding.
  * An adapter's values reach only the rows that name it. Rows routed to experts with
