@@ -1261,18 +1261,15 @@ geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes
                       workspace_bytes, opts, stream);
 }
 
-// Workspace of the request adapters: the header, the units and the rows in their order (batches past
-// kRequestScan), x A^T.
+// Workspace of the request adapters: the header, the units and the rows in their order, x A^T.
 struct RequestLayout {
   size_t units, rows, u, total;
 };
 static RequestLayout request_layout(int64_t M, int64_t K, int32_t L, int32_t r) {
   RequestLayout w{};
-  w.units = w.rows = w.u = kHeader;
-  if (M > geg::kRequestScan) {
-    w.rows = w.units + round256((size_t)(geg::request_units(M, L, r) + 1) * 16);   // (their number first)
-    w.u = w.rows + round256((size_t)M * 4);
-  }
+  w.units = kHeader;
+  w.rows = w.units + round256((size_t)(geg::request_units(M, L, r, false) + 1) * 16);   // (their number first)
+  w.u = w.rows + round256((size_t)M * 4);
   w.total = w.u + round256((size_t)geg::request_splits(M, K, r) * (size_t)M * (size_t)r * 4);
   return w;
 }
@@ -1300,7 +1297,8 @@ geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t l
     return fail(GEG_ERR_BAD_SHAPE, "256 rows of 16-bit values, pitch included, must fit in 0x7FFFFFF0 bytes");
   // a launch holds fewer than 2^32 threads: a workgroup of 256 per unit and at most 16 ranges of K, or
   // per unit and four to 32 chunks of 64 columns
-  const int64_t units = geg::request_units(M, L, r);
+  const bool scan = geg::request_scan(M, N);
+  const int64_t units = geg::request_units(M, L, r, scan);
   if (units > (int64_t)1 << 19 || units * ((N + 255) / 256) > (int64_t)1 << 23)
     return fail(GEG_ERR_BAD_SHAPE, "ceil(M / 32) + L must not exceed 2^19, times ceil(N / 256) 2^23");
   if (M == 0) return GEG_OK;
@@ -1324,7 +1322,7 @@ geg_status geg_request_lora(const void* y, int64_t ldy, const void* x, int64_t l
   geg::RequestArgs g{reinterpret_cast<const uint16_t*>(y), reinterpret_cast<const uint16_t*>(x), ids,
                      reinterpret_cast<const uint16_t*>(lora_a), reinterpret_cast<const uint16_t*>(lora_b), scales,
                      reinterpret_cast<uint16_t*>(out), reinterpret_cast<float*>(wsb + w.u),
-                     M > geg::kRequestScan ? reinterpret_cast<int32_t*>(wsb + w.units) + 4 : nullptr,
+                     scan ? nullptr : reinterpret_cast<int32_t*>(wsb + w.units) + 4,
                      reinterpret_cast<int32_t*>(wsb + w.units), reinterpret_cast<int32_t*>(wsb + w.rows),
                      // a single row has no pitch
                      M == 1 ? N : ldy, M == 1 ? K : ldx, M == 1 ? N : ldo, M, N, K, L, r,

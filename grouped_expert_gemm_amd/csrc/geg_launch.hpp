@@ -208,7 +208,11 @@ hipError_t launch_dense_narrow(int dtype, const DenseArgs& g, int cus, hipStream
 // Low-rank adapters of many requests beside a shared projection (see request.hip).
 constexpr int kRequestMaxRank = 128;
 constexpr int kRequestMaxAdapters = 32768;   // counters in LDS
-constexpr int kRequestScan = 128;   // rows up to which the units come from the ids directly
+constexpr int kRequestScan = 256;   // rows up to which the units may come from the ids directly,
+// with a workgroup per row and 256 columns, most of which find nothing to do. Measured (us, from the
+// ids, listed by a launch before; L, r, K, N, rows): 32, 16, 4096, 4096, 96 10, 15; 256 13, 16; 64, 32, 2048,
+// 2048, 256 13, 18; 8, 64, 4096, 14336, 96 23, 24; 128 27, 25; 192 31, 27; 256 38, 28.
+inline bool request_scan(int64_t M, int64_t N) { return M <= kRequestScan && M * ((N + 255) / 256) <= 6144; }
 struct RequestArgs {
   const uint16_t* y;      // [M, N], rows ldy apart, or NULL: zeros
   const uint16_t* x;      // [M, K], rows ldx apart
@@ -226,7 +230,7 @@ struct RequestArgs {
   uint32_t* err;
 };
 int request_splits(int64_t M, int64_t K, int32_t r);
-int64_t request_units(int64_t M, int32_t L, int32_t r);
+int64_t request_units(int64_t M, int32_t L, int32_t r, bool scan);
 hipError_t launch_request_lora(const RequestArgs& g, int dtype, int cus, hipStream_t s);
 // Dropout: out = [res +] keep ? x * scale : 0 for n values (see dropout.hip, philox.hpp).
 // bits: the mask [n / 8] too, a bit per value (bf16, n % 8 == 0, no residual, aligned), or NULL.

@@ -5,9 +5,9 @@
 // batch: an adapter's bytes are then read once per unit, and a value of another row's adapter
 // cannot reach a row. Two products follow each other in two launches, u = x A^T and the rest.
 //
-// Up to kRequestScan rows the units come from the ids directly: a workgroup is started for every
-// row, and works if its row is the first, or the 17th, ... that names its adapter (ballots over
-// the ids, a few instructions). Larger batches get a launch before that lists the units.
+// In small batches (request_scan()) the units come from the ids directly: a workgroup is started for
+// every row, and works if its row is the first, or the 17th, ... that names its adapter (ballots over
+// the ids, a few instructions). Others get a launch before that lists the units.
 #include <algorithm>
 
 #include "geg_device.hpp"
@@ -177,24 +177,41 @@ struct Unit {
       }
       return;
     }
+    constexpr int kWords = kRequestScan / 64;
     const int M = (int)g.M;
-    const int raw0 = lane < M ? g.ids[lane] : -1, raw1 = lane + 64 < M ? g.ids[lane + 64] : -1;
-    if (flag && (raw0 >= g.L || raw1 >= g.L)) atomicOr(g.err, kErrBadExpertId);
-    const int id0 = named(raw0, g.L), id1 = named(raw1, g.L);
-    id = unit < 64 ? __builtin_amdgcn_readlane(id0, unit) : __builtin_amdgcn_readlane(id1, unit - 64);
-    const uint64_t m0 = __ballot(lane < M && id0 == id), m1 = __ballot(lane + 64 < M && id1 == id);
-    // this lane's two rows' places among those of the adapter, and the unit's first row's
+    int ids[kWords];   // of rows 64 w + lane
+    bool bad = false;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const int raw = 64 * w + lane < M ? g.ids[64 * w + lane] : -1;
+      bad |= raw >= g.L;
+      ids[w] = named(raw, g.L);
+    }
+    if (flag && bad) atomicOr(g.err, kErrBadExpertId);
+    id = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+      if (unit >> 6 == w) id = __builtin_amdgcn_readlane(ids[w], unit & 63);
+    // the places of the unit's first row and of this lane's among the adapter's
     const uint64_t below = (1ull << lane) - 1;
-    const int c0 = __builtin_popcountll(m0);
-    const int p0 = __builtin_popcountll(m0 & below), p1 = c0 + __builtin_popcountll(m1 & below);
-    const int all = c0 + __builtin_popcountll(m1);
-    const int at = unit < 64 ? __builtin_popcountll(m0 & ((1ull << unit) - 1))
-                             : c0 + __builtin_popcountll(m1 & ((1ull << (unit - 64)) - 1));
+    uint64_t m[kWords];
+    int all = 0, at = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      m[w] = __ballot(64 * w + lane < M && ids[w] == id);
+      if (unit >> 6 == w) at = all + __builtin_popcountll(m[w] & ((1ull << (unit & 63)) - 1));
+      all += __builtin_popcountll(m[w]);
+    }
     n = at % (16 * RB) == 0 ? min(16 * RB, all - at) : 0;
     if (n == 0) return;
     // (every wavefront writes the same words)
-    if (((m0 >> lane) & 1) && p0 >= at && p0 < at + n) pick[p0 - at] = lane;
-    if (((m1 >> lane) & 1) && p1 >= at && p1 < at + n) pick[p1 - at] = lane + 64;
+    int place = -at;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const int mine = place + (int)__builtin_popcountll(m[w] & below);
+      if (((m[w] >> lane) & 1) && mine >= 0 && mine < n) pick[mine] = 64 * w + lane;
+      place += __builtin_popcountll(m[w]);
+    }
     __syncthreads();
 #pragma unroll
     for (int b = 0; b < RB; ++b) {
@@ -275,7 +292,7 @@ __global__ __launch_bounds__(kThreads) void request_down_kernel(RequestArgs g) {
 
 // ------------------------------------------------------------------ out = y + s u B^T
 // out[t, n] = y[t, n] + sum_j (s_i u[t, j]) B_i[n, j]. The work is (unit, 4 chunks of 64 columns, one
-// per wavefront): one of these to a workgroup for batches of kRequestScan rows, equal runs of them to
+// per wavefront): one of these to a workgroup where the units come from the ids, equal runs of them to
 // two workgroups per CU for others, so that a unit's start (its rows, the parts of u) is paid once per
 // run and no second round of workgroups is half empty. Bound by y and out: 8000 rows of 14336
 // columns, fp16, rank 64, read and write 459 MB in 116 to 125 us, 3.8 TB/s (a copy of 1 GiB: 5.2);
@@ -554,7 +571,7 @@ __global__ __launch_bounds__(kThreads, 2) void request_up_kernel(RequestArgs g, 
 
 template <int T, int RB, int NCB, int NB, bool PACK>
 hipError_t request_one(const RequestArgs& g, int cus, hipStream_t s) {
-  const int64_t units = request_units(g.M, g.L, g.r);
+  const int64_t units = request_units(g.M, g.L, g.r, !g.units);
   hipLaunchKernelGGL((request_down_kernel<T, RB, NCB>), dim3((unsigned)(units * g.splits)), dim3(kThreads), 0, s, g);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -568,12 +585,12 @@ hipError_t request_one(const RequestArgs& g, int cus, hipStream_t s) {
 
 // Rows of a unit, in blocks of 16: more rows read an adapter's bytes less often, a small batch has
 // few rows per adapter.
-int request_rows(int64_t M, int32_t r) { return M <= kRequestScan ? 1 : (r > 64 ? 2 : 4); }
+int request_rows(int32_t r, bool scan) { return scan ? 1 : (r > 64 ? 2 : 4); }
 
 // An upper bound of a batch's units.
-int64_t request_units(int64_t M, int32_t L, int32_t r) {
-  if (M <= kRequestScan) return M;
-  const int rows = 16 * request_rows(M, r);
+int64_t request_units(int64_t M, int32_t L, int32_t r, bool scan) {
+  if (scan) return M;
+  const int rows = 16 * request_rows(r, scan);
   return (M + rows - 1) / rows + std::min<int64_t>((int64_t)L + 1, M);
 }
 
@@ -582,13 +599,13 @@ int64_t request_units(int64_t M, int32_t L, int32_t r) {
 // per wavefront, for the second product reads every range's sums again (96 rows, 4096 x 4096,
 // rank 16: 16, 8, 4 ranges 4.5 + 8.6, 4.9 + 6.8, 5.1 + 5.6 us).
 int request_splits(int64_t M, int64_t K, int32_t r) {
-  const int rows = 16 * request_rows(M, r);
+  const int rows = 16 * request_rows(r, M <= kRequestScan / 2);
   const int64_t blocks = (M + rows - 1) / rows, steps = (K + 31) / 32;
   return (int)std::max<int64_t>(1, std::min<int64_t>({512 / std::max<int64_t>(blocks, 1), steps / (8 * kWaves), 16}));
 }
 
 hipError_t launch_request_lora(const RequestArgs& g, int dtype, int cus, hipStream_t s) {
-  const int rb = request_rows(g.M, g.r), ncb = (g.r + 15) / 16;
+  const int rb = request_rows(g.r, !g.units), ncb = (g.r + 15) / 16;
   if (g.units) {
     const size_t bytes = ((size_t)g.L + 1) * 4;
     if (bytes > (48u << 10)) {

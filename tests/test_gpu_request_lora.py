@@ -71,9 +71,10 @@ def _check(got, ref, tol, what):
     (1, 8, 8, 1, 8, True), (1, 2048, 1024, 8, 16, True), (5, 264, 72, 3, 24, True), (17, 4096, 200, 40, 64, True),
     (96, 1000, 520, 32, 128, True), (300, 512, 64, 7, 40, False), (513, 136, 264, 5, 16, False), (700, 72, 136, 300, 32, True),
     (1025, 320, 328, 6, 104, False), (640, 256, 96, 4, 72, True),
-    # both sides of the row count past which the units are listed; runs of work that pass from unit to
+    # both sides of the rule by which the units are listed; runs of work that pass from unit to
     # unit; counters of every adapter past 48 KB
-    (128, 128, 776, 40, 16, True), (129, 264, 4104, 5, 64, True), (1500, 64, 2056, 3, 128, False),
+    (128, 128, 776, 40, 16, True), (129, 264, 4104, 5, 64, True), (256, 72, 520, 9, 40, True), (257, 72, 520, 9, 40, True),
+    (100, 64, 16392, 5, 32, True), (200, 64, 16392, 70, 128, True), (1500, 64, 2056, 3, 128, False),
     (900, 40, 16392, 2, 24, False), (20000, 8, 8, 32768, 8, True)])
 def test_shapes(geg, dtype, M, K, N, L, r, mixed):
     log(f"case: request adapters {dtype} M={M} K={K} N={N} L={L} r={r} mixed={mixed}")
@@ -103,7 +104,7 @@ def test_rows_without_an_adapter_and_in_place(geg):
 def test_one_adapter_and_all_different(geg):
     import torch
     log("case: request adapters, every row the same and every row another")
-    for M in (128, 1000):
+    for M in (128, 256, 1000):
         y, x, _, A, B, scales = _case("bf16", M, 64, 72, M, 8, seed=9)
         for ids in (torch.zeros(M), torch.arange(M), torch.arange(M).flip(0), torch.full((M,), M - 1)):
             ids = ids.to(torch.int32).cuda()
@@ -113,7 +114,7 @@ def test_one_adapter_and_all_different(geg):
 def test_ids_out_of_range(geg):
     import torch
     log("case: request adapters, ids past L")
-    for M, row in ((33, 20), (128, 127), (300, 299)):
+    for M, row in ((33, 20), (128, 127), (256, 255), (300, 299)):
         y, x, ids, A, B, scales = _case("bf16", M, 64, 64, 3, 8, seed=2)
         ids[row] = 3
         with pytest.raises(geg.GegDeviceError) as e:

@@ -40,10 +40,10 @@ def test_request_refusals():
     assert _req(out=P, ldo=72) == 8 and _req(out=P) not in passes  # in place: one pitch
     assert _req(ws=None) == 5 and _req(ws=P + 16) == 5
     need = L().geg_request_lora_workspace_bytes(4, 128, 3, 16)
-    assert need == 256 + 256      # one range of the contraction
+    # 5 units at most and their number, the rows in the units' order, one range of the contraction
+    assert need == 256 + 256 + 256 + 256
     assert _req(nbytes=need - 1) == 5 and _req(nbytes=need) not in passes
     assert L().geg_request_lora_workspace_bytes(4, 128, 3, 136) == 0
-    # past 128 rows: 5 units at most and their number, and the rows in the units' order
     assert L().geg_request_lora_workspace_bytes(200, 128, 1, 16) == 256 + 256 + 1024 + 200 * 64
 
 
