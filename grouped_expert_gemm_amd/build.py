@@ -18,8 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgeg.so")
 
-SOURCES = ["geg.cpp", "skinny.hip", "tile.hip", "util.hip", "vec.hip", "narrow.hip", "route.hip", "w4a8.hip", "lora.hip",
-           "noalloc.hip", "mxfp4.hip", "gate.hip", "moe.hip", "w4a4.hip",
+SOURCES = ["geg.cpp", "skinny.hip", "tile.hip", "tile_masked.hip", "util.hip", "vec.hip", "narrow.hip", "route.hip", "w4a8.hip",
+           "lora.hip", "noalloc.hip", "mxfp4.hip", "gate.hip", "moe.hip", "w4a4.hip",
            "dense.hip", "request.hip", "dropout.hip"]
 ARCH = "gfx950"
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

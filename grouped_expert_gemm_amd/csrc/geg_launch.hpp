@@ -93,6 +93,7 @@ hipError_t launch_vec(int fmt, const GemmArgs& g, int cus, hipStream_t s);      
 hipError_t launch_narrow(int fmt, const GemmArgs& g, int cus, hipStream_t s);   // sizes its own grid
 hipError_t launch_tile(int fmt, const GemmArgs& g, int grid, hipStream_t s);
 hipError_t launch_tile_dgrad(int fmt, const GemmArgs& g, int grid, hipStream_t s);
+hipError_t launch_tile_dgrad_masked(int fmt, const GemmArgs& g, int grid, hipStream_t s);   // with g.lora_mask
 // After a tiled launch with tail_split > 1 (same arguments and grid): sums the
 // partials of the split remainder tiles into `out` (exits when nothing was split).
 hipError_t launch_tile_fixup(const GemmArgs& g, bool dgrad, int tile_grid, hipStream_t s);

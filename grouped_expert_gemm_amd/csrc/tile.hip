@@ -587,8 +587,9 @@ __device__ __forceinline__ void lora_block(const Split8& u, const Split8& q, f32
   }
 }
 
-// DROP (dgrad): the adapter delta is masked by g.lora_mask. An instantiation of its own: the others
-// keep their registers.
+// DROP (dgrad): the adapter delta is masked by g.lora_mask. Compiled in a unit of its own
+// (tile_masked.hip): instantiated beside the plain ones it changes how the compiler treats what they
+// share, and those spill 4 to 8 registers more each (MXFP4 dgrad: 0 -> 4, NF4 dgrad: 76 -> 83).
 template <Fmt F, bool DG, bool TAIL, bool DROP>
 __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(GemmArgs g) {
   __shared__ int32_t p_off[kMaxExperts + 1];
@@ -935,6 +936,7 @@ __global__ __launch_bounds__(kTileThreads, 1) void tile_kernel(GemmArgs g) {
   }
 }
 
+#ifndef GEG_TILE_MASKED
 // Split class-1 tiles (see tile_kernel): out = bf16 of the S pieces' partial
 // sums added in piece order; with the gated epilogue, of silu(gate) * up over
 // the column pairs (2c, 2c + 1). Recomputes the tiled kernel's plan and split
@@ -1002,8 +1004,27 @@ __global__ __launch_bounds__(kThreads) void tile_fixup_kernel(GemmArgs g, int dg
   }
 }
 
+#endif
+
+template <Fmt F, bool DG, bool TAIL, bool DROP>
+hipError_t launch_tile_t(const GemmArgs& g, int grid, hipStream_t s) {
+  hipLaunchKernelGGL((tile_kernel<F, DG, TAIL, DROP>), dim3(grid), dim3(kTileThreads), 0, s, g);
+  return hipGetLastError();
+}
+
+template <bool DROP>
+hipError_t launch_dgrad_t(int fmt, const GemmArgs& g, int grid, hipStream_t s) {
+  if (fmt == MXFP4) {
+    if (g.N % BK) return launch_tile_t<MXFP4, true, true, DROP>(g, grid, s);
+    return launch_tile_t<MXFP4, true, false, DROP>(g, grid, s);
+  }
+  if (g.N % BK) return launch_tile_t<NF4, true, true, DROP>(g, grid, s);
+  return launch_tile_t<NF4, true, false, DROP>(g, grid, s);
+}
+
 }  // namespace
 
+#ifndef GEG_TILE_MASKED
 hipError_t launch_tile_fixup(const GemmArgs& g, bool dgrad, int tile_grid, hipStream_t s) {
   // at most tile_grid split tiles of 16 work items each; two workgroups per CU
   const int grid = std::max(1, 2 * tile_grid);
@@ -1011,31 +1032,19 @@ hipError_t launch_tile_fixup(const GemmArgs& g, bool dgrad, int tile_grid, hipSt
   return hipGetLastError();
 }
 
-template <Fmt F, bool DG, bool TAIL>
-hipError_t launch_tile_t(const GemmArgs& g, int grid, hipStream_t s) {
-  if constexpr (DG) {
-    if (g.lora_mask) {
-      hipLaunchKernelGGL((tile_kernel<F, DG, TAIL, true>), dim3(grid), dim3(kTileThreads), 0, s, g);
-      return hipGetLastError();
-    }
-  }
-  hipLaunchKernelGGL((tile_kernel<F, DG, TAIL, false>), dim3(grid), dim3(kTileThreads), 0, s, g);
-  return hipGetLastError();
-}
-
 hipError_t launch_tile(int fmt, const GemmArgs& g, int grid, hipStream_t s) {
-  if (fmt == NF4) return launch_tile_t<NF4, false, false>(g, grid, s);
-  if (g.K % BK) return launch_tile_t<MXFP4, false, true>(g, grid, s);
-  return launch_tile_t<MXFP4, false, false>(g, grid, s);
+  if (fmt == NF4) return launch_tile_t<NF4, false, false, false>(g, grid, s);
+  if (g.K % BK) return launch_tile_t<MXFP4, false, true, false>(g, grid, s);
+  return launch_tile_t<MXFP4, false, false, false>(g, grid, s);
 }
 
 hipError_t launch_tile_dgrad(int fmt, const GemmArgs& g, int grid, hipStream_t s) {
-  if (fmt == MXFP4) {
-    if (g.N % BK) return launch_tile_t<MXFP4, true, true>(g, grid, s);
-    return launch_tile_t<MXFP4, true, false>(g, grid, s);
-  }
-  if (g.N % BK) return launch_tile_t<NF4, true, true>(g, grid, s);
-  return launch_tile_t<NF4, true, false>(g, grid, s);
+  return g.lora_mask ? launch_tile_dgrad_masked(fmt, g, grid, s) : launch_dgrad_t<false>(fmt, g, grid, s);
 }
+#else
+hipError_t launch_tile_dgrad_masked(int fmt, const GemmArgs& g, int grid, hipStream_t s) {
+  return launch_dgrad_t<true>(fmt, g, grid, s);
+}
+#endif
 
 }  // namespace geg
