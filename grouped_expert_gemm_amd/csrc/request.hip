@@ -54,6 +54,13 @@ __device__ __forceinline__ void unpack2(uint32_t v, float& a, float& b) {
   }
 }
 
+// Two 16-bit values, infinities and NaN replaced by 0.
+template <int T>
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+  constexpr uint32_t top = T == kBF16 ? 0x7F80u : 0x7C00u;
+  return ((v & 0x7FFFu) >= top ? 0 : v & 0xFFFFu) | (((v >> 16) & 0x7FFFu) >= top ? 0 : v & 0xFFFF0000u);
+}
+
 // Ids outside [0, L) name no adapter.
 __device__ __forceinline__ int named(int id, int L) { return id >= 0 && id < L ? id : -1; }
 
@@ -350,14 +357,14 @@ __global__ __launch_bounds__(kThreads, 2) void request_up_kernel(RequestArgs g, 
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             v[m][i] *= s;
-            top = fmaxf(top, fabsf(v[m][i]));
+            if (fabsf(v[m][i]) < __builtin_inff()) top = fmaxf(top, fabsf(v[m][i]));   // of the finite ones
           }
         }
         int e = 0;
         if constexpr (T == kF16) {
           top = fmaxf(top, __shfl_xor(top, 16));
           top = fmaxf(top, __shfl_xor(top, 32));
-          if (top > 0.f && top < __builtin_inff()) e = (int)__builtin_amdgcn_frexp_expf(top) - 11;
+          if (top > 0.f) e = (int)__builtin_amdgcn_frexp_expf(top) - 11;
           if (grp == 0) power[16 * b + r16] = e;
         }
 #pragma unroll
@@ -410,10 +417,12 @@ __global__ __launch_bounds__(kThreads, 2) void request_up_kernel(RequestArgs g, 
     uint32_t bat[NB];
 #pragma unroll
     for (int m = 0; m < NB; ++m) bat[m] = oob_unless(slot(m) < 16, (uint32_t)((r16 * g.r + 8 * slot(m)) * 2));
-    auto load_b = [&](int ch, u32x4 (&bf)[NB][4]) {
+    auto b_window = [&](int ch) {
       const int64_t n0 = 64 * (int64_t)ch;
-      const __amdgpu_buffer_rsrc_t B =
-          window(g.b + ((int64_t)u.id * g.N + n0) * g.r, std::min<int64_t>(64, g.N - n0) * g.r * 2);
+      return window(g.b + ((int64_t)u.id * g.N + n0) * g.r, std::min<int64_t>(64, g.N - n0) * g.r * 2);
+    };
+    auto load_b = [&](int ch, u32x4 (&bf)[NB][4]) {
+      const __amdgpu_buffer_rsrc_t B = b_window(ch);
 #pragma unroll
       for (int m = 0; m < NB; ++m)
 #pragma unroll
@@ -431,7 +440,7 @@ __global__ __launch_bounds__(kThreads, 2) void request_up_kernel(RequestArgs g, 
       if (all || (((live >> (2 * b + h)) & 1) && n < g.N))
         __builtin_nontemporal_store(o, reinterpret_cast<u32x4*>(g.out + row[b][h] * g.ldo + n));
     };
-    auto product = [&](const u32x4 (&bf)[NB][4], int b, float (&d)[2][8]) {
+    auto product = [&](int ch, const u32x4 (&bf)[NB][4], int b, float (&d)[2][8]) {
       f32x4 acc[4] = {};
 #pragma unroll
       for (int m = 0; m < NB; ++m) {
@@ -442,6 +451,34 @@ __global__ __launch_bounds__(kThreads, 2) void request_up_kernel(RequestArgs g, 
           const u32x4 rest = parts[b][NB + m][lane];
 #pragma unroll
           for (int j = 0; j < 4; ++j) acc[j] = mfma<T>(bf[m][j], rest, acc[j]);
+        }
+      }
+      // An infinity in B times the second part (0, or of the other sign) makes its column NaN: a product
+      // with a result that is not finite is done again, the infinities beside the first part only.
+      f32x4 z;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        z[i] = __builtin_fmaf(acc[0][i], 0.f, __builtin_fmaf(acc[1][i], 0.f, __builtin_fmaf(acc[2][i], 0.f, acc[3][i] * 0.f)));
+      const float odd = (z[0] + z[1]) + (z[2] + z[3]);   // 0, or NaN
+      if (__builtin_expect(__ballot(odd != odd) != 0, 0)) {
+        const __amdgpu_buffer_rsrc_t B = b_window(ch);   // (read again: kept, B would cost the others registers)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int m = 0; m < NB; ++m) {
+            const u32x4 q = __builtin_amdgcn_raw_buffer_load_b128(B, bat[m] + 32 * j * (uint32_t)g.r, 0, 0);
+            u32x4 f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = finite2<T>(q[i]);
+            if constexpr (PACK) {
+              acc[j] = mfma<T>(grp < pr ? q : f, parts[b][m][lane], acc[j]);
+            } else {
+              acc[j] = mfma<T>(q, parts[b][m][lane], acc[j]);
+              acc[j] = mfma<T>(f, parts[b][NB + m][lane], acc[j]);
+            }
+            __builtin_amdgcn_sched_barrier(0);   // one piece at a time: registers
+          }
         }
       }
 #pragma unroll
@@ -500,7 +537,7 @@ __global__ __launch_bounds__(kThreads, 2) void request_up_kernel(RequestArgs g, 
         for (int b = 0; b < RB; ++b) {
           if (b > 0 && 16 * b >= u.n) continue;
           float d[2][8];
-          product(bf, b, d);
+          product(ch, bf, b, d);
 #pragma unroll
           for (int h = 0; h < 2; ++h) store(ch, b, h, add(y[b][h], d[h]), false);
         }
@@ -525,7 +562,7 @@ __global__ __launch_bounds__(kThreads, 2) void request_up_kernel(RequestArgs g, 
 #pragma unroll
           for (int b = 0; b < RB; ++b) {
             float d[2][8];
-            product(bf, b, d);
+            product(ch, bf, b, d);
 #pragma unroll
             for (int h = 0; h < 2; ++h) store(ch, b, h, add(y[b][h], d[h]), decltype(all)::value);
             load_y(next, b, y);

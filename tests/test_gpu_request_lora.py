@@ -267,3 +267,66 @@ def test_beside_quantised_experts(geg):
     rows = torch.where(own < 0, -1, own * E + expert).to(torch.int32)
     AE, BE = (rand(P * E, r, H) * H ** -0.5).bfloat16(), rand(P * E, N, r).bfloat16()
     _check(geg.request_lora(h, xs, rows, AE, BE), *_ref(h, xs, rows, AE, BE, None), "routed experts")
+
+
+def _by_element(y, x, ids, A, B):
+    """The result in fp64, summed element by element: infinities and NaN go where the definition has them."""
+    import torch
+    out = y.double()
+    for i in range(A.shape[0]):
+        rows = torch.nonzero(ids == i).flatten()
+        u = (x[rows].double()[:, None, :] * A[i].double()[None]).sum(-1)
+        out[rows] += (u[:, None, :] * B[i].double()[None]).sum(-1)
+    return out
+
+
+def _same_places(got, ref, tol, what):
+    """Infinities and NaN in the same places, the rest within the bound."""
+    import torch
+    got = got.double()
+    big = ref.abs().isinf()
+    log(f"  {what}: {int(big.sum())} infinities, {int(ref.isnan().sum())} NaN of {ref.numel()}")
+    assert torch.equal(got.isnan(), ref.isnan()), what
+    assert torch.equal(got[big], ref[big]), what
+    rest = ref.isfinite()
+    assert ((got - ref).abs() <= tol)[rest].all(), what
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("r", [8, 16, 24, 64, 128])
+@pytest.mark.parametrize("M", [30, 530])
+def test_an_infinity_in_an_adapter(geg, dtype, r, M):
+    """u times an infinity is an infinity of u's sign, whatever u's low bits are; a row of u with an
+    infinity keeps its other values."""
+    import torch
+    log(f"case: request adapters {dtype} rank {r}, {M} rows, infinities in an adapter")
+    inf = float("inf")
+    y, x, ids, A, B, _ = _case(dtype, M, 72, 136, 3, r, seed=r + M)
+    ids = ids.clamp(min=0)
+    exact = x.clone()
+    exact[:, 1:] = 0      # u = x[:, 0] A[:, 0]: with A = 1 there, few bits and no second part
+    exact[:, 0] = torch.where(exact[:, 0] == 0, 1, exact[:, 0])
+    ones = A.clone()
+    ones[:, :, 0] = 1
+    for name, x1, A1 in (("u of few bits", exact, ones), ("u of many bits", x, A)):
+        B1 = B.clone()
+        B1[0, 5, 3], B1[0, 70, 0], B1[1, 135, r - 1] = inf, -inf, inf
+        B1[2, 9, 1], B1[2, 9, 2], B1[2, 64, 4] = inf, -inf, float("nan")
+        clean = torch.where(B1.isfinite(), B1, torch.zeros_like(B1))
+        _, tol = _ref(y, x1, ids, A1, clean, None)
+        _same_places(geg.request_lora(y, x1, ids, A1, B1), _by_element(y, x1, ids, A1, B1), tol, name)
+    zero = exact.clone()
+    zero[::2] = 0         # u = 0: times an infinity NaN
+    ref = _by_element(y, zero, ids, ones, B1)
+    assert ref[(ids == 0)][:, 5].isnan().any()
+    _, tol = _ref(y, zero, ids, ones, clean, None)
+    _same_places(geg.request_lora(y, zero, ids, ones, B1), ref, tol, "u of zeros")
+    # u with an infinity and values past 65504 of either sign
+    big, wide = A.clone(), x * 2.0 ** 6
+    big[:, 1:] *= 2.0 ** 12
+    big[1, 0, 3] = inf
+    small = B * 2.0 ** -12
+    ref = _by_element(y, wide, ids, big, small)
+    assert ref[ids == 1].isinf().all()
+    _, tol = _ref(y, wide, ids, torch.where(big.isfinite(), big, torch.zeros_like(big)), small, None)
+    _same_places(geg.request_lora(y, wide, ids, big, small), ref, tol, "an infinity in u")
