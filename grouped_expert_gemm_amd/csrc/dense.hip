@@ -63,6 +63,9 @@ __device__ __forceinline__ int fresh_lane() {
   return l;
 }
 
+// Blocks of d that hold n rows, n up to the largest int32.
+__device__ __forceinline__ int32_t blocks_of(int32_t n, int32_t d) { return (int32_t)(((uint32_t)n + (uint32_t)d - 1) / (uint32_t)d); }
+
 // Rows [row0, M) of a 16-bit matrix set to zero by the whole grid.
 __device__ __forceinline__ void zero_rows(uint16_t* out, int64_t row0, int64_t M, int64_t width) {
   const int64_t n = (M - row0) * width, stride = (int64_t)gridDim.x * blockDim.x;
@@ -124,7 +127,7 @@ struct Tiles {
       const int e = __builtin_amdgcn_readfirstlane(find_expert(p_u, g.E, u, fresh_lane()));
       const int32_t lu = u - __builtin_amdgcn_readfirstlane(p_u[e]);
       const int32_t o0 = __builtin_amdgcn_readfirstlane(p_off[e]), o1 = __builtin_amdgcn_readfirstlane(p_off[e + 1]);
-      const int rblocks = (o1 - o0 + TM - 1) / TM;
+      const int rblocks = blocks_of(o1 - o0, TM);
       const int ct = __builtin_amdgcn_readfirstlane(lu / rblocks), rt = lu - ct * rblocks;   // (vector ALUs)
       x.row0 = o0 + (int64_t)rt * TM;
       x.rows = min(TM, o1 - o0 - rt * TM);
@@ -139,13 +142,13 @@ struct Tiles {
     x.stages = stages_of(x.n);
     return x;
   }
-  static __device__ __forceinline__ int stages_of(int n) { return max(kRing, kRing * ((n + kRing * TK - 1) / (kRing * TK))); }
+  static __device__ __forceinline__ int stages_of(int n) { return max(kRing, kRing * blocks_of(n, kRing * TK)); }
   // Piece `i` of `split` of a tile's contraction, in whole stages.
   __device__ __forceinline__ Tile piece_of(int32_t u, int split) const {
     const int32_t t = __builtin_amdgcn_readfirstlane(u / split);   // (vector ALUs)
     const int i = u - t * split;
     Tile x = tile_of(t);
-    const int len = __builtin_amdgcn_readfirstlane(((x.n + TK - 1) / TK + split - 1) / split) * TK;
+    const int len = __builtin_amdgcn_readfirstlane((blocks_of(x.n, TK) + split - 1) / split) * TK;
     x.k0 = min(i * len, x.n);
     x.n = min(len, x.n - x.k0);
     x.p += x.k0 * (kPAlong ? 1 : g.N);
@@ -349,7 +352,7 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   const int blocks_n = (int)((g.N + TM - 1) / TM), blocks_k = (int)((g.K + TN - 1) / TN);
   const int c_tiles = (int)((O + TN - 1) / TN);
   int32_t total = build_plan(p_off, p_u, g.sizes, g.E, g.M, g.err,
-                             [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : (s + TM - 1) / TM * c_tiles; });
+                             [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : blocks_of(s, TM) * c_tiles; });
   total = D == kDenseWgrad ? g.E * blocks_n * blocks_k : __builtin_amdgcn_readfirstlane(total);
   if constexpr (D != kDenseWgrad) {
     if (g.zero_rest) zero_rows((uint16_t*)g.out, p_off[g.E], g.M, O);
@@ -516,7 +519,7 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
         for (int j = 0; j < 4; ++j) acc[h][v][i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (;;) {
     begin();
-    int real = (cur.n + TK - 1) / TK;
+    int real = blocks_of(cur.n, TK);
     auto second = [&]() {   // the products of a pair's second stage
       real -= 2;
       on = __builtin_amdgcn_readfirstlane(real < 0 ? 0 : on);
@@ -570,7 +573,7 @@ __global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
   const int blocks_n = (int)((g.N + TM - 1) / TM), blocks_k = (int)((g.K + TN - 1) / TN);
   const int c_tiles = (int)((O + TN - 1) / TN);
   int32_t total = build_plan(p_off, p_u, g.sizes, g.E, g.M, g.err,
-                             [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : (s + TM - 1) / TM * c_tiles; });
+                             [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : blocks_of(s, TM) * c_tiles; });
   total = D == kDenseWgrad ? g.E * blocks_n * blocks_k : __builtin_amdgcn_readfirstlane(total);
   if constexpr (D != kDenseWgrad) {
     if (g.zero_rest) zero_rows((uint16_t*)g.out, p_off[g.E], g.M, O);
@@ -647,7 +650,7 @@ __global__ __launch_bounds__(TThreads, 1) void dense_small_kernel(DenseArgs g) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     const int want = __builtin_amdgcn_readfirstlane((int)(32 * wm < cur.rows && 64 * wn < cur.cols));
-    int real = (cur.n + TK - 1) / TK;   // stages with products
+    int real = blocks_of(cur.n, TK);   // stages with products
     auto due = [&]() {
       on = __builtin_amdgcn_readfirstlane(real > 0 ? want : 0);
       --real;
@@ -702,7 +705,7 @@ __global__ __launch_bounds__(TThreads) void dense_join_kernel(DenseArgs g) {
   const int blocks_n = (int)((g.N + TM - 1) / TM), blocks_k = (int)((g.K + TN - 1) / TN);
   const int c_tiles = (int)((O + TN - 1) / TN);
   int32_t total = build_plan(p_off, p_u, g.sizes, g.E, g.M, g.err,
-                             [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : (s + TM - 1) / TM * c_tiles; });
+                             [&](int32_t s) -> int32_t { return D == kDenseWgrad ? 0 : blocks_of(s, TM) * c_tiles; });
   total = D == kDenseWgrad ? g.E * blocks_n * blocks_k : __builtin_amdgcn_readfirstlane(total);
   const W w{g, lane, wave, p_off, p_u, D == kDenseDgrad ? g.N : g.K, O, blocks_n, blocks_k};
   for (int32_t u = blockIdx.x; u < total; u += gridDim.x) {
@@ -734,7 +737,7 @@ __global__ __launch_bounds__(NThreads) void dense_narrow_kernel(DenseArgs g) {
   const int64_t K = g.K, N = g.N;
   const int nblk = (int)((N + 15) / 16);
   const int32_t total = __builtin_amdgcn_readfirstlane(build_plan(
-      p_off, p_u, g.sizes, g.E, g.M, g.err, [&](int32_t s) -> int32_t { return (s + 15) / 16 * nblk; }));
+      p_off, p_u, g.sizes, g.E, g.M, g.err, [&](int32_t s) -> int32_t { return blocks_of(s, 16) * nblk; }));
   if (g.zero_rest) zero_rows((uint16_t*)g.out, p_off[g.E], g.M, N);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);

@@ -448,3 +448,31 @@ def test_training_layer(geg):
         off = ((got.detach().double().cpu() - want.detach()).abs().max() / want.detach().abs().max()).item()
         log(f"  {what}: {off:.2e} of the largest value")
         assert off <= 12 * 2.0 ** -8, what
+
+
+def test_an_expert_of_nearly_2_31_rows(geg):
+    """Rows past 2^31 - 256 in one expert, where a count of its tiles no longer fits the sum of the rows
+    and a tile less one."""
+    import torch
+    log("case: 16-bit products with one expert of 2^31 - 100 rows")
+    t, M = torch.bfloat16, (1 << 31) - 100
+    rows = torch.cat([torch.arange(0, 50), torch.arange(1 << 30, (1 << 30) + 50), torch.arange(M - 300, M)]).cuda()
+    a = torch.zeros(M, 8, dtype=t, device="cuda")
+    a[rows] = torch.randn(len(rows), 8, device="cuda").to(t)
+    w, sz = torch.randn(2, 8, 8, device="cuda").to(t), torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    x = a[rows]
+    out = torch.empty(M, 8, dtype=t, device="cuda")
+    n = len(rows)
+    ref, mag = _ref(x, w, [0, n], "forward")
+    for path in (0, 4, 5):
+        out.fill_(float("nan"))
+        geg.grouped_gemm(a, sz, w, out=out, opts=geg.Opts(path, 0), check_errors=True)
+        _check(out[rows], ref, mag, 8, f"forward path {path}")
+    ref, mag = _ref(x, w, [0, n], "dgrad")
+    for path in (0, 5):
+        out.fill_(float("nan"))
+        geg.grouped_dgrad(a, sz, w, dx=out, opts=geg.Opts(path, 0), check_errors=True)
+        _check(out[rows], ref, mag, 8, f"dgrad path {path}")
+    # the zeros between are exact; the three blocks of rows pass at most 20 instructions and 8 pieces
+    _check(geg.grouped_wgrad(a, out, sz, dtype=torch.float32, check_errors=True), *_ref(x, out[rows], [0, n], "wgrad"), 28 * 32,
+           "wgrad")
