@@ -528,13 +528,14 @@ def _check_lora(x, sizes, lora_a, lora_b):
     return M, N, K, E, r
 
 
-def _lora_call(name, dropout):
-    """The entry point of an adapter call and what dropout = (p, seed, offset) adds to its arguments."""
+def _lora_call(name, dropout, x):
+    """The entry point of an adapter call and what dropout = (p, seed, offset) of x adds to its arguments."""
     if dropout is None:
         return getattr(lib(), name), lib().geg_lora_workspace_bytes, ()
     p, seed, offset = dropout
     seed, offset, rng = _seed(seed, offset)
-    _require_gpu(rng)
+    if rng is not None:
+        _on_device(x, rng)
     return (getattr(lib(), name + "_dropout"), lib().geg_lora_dropout_workspace_bytes, (float(p), seed, offset, _ptr(rng)))
 
 
@@ -543,6 +544,7 @@ def _gemm_lora(fmt, a, sizes, w, scales, lora_a, lora_b, scale, out, u, workspac
     import torch
     M, N, K, E, r = _check_lora(a, sizes, lora_a, lora_b)
     _check_packed(fmt == "nf4", w, scales, E, N, K, "weights", "scales")
+    fn, need, drop = _lora_call("gnf4_grouped_gemm_lora" if fmt == "nf4" else "gmxfp4_grouped_gemm_lora", dropout, a)
     if out is None:
         out = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     if u is None:
@@ -551,7 +553,6 @@ def _gemm_lora(fmt, a, sizes, w, scales, lora_a, lora_b, scale, out, u, workspac
     _check_tensor(u, "u", torch.float32, (M, r))
     _require_gpu(a, sizes, w, scales, lora_a, lora_b, out, u)
     op = GEG_OP_NF4_FWD if fmt == "nf4" else GEG_OP_MXFP4_FWD
-    fn, need, drop = _lora_call("gnf4_grouped_gemm_lora" if fmt == "nf4" else "gmxfp4_grouped_gemm_lora", dropout)
     ws = _workspace(workspace, need(op, M, N, K, E, r), a.device, stream, check_errors)
     _check(fn(_ptr(a), _ptr(sizes), _ptr(w), _ptr(scales), _ptr(lora_a), _ptr(lora_b), float(scale), *drop, _ptr(out),
               _ptr(u), M, N, K, E, r, _ptr(ws.buf), ws.nbytes, ctypes.byref(opts) if opts else None, _stream(stream)))
@@ -586,6 +587,7 @@ def _dgrad_lora(fmt, dy, sizes, w, scales, x, lora_a, lora_b, u, scale, dx, grad
     _check_packed(fmt == "nf4", w, scales, E, N, K, "weights", "scales")
     _check_tensor(dy, "dy", torch.bfloat16, (M, N))
     _check_tensor(u, "u", torch.float32, (M, r))
+    fn, need, drop = _lora_call("gnf4_grouped_dgrad_lora" if fmt == "nf4" else "gmxfp4_grouped_dgrad_lora", dropout, x)
     if dx is None:
         dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
     if grad_a is None:
@@ -597,7 +599,6 @@ def _dgrad_lora(fmt, dy, sizes, w, scales, x, lora_a, lora_b, u, scale, dx, grad
     _check_tensor(grad_b, "grad_b", torch.float32, (E, N, r))
     _require_gpu(dy, sizes, w, scales, x, lora_a, lora_b, u, dx, grad_a, grad_b)
     op = GEG_OP_NF4_DGRAD if fmt == "nf4" else GEG_OP_MXFP4_DGRAD
-    fn, need, drop = _lora_call("gnf4_grouped_dgrad_lora" if fmt == "nf4" else "gmxfp4_grouped_dgrad_lora", dropout)
     ws = _workspace(workspace, need(op, M, N, K, E, r), dy.device, stream, check_errors)
     _check(fn(_ptr(dy), _ptr(sizes), _ptr(w), _ptr(scales), _ptr(x), _ptr(lora_a), _ptr(lora_b), _ptr(u),
               float(scale), *drop, _ptr(dx), _ptr(grad_a), _ptr(grad_b), M, N, K, E, r, _ptr(ws.buf), ws.nbytes,

@@ -104,3 +104,28 @@ def test_python_refusals():
             call()
     with pytest.raises(geg.GegError, match="seed"):
         geg.grouped_linear_lora(x, sz, w, sc, la, lb, 1.0, dropout=0.1)
+
+
+def test_a_seed_on_another_device():
+    """The words of a seed are read by the kernels: they have to be where the operands are."""
+    torch = pytest.importorskip("torch")
+
+    class On(torch.Tensor):
+        """A tensor that says it is on a GPU."""
+        __torch_function__ = torch._C._disabled_torch_function_impl
+        index = 0
+        device = property(lambda self: torch.device("cuda", self.index))
+
+        def get_device(self):
+            return self.index
+
+    on = lambda t: t.as_subclass(On)
+    x, sz = on(torch.zeros(6, 128, dtype=torch.bfloat16)), on(torch.zeros(2, dtype=torch.int32))
+    w, sc = on(torch.zeros(2, 64, 64, dtype=torch.uint8)), on(torch.zeros(2, 64, 2))
+    la, lb = on(torch.zeros(2, 16, 128)), on(torch.zeros(2, 64, 16))
+    words = on(torch.zeros(2, dtype=torch.int64))
+    words.index = 1
+    with pytest.raises(geg.GegError, match="several devices"):
+        geg.grouped_linear_lora(x, sz, w, sc, la, lb, 1.0, dropout=0.1, seed=words)
+    with pytest.raises(geg.GegError, match="several devices"):
+        geg.philox_dropout(x, 0.1, words)
