@@ -476,3 +476,83 @@ def test_an_expert_of_nearly_2_31_rows(geg):
     # the zeros between are exact; the three blocks of rows pass at most 20 instructions and 8 pieces
     _check(geg.grouped_wgrad(a, out, sz, dtype=torch.float32, check_errors=True), *_ref(x, out[rows], [0, n], "wgrad"), 28 * 32,
            "wgrad")
+
+
+def _pieces(seed):
+    """One expert, few tiles and a contraction of 8192."""
+    return _case("bf16", [64], 256, 8192, seed=seed)
+
+
+def test_pieces_are_chosen_by_the_sizes(geg):
+    log("case: 16-bit products, which kernels the sizes choose")
+    # tiles in eight and in four pieces, two launches; where two is the most, few rows go to the narrow kernel
+    for M, N, path, launches in ((3, 256, 0, 2), (64, 256, 0, 2), (3, 4096, 0, 2), (3, 8192, 0, 1), (64, 256, 4, 1)):
+        a, _, w, sz = _case("bf16", [M], N, 8192, seed=M)
+        geg.grouped_gemm(a, sz, w)   # (a workspace that grows is a launch)
+        before = geg.geg_launch_count()
+        got = geg.grouped_gemm(a, sz, w, opts=geg.Opts(path, 0))
+        assert geg.geg_launch_count() - before == launches
+        _check(got, *_ref(a, w, [M], "forward"), 8192, f"{M} rows, {N} columns, path {path}")
+
+
+def test_pieces_without_room_for_them(geg):
+    """A workspace of the error word alone: whole tiles, as documented."""
+    import ctypes
+    import torch
+    log("case: 16-bit products, a workspace too small for the pieces")
+    a, dy, w, sz = _pieces(3)
+    need = geg.lib().geg_grouped_workspace_bytes(0, 64, 256, 8192, 1)
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    ref = _ref(a, w, [64], "forward")
+    for nbytes in (256, need - 1, need):
+        ws = torch.zeros(max(nbytes, 512) + 256, dtype=torch.uint8, device="cuda")
+        ws[nbytes:] = 7
+        out = torch.empty(64, 256, dtype=a.dtype, device="cuda")
+        before = geg.geg_launch_count()
+        assert geg.lib().geg_grouped_gemm(a.data_ptr(), sz.data_ptr(), w.data_ptr(), out.data_ptr(), 0, 64, 256, 8192, 1, 0,
+                                          ws.data_ptr(), nbytes, None, stream) == 0
+        assert geg.geg_launch_count() - before == (2 if nbytes == need else 1)
+        _check(out, *ref, 8192, f"{nbytes} bytes")
+        assert (ws[nbytes:] == 7).all()
+
+
+def test_pieces_captured_and_on_streams_at_once(geg):
+    """The sums of the pieces stand in a workspace between two launches."""
+    import torch
+    log("case: 16-bit products in pieces, captured and on two streams")
+    a, _, w, sz = _pieces(1)
+    ga, dy, gw, gsz = _case("bf16", [5000], 128, 136, seed=2)      # the weights' gradient in pieces
+    _, da, dw, dsz = _case("bf16", [60], 4096, 136, seed=3)        # the activations' gradient in pieces
+
+    def step():
+        return geg.grouped_gemm(a, sz, w), geg.grouped_wgrad(dy, ga, gsz), geg.grouped_dgrad(da, dsz, dw)
+    step()
+    before = geg.geg_launch_count()
+    step()
+    assert geg.geg_launch_count() - before == 6
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in range(3):
+        a.copy_(_pieces(10 + seed)[0])
+        ga.copy_(_case("bf16", [5000], 128, 136, seed=20 + seed)[0])
+        da.copy_(_case("bf16", [60], 4096, 136, seed=30 + seed)[1])
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+    others = [_pieces(40 + i)[0] for i in range(2)]
+    want = [geg.grouped_gemm(o, sz, w) for o in others]
+    streams = [torch.cuda.Stream() for _ in others]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i].append(geg.grouped_gemm(others[i], sz, w))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, want[i]) for o in outs[i])

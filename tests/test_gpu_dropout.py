@@ -203,3 +203,40 @@ def test_adapter_dropout_leaves_the_projection_and_p_0(geg):
     assert torch.equal(geg.grouped_linear_lora(a, szt, wt, st, At, zero, 0.5, dropout=0.5, seed=1), base)
     with pytest.raises(geg.GegError, match="seed"):
         geg.grouped_linear_lora(a, szt, wt, st, At, Bt, 0.5, dropout=0.1)
+
+
+def test_captured_adapter_step(geg):
+    """Forward and backward of the adapter's path captured: the words of the seed and the inputs
+    change between replays, each as the eager step."""
+    import torch
+    from test_gpu_lora import _case
+    log("case: adapter dropout, a captured training step")
+    x, dy, A, B, sz, W, codes, scales = _case("nf4", 3, 256, 136, 16, [5, 40, 300], seed=4)
+    a, A, B = up_u16_as_bf16(x).requires_grad_(True), up(A).requires_grad_(True), up(B).requires_grad_(True)
+    szt, wt, st, d = up(sz), up(codes), up(scales), up_u16_as_bf16(dy)
+    words = torch.tensor([3, 0], dtype=torch.int64, device="cuda")
+
+    def step():
+        out = geg.grouped_linear_lora(a, szt, wt, st, A, B, 0.5, dropout=0.3, seed=words)
+        return (out.detach(), *torch.autograd.grad(out, (a, A, B), d))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    before = None
+    for i in range(4):
+        words.copy_(torch.tensor([3, 7 + i]))
+        with torch.no_grad():
+            a.mul_(0.5)
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
+        assert before is None or not torch.equal(before, want[0])
+        before = want[0]

@@ -330,3 +330,23 @@ def test_an_infinity_in_an_adapter(geg, dtype, r, M):
     assert ref[ids == 1].isinf().all()
     _, tol = _ref(y, wide, ids, torch.where(big.isfinite(), big, torch.zeros_like(big)), small, None)
     _same_places(geg.request_lora(y, wide, ids, big, small), ref, tol, "an infinity in u")
+
+
+def test_captured_with_many_adapters(geg):
+    """Counters of every adapter past the launch's usual LDS, in a captured call."""
+    import torch
+    log("case: request adapters, 20000 adapters captured")
+    y, x, ids, A, B, scales = _case("bf16", 700, 40, 72, 20000, 8, seed=12)
+    geg.request_lora(y, x, ids, A, B, scales)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = geg.request_lora(y, x, ids, A, B, scales)
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        ids.copy_(torch.randint(-1, 20000 >> (6 * seed), (700,), generator=g, device="cuda"))
+        want = geg.request_lora(y, x, ids, A, B, scales)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        _check(got, *_ref(y, x, ids, A, B, scales), f"replay {seed}")
