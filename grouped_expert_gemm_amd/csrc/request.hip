@@ -304,7 +304,7 @@ __global__ __launch_bounds__(kThreads) void request_down_kernel(RequestArgs g) {
 // run and no second round of workgroups is half empty. Bound by y and out: 8000 rows of 14336
 // columns, fp16, rank 64, read and write 459 MB in 116 to 125 us, 3.8 TB/s (a copy of 1 GiB: 5.2);
 // both pass the L2 by, 160 -> 152 us with the launches before. u enters the matrix instructions in two 16-bit parts, high and
-// rest (together 16 bits of it in bf16, 22 in fp16): for r <= 16 (PACK) side by side in one
+// rest (together within 2^-17 of it in bf16; in fp16 within 2^-22, or 2^-35 of its row's largest): for r <= 16 (PACK) side by side in one
 // instruction's contraction (slot group q, 8 wide, holds part q / (r / 8) of j = 8 (q % (r / 8)) ..),
 // else NB blocks of 32 of either against the same B. fp16 has too few exponents for that: a row of u
 // is scaled by a power of two that brings its largest value to [2^10, 2^11), undone in the fp32

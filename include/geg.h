@@ -545,7 +545,8 @@ geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes
  *   workspace: geg_request_lora_workspace_bytes(M, K, L, r) bytes (its first 256: the error word)
  * ceil(M / 32) + L at most 2^19, times ceil(N / 256) at most 2^23.
  * N, K and the pitches are multiples of 8, every tensor is 16-byte aligned. Sums run in fp32;
- * x A^T keeps at least 16 significant bits on its way into the second product; one rounding.
+ * x A^T enters the second product in two 16-bit parts: within 2^-17 of each value in bf16; in fp16
+ * within 2^-22 of the value or 2^-35 of its row's largest finite one, whichever is more. One rounding.
  * An adapter's values reach only the rows that name it. Rows routed to experts with
  * an adapter each have ids = adapter * E + expert over lora_a [adapters * E, r, K].
  */

@@ -350,3 +350,26 @@ def test_captured_with_many_adapters(geg):
         torch.cuda.synchronize()
         assert torch.equal(got, want)
         _check(got, *_ref(y, x, ids, A, B, scales), f"replay {seed}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("below", [0, 11, 25, 30])
+def test_how_exactly_u_is_kept(geg, dtype, below):
+    """One value of u 2^-below of its row's largest, whose column of B is zero: in bf16 within 2^-17 of
+    itself, in fp16 within 2^-22 of itself or 2^-35 of the largest; the output's rounding comes on top."""
+    import torch
+    log(f"case: request adapters {dtype}, u at 2^-{below} of its row's largest")
+    t, N, K = _types()[dtype], 72, 8
+    for M in (20, 400):
+        g = torch.Generator(device="cuda").manual_seed(below)
+        x, A, B = torch.zeros(M, K, device="cuda"), torch.zeros(1, 8, K, device="cuda"), torch.zeros(1, N, 8, device="cuda")
+        x[:, 0], x[:, 1] = torch.rand(M, generator=g, device="cuda") + 1, 1
+        A[0, 0, 1], A[0, 3, 0] = 2.0 ** 14, 1.3125 * 2.0 ** (14 - below)
+        B[0, :, 3] = (torch.rand(N, generator=g, device="cuda") + 1) * 2.0 ** (below - 16)   # below 2^15
+        x, A, B = x.to(t), A.to(t), B.to(t)
+        u = x[:, :1].double() * A[0, 3, 0].double()      # exact in fp32: two 16-bit values
+        kept = 2.0 ** -17 * u if dtype == "bf16" else torch.maximum(2.0 ** -22 * u, torch.full_like(u, 2.0 ** -35 * 2.0 ** 14))
+        ref = u * B[0, :, 3].double()
+        tol = kept * B[0, :, 3].double() + 2.0 ** -23 * ref
+        got = geg.request_lora(None, x, torch.zeros(M, dtype=torch.int32, device="cuda"), A, B)
+        _check(got, ref, tol + torch.finfo(t).eps / 2 * (ref + tol), f"{M} rows")
