@@ -13,6 +13,7 @@
 
 #include "geg_device.hpp"
 #include "geg_launch.hpp"
+#include "wide16.hpp"
 
 namespace geg {
 
@@ -21,32 +22,6 @@ namespace {
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
-
-__device__ __forceinline__ uint32_t oob_unless(bool ok, uint32_t off) { return off | ((uint32_t)!ok << 31); }
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t window(const void* base, int64_t bytes) {
-  const int32_t n = bytes <= 0 ? 0 : (bytes > 0x7FFFFFF0 ? 0x7FFFFFF0 : (int32_t)bytes);
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, n, 0x00020000);
-}
-
-// acc += first . second for one 16x16x32 block; a lane's results are four adjacent indices of
-// the first operand for one of the second.
-template <int T>
-__device__ __forceinline__ f32x4 mfma(const u32x4& first, const u32x4& second, const f32x4& acc) {
-  return mfma16<T == kBF16 ? MXFP4 : NF4>(first, second, acc);
-}
-
-template <int T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (T == kBF16) {
-    return pack_bf16x2(a, b);
-  } else {
-    f16x2 h;
-    h[0] = (_Float16)a;
-    h[1] = (_Float16)b;
-    return __builtin_bit_cast(uint32_t, h);
-  }
-}
 
 template <int N>
 __device__ __forceinline__ void step_barrier() {
@@ -345,7 +320,6 @@ __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int wm = wave >> 1, wn = wave & 1;
-  const int r16 = lane & 15, grp = lane >> 4;
   using W = Tiles<D, 256>;
   constexpr int TM = W::TM, TN = W::TN;
   const int64_t O = D == kDenseFwd ? g.N : g.K;
