@@ -211,12 +211,14 @@ struct Frag {
 
 // Cache policy of the tiles' stores: streamed past the XCD's L2, where they would displace the
 // operands that its tiles share (non-temporal, system scope). Both gradients of 1200 rows over 32
-// experts of 2880 x 2880, the weights' in fp32: 389 us without, 348 with; of 16384 rows over 64 of 2048 x
-// 2048, 16 bits: 452, 446.
+// experts of 2880 x 2880, the weights' in fp32: 387 us without, 346 with; of 16384 rows over 64 of 2048 x
+// 2048, 16 bits: 432, 409.
 constexpr int kStream = 18;
 
 // How results are stored: 16 bits in rows of whole 16-byte pieces, fp32, or 16 bits in rows of any
-// width, value by value (forward).
+// width, value by value (forward; a tile's stores are waited for before the next tile: one column less
+// than 5760 in 3108 rows over 32 experts of 2880 238 us for 217, than 14336 in 4096 over 8 of 4096 547 for
+// 463; the narrow kernel and tiles of 128 with one row per expert lose nothing).
 enum Out : int { kWide = 0, kF32Out = 1, kAnyWidth = 2 };
 // Stores per wavefront of 128 x 128 results (what lies past the rows and columns is dropped by the
 // window); value by value, none is left in flight.
@@ -300,14 +302,15 @@ __device__ __forceinline__ void store_quadrant(void* out, int64_t O, int64_t row
 // and the next four (in twos and threes: 4% slower with all CUs at work, 10% with half). The loads run on
 // across tiles, at their own place in the list.
 // Measured: 8192 rows over 8 experts of 28672 x 4096 1.47 ms with 1024 each, 1.31 PFLOP/s, 1.63 ms with the
-// sizes that a router gives (a library product of that many rows by one such expert: 1.33 to 1.48): an
+// sizes that a router gives (to 1.74 on other cards; a library product of that many rows by one such expert: 1.33 to 1.48): an
 // expert's last row block of 6 rows costs 0.4 of a whole one. LDS is as busy as the matrix pipes: 192 KB of
 // fragments and 64 KB of loads per stage, 2048 clocks, as 2048 of products; a stage takes 1.24 us on
 // one CU in eight at 2.4 GHz and 1.7 on all at 1.8. (Four wavefronts of 128 x 128 read a third less
 // and were slower, 1.36 and 1.9: alone on its SIMD a wavefront's loads hold its products up.) 3108 rows
-// over 32 experts of 5760 x 2880 215 us, 1.1 GB at 5.2 TB/s. 16384 rows over 64 of 2048 x 2048, both gradients one after
-// the other, 415 us: tiles of four stages in the weights', whose bursts of stores the next tile's loads wait
-// behind (with the stores dropped it takes 184 of its 270).
+// over 32 experts of 5760 x 2880 210 to 219 us, 1.1 GB at 5.2 TB/s. 16384 rows over 64 of 2048 x 2048, both
+// gradients one after the other, 406 to 432 us: tiles of four stages in the weights', whose bursts of stores the
+// next tile's loads wait behind (with the stores dropped it takes 184 of its 270), and whose contraction, an
+// expert's rows, is rounded up to two stages (257 rows run six of 64).
 template <int D, int T, int OUT>
 __global__ __launch_bounds__(TThreads, 1) void dense_tile_kernel(DenseArgs g) {
   __shared__ int32_t p_off[kMaxExperts + 1];

@@ -23,8 +23,10 @@
 //             dA_e = sum_rows g^T (m x)
 // Masking x is exact, the factor stays in fp32, and the tiled kernel masks the delta in its
 // epilogue, so dx is rounded once. The pass that masks x for dA writes the mask's bits for that:
-// drawn in the epilogue, they cost the kernel 150 us of 16384 x 2048 x 2048 (169 without dropout). A lane of the x A^T pass loads just the 8 values that one
-// generator call covers.
+// drawn in the epilogue, they cost the kernel 150 us of 16384 x 2048 x 2048 (169 without dropout). A lane of
+// the x A^T pass loads just the 8 values that one generator call covers. 16384 rows over 64 experts of
+// 2048 x 2048, rank 16 (without, with dropout): x A^T 35, 39 us; the pass that masks x 24; dgrad NF4 241, 250,
+// MXFP4 178, 186.
 #include <algorithm>
 
 #include "geg_device.hpp"

@@ -547,6 +547,7 @@ geg_status geg_grouped_wgrad(const void* dy, const void* a, const int32_t* sizes
  * N, K and the pitches are multiples of 8, every tensor is 16-byte aligned. Sums run in fp32;
  * x A^T enters the second product in two 16-bit parts: within 2^-17 of each value in bf16; in fp16
  * within 2^-22 of the value or 2^-35 of its row's largest finite one, whichever is more. One rounding.
+ * An infinity in an adapter gives infinities, and NaN where it meets 0 (or a value that the bound makes 0).
  * An adapter's values reach only the rows that name it. Rows routed to experts with
  * an adapter each have ids = adapter * E + expert over lora_a [adapters * E, r, K].
  */
